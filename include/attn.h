@@ -75,7 +75,8 @@ enum attn_status {
     ATTN_ERR_UNSUPPORTED = -2, /* valid attention, but outside what the kernels implement */
     ATTN_ERR_CUDA = -3,        /* a CUDA runtime / driver call failed */
     ATTN_ERR_TIMEOUT = -4,     /* (status word) a pipeline wait gave up after its time limit */
-    ATTN_ERR_BOUNDS = -5,      /* (status word) block-table entry outside [0, num_pages) */
+    ATTN_ERR_BOUNDS = -5,      /* (status word) block-table entry outside [0, num_pages), or a
+                                  position outside the rotation table */
     ATTN_ERR_WORKSPACE = -6,   /* workspace missing or smaller than attn_workspace_bytes() */
     ATTN_ERR_SEQLENS = -7      /* (status word) cu_seqlens not monotone / not ending at N */
 };
@@ -246,6 +247,138 @@ int attn_paged_decode_noalloc(const void *q, const void *k, const void *v, void 
  * tickets come on top): a request is served iff attn_workspace_bytes() of it, with mask_kind
  * PAGED_DECODE, is at most this. */
 size_t attn_noalloc_scratch_bytes(void);
+
+/*
+ * attn_norm_rope — queries and keys from a projection, ready for attention: the RMS norm of
+ * every head's row and the position rotation in one pass, written in the layouts attn_fwd
+ * reads. (No counterpart on the pages; the attention entry points take q and k so prepared.)
+ *
+ * A row x of d channels, in fp32, rounded to bf16 once at the end:
+ *   norm      y_c = x_c * weight_c / sqrt(mean_c x_c^2 + eps)        (weight NULL: y = x)
+ *   rotation  for i < rot_dim / 2 the pair (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved,
+ *             turns by the angle of position pos:  a' = a cos - b sin,  b' = b cos + a sin;
+ *             channels >= rot_dim pass              (rot_dim 0: no rotation)
+ * q, k      bf16 token rows: head h of token t at x + t * stride + h * d. Strides count elements:
+ *           at least the heads' Hq * d (Hkv * d), a multiple of 8; a fused projection's width
+ *           where q, k and v share one buffer. q or k may be NULL (not both): it is left out.
+ * q_out, k_out bf16 [total / N, H, N, d]: token t is row t % N of block t / N. N = 1 gives
+ *           decode's [B, H, 1, d]; N = total the packed [1, H, total, d]; a prompt length N
+ *           the dense [B, H, N, d]. Must not overlap q or k.
+ * total     tokens, a multiple of N. Hq, Hkv: any counts; d 64 or 128.
+ * q_weight, k_weight fp32 [d], each may be NULL. eps >= 0 (read if a weight is given).
+ * cos_sin   fp32 [max_pos, rot_dim]: of every position rot_dim/2 cosines, then rot_dim/2 sines.
+ * rot_dim   0 or a multiple of 16 up to d.
+ * positions int32 [total]; NULL: t % N. A position outside [0, max_pos) sets ATTN_ERR_BOUNDS
+ *           and its token's rows are not written.
+ * Every tensor is 16-byte aligned (positions 4). No workspace; asynchronous on `stream`.
+ */
+int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int total, int N,
+                   int Hq, int Hkv, int d, int64_t q_stride, int64_t k_stride,
+                   const float *q_weight, const float *k_weight, float eps,
+                   const float *cos_sin, int max_pos, int rot_dim, int interleaved,
+                   const int32_t *positions, void *stream);
+
+/*
+ * attn_append_paged — new tokens' keys and values into a paged cache, normed and rotated on the
+ * way, and their queries made ready in the same launch. The block-table layout is that of
+ * attn_fwd's PAGED_DECODE and attn_fwd_paged_prefill, which read the pools next.
+ *
+ * Sequence b's new tokens are rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 of q, k and v, the
+ * last ones of its context of seqlens_k[b] tokens: row t is context position
+ * pos = seqlens_k[b] - Lq_b + t. Its key goes to slot pos % page_size of page
+ * block_table[b][pos / page_size], normed and rotated (as attn_norm_rope's k, by pos), its value
+ * as it is. Other slots are left as they are. One page must not take new tokens of two
+ * sequences.
+ * q, k, v   bf16 token rows with strides q_stride, k_stride, v_stride, as for attn_norm_rope. q
+ *           may be NULL (then q_out, Hq and q_weight are not used).
+ * q_out     bf16 [total_q / N, Hq, N, d]: N = 1 for decode's [B, Hq, 1, d], N = total_q for
+ *           chunked prefill's [1, Hq, total_q, d].
+ * k_pool, v_pool bf16 [num_pages, Hkv, page_size, d].
+ * cu_seqlens_q int32 [B+1]: cu[0] = 0, nondecreasing, cu[B] <= total_q. Rows from cu[B] on belong
+ *           to no sequence and nothing is written for them (a padded batch of a captured graph).
+ * seqlens_k int32 [B]: Lq_b <= seqlens_k[b] <= max_pages * page_size.
+ *           Both are checked on the device (ATTN_ERR_SEQLENS); a sequence that breaks them is
+ *           not written.
+ * block_table int32 [B, max_pages]. Only the new tokens' entries are read; one outside
+ *           [0, num_pages) sets ATTN_ERR_BOUNDS and that token's key and value are not written.
+ * cos_sin, max_pos, rot_dim, interleaved, q_weight, k_weight, eps, d as for attn_norm_rope.
+ *           A position outside [0, max_pos) sets ATTN_ERR_BOUNDS; nothing of its token is
+ *           written.
+ * page_size 16, 32, 64 or 128. No workspace; asynchronous on `stream`.
+ */
+int attn_append_paged(const void *q, const void *k, const void *v, void *q_out, void *k_pool,
+                      void *v_pool, int B, int Hq, int Hkv, int total_q, int N, int d,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      const float *q_weight, const float *k_weight, float eps,
+                      const float *cos_sin, int max_pos, int rot_dim, int interleaved,
+                      const int32_t *cu_seqlens_q, const int32_t *seqlens_k,
+                      const int32_t *block_table, int max_pages, int page_size, int num_pages,
+                      void *stream);
+
+/*
+ * attn_append_paged_fp4 — attn_append_paged into a cache held in 4 bits.
+ *
+ * Pool format: bytes [num_pages, Hkv, page_size * (d/2 + d/16)]. A (page, kv head) block holds its
+ * tokens' codes, d/2 bytes each (channel 2c in the low nibble of byte c), then their scales,
+ * d/16 bytes each, one E4M3 scale per 16 channels: 4.5 bits an element. Codes are E2M1 (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and a sign); a value is code * scale * k_scale (v_scale).
+ * Of a key or value y (fp32, not rounded to bf16 in between):
+ *   xs    = y * (1 / k_scale)                       (the reciprocal rounded to fp32)
+ *   scale = E4M3(max over the 16 channels |xs| / 6) (to nearest even, saturating at 448)
+ *   code  = E2M1(xs / scale)                        (to nearest even, saturating; 0 if scale is 0)
+ * with IEEE fp32 products, sums and divisions throughout (the rotation's too). y must be
+ * finite.
+ * k_scale, v_scale > 0, finite, with finite reciprocals: one scale a tensor. About
+ * max |y| / 2688 uses the scales' whole range; 1 serves values between about 0.05 and 2688.
+ * rot_dim   a multiple of 32, or of 16 if interleaved (else ATTN_ERR_UNSUPPORTED).
+ * Everything else as for attn_append_paged.
+ */
+int attn_append_paged_fp4(const void *q, const void *k, const void *v, void *q_out, void *k_pool,
+                          void *v_pool, float k_scale, float v_scale, int B, int Hq, int Hkv,
+                          int total_q, int N, int d, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, const float *q_weight, const float *k_weight,
+                          float eps, const float *cos_sin, int max_pos, int rot_dim,
+                          int interleaved, const int32_t *cu_seqlens_q,
+                          const int32_t *seqlens_k, const int32_t *block_table, int max_pages,
+                          int page_size, int num_pages, void *stream);
+
+/*
+ * attn_unpack_pages_fp4 — pages of a 4-bit pool as bf16 pages, for readers of bf16 pools (chunked
+ * prefill on a 4-bit cache: attn_fwd_paged_prefill with the table of consecutive pages).
+ * dst bf16 [B * max_pages, Hkv, page_size, d]: page block_table[b][p] goes to dst page
+ * b * max_pages + p, every value rounded to bf16 once. seqlens int32 [B] (0 <= seqlens[b] <=
+ * max_pages * page_size, else ATTN_ERR_SEQLENS and sequence b is skipped): slots of the last
+ * page past it are written as zeros, whatever the pool holds there; pages past it are neither
+ * read nor written. An entry outside [0, num_pages) sets ATTN_ERR_BOUNDS and its page is
+ * skipped. pool and dst 16-byte aligned; B <= 65535. Asynchronous on `stream`.
+ */
+int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
+                          const int32_t *block_table, const int32_t *seqlens, int B,
+                          int max_pages, int Hkv, int page_size, int d, int num_pages,
+                          void *stream);
+
+/*
+ * attn_fwd_paged_decode_fp4 — paged decode over a 4-bit cache: attn_fwd's PAGED_DECODE with pools
+ * in attn_append_paged_fp4's format. K and V are their exact values code * scale * k_scale
+ * (v_scale); products accumulate in fp32, softmax weights enter the second product in f16.
+ * q, o      bf16 [B, Hq, 1, d]; lse fp32 [B, Hq], natural log.
+ * k, v      4-bit pools (16-byte aligned). Slots past a sequence's context may hold anything.
+ * N         the longest context (block_table has ceil(N / page_size) columns); N <= 2^30.
+ * cu_seqlens, block_table, num_pages, page_size, Hq, Hkv, scale as for attn_fwd's PAGED_DECODE:
+ *           at most 16 query heads per kv head; a bad length gives O = 0, LSE = -inf and
+ *           ATTN_ERR_SEQLENS; a table entry outside the pool sets ATTN_ERR_BOUNDS and its page
+ *           reads as zeros. L_b = 0 gives O = 0 and LSE = -inf.
+ * workspace of at least attn_workspace_bytes_fp4(...) bytes (may be NULL when that is 0); contents
+ *           need not be initialised; concurrent calls need separate ones.
+ */
+int attn_fwd_paged_decode_fp4(const void *q, const void *k, const void *v, void *o, float *lse,
+                              int B, int Hq, int Hkv, int N, int d, float scale, float k_scale,
+                              float v_scale, const int32_t *cu_seqlens,
+                              const int32_t *block_table, int page_size, int num_pages,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace attn_fwd_paged_decode_fp4 needs for these arguments. */
+size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d);
 
 /* Synchronises `stream`, then returns and clears the device status word (ATTN_OK or one of
  * ATTN_ERR_TIMEOUT / ATTN_ERR_BOUNDS / ATTN_ERR_SEQLENS), or ATTN_ERR_CUDA if the stream

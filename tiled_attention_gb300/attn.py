@@ -38,6 +38,8 @@ _lib = None
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
+_l = ctypes.c_int64
+_f = ctypes.c_float
 _SIGS = {
     "attn_fwd": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _p, _p, _i,
                       _i, _p, ctypes.c_size_t, _p]),
@@ -62,6 +64,16 @@ _SIGS = {
     "attn_bench_ex2": (_i, [_p, _i, _i, _p]),
     "attn_noalloc_scratch_bytes": (ctypes.c_size_t, []),
     "attn_cached_device_state": (_i, [_i]),
+    "attn_norm_rope": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _l, _l, _p, _p, _f, _p, _i, _i,
+                            _i, _p, _p]),
+    "attn_append_paged": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _l, _l, _l, _p, _p,
+                               _f, _p, _i, _i, _i, _p, _p, _p, _i, _i, _i, _p]),
+    "attn_append_paged_fp4": (_i, [_p, _p, _p, _p, _p, _p, _f, _f, _i, _i, _i, _i, _i, _i, _l, _l,
+                                   _l, _p, _p, _f, _p, _i, _i, _i, _p, _p, _p, _i, _i, _i, _p]),
+    "attn_unpack_pages_fp4": (_i, [_p, _p, _f, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
+    "attn_fwd_paged_decode_fp4": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _f, _p, _p,
+                                       _i, _i, _p, ctypes.c_size_t, _p]),
+    "attn_workspace_bytes_fp4": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
 }
 
 
@@ -168,6 +180,67 @@ def attn_gather_pages(pool, dst, block_table, B, max_pages, Hkv, page_size, d, n
                       stream=None) -> int:
     return lib().attn_gather_pages(_ptr(pool), _ptr(dst), _ptr(block_table), B, max_pages, Hkv,
                                    page_size, d, num_pages, _stream(stream))
+
+
+def attn_norm_rope(q, k, q_out, k_out, total, N, Hq, Hkv, d, q_stride, k_stride, q_weight=None,
+                   k_weight=None, eps=1e-6, cos_sin=None, max_pos=0, rot_dim=0,
+                   interleaved=False, positions=None, stream=None) -> int:
+    """Per-head RMS norm and rotation of q and k token rows (strides in elements, so q and k may
+    be views into one projection) into attention's layouts."""
+    return lib().attn_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), total, N, Hq, Hkv, d,
+                                q_stride, k_stride, _ptr(q_weight), _ptr(k_weight), eps,
+                                _ptr(cos_sin), max_pos, rot_dim, interleaved, _ptr(positions),
+                                _stream(stream))
+
+
+def attn_append_paged(q, k, v, q_out, k_pool, v_pool, B, Hq, Hkv, total_q, N, d, q_stride,
+                      k_stride, v_stride, q_weight, k_weight, eps, cos_sin, max_pos, rot_dim,
+                      interleaved, cu_seqlens_q, seqlens_k, block_table, max_pages, page_size,
+                      num_pages, stream=None) -> int:
+    """New tokens' K / V into bf16 page pools, normed and rotated, with their queries."""
+    return lib().attn_append_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool),
+                                   _ptr(v_pool), B, Hq, Hkv, total_q, N, d, q_stride, k_stride,
+                                   v_stride, _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin),
+                                   max_pos, rot_dim, interleaved, _ptr(cu_seqlens_q),
+                                   _ptr(seqlens_k), _ptr(block_table), max_pages, page_size,
+                                   num_pages, _stream(stream))
+
+
+def attn_append_paged_fp4(q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, B, Hq, Hkv, total_q,
+                          N, d, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin,
+                          max_pos, rot_dim, interleaved, cu_seqlens_q, seqlens_k, block_table,
+                          max_pages, page_size, num_pages, stream=None) -> int:
+    """attn_append_paged into 4-bit pools (uint8 [num_pages, Hkv, page_size * (d/2 + d/16)])."""
+    return lib().attn_append_paged_fp4(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool),
+                                       _ptr(v_pool), k_scale, v_scale, B, Hq, Hkv, total_q, N, d,
+                                       q_stride, k_stride, v_stride, _ptr(q_weight),
+                                       _ptr(k_weight), eps, _ptr(cos_sin), max_pos, rot_dim,
+                                       interleaved, _ptr(cu_seqlens_q), _ptr(seqlens_k),
+                                       _ptr(block_table), max_pages, page_size, num_pages,
+                                       _stream(stream))
+
+
+def attn_unpack_pages_fp4(pool, dst, pool_scale, block_table, seqlens, B, max_pages, Hkv,
+                          page_size, d, num_pages, stream=None) -> int:
+    """4-bit pages, as the table lists them, to bf16 pages [B * max_pages, Hkv, page_size, d]."""
+    return lib().attn_unpack_pages_fp4(_ptr(pool), _ptr(dst), pool_scale, _ptr(block_table),
+                                       _ptr(seqlens), B, max_pages, Hkv, page_size, d, num_pages,
+                                       _stream(stream))
+
+
+def attn_fwd_paged_decode_fp4(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, k_scale, v_scale,
+                              cu_seqlens, block_table, page_size, num_pages, workspace=None,
+                              stream=None) -> int:
+    """Paged decode over 4-bit pools (torch tensors in device memory)."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return lib().attn_fwd_paged_decode_fp4(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq,
+                                           Hkv, N, d, scale, k_scale, v_scale, _ptr(cu_seqlens),
+                                           _ptr(block_table), page_size, num_pages,
+                                           _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def attn_workspace_bytes_fp4(B, Hq, Hkv, N, d) -> int:
+    return lib().attn_workspace_bytes_fp4(B, Hq, Hkv, N, d)
 
 
 def attn_selftest_wait_timeout(timeout_ns: int, stream=None) -> int:

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/attn.h"
+#include "api.h"
 #include "launch.h"
 #include "sched.h"
 
@@ -22,6 +23,7 @@ namespace ta {
 // ------------------------------------------------------------------ errors
 namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -36,7 +38,8 @@ int fail(int code, const char* fmt, ...) {
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(ATTN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
-}  // namespace
+
+void clear_error() { g_last_error.clear(); }
 
 // ------------------------------------------------------------------ device status word
 // One int per device (a __device__ variable exists once per device context).
@@ -77,6 +80,7 @@ int sm_count(int* out) {
   *out = g_num_sms[dev];
   return ATTN_OK;
 }
+}  // namespace
 
 int status_ptr(int** out) {
   int dev = 0;
@@ -94,6 +98,7 @@ int status_ptr(int** out) {
   return ATTN_OK;
 }
 
+namespace {
 // ------------------------------------------------------------------ tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
@@ -147,8 +152,6 @@ int encode_3d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
   return ATTN_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Mask kinds served by the prefill kernel.
 bool prefill_kind(int m) {
   return m == ATTN_MASK_NONE || m == ATTN_MASK_CAUSAL || m == ATTN_MASK_SLIDING ||
@@ -158,17 +161,6 @@ bool prefill_kind(int m) {
 
 bool document_kind(int m) { return m == ATTN_MASK_DOCUMENT || m == ATTN_MASK_DOCUMENT_BIDIR; }
 
-// Page sizes of the paged kinds: multiples of the 8-row swizzle atom that divide the
-// 128-row prefill tile and either divide or are twice the 64-row decode stage.
-bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
-
-// log2 of a power of two (the page sizes page_size_ok accepts).
-int log2_exact(int p) {
-  int s = 0;
-  while ((1 << s) < p) ++s;
-  return s;
-}
-
 // The window argument: SLIDING needs >= 1 key, SLIDING_BIDIR >= 0 keys per side, PREFIX_LM a
 // prefix of >= 0 tokens; the other kinds ignore it.
 bool window_ok(int m, int window) {
@@ -177,17 +169,14 @@ bool window_ok(int m, int window) {
   return true;
 }
 
-constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kDecodeStage = 64;       // tokens per decode ring stage
-constexpr int kMaxDecodeGroup = 16;    // query heads per kv head: the rows of one MMA tile
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeLayout {
   size_t part_o, part_ml, counters, total;
   int max_pages, max_splits, chunk_pages;
 };
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+}  // namespace
 
 // Streaming multiprocessors of the current device, or 152 (GB300's count) when no device is
 // visible, so that host-only callers size workspaces the same way. Sets no error message.
@@ -208,6 +197,7 @@ int sms_or_default() {
   return g_num_sms[dev];
 }
 
+namespace {
 // 64-token stages per split-KV CTA. Longer CTAs spend less on start-up and on the combine,
 // but need enough (sequence, kv head) groups to fill the GPU. Measured on GB300: with 32
 // sequences x 8 kv heads of 1K-16K tokens, 32 stages run 3.5 % faster than 16 with 64-token
