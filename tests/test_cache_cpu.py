@@ -196,6 +196,7 @@ def _decode(**kw):
     (dict(q=ODD), INVALID),
     (dict(k=ODD), INVALID),
     (dict(B=70000), UNSUPPORTED),
+    (dict(B=60000, N=2 ** 29), UNSUPPORTED),  # more blocks than an int counts
     (dict(B=-1), INVALID),
     (dict(), WORKSPACE),
 ])
@@ -211,13 +212,13 @@ def test_decode_fp4_empty_is_a_no_op():
 
 def test_decode_fp4_workspace():
     need = attn.attn_workspace_bytes_fp4(32, 32, 8, 16384, 128)
-    assert need > 0
-    # partial O and (max, sum) of every split and head, and one ticket a group
-    assert need % 256 == 0
-    assert attn.attn_workspace_bytes_fp4(1, 32, 8, 128, 128) == 0  # one split: no partials
+    # two partial rows of 4 heads a resident CTA, O and (max, sum): the batch and the contexts
+    # do not matter, the group does
+    assert need > 0 and need % 256 == 0
+    assert attn.attn_workspace_bytes_fp4(1, 32, 8, 131072, 128) == need
+    assert attn.attn_workspace_bytes_fp4(32, 64, 8, 16384, 128) > need
     assert attn.attn_workspace_bytes_fp4(0, 32, 8, 128, 128) == 0
-    big = attn.attn_workspace_bytes_fp4(32, 32, 8, 131072, 128)
-    assert big > need
+    assert attn.attn_workspace_bytes_fp4(1, 32, 8, 128, 96) == 0
 
 
 # ------------------------------------------------------------------ the oracle's own pins

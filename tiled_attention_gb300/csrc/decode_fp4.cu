@@ -8,42 +8,58 @@
 #include "api.h"
 #include "launch.h"
 
+#ifndef FP4_MIN
+#define FP4_MIN 4
+#define FP4_OVER 1
+#endif
 namespace ta {
 namespace {
 
-struct Fp4Layout {
-  size_t part_ml, counters, total;
-  int chunk_stages, max_splits;
-};
+constexpr int kFp4MinBlocks = FP4_MIN;
 
-// 128-token stages per split-KV CTA.
-int fp4_chunk_stages(int B, int Hkv) {
-  return static_cast<long long>(B) * Hkv >= sms_or_default() ? 16 : 4;
+// CTAs of the decode kernel: as many as the GPU holds at once.
+int fp4_slots(int d, int group) {
+  const int per = d == 64 ? (group <= 8 ? DecodeFp4Cfg<64, 1>::kCtas : DecodeFp4Cfg<64, 2>::kCtas)
+                          : (group <= 8 ? DecodeFp4Cfg<128, 1>::kCtas : DecodeFp4Cfg<128, 2>::kCtas);
+  return per * sms_or_default() * FP4_OVER;
 }
 
-Fp4Layout fp4_layout(int B, int Hq, int Hkv, int N, int d) {
+struct Fp4Layout {
+  size_t part_ml, total;
+  int slots;
+};
+
+// Two partial rows of every query head of a group a CTA: O, then (max, sum).
+Fp4Layout fp4_layout(int Hq, int Hkv, int d) {
   Fp4Layout L{};
-  L.chunk_stages = fp4_chunk_stages(B, Hkv);
-  const long long stages = (static_cast<long long>(N) + 127) / 128;
-  L.max_splits = static_cast<int>((stages + L.chunk_stages - 1) / L.chunk_stages);
-  if (L.max_splits <= 1) return L;  // one CTA per (sequence, kv head): no partials
-  const size_t groups = static_cast<size_t>(B) * Hkv;
-  const size_t rows = groups * L.max_splits * static_cast<size_t>(Hq / Hkv);
+  const int group = Hq / Hkv;
+  L.slots = fp4_slots(d, group);
+  const size_t rows = 2 * static_cast<size_t>(L.slots) * group;
   L.part_ml = align256(rows * d * sizeof(float));
-  L.counters = L.part_ml + align256(rows * 2 * sizeof(float));
-  L.total = L.counters + align256(groups * sizeof(int));
+  L.total = L.part_ml + align256(rows * 2 * sizeof(float));
   return L;
 }
 
 template <int D, int NT>
-cudaError_t launch_one(const DecodeFp4Params& p, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_one(const DecodeFp4Params& p, cudaStream_t stream) {
   static unsigned long long done = 0;
   auto kern = decode_fp4_kernel<D, NT>;
   using C = DecodeFp4Cfg<D, NT>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  kern<<<p.slots, C::kThreads, C::kSmemBytes, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // The joining kernel may start before the decode kernel has ended (it waits for it).
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.Hq, p.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_fp4_kernel<D>, p);
 }
 
 }  // namespace
@@ -54,8 +70,8 @@ using namespace ta;
 extern "C" {
 
 size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0) return 0;
-  return fp4_layout(B, Hq, Hkv, N, d).total;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || (d != 64 && d != 128) || Hq < Hkv) return 0;
+  return fp4_layout(Hq, Hkv, d).total;
 }
 
 int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -88,9 +104,11 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   if (num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
-  const Fp4Layout L = fp4_layout(B, Hq, Hkv, N, d);
-  if (Hkv > 65535 || B > 65535) return fail(ATTN_ERR_UNSUPPORTED, "decode grid too large");
-  if (L.total && (!workspace || workspace_bytes < L.total || !aligned16(workspace)))
+  if (B > 65535 ||
+      static_cast<long long>(B) * Hkv >= (1ll << 31) / ((static_cast<long long>(N) + 127) / 128))
+    return fail(ATTN_ERR_UNSUPPORTED, "decode batch too large");
+  const Fp4Layout L = fp4_layout(Hq, Hkv, d);
+  if (!workspace || workspace_bytes < L.total || !aligned16(workspace))
     return fail(ATTN_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned)", L.total);
   DecodeFp4Params p{};
   int rc = status_ptr(&p.status);
@@ -105,13 +123,13 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
-  p.counters = reinterpret_cast<int*>(ws + L.counters);
+  p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.max_pages = (N + page_size - 1) / page_size;
   p.num_pages = num_pages;
-  p.max_splits = L.max_splits;
-  p.chunk_stages = L.chunk_stages;
+  p.slots = L.slots;
+  p.min_blocks = kFp4MinBlocks;
   p.group = group;
   p.page_shift = log2_exact(page_size);
   p.max_len = N;
@@ -120,15 +138,10 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.timeout_ns = kTimeoutNs;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   cudaError_t e;
-  if (L.total) {
-    e = cudaMemsetAsync(p.counters, 0, sizeof(int) * static_cast<size_t>(B) * Hkv, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(counters)");
-  }
-  const dim3 grid(L.max_splits, Hkv, B);
   if (d == 64)
-    e = group <= 8 ? launch_one<64, 1>(p, grid, stream) : launch_one<64, 2>(p, grid, stream);
+    e = group <= 8 ? launch_one<64, 1>(p, stream) : launch_one<64, 2>(p, stream);
   else
-    e = group <= 8 ? launch_one<128, 1>(p, grid, stream) : launch_one<128, 2>(p, grid, stream);
+    e = group <= 8 ? launch_one<128, 1>(p, stream) : launch_one<128, 2>(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   return ATTN_OK;
 }

@@ -23,9 +23,21 @@
 //     the head's scale. P in f16: 2^(s - m + 7), at most 2^15, where m trails the running
 //     max by less than 8; f16 keeps 11 bits of it where bf16 would keep 8.
 //
-// CTA: one split (a run of 128-token stages) of one (sequence, kv head); four consumer warps,
-// 32 tokens of a stage each, and a producer warp that brings every page of a stage in with one
-// bulk copy for K and one for V. The split, merge and ticket scheme is the bf16 decode's.
+// Work: the contexts are cut into 128-token blocks, numbered over sequence, kv head and
+// position, and CTA i of nn takes blocks [i U / nn, (i + 1) U / nn): every CTA streams the same
+// number of bytes whatever the lengths are, and finds its range from cu_seqlens alone. A range
+// is one or more segments, each of one (sequence, kv head). A segment that is the whole
+// context writes O and LSE itself; the others (a CTA's first and last at most) leave the
+// unnormalised O, the reference max and the sum in the workspace, two slots a CTA, and a
+// second kernel joins them in CTA order, so results do not depend on timing:
+//   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  O = sum_c O_c 2^(m_c - M) / L,
+//   LSE = (M + log2 L) ln 2.
+// The second kernel starts under programmatic dependent launch: it finds its parts while the
+// first still runs. No counters, so no memset.
+//
+// CTA: four warps; warp w takes tokens [32 w, 32 w + 32) of every block, through a ring of its
+// own in shared memory: it brings the next slices in with bulk copies while it works on one, so
+// no warp waits for another before a segment's end.
 #pragma once
 
 #include "fp4.cuh"
@@ -33,6 +45,8 @@
 #include "sched.h"
 
 namespace ta {
+
+constexpr int kFp4Block128 = 128;  // tokens per block of the work list
 
 struct DecodeFp4Params {
   const uint4* q;        // bf16 [B, Hq, 1, D]
@@ -42,10 +56,11 @@ struct DecodeFp4Params {
   const int* table;      // [B, max_pages]
   uint16_t* o;           // bf16 [B, Hq, 1, D]
   float* lse;            // [B, Hq]
-  float* part_o;         // [B*Hkv, max_splits, G, D]
-  float* part_ml;        // [B*Hkv, max_splits, G, 2]
-  int* counters;         // [B*Hkv], zero before the launch
-  int Hq, Hkv, max_pages, num_pages, max_splits, chunk_stages, group, page_shift, max_len;
+  float* part_o;         // [2 * slots, group, D]
+  float* part_ml;        // [2 * slots, group, 2]
+  int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
+  int slots;             // CTAs of the decode kernel
+  int min_blocks;        // least blocks a CTA takes
   float scale_log2;      // softmax scale * K tensor scale * log2 e
   float v_scale;
   int* status;
@@ -54,27 +69,29 @@ struct DecodeFp4Params {
 
 template <int D, int NT>  // NT: 8-head column tiles (1 or 2)
 struct DecodeFp4Cfg {
-  static constexpr int kTok = 128;  // tokens per ring stage
+  static constexpr int kTok = 32;  // tokens per slice: two 16-row tiles
   static constexpr int kWarps = 4;
-  static constexpr int kConsumers = kWarps * 32;
-  static constexpr int kThreads = kConsumers + 32;
-  static constexpr int kCode = D / 2, kScale = D / 16, kRow = kCode + kScale;
-  static constexpr int kHalf = kTok * kRow;        // K (or V) of a stage
-  static constexpr int kStageBytes = 2 * kHalf;
-  static constexpr int kStages = 4 * 128 / D;      // 4 x 18 KB (D = 128), 8 x 9 KB (D = 64)
-  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kCtas = D == 128 && NT == 2 ? 3 : 4;  // per SM
+  static constexpr int kCode = D / 2, kScale = D / 16;
+  // A slice in shared memory: K codes, K scales, V codes, V scales.
+  static constexpr int kOffKs = kTok * kCode, kOffV = kOffKs + kTok * kScale;
+  static constexpr int kSliceBytes = 2 * kOffV;      // 4608 (D = 128), 2304 (D = 64)
+  static constexpr int kStages = 3 * 128 / D;        // slices per warp's ring
+  static constexpr int kRingBytes = kStages * kSliceBytes;
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kSteps = D / 16;            // k-steps of S^T, m-tiles of O^T
+  static constexpr int kSteps = D / 16;              // k-steps of S^T, m-tiles of O^T
   static constexpr int kMiscBytes = 256 + 2 * kWarps * 16 * 4;
-  static constexpr int kSmemBytes = kRingBytes + kMiscBytes + 128;
-  static_assert(kWarps * kHeads * D * 4 <= kRingBytes, "the warps' O rows reuse the ring");
+  static constexpr int kSmemBytes = kWarps * kRingBytes + kMiscBytes + 128;
+  static_assert(kWarps * kHeads * D * 4 <= kWarps * kRingBytes, "the O rows reuse the rings");
+  static_assert(kWarps * kStages * 8 <= 192, "barriers");
 };
 
 struct DecodeFp4Ctrl {
-  uint64_t full[8];
-  uint64_t empty[8];
+  uint64_t full[24];  // [warps][stages]
   int abort_flag;
-  int is_last;
+  int seq, seq_before;
+  int warp_sum[4];
 };
 
 // D(16x8, fp32) += A(16x16, f16, row-major) * B(16x8, f16, column-major).
@@ -108,444 +125,573 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t dup_lo(uint32_t a) { return __byte_perm(a, a, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t a) { return __byte_perm(a, a, 0x3232); }
 
+// One slice: S^T, the softmax step and O^T of 32 tokens, of which the first `left` belong to
+// the context. EDGE: some do not; the others run without a mask.
+template <int D, int NT, bool EDGE>
+__device__ __forceinline__ void fp4_slice(const uint8_t* sl, int left, int r, int q,
+                                          const uint32_t (&qb)[NT][D / 16][2],
+                                          const float (&sc)[NT][2], float (&o)[NT][D / 16][4],
+                                          float (&mref)[NT][2], float (&l)[NT][2]) {
+  using C = DecodeFp4Cfg<D, NT>;
+  constexpr int kWords = D / 64;  // 32-bit words of V codes per lane and token; K: 2 kWords
+  // ---- S^T = K Q^T, tiles of 16 tokens
+  float s[2][NT][4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t w[2][2 * kWords], sf[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 16 * u + r + 8 * x;
+      if constexpr (D == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sl + row * C::kCode + 16 * q);
+        w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+        sf[x] = e4m3x2_to_f16(
+            *reinterpret_cast<const uint16_t*>(sl + C::kOffKs + row * C::kScale + 2 * q));
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(sl + row * C::kCode + 8 * q);
+        w[x][0] = v.x, w[x][1] = v.y;
+        sf[x] = e4m3x2_to_f16(sl[C::kOffKs + row * C::kScale + q]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * kWords; ++i) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t ss = i < 2 ? dup_lo(sf[x]) : dup_hi(sf[x]);
+        e2m1x8_to_f16(w[x][i], a[x]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[x][e] = hmul2(a[x][e], ss);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16_16816(s[u][nt], a[0][0], a[1][0], a[0][1], a[1][1], qb[nt][2 * i][0],
+                      qb[nt][2 * i][1]);
+        mma_f16_16816(s[u][nt], a[0][2], a[1][2], a[0][3], a[1][3], qb[nt][2 * i + 1][0],
+                      qb[nt][2 * i + 1][1]);
+      }
+    }
+  }
+  // ---- softmax: columns are heads 2q, 2q + 1, rows tokens r and r + 8 of each tile
+  bool live[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) live[x] = !EDGE || r + 8 * x < left;
+  float y[2][NT][4];
+  float top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[u][nt][e] = fmaf(s[u][nt][e], sc[nt][e & 1], -mref[nt][e & 1]);
+        if (EDGE && !live[2 * u + (e >> 1)]) y[u][nt][e] = -INFINITY;
+        top = fmaxf(top, y[u][nt][e]);
+      }
+  if (__any_sync(0xffffffffu, top > 15.f)) {
+    // Some score passed the reference max by more than 8: move that head's.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (live[x]) mx = fmaxf(mx, s[x >> 1][nt][c + 2 * (x & 1)] * sc[nt][c]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        if (mx > mref[nt][c] + 15.f) {
+          const float mn = mx - 7.f;
+          const float f = fast_exp2(mref[nt][c] - mn);
+          mref[nt][c] = mn;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int i = 0; i < C::kSteps; ++i) o[nt][i][c] *= f, o[nt][i][c + 2] *= f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int u = x >> 1, e = c + 2 * (x & 1);
+            y[u][nt][e] = live[x] ? fmaf(s[u][nt][e], sc[nt][c], -mn) : -INFINITY;
+          }
+        }
+      }
+  }
+  uint32_t pb[2][NT][2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = fast_exp2(y[u][nt][i]);
+      l[nt][0] += e[0] + e[2];
+      l[nt][1] += e[1] + e[3];
+      // The scores' fragment, transposed, is the B operand of O^T: k = tokens.
+      pb[u][nt][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+      pb[u][nt][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+    }
+  // ---- O^T += V^T P^T
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t w[4][kWords], sv[2];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int tok = 16 * u + 2 * q + (x & 1) + 8 * (x >> 1);
+      if constexpr (D == 128) {
+        const uint2 v = *reinterpret_cast<const uint2*>(sl + C::kOffV + tok * C::kCode + 8 * r);
+        w[x][0] = v.x, w[x][1] = v.y;
+      } else {
+        w[x][0] = *reinterpret_cast<const uint32_t*>(sl + C::kOffV + tok * C::kCode + 4 * r);
+      }
+    }
+    constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int tok = 16 * u + 2 * q + 8 * x;
+      const uint8_t* at = sl + C::kOffV + C::kOffKs + tok * C::kScale + r / kPer;
+      uint32_t two = __byte_perm(at[0], at[C::kScale], 0x5540);
+      if (EDGE) {
+        // Slots past the context may hold anything; a NaN scale would survive p = 0.
+        if (tok >= left) two &= 0xFF00u;
+        if (tok + 1 >= left) two &= 0x00FFu;
+      }
+      sv[x] = e4m3x2_to_f16(two);
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      // Token pairs side by side: byte j holds channel 2j (lo) or 2j + 1 (hi) of both.
+      constexpr uint32_t kLow = 0x0F0F0F0Fu;
+      uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t w0 = w[2 * x][i], w1 = w[2 * x + 1][i];
+        e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), lo[x]);
+        e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), hi[x]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[x][e] = hmul2(lo[x][e], sv[x]);
+          hi[x][e] = hmul2(hi[x][e], sv[x]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16_16816(o[nt][4 * i + e], lo[0][e], hi[0][e], lo[1][e], hi[1][e], pb[u][nt][0],
+                        pb[u][nt][1]);
+    }
+  }
+}
+
+// Context length of sequence b; 0 (and a report, if asked) where cu_seqlens is malformed.
+__device__ __forceinline__ int fp4_length(const DecodeFp4Params& p, int b, bool report) {
+  const int L = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
+  if (L >= 0 && L <= p.max_len) return L;
+  if (report) report_status(p.status, -7);
+  return 0;
+}
+
+__device__ __forceinline__ int fp4_blocks(int L) { return (L + kFp4Block128 - 1) / kFp4Block128; }
+
+// The work list as every CTA (of 128 threads) sees it: thread t sums the blocks of sequences
+// [t c, (t + 1) c), a scan over the threads gives `before` (blocks of the sequences before its
+// own) and `total`. The host has checked that all blocks of all heads fit an int.
+struct Fp4Plan {
+  int first, count, before, mine, total;
+};
+__device__ __forceinline__ Fp4Plan fp4_plan(const DecodeFp4Params& p, int* warp_sum, bool report) {
+  Fp4Plan w;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const int c = (p.B + 127) / 128;
+  w.first = imin(tid * c, p.B);
+  w.count = imin(c, p.B - w.first);
+  int sum = 0;
+  for (int i = 0; i < w.count; ++i) sum += fp4_blocks(fp4_length(p, w.first + i, report));
+  w.mine = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += x;
+  }
+  if (lane == 31) warp_sum[tid >> 5] = sum;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < (tid >> 5)) before += warp_sum[i];
+    total += warp_sum[i];
+  }
+  w.before = before + sum - w.mine;
+  w.total = total;
+  return w;
+}
+
+// CTAs that share U blocks: all, unless that leaves them fewer than min_blocks each.
+__device__ __forceinline__ int fp4_ctas(const DecodeFp4Params& p, int U) {
+  return imax(1, imin(p.slots, U / p.min_blocks));
+}
+__device__ __forceinline__ int fp4_start(int i, int U, int nn) {
+  return static_cast<int>(static_cast<long long>(i) * U / nn);
+}
+// The CTA that takes block u.
+__device__ __forceinline__ int fp4_cta_of(int u, int U, int nn) {
+  return static_cast<int>(((static_cast<long long>(u) + 1) * nn - 1) / U);
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(160, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     decode_fp4_kernel(const DecodeFp4Params p) {
   using C = DecodeFp4Cfg<D, NT>;
   constexpr int S = C::kStages;
-  constexpr int kWords = D / 64;  // 32-bit words of V codes per lane and token; K: 2 kWords
-  const int G = p.group;          // 1 <= G <= 8 NT
-  const int split = static_cast<int>(blockIdx.x);
-  const int g = static_cast<int>(blockIdx.y);
-  const int b = static_cast<int>(blockIdx.z);
+  const int G = p.group;  // 1 <= G <= 8 NT
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
-
-  int L = p.cu[b + 1] - p.cu[b];
-  if (L < 0 || L > p.max_len) {
-    if (split == 0 && tid == 0) report_status(p.status, -7);
-    L = 0;
-  }
-  const int nstages = (L + C::kTok - 1) / C::kTok;
-  const int nsplit = (nstages + p.chunk_stages - 1) / p.chunk_stages;
-  if (L == 0) {
-    // Empty context: O = 0, LSE = -inf.
-    if (split == 0) {
-      for (int idx = tid; idx < G * D; idx += C::kThreads) p.o[head0 * D + idx] = 0;
-      if (tid < G) p.lse[head0 + tid] = -INFINITY;
-    }
-    return;
-  }
-  if (split >= nsplit) return;
-  const int st0 = split * p.chunk_stages;
-  const int n = imin(nstages - st0, p.chunk_stages);
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>(
+  uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  uint8_t* misc = ring + C::kRingBytes;
+  uint8_t* ring = base + warp * C::kRingBytes;
+  uint8_t* misc = base + C::kWarps * C::kRingBytes;
   DecodeFp4Ctrl* ctl = reinterpret_cast<DecodeFp4Ctrl*>(misc);
   float* red_m = reinterpret_cast<float*>(misc + 256);   // [warps][16 heads]
   float* red_l = red_m + C::kWarps * 16;
+  uint64_t* full = ctl->full + warp * S;
 
-  if (tid == C::kConsumers) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&ctl->full[s], 1);
-      mbar_init(&ctl->empty[s], C::kWarps);
-    }
-    ctl->abort_flag = 0;
-    ctl->is_last = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 8);
+    if (warp == 0) ctl->abort_flag = 0;
     fence_mbar_init();
   }
+  const Fp4Plan plan = fp4_plan(p, ctl->warp_sum, blockIdx.x == 0);
+  const int U = plan.total * p.Hkv;
+  const int nn = fp4_ctas(p, U);
+  const int cta = static_cast<int>(blockIdx.x);
+  if (U == 0 || cta >= nn) return;
+  int u = fp4_start(cta, U, nn);
+  const int end = fp4_start(cta + 1, U, nn);
+  if (plan.before * p.Hkv <= u && u < (plan.before + plan.mine) * p.Hkv) {
+    int x = plan.before, b = plan.first;
+    for (;; ++b) {
+      const int nb = fp4_blocks(fp4_length(p, b, false));
+      if (u < (x + nb) * p.Hkv) break;
+      x += nb;
+    }
+    ctl->seq = b;
+    ctl->seq_before = x;
+  }
   __syncthreads();
+  int b = ctl->seq;
+  int seq_u = ctl->seq_before * p.Hkv;  // first block of sequence b
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
+
+  // Copies of one slice: lane 4 sub + part < 8 brings K codes, K scales, V codes or V scales
+  // (part 0..3) of the slice's tokens in its page `sub` (two pages of 16 tokens, else one), and
+  // arrives on the slice's barrier with the bytes it asked for. A slice lies at the same place
+  // of its page in every block. Pages past the context are not copied. A page whose entry lies
+  // outside the pool is never addressed: the status word reports it and it reads as zeros.
+  // A slice's table entry is read one slice ahead of its copies.
   const int lp = p.page_shift;
+  const int sub = lane >> 2, part = lane & 3;
+  const int run = imin(C::kTok, 1 << lp);  // tokens of the slice in one page
+  const bool copies = sub * run < C::kTok;
+  const int tok0 = warp * C::kTok + sub * run;  // this lane's first token in a block
+  const uint32_t bytes = static_cast<uint32_t>(run) * ((part & 1) ? C::kScale : C::kCode);
+  uint8_t* const dst0 = ring + ((part & 2) ? C::kOffV : 0) + ((part & 1) ? C::kOffKs : 0) +
+                        sub * static_cast<int>(bytes);
+  const int in_page = tok0 & ((1 << lp) - 1);
+  const uint8_t* const src0 =
+      ((part & 2) ? p.v : p.k) +
+      ((part & 1) ? (C::kCode << lp) + in_page * C::kScale : in_page * C::kCode);
+  const size_t blk_bytes = static_cast<size_t>(C::kCode + C::kScale) << lp;
 
-  if (warp == C::kWarps) {
-    // ---------------------------------------------------------------- producer
-    // Lane 2i + kv < 2 * (128 >> lp) brings K (kv = 0) or V of page i of every stage: whole
-    // (page, head) blocks, one copy each. It reads its table entry one stage ahead. Pages
-    // past the context are not copied (no consumer reads them). A page whose entry lies
-    // outside the pool is never addressed: the status word reports it and it reads as zeros.
-    const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-    const int pages = C::kTok >> lp;
-    const uint32_t bytes = static_cast<uint32_t>(C::kRow) << lp;
-    const uint8_t* pool = (lane & 1) ? p.v : p.k;
-    const int sub = lane >> 1;
-    int issued = 0;
-    auto entry = [&](int k) {  // -2: nothing to copy, -1: bad entry
-      const int tok = (st0 + k) * C::kTok + (sub << lp);
-      if (sub >= pages || tok >= L) return -2;
-      const int e = __ldg(row + (tok >> lp));
-      return e < 0 || e >= p.num_pages ? -1 : e;
-    };
-    int next = entry(0);
-    for (int k = 0; k < n; ++k) {
-      const int st = k % S;
-      bool okw = true;
-      if (lane == 0) okw = mbar_wait(&ctl->empty[st], ((k / S) & 1) ^ 1, wc);
-      if (!__shfl_sync(0xffffffffu, okw, 0)) break;
-      ++issued;
-      const int phys = next;
-      uint8_t* dst = ring + st * C::kStageBytes + (lane & 1) * C::kHalf + sub * bytes;
-      const uint32_t good = __ballot_sync(0xffffffffu, phys >= 0);
-      if (phys == -1) {
-        report_status(p.status, -5);
-        for (uint32_t i = 0; i < bytes; i += 16)
-          *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], __popc(good) * bytes);
-      __syncwarp();
-      if (phys >= 0)
-        bulk_load(dst, pool + (static_cast<size_t>(phys) * p.Hkv + g) * bytes, bytes,
-                  &ctl->full[st]);
-      if (k + 1 < n) next = entry(k + 1);
-    }
-    if (lane == 0) {
-      for (int k = imax(0, issued - S); k < issued; ++k)
-        mbar_wait(&ctl->full[k % S], (k / S) & 1, wc_drain);
-    }
-    return;  // the producer takes no part in the consumer barriers below
-  }
-
-  // ------------------------------------------------------------------ consumers
   const int r = lane >> 2, q = lane & 3;
-  // Q as the B operand: column (head) r, k-step kk = channels D/4 q + 4 kk + {0, 1 | 2, 3}.
-  uint32_t qb[NT][C::kSteps][2];
-  float sc[NT][2];  // scale of heads 8 nt + 2 q, + 1
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    uint4 w[D / 32];
-    const int h = 8 * nt + r;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      w[i] = h < G ? __ldg(p.q + (head0 + h) * (D / 8) + q * (D / 32) + i) : make_uint4(0, 0, 0, 0);
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[e] << 16)),
-                                 fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    int e2 = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-    e2 = amax == 0.f ? 0 : imax(-126, imin(126, e2));
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);  // 2^-e2
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        qb[nt][2 * i + (e >> 1)][e & 1] = pack_f16x2(__uint_as_float(x[e] << 16) * down,
-                                                     __uint_as_float(x[e] & 0xFFFF0000u) * down);
-    }
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) * p.scale_log2;
-    sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * q);
-    sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * q + 4);
-  }
-  float o[NT][C::kSteps][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < C::kSteps; ++i)
-      o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-  // p = 2^(x - mref): mref is the running max less 7, and the max trails by less than 8.
-  float mref[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    mref[nt][0] = mref[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-  const uint32_t pmask = (1u << lp) - 1;
-  bool ok = true;
+  int st_in = 0, st_out = 0;   // ring slots of the next copy and the next slice
+  uint32_t parity = 0;         // of slot st_out
+  bool aborted = false;
 
-  for (int k = 0; k < n; ++k) {
-    const int st = k % S;
-    ok = __all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (k / S) & 1, wc));
-    if (ok) {
-      const uint8_t* stage = ring + st * C::kStageBytes;
-      const int left = L - (st0 + k) * C::kTok;  // tokens of the context from this stage on
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int tb = warp * 32 + half * 16;
-        if (tb < left) {  // the same for the whole warp
-          const uint8_t* kblk = stage + (tb >> lp) * (C::kRow << lp);
-          const int in = tb & pmask;  // the tile's first token in its page
-          const uint8_t* kc = kblk + in * C::kCode;
-          const uint8_t* ks = kblk + (C::kCode << lp) + in * C::kScale;
-          const uint8_t* vc = kc + C::kHalf;
-          const uint8_t* vs = ks + C::kHalf;
-          const bool edge = tb + 16 > left;
-          // ---- S^T = K Q^T
-          float s[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-          {
-            uint32_t w[2][2 * kWords], sf[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int row = r + 8 * x;
-              if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(kc + row * C::kCode + 16 * q);
-                w[x][0] = u.x, w[x][1] = u.y, w[x][2] = u.z, w[x][3] = u.w;
-                sf[x] = e4m3x2_to_f16(
-                    *reinterpret_cast<const uint16_t*>(ks + row * C::kScale + 2 * q));
-              } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(kc + row * C::kCode + 8 * q);
-                w[x][0] = u.x, w[x][1] = u.y;
-                sf[x] = e4m3x2_to_f16(ks[row * C::kScale + q]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * kWords; ++i) {
-              uint32_t a[2][4];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t ss = i < 2 ? dup_lo(sf[x]) : dup_hi(sf[x]);
-                e2m1x8_to_f16(w[x][i], a[x]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a[x][e] = hmul2(a[x][e], ss);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(s[nt], a[0][0], a[1][0], a[0][1], a[1][1], qb[nt][2 * i][0],
-                              qb[nt][2 * i][1]);
-                mma_f16_16816(s[nt], a[0][2], a[1][2], a[0][3], a[1][3], qb[nt][2 * i + 1][0],
-                              qb[nt][2 * i + 1][1]);
-              }
-            }
+  for (bool first = true; u < end; first = false) {
+    int L = fp4_length(p, b, false), nb = fp4_blocks(L);
+    while (u >= seq_u + nb * p.Hkv) {  // the sequence is done: on to the next that has blocks
+      seq_u += nb * p.Hkv;
+      L = fp4_length(p, ++b, false);
+      nb = fp4_blocks(L);
+    }
+    const int g = (u - seq_u) / nb;
+    const int blk0 = (u - seq_u) % nb;
+    const int nblk = imin(nb - blk0, end - u);
+    const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
+    // Slices of this warp: one a block, but none in the last block if it ends before.
+    int n = nblk;
+    if ((blk0 + nblk - 1) * kFp4Block128 + warp * C::kTok >= L) --n;
+    if (aborted) n = 0;
+
+    const int* const row =
+        p.table + static_cast<size_t>(b) * p.max_pages + (tok0 >> lp);
+    const uint8_t* const src_g = src0 + g * blk_bytes;
+    auto entry = [&](int i) {  // -2: nothing to copy, -1: bad entry
+      const int tok = (blk0 + i) * kFp4Block128;
+      if (!copies || i >= n || tok + tok0 >= L) return -2;
+      const int e = __ldg(row + (tok >> lp));
+      return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
+    };
+    auto issue = [&](int phys) {
+      if (lane < 8) {
+        uint8_t* dst = dst0 + st_in * C::kSliceBytes;
+        if (phys >= 0) {
+          mbar_arrive_expect_tx(&full[st_in], bytes);
+          bulk_load(dst, src_g + static_cast<size_t>(phys) * p.Hkv * blk_bytes, bytes,
+                    &full[st_in]);
+        } else {
+          if (phys == -1) {
+            report_status(p.status, -5);
+            for (uint32_t x = 0; x < bytes; x += 16)
+              *reinterpret_cast<uint4*>(dst + x) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
           }
-          // ---- softmax: columns are heads 2q, 2q + 1, rows tokens r and r + 8
-          const bool live0 = !edge || tb + r < left, live1 = !edge || tb + r + 8 < left;
-          float y[NT][4];
-          bool over = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[nt][e] = fmaf(s[nt][e], sc[nt][e & 1], -mref[nt][e & 1]);
-              if (!((e & 2) ? live1 : live0)) y[nt][e] = -INFINITY;
-              over |= y[nt][e] > 15.f;
-            }
-          if (__any_sync(0xffffffffu, over)) {
-            // Some score passed the reference max by more than 8: move that head's.
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float x0 = live0 ? s[nt][c] * sc[nt][c] : -INFINITY;
-                float x1 = live1 ? s[nt][c + 2] * sc[nt][c] : -INFINITY;
-                float mx = fmaxf(x0, x1);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                if (mx > mref[nt][c] + 15.f) {
-                  const float mn = mx - 7.f;
-                  const float f = fast_exp2(mref[nt][c] - mn);
-                  mref[nt][c] = mn;
-                  l[nt][c] *= f;
-#pragma unroll
-                  for (int i = 0; i < C::kSteps; ++i) o[nt][i][c] *= f, o[nt][i][c + 2] *= f;
-                  y[nt][c] = live0 ? fmaf(s[nt][c], sc[nt][c], -mn) : -INFINITY;
-                  y[nt][c + 2] = live1 ? fmaf(s[nt][c + 2], sc[nt][c], -mn) : -INFINITY;
-                }
-              }
-          }
-          uint32_t pb[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = fast_exp2(y[nt][i]);
-            l[nt][0] += e[0] + e[2];
-            l[nt][1] += e[1] + e[3];
-            // The scores' fragment, transposed, is the B operand of O^T: k = tokens.
-            pb[nt][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
-            pb[nt][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
-          }
-          // ---- O^T += V^T P^T
-          {
-            uint32_t w[4][kWords], sv[2];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int tok = 2 * q + (x & 1) + 8 * (x >> 1);
-              if constexpr (D == 128) {
-                const uint2 u = *reinterpret_cast<const uint2*>(vc + tok * C::kCode + 8 * r);
-                w[x][0] = u.x, w[x][1] = u.y;
-              } else {
-                w[x][0] = *reinterpret_cast<const uint32_t*>(vc + tok * C::kCode + 4 * r);
-              }
-            }
-            constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int tok = 2 * q + 8 * x;
-              const uint8_t* at = vs + tok * C::kScale + r / kPer;
-              uint32_t two = at[0] | (static_cast<uint32_t>(at[C::kScale]) << 8);
-              if (edge) {
-                // Slots past the context may hold anything; a NaN scale would survive p = 0.
-                if (tb + tok >= left) two &= 0xFF00u;
-                if (tb + tok + 1 >= left) two &= 0x00FFu;
-              }
-              sv[x] = e4m3x2_to_f16(two);
-            }
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-              // Token pairs side by side: byte j holds channel 2j (lo) or 2j + 1 (hi) of both.
-              constexpr uint32_t kLow = 0x0F0F0F0Fu;
-              uint32_t lo[2][4], hi[2][4];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t w0 = w[2 * x][i], w1 = w[2 * x + 1][i];
-                e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), lo[x]);
-                e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), hi[x]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  lo[x][e] = hmul2(lo[x][e], sv[x]);
-                  hi[x][e] = hmul2(hi[x][e], sv[x]);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16_16816(o[nt][4 * i + e], lo[0][e], hi[0][e], lo[1][e], hi[1][e],
-                                pb[nt][0], pb[nt][1]);
-            }
-          }
+          mbar_arrive(&full[st_in]);
         }
       }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->empty[st]);
-  }
+      st_in = st_in + 1 == S ? 0 : st_in + 1;
+    };
+    int issued = 0;
+    for (; issued < S - 1 && issued < n; ++issued) issue(entry(issued));
+    int next = entry(issued);
 
-  // ------------------------------------------------------------------ merge the four warps
+    // Q as the B operand: column (head) r, k-step kk = channels D/4 q + 4 kk + {0, 1 | 2, 3}.
+    uint32_t qb[NT][C::kSteps][2];
+    float sc[NT][2];  // scale of heads 8 nt + 2 q, + 1
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      uint4 w[D / 32];
+      const int h = 8 * nt + r;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int i = 0; i < D / 32; ++i)
+        w[i] =
+            h < G ? __ldg(p.q + (head0 + h) * (D / 8) + q * (D / 32) + i) : make_uint4(0, 0, 0, 0);
+      float amax = 0.f;
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
-  named_barrier_sync(1, C::kConsumers);  // every consumer is past its last ring read
-  // [warp][head][D] fp32 in the idle ring. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
-  // m-tile i holds channels 2i and 2i + 1 of them.
-  float* buf = reinterpret_cast<float*>(ring);
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int h = 8 * nt + 2 * q + c;
-      if (r == 0) {
-        red_m[warp * 16 + h] = mref[nt][c];
-        red_l[warp * 16 + h] = l[nt][c];
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[e] << 16)),
+                                   fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
       }
-      if (h < G) {
-        float* to = buf + (warp * C::kHeads + h) * D + r * (D / 8);
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      int e2 = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+      e2 = amax == 0.f ? 0 : imax(-126, imin(126, e2));
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);  // 2^-e2
 #pragma unroll
-        for (int i = 0; i < C::kSteps; i += 2)
-          *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
-              o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          qb[nt][2 * i + (e >> 1)][e & 1] = pack_f16x2(__uint_as_float(x[e] << 16) * down,
+                                                       __uint_as_float(x[e] & 0xFFFF0000u) * down);
       }
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) * p.scale_log2;
+      sc[nt][0] = __shfl_sync(0xffffffffu, up, 8 * q);
+      sc[nt][1] = __shfl_sync(0xffffffffu, up, 8 * q + 4);
     }
-  named_barrier_sync(1, C::kConsumers);
+    float o[NT][C::kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < C::kSteps; ++i)
+        o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    // p = 2^(x - mref): mref is the running max less 7, and the max trails by less than 8.
+    float mref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mref[nt][0] = mref[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-  const size_t bg = static_cast<size_t>(b) * p.Hkv + g;
-  const bool single = nsplit == 1;
-  constexpr int kQuads = D / 4;  // four-column groups of one head's row
-  for (int idx = tid; idx < G * kQuads; idx += C::kConsumers) {
-    const int hh = idx / kQuads, d0 = (idx % kQuads) * 4;
-    float M = red_m[hh];
-#pragma unroll
-    for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * 16 + hh]);
-    float Ls = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-      const float mw = red_m[w * 16 + hh];
-      if (mw != -INFINITY) {
-        const float f = fast_exp2(mw - M);
-        const float4 x = *reinterpret_cast<const float4*>(buf + (w * C::kHeads + hh) * D + d0);
-        Ls += red_l[w * 16 + hh] * f;
-        a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+    int left = L - blk0 * kFp4Block128 - warp * C::kTok;  // tokens from the slice's first on
+    for (int i = 0; i < n; ++i, left -= kFp4Block128) {
+      if (issued < n) {  // into the slot of slice i - 1, which the whole warp has left
+        issue(next);
+        next = entry(++issued);
       }
-    }
-    const size_t orow = head0 + hh;
-    if (single) {
-      const float inv = Ls > 0.f ? p.v_scale / Ls : 0.f;
-      *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
-          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-      if (d0 == 0)
-        p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
-    } else {
-      const size_t base = (bg * p.max_splits + split) * G + hh;
-      *reinterpret_cast<float4*>(p.part_o + base * D + d0) = a;
-      if (d0 == 0) {
-        p.part_ml[2 * base] = M;
-        p.part_ml[2 * base + 1] = Ls;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st_out], parity, wc))) {
+        aborted = true;
+        break;
       }
+      const uint8_t* sl = ring + st_out * C::kSliceBytes;
+      if (left >= C::kTok)
+        fp4_slice<D, NT, false>(sl, left, r, q, qb, sc, o, mref, l);
+      else
+        fp4_slice<D, NT, true>(sl, left, r, q, qb, sc, o, mref, l);
+      if (++st_out == S) st_out = 0, parity ^= 1;
+      __syncwarp();
     }
-  }
-  if (single) return;
+    // After a timeout, let copies still in flight land (with a limit) before the rings are used
+    // again.
+    if (aborted)
+      for (int s = 0; s < S - 1; ++s)
+        mbar_wait(&full[(st_out + s) % S], parity ^ (st_out + s >= S ? 1 : 0), wc_drain);
 
-  // Ticket: the split that draws the last one merges all splits in split order, so the result
-  // does not depend on which CTA finishes last.
-  named_barrier_sync(1, C::kConsumers);
-  if (tid == 0) {
-    __threadfence();
-    const int ticket = atomicAdd(&p.counters[bg], 1);
-    __threadfence();
-    ctl->is_last = ticket == nsplit - 1;
-  }
-  named_barrier_sync(1, C::kConsumers);
-  if (!ctl->is_last) return;
-  __threadfence();
-  constexpr int kBatch = 8;
-  const size_t base_bg = bg * p.max_splits * G;
-  for (int idx = tid; idx < G * kQuads; idx += C::kConsumers) {
-    const int hh = idx / kQuads, d0 = (idx % kQuads) * 4;
-    const float* ml = p.part_ml + 2 * (base_bg + hh);
-    const float* po = p.part_o + (base_bg + hh) * D + d0;
-    // The running max over batches of splits, with the sums rescaled when it grows.
-    float M = -INFINITY, Ls = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < nsplit; c0 += kBatch) {
-      float2 mlv[kBatch];
-      float4 ov[kBatch];
+    // ---------------------------------------------------------------- merge the four warps
 #pragma unroll
-      for (int t = 0; t < kBatch; ++t) {
-        const size_t c = static_cast<size_t>(imin(c0 + t, nsplit - 1));
-        mlv[t] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * c * G));
-        ov[t] = __ldcg(reinterpret_cast<const float4*>(po + c * G * D));
-      }
-      float Mn = M;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, mlv[t].x);
-      const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-      M = Mn;
-      Ls *= f;
-      a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int t = 0; t < kBatch; ++t)
-        if (c0 + t < nsplit) {
-          const float wt = exp2f(mlv[t].x - M);
-          Ls += mlv[t].y * wt;
-          a.x += ov[t].x * wt, a.y += ov[t].y * wt, a.z += ov[t].z * wt, a.w += ov[t].w * wt;
+        for (int off = 4; off < 32; off <<= 1)
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
+    __syncthreads();  // every warp is past its last ring read
+    // [warp][head][D] fp32 in the idle rings. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
+    // m-tile i holds channels 2i and 2i + 1 of them.
+    float* buf = reinterpret_cast<float*>(base);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = 8 * nt + 2 * q + c;
+        if (r == 0) {
+          red_m[warp * 16 + h] = mref[nt][c];
+          red_l[warp * 16 + h] = l[nt][c];
         }
+        if (h < G) {
+          float* to = buf + (warp * C::kHeads + h) * D + r * (D / 8);
+#pragma unroll
+          for (int i = 0; i < C::kSteps; i += 2)
+            *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
+                o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+        }
+      }
+    __syncthreads();
+    const bool whole = nblk == nb;
+    const size_t slot = 2 * static_cast<size_t>(cta) + (first ? 0 : 1);
+    constexpr int kQuads = D / 4;  // four-column groups of one head's row
+    for (int idx = tid; idx < G * kQuads; idx += C::kThreads) {
+      const int hh = idx / kQuads, d0 = (idx % kQuads) * 4;
+      float M = red_m[hh];
+#pragma unroll
+      for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * 16 + hh]);
+      float Ls = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) {
+        const float mw = red_m[w * 16 + hh];
+        if (mw != -INFINITY) {
+          const float f = fast_exp2(mw - M);
+          const float4 x = *reinterpret_cast<const float4*>(buf + (w * C::kHeads + hh) * D + d0);
+          Ls += red_l[w * 16 + hh] * f;
+          a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+        }
+      }
+      if (whole) {
+        const size_t orow = head0 + hh;
+        const float inv = Ls > 0.f ? p.v_scale / Ls : 0.f;
+        *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (d0 == 0)
+          p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * G + hh) * D + d0) = a;
+        if (d0 == 0)
+          *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * G + hh)) = make_float2(M, Ls);
+      }
     }
-    const size_t orow = head0 + hh;
-    const float inv = p.v_scale / Ls;
-    *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    if (d0 == 0) p.lse[orow] = (M + log2f(Ls)) * 0.69314718055994530942f;
+    u += nblk;
+    fence_proxy_async_smem();  // the merge's plain writes, before the next segment's copies
+    __syncthreads();
   }
+}
+
+// Joins the parts of contexts that several CTAs share, and writes the rows of empty ones. One
+// CTA per (query head, sequence): four threads a four-column group, thread s of them the parts
+// s, s + 4, ...; the four sums are added in order.
+template <int D>
+__global__ void __launch_bounds__(128) combine_fp4_kernel(const DecodeFp4Params p) {
+  constexpr int kQuads = D / 4, kSets = 128 / kQuads, kBatch = 8;
+  __shared__ int warp_sum[4];
+  __shared__ int seq_before;
+  __shared__ float sm[kSets], sl[kSets];
+  __shared__ float4 so[kSets][kQuads];
+  const int h = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
+  const int tid = static_cast<int>(threadIdx.x);
+  const Fp4Plan plan = fp4_plan(p, warp_sum, false);
+  if (plan.first <= b && b < plan.first + plan.count) {
+    int x = plan.before;
+    for (int i = plan.first; i < b; ++i) x += fp4_blocks(fp4_length(p, i, false));
+    seq_before = x;
+  }
+  __syncthreads();
+  const int nb = fp4_blocks(fp4_length(p, b, false));
+  const size_t orow = static_cast<size_t>(b) * p.Hq + h;
+  if (nb == 0) {  // empty context: O = 0, LSE = -inf
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid < D / 2) reinterpret_cast<uint32_t*>(p.o + orow * D)[tid] = 0;
+    if (tid == 0) p.lse[orow] = -INFINITY;
+    return;
+  }
+  const int G = p.group, g = h / G, hh = h % G;
+  const int U = plan.total * p.Hkv, nn = fp4_ctas(p, U);
+  const int u0 = seq_before * p.Hkv + g * nb;
+  const int c0 = fp4_cta_of(u0, U, nn), c1 = fp4_cta_of(u0 + nb - 1, U, nn);
+  // Every CTA waits, those without work too: this kernel must not end before the first one.
+  if (c0 == c1) {  // one CTA held the whole context
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  // The first part is its CTA's first segment only if the CTA starts with this context.
+  const int slot0 = 2 * c0 + (fp4_start(c0, U, nn) == u0 ? 0 : 1);
+  const int parts = c1 - c0 + 1;
+  const int quad = tid % kQuads, set = tid / kQuads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float M = -INFINITY, Ls = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x0 = set; x0 < parts; x0 += kSets * kBatch) {
+    float2 ml[kBatch];
+    float4 ov[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int x = imin(x0 + t * kSets, parts - 1);
+      const size_t at = static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * G + hh;
+      ml[t] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
+      ov[t] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * quad));
+    }
+    float Mn = M;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, ml[t].x);
+    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    M = Mn;
+    Ls *= f;
+    a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t)
+      if (x0 + t * kSets < parts) {
+        const float wt = exp2f(ml[t].x - M);
+        Ls += ml[t].y * wt;
+        a.x += ov[t].x * wt, a.y += ov[t].y * wt, a.z += ov[t].z * wt, a.w += ov[t].w * wt;
+      }
+  }
+  so[set][quad] = a;
+  if (quad == 0) sm[set] = M, sl[set] = Ls;
+  __syncthreads();
+  if (set) return;
+#pragma unroll
+  for (int i = 1; i < kSets; ++i) M = fmaxf(M, sm[i]);
+  Ls = 0.f;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kSets; ++i)
+    if (sm[i] != -INFINITY) {
+      const float f = exp2f(sm[i] - M);
+      const float4 x = so[i][quad];
+      Ls += sl[i] * f;
+      a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+    }
+  const float inv = p.v_scale / Ls;
+  *reinterpret_cast<uint2*>(p.o + orow * D + 4 * quad) =
+      make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  if (quad == 0) p.lse[orow] = (M + log2f(Ls)) * 0.69314718055994530942f;
 }
 
 }  // namespace ta
