@@ -35,8 +35,8 @@
 // The second kernel starts under programmatic dependent launch: it finds its parts while the
 // first still runs. No counters, so no memset.
 //
-// CTA: four warps; warp w takes tokens [32 w, 32 w + 32) of every block, through a ring of its
-// own in shared memory: it brings the next slices in with bulk copies while it works on one, so
+// CTA: four warps; warp w takes 64-token stages w, w + 4, ... of a segment, through a ring of its
+// own in shared memory: it brings the next stages in with bulk copies while it works on one, so
 // no warp waits for another before a segment's end.
 #pragma once
 
@@ -69,22 +69,23 @@ struct DecodeFp4Params {
 
 template <int D, int NT>  // NT: 8-head column tiles (1 or 2)
 struct DecodeFp4Cfg {
-  static constexpr int kTok = 32;  // tokens per slice: two 16-row tiles
+  static constexpr int kTok = 32;     // tokens per slice: two 16-row tiles
+  static constexpr int kStage = 64;    // tokens per ring stage
   static constexpr int kWarps = 4;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kCtas = D == 128 && NT == 2 ? 3 : 4;  // per SM
+  static constexpr int kCtas = 3;  // per SM
   static constexpr int kCode = D / 2, kScale = D / 16;
-  // A slice in shared memory: K codes, K scales, V codes, V scales.
-  static constexpr int kOffKs = kTok * kCode, kOffV = kOffKs + kTok * kScale;
-  static constexpr int kSliceBytes = 2 * kOffV;      // 4608 (D = 128), 2304 (D = 64)
-  static constexpr int kStages = 3 * 128 / D;        // slices per warp's ring
-  static constexpr int kRingBytes = kStages * kSliceBytes;
+  // A stage in shared memory: K codes, K scales, V codes, V scales.
+  static constexpr int kOffKs = kStage * kCode, kOffV = kOffKs + kStage * kScale;
+  static constexpr int kStageBytes = 2 * kOffV;      // 9216 (D = 128), 4608 (D = 64)
+  static constexpr int kStages = 2 * 128 / D;     // of one warp's ring
+  static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kSteps = D / 16;              // k-steps of S^T, m-tiles of O^T
   static constexpr int kMiscBytes = 256 + 2 * kWarps * 16 * 4;
   static constexpr int kSmemBytes = kWarps * kRingBytes + kMiscBytes + 128;
   static_assert(kWarps * kHeads * D * 4 <= kWarps * kRingBytes, "the O rows reuse the rings");
-  static_assert(kWarps * kStages * 8 <= 192, "barriers");
+  static_assert(kWarps * kStages <= 24, "barriers");
 };
 
 struct DecodeFp4Ctrl {
@@ -102,6 +103,17 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -122,13 +134,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t dup_lo(uint32_t a) { return __byte_perm(a, a, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t a) { return __byte_perm(a, a, 0x3232); }
+// a * (b.lo, b.lo) or (b.hi, b.hi).
+template <bool HI>
+__device__ __forceinline__ uint32_t hmul2_dup(uint32_t a, uint32_t b) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&a);
+  const __half2 y = *reinterpret_cast<const __half2*>(&b);
+  const __half2 z = __hmul2(x, HI ? __high2half2(y) : __low2half2(y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
 
 // One slice: S^T, the softmax step and O^T of 32 tokens, of which the first `left` belong to
 // the context. EDGE: some do not; the others run without a mask.
 template <int D, int NT, bool EDGE>
-__device__ __forceinline__ void fp4_slice(const uint8_t* sl, int left, int r, int q,
+__device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, int r, int q,
                                           const uint32_t (&qb)[NT][D / 16][2],
                                           const float (&sc)[NT][2], float (&o)[NT][D / 16][4],
                                           float (&mref)[NT][2], float (&l)[NT][2]) {
@@ -143,32 +161,34 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int left, int r, in
     for (int x = 0; x < 2; ++x) {
       const int row = 16 * u + r + 8 * x;
       if constexpr (D == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sl + row * C::kCode + 16 * q);
+        const uint4 v = *reinterpret_cast<const uint4*>(sl + (32 * h + row) * C::kCode + 16 * q);
         w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
         sf[x] = e4m3x2_to_f16(
-            *reinterpret_cast<const uint16_t*>(sl + C::kOffKs + row * C::kScale + 2 * q));
+            *reinterpret_cast<const uint16_t*>(sl + C::kOffKs + (32 * h + row) * C::kScale + 2 * q));
       } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(sl + row * C::kCode + 8 * q);
+        const uint2 v = *reinterpret_cast<const uint2*>(sl + (32 * h + row) * C::kCode + 8 * q);
         w[x][0] = v.x, w[x][1] = v.y;
-        sf[x] = e4m3x2_to_f16(sl[C::kOffKs + row * C::kScale + q]);
+        sf[x] = e4m3x2_to_f16(sl[C::kOffKs + (32 * h + row) * C::kScale + q]);
       }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2 * kWords; ++i) {
       uint32_t a[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t ss = i < 2 ? dup_lo(sf[x]) : dup_hi(sf[x]);
         e2m1x8_to_f16(w[x][i], a[x]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[x][e] = hmul2(a[x][e], ss);
+        for (int e = 0; e < 4; ++e)
+          a[x][e] = i < 2 ? hmul2_dup<false>(a[x][e], sf[x]) : hmul2_dup<true>(a[x][e], sf[x]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_f16_16816(s[u][nt], a[0][0], a[1][0], a[0][1], a[1][1], qb[nt][2 * i][0],
-                      qb[nt][2 * i][1]);
+        if (i == 0)
+          mma_f16_16816_zero(s[u][nt], a[0][0], a[1][0], a[0][1], a[1][1], qb[nt][0][0],
+                             qb[nt][0][1]);
+        else
+          mma_f16_16816(s[u][nt], a[0][0], a[1][0], a[0][1], a[1][1], qb[nt][2 * i][0],
+                        qb[nt][2 * i][1]);
         mma_f16_16816(s[u][nt], a[0][2], a[1][2], a[0][3], a[1][3], qb[nt][2 * i + 1][0],
                       qb[nt][2 * i + 1][1]);
       }
@@ -240,17 +260,17 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int left, int r, in
     for (int x = 0; x < 4; ++x) {
       const int tok = 16 * u + 2 * q + (x & 1) + 8 * (x >> 1);
       if constexpr (D == 128) {
-        const uint2 v = *reinterpret_cast<const uint2*>(sl + C::kOffV + tok * C::kCode + 8 * r);
+        const uint2 v = *reinterpret_cast<const uint2*>(sl + C::kOffV + (32 * h + tok) * C::kCode + 8 * r);
         w[x][0] = v.x, w[x][1] = v.y;
       } else {
-        w[x][0] = *reinterpret_cast<const uint32_t*>(sl + C::kOffV + tok * C::kCode + 4 * r);
+        w[x][0] = *reinterpret_cast<const uint32_t*>(sl + C::kOffV + (32 * h + tok) * C::kCode + 4 * r);
       }
     }
     constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int tok = 16 * u + 2 * q + 8 * x;
-      const uint8_t* at = sl + C::kOffV + C::kOffKs + tok * C::kScale + r / kPer;
+      const uint8_t* at = sl + C::kOffV + C::kOffKs + (32 * h + tok) * C::kScale + r / kPer;
       uint32_t two = __byte_perm(at[0], at[C::kScale], 0x5540);
       if (EDGE) {
         // Slots past the context may hold anything; a NaN scale would survive p = 0.
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 8);
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 16);
     if (warp == 0) ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -389,17 +409,17 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
-  // Copies of one slice: lane 4 sub + part < 8 brings K codes, K scales, V codes or V scales
-  // (part 0..3) of the slice's tokens in its page `sub` (two pages of 16 tokens, else one), and
-  // arrives on the slice's barrier with the bytes it asked for. A slice lies at the same place
-  // of its page in every block. Pages past the context are not copied. A page whose entry lies
-  // outside the pool is never addressed: the status word reports it and it reads as zeros.
-  // A slice's table entry is read one slice ahead of its copies.
+  // Copies of one stage: lane 4 sub + part < 16 brings K codes, K scales, V codes or V scales
+  // (part 0..3) of the stage's tokens in its page `sub` (four pages of 16 tokens, two of 32, else
+  // one), and arrives on the stage's barrier with the bytes it asked for. A warp's stages all
+  // lie at the same place of their pages. Pages past the context are not copied. A page whose
+  // entry lies outside the pool is never addressed: the status word reports it and it reads as
+  // zeros. A stage's table entries are read one stage ahead of its copies.
   const int lp = p.page_shift;
   const int sub = lane >> 2, part = lane & 3;
-  const int run = imin(C::kTok, 1 << lp);  // tokens of the slice in one page
-  const bool copies = sub * run < C::kTok;
-  const int tok0 = warp * C::kTok + sub * run;  // this lane's first token in a block
+  const int run = imin(C::kStage, 1 << lp);  // tokens of the stage in one page
+  const bool copies = sub * run < C::kStage;
+  const int tok0 = warp * C::kStage + sub * run;  // this lane's first token in the warp's stage 0
   const uint32_t bytes = static_cast<uint32_t>(run) * ((part & 1) ? C::kScale : C::kCode);
   uint8_t* const dst0 = ring + ((part & 2) ? C::kOffV : 0) + ((part & 1) ? C::kOffKs : 0) +
                         sub * static_cast<int>(bytes);
@@ -407,7 +427,8 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const uint8_t* const src0 =
       ((part & 2) ? p.v : p.k) +
       ((part & 1) ? (C::kCode << lp) + in_page * C::kScale : in_page * C::kCode);
-  const size_t blk_bytes = static_cast<size_t>(C::kCode + C::kScale) << lp;
+  const uint32_t blk_bytes = static_cast<uint32_t>(C::kCode + C::kScale) << lp;
+  const uint64_t page_bytes = static_cast<uint64_t>(p.Hkv) * blk_bytes;
 
   const int r = lane >> 2, q = lane & 3;
   int st_in = 0, st_out = 0;   // ring slots of the next copy and the next slice
@@ -425,26 +446,26 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     const int blk0 = (u - seq_u) % nb;
     const int nblk = imin(nb - blk0, end - u);
     const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
-    // Slices of this warp: one a block, but none in the last block if it ends before.
-    int n = nblk;
-    if ((blk0 + nblk - 1) * kFp4Block128 + warp * C::kTok >= L) --n;
-    if (aborted) n = 0;
+    // Stages of the segment's tokens [t0, t1): this warp takes stage warp, warp + 4, ...
+    const int t0 = blk0 * kFp4Block128;
+    const int t1 = imin(t0 + nblk * kFp4Block128, L);
+    const int n = aborted ? 0 : (t1 - t0 + (C::kWarps - 1 - warp) * C::kStage + C::kStage - 1) /
+                                    (C::kWarps * C::kStage);
 
-    const int* const row =
-        p.table + static_cast<size_t>(b) * p.max_pages + (tok0 >> lp);
-    const uint8_t* const src_g = src0 + g * blk_bytes;
+    const int* const row = p.table + static_cast<size_t>(b) * p.max_pages;
+    const uint8_t* const src_g = src0 + static_cast<size_t>(g) * blk_bytes;
     auto entry = [&](int i) {  // -2: nothing to copy, -1: bad entry
-      const int tok = (blk0 + i) * kFp4Block128;
-      if (!copies || i >= n || tok + tok0 >= L) return -2;
+      const int tok = t0 + tok0 + i * (C::kWarps * C::kStage);
+      if (!copies || i >= n || tok >= t1) return -2;
       const int e = __ldg(row + (tok >> lp));
       return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
     };
     auto issue = [&](int phys) {
-      if (lane < 8) {
-        uint8_t* dst = dst0 + st_in * C::kSliceBytes;
+      if (lane < 16) {
+        uint8_t* dst = dst0 + st_in * C::kStageBytes;
         if (phys >= 0) {
           mbar_arrive_expect_tx(&full[st_in], bytes);
-          bulk_load(dst, src_g + static_cast<size_t>(phys) * p.Hkv * blk_bytes, bytes,
+          bulk_load(dst, src_g + static_cast<uint64_t>(phys) * page_bytes, bytes,
                     &full[st_in]);
         } else {
           if (phys == -1) {
@@ -511,9 +532,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     for (int nt = 0; nt < NT; ++nt)
       mref[nt][0] = mref[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-    int left = L - blk0 * kFp4Block128 - warp * C::kTok;  // tokens from the slice's first on
-    for (int i = 0; i < n; ++i, left -= kFp4Block128) {
-      if (issued < n) {  // into the slot of slice i - 1, which the whole warp has left
+    int left = t1 - t0 - warp * C::kStage;  // tokens from the stage's first on
+    for (int i = 0; i < n; ++i, left -= C::kWarps * C::kStage) {
+      if (issued < n) {  // into the slot of stage i - 1, which the whole warp has left
         issue(next);
         next = entry(++issued);
       }
@@ -521,11 +542,16 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
         aborted = true;
         break;
       }
-      const uint8_t* sl = ring + st_out * C::kSliceBytes;
-      if (left >= C::kTok)
-        fp4_slice<D, NT, false>(sl, left, r, q, qb, sc, o, mref, l);
-      else
-        fp4_slice<D, NT, true>(sl, left, r, q, qb, sc, o, mref, l);
+      const uint8_t* sl = ring + st_out * C::kStageBytes;
+      if (left >= C::kStage) {
+#pragma unroll 1
+        for (int h = 0; h < C::kStage / C::kTok; ++h)
+          fp4_slice<D, NT, false>(sl, h, C::kTok, r, q, qb, sc, o, mref, l);
+      } else {
+#pragma unroll 1
+        for (int h = 0; h * C::kTok < left; ++h)
+          fp4_slice<D, NT, true>(sl, h, left - h * C::kTok, r, q, qb, sc, o, mref, l);
+      }
       if (++st_out == S) st_out = 0, parity ^= 1;
       __syncwarp();
     }
