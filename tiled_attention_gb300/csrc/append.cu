@@ -105,15 +105,16 @@ int launch_rows(RowParams& p, int d, void* stream) {
   long long per = (want + p.total - 1) / p.total;
   if (per > all) per = all;
   p.groups_per_task = static_cast<int>((all + per - 1) / per);
-  p.tasks_per_token = (all + p.groups_per_task - 1) / p.groups_per_task;
-  const long long tasks = static_cast<long long>(p.total) * p.tasks_per_token;
-  const long long blocks = (tasks + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  if (blocks >= (1ll << 31)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows");
+  const long long parts = (all + p.groups_per_task - 1) / p.groups_per_task;
+  if (parts > 65535) return fail(ATTN_ERR_UNSUPPORTED, "too many heads");
+  const int warps = kRowThreads / 32;
+  const dim3 grid((static_cast<unsigned>(p.total) + warps - 1) / warps,
+                  static_cast<unsigned>(parts));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    rows_kernel<64, CACHE><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(p);
+    rows_kernel<64, CACHE><<<grid, kRowThreads, 0, s>>>(p);
   else
-    rows_kernel<128, CACHE><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(p);
+    rows_kernel<128, CACHE><<<grid, kRowThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "row kernel launch");
   return ATTN_OK;
@@ -214,7 +215,7 @@ int attn_unpack_pages_fp4(const void* pool, void* dst, float pool_scale,
   if (!aligned16(pool) || !aligned16(dst))
     return fail(ATTN_ERR_INVALID, "pool and dst must be 16-byte aligned");
   if (B > 65535 || static_cast<long long>(max_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > (1 << 16))
+      static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 32768)
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or block table too large");
   UnpackParams p{};
   int rc = status_ptr(&p.status);
@@ -228,7 +229,9 @@ int attn_unpack_pages_fp4(const void* pool, void* dst, float pool_scale,
   p.Hkv = Hkv;
   p.page_shift = log2_exact(page_size);
   p.num_pages = num_pages;
-  const dim3 grid(max_pages, B);
+  const long long chunks = static_cast<long long>(Hkv) * page_size * (d / 8);
+  const dim3 grid(max_pages, B,
+                  static_cast<unsigned>((chunks + 256 * kUnpackBatch - 1) / (256 * kUnpackBatch)));
   if (d == 64)
     unpack_fp4_kernel<64><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
   else

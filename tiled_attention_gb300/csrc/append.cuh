@@ -6,8 +6,8 @@
 //   norm      y_c = x_c * rsqrt(mean_c x_c^2 + eps) * w_c                   (optional)
 //   rotation  pairs (i, i + R/2), or (2i, 2i + 1), i < R/2, by the position's angle i:
 //             a' = a cos - b sin,  b' = b cos + a sin                       (optional)
-//             each product and each sum rounded on its own (no FMA): the 4-bit codes then
-//             depend on the inputs alone, not on how a compiler contracts
+//             for keys that go to 4 bits each product and sum is rounded on its own (no FMA):
+//             the codes then depend on the inputs alone, not on how a compiler contracts
 //   bf16 out  round to nearest even, once
 //   4-bit out xs = y * RN(1 / tensor scale); s = E4M3(max over 16 channels |xs| / 6);
 //             code = E2M1(xs / s), the division rounded as IEEE does; 0 where s is 0
@@ -20,6 +20,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "ptx.cuh"
@@ -45,7 +47,7 @@ struct RowParams {
   int heads[3];              // rows of a token: Hq, Hkv, Hkv (0: absent)
   int groups[3];             // row groups of a token: heads over rows per warp, rounded up
   int total, N, B, max_pos, rot, interleaved, max_pages, page_shift, num_pages;
-  int tasks_per_token, groups_per_task;
+  int groups_per_task;       // row groups a warp takes of its token; the grid's y picks which
   int* status;
 };
 
@@ -71,19 +73,31 @@ __device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, 
   return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -2;
 }
 
+// x / s as IEEE division rounds it, for every element of four pairs and one s >= 2^-9 with
+// rc = RN(1/s): q = RN(x rc) is within an ulp, its remainder is exact in one FMA, and one more
+// FMA rounds correctly (Markstein's correction, as in the FP8 quantizer). A zero quotient keeps
+// the sign of x.
+__device__ __forceinline__ void divide8(float2 (&x)[4], float s, float rc) {
+  const float2 rc2 = make_float2(rc, rc), ns2 = make_float2(-s, -s);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 q0 = __fmul2_rn(x[e], rc2);
+    const float2 q1 = __ffma2_rn(__ffma2_rn(q0, ns2, x[e]), rc2, q0);
+    x[e] = make_float2(copysignf(q1.x, x[e].x), copysignf(q1.y, x[e].y));
+  }
+}
+
 template <int D, int CACHE>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p) {
   constexpr int R = D / 16;          // lanes per row
   constexpr int kRows = 32 / R;      // rows per warp
   constexpr int kBatch = 4;          // row groups in flight
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int l = lane % R, rr = lane / R;
-  const long long task =
-      static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
 
-  // Block 0 looks the lengths over, so that a fault in a sequence without tokens is reported
-  // too; each warp checks its own token's sequence before it writes.
-  if (CACHE != kCacheNone && blockIdx.x == 0) {
+  // Block (0, 0) looks the lengths over, so that a fault in a sequence without tokens is
+  // reported too; each warp checks its own token's sequence before it writes.
+  if (CACHE != kCacheNone && blockIdx.x == 0 && blockIdx.y == 0) {
     bool bad = threadIdx.x == 0 && (p.cu[0] != 0 || p.cu[p.B] > p.total);
     for (int b = static_cast<int>(threadIdx.x); b < p.B; b += kRowThreads) {
       const long long n = static_cast<long long>(p.cu[b + 1]) - p.cu[b];
@@ -93,9 +107,10 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowParams p) {
     if (bad) report_status(p.status, -7);
   }
 
-  const int t = static_cast<int>(task / p.tasks_per_token);
-  if (t >= p.total) return;
-  const int part = static_cast<int>(task % p.tasks_per_token);
+  const long long tl =
+      static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (tl >= p.total) return;
+  const int t = static_cast<int>(tl);
 
   int pos, phys = -1;
   if constexpr (CACHE == kCacheNone) {
@@ -136,177 +151,214 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowParams p) {
   const int ca = paired ? l : 2 * hl + 2 * (l - hl);
   const int cb = paired ? l + hl : ca + 1;
   const bool turn_a = p.rot && 8 * ca < p.rot, turn_b = p.rot && 8 * cb < p.rot;
-  float cs[8], sn[8];
+  // Angles: half-split, of the eight pairs (a, b); interleaved, of the four pairs of a, then of
+  // b. Channels that do not turn get no angle and are left alone below.
+  float2 cs[4], sn[4], ns[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+  for (int i = 0; i < 4; ++i) cs[i] = make_float2(1.f, 1.f), sn[i] = make_float2(0.f, 0.f);
   if (p.rot) {
     const float* row = p.cos_sin + static_cast<size_t>(pos) * p.rot;
     const float* srow = row + p.rot / 2;
-    auto four = [](const float* from, float* to) {
+    auto four = [](const float* from, float2* to) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(from));
-      to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+      to[0] = make_float2(v.x, v.y), to[1] = make_float2(v.z, v.w);
     };
     if (split) {
       if (paired) {
-        four(row + 8 * l, cs), four(row + 8 * l + 4, cs + 4);
-        four(srow + 8 * l, sn), four(srow + 8 * l + 4, sn + 4);
+        four(row + 8 * l, cs), four(row + 8 * l + 4, cs + 2);
+        four(srow + 8 * l, sn), four(srow + 8 * l + 4, sn + 2);
       }
     } else {
       if (turn_a) four(row + 4 * ca, cs), four(srow + 4 * ca, sn);
-      if (turn_b) four(row + 4 * cb, cs + 4), four(srow + 4 * cb, sn + 4);
+      if (turn_b) four(row + 4 * cb, cs + 2), four(srow + 4 * cb, sn + 2);
     }
   }
-
-  const int all = p.groups[0] + p.groups[1] + p.groups[2];
-  const int g0 = part * p.groups_per_task;
-  const int g1 = imin(g0 + p.groups_per_task, all);
-  // (kind, head) of row group g on this lane; head < 0: no row.
-  auto row_of = [&](int g, int& kind, int& head) {
-    kind = g < p.groups[0] ? 0 : g < p.groups[0] + p.groups[1] ? 1 : 2;
-    const int first = kind == 0 ? 0 : kind == 1 ? p.groups[0] : p.groups[0] + p.groups[1];
-    head = (g - first) * kRows + rr;
-    if (g >= g1 || head >= p.heads[kind]) head = -1;
-  };
-  for (int gb = g0; gb < g1; gb += kBatch) {
-    uint4 va[kBatch], vb[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      int kind, head;
-      row_of(gb + i, kind, head);
-      va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-      if (head >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.in[kind] + t * p.stride[kind] + static_cast<size_t>(head) * (2 * D));
-        va[i] = __ldg(src + ca);
-        vb[i] = __ldg(src + cb);
+  for (int i = 0; i < 4; ++i) ns[i] = make_float2(-sn[i].x, -sn[i].y);
+
+  // Rows of one kind (0 q, 1 k, 2 v): groups [g0, g1) of kRows heads.
+  auto rows = [&](auto kind_c, int g0, int g1) {
+    constexpr int kind = decltype(kind_c)::value;
+    const int heads = p.heads[kind];
+    const uint8_t* src = p.in[kind] + t * p.stride[kind];
+    const float* w = kind < 2 ? p.weight[kind] : nullptr;
+    float2 wa[4], wb[4];
+    if (kind < 2 && w) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(w + 8 * ca) + e);
+        const float4 y = __ldg(reinterpret_cast<const float4*>(w + 8 * cb) + e);
+        wa[2 * e] = make_float2(x.x, x.y), wa[2 * e + 1] = make_float2(x.z, x.w);
+        wb[2 * e] = make_float2(y.x, y.y), wb[2 * e + 1] = make_float2(y.z, y.w);
       }
     }
+    uint8_t* dst = nullptr;   // of head 0; null: this token has no page
+    size_t dst_step = 0;      // from head to head
+    const int slot = pos & ((1 << p.page_shift) - 1);
+    if (CACHE == kCacheNone || kind == 0) {
+      const unsigned blk = static_cast<unsigned>(t) / static_cast<unsigned>(p.N);
+      const unsigned row = static_cast<unsigned>(t) - blk * static_cast<unsigned>(p.N);
+      dst_step = static_cast<size_t>(p.N) * (2 * D);
+      dst = p.out[kind == 0 ? 0 : 1] + static_cast<size_t>(blk) * heads * dst_step +
+            static_cast<size_t>(row) * (2 * D);
+    } else if (phys >= 0) {
+      const size_t tok = CACHE == kCacheFp4 ? fp4_row_bytes(D) : 2 * D;
+      dst_step = tok << p.page_shift;
+      dst = p.pool[kind - 1] + static_cast<size_t>(phys) * heads * dst_step;
+      if (CACHE == kCacheBf16) dst += static_cast<size_t>(slot) * (2 * D);
+    }
+    for (int gb = g0; gb < g1; gb += kBatch) {
+      uint4 va[kBatch], vb[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (gb + i >= g1) break;  // the same for the whole warp
-      int kind, head;
-      row_of(gb + i, kind, head);
-      float a[8], b[8];
-      {
-        const uint32_t wa[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
-        const uint32_t wb[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[2 * e] = __uint_as_float(wa[e] << 16);
-          a[2 * e + 1] = __uint_as_float(wa[e] & 0xFFFF0000u);
-          b[2 * e] = __uint_as_float(wb[e] << 16);
-          b[2 * e + 1] = __uint_as_float(wb[e] & 0xFFFF0000u);
+      for (int i = 0; i < kBatch; ++i) {
+        const int head = (gb + i) * kRows + rr;
+        va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+        if (gb + i < g1 && head < heads) {
+          const uint4* from = reinterpret_cast<const uint4*>(src + static_cast<size_t>(head) * (2 * D));
+          va[i] = __ldg(from + ca);
+          vb[i] = __ldg(from + cb);
         }
       }
-      const float* w = kind < 2 ? p.weight[kind] : nullptr;
-      if (w) {
-        float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-#pragma unroll
-        for (int off = R / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(w + 8 * ca + e));
-          const float4 y = __ldg(reinterpret_cast<const float4*>(w + 8 * cb + e));
-          a[e] *= rs * x.x, a[e + 1] *= rs * x.y, a[e + 2] *= rs * x.z, a[e + 3] *= rs * x.w;
-          b[e] *= rs * y.x, b[e + 1] *= rs * y.y, b[e + 2] *= rs * y.z, b[e + 3] *= rs * y.w;
-        }
-      }
-      if (kind < 2 && p.rot) {
-        if (split) {
-          if (paired) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float x = a[e], y = b[e];
-              a[e] = __fsub_rn(__fmul_rn(x, cs[e]), __fmul_rn(y, sn[e]));
-              b[e] = __fadd_rn(__fmul_rn(y, cs[e]), __fmul_rn(x, sn[e]));
-            }
+      for (int i = 0; i < kBatch; ++i) {
+        if (gb + i >= g1) break;  // the same for the whole warp
+        const int head = (gb + i) * kRows + rr;
+        const bool live = head < heads && dst != nullptr;
+        uint8_t* to = dst + static_cast<size_t>(head) * dst_step;
+        if constexpr (kind == 2 && CACHE == kCacheBf16) {
+          if (live) {
+            reinterpret_cast<uint4*>(to)[ca] = va[i];
+            reinterpret_cast<uint4*>(to)[cb] = vb[i];
           }
-        } else {
+          continue;
+        }
+        float2 a[4], b[4];
+        {
+          const uint32_t xa[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
+          const uint32_t xb[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (turn_a) {
-              const float x = a[2 * e], y = a[2 * e + 1];
-              a[2 * e] = __fsub_rn(__fmul_rn(x, cs[e]), __fmul_rn(y, sn[e]));
-              a[2 * e + 1] = __fadd_rn(__fmul_rn(y, cs[e]), __fmul_rn(x, sn[e]));
+            a[e] = make_float2(__uint_as_float(xa[e] << 16), __uint_as_float(xa[e] & 0xFFFF0000u));
+            b[e] = make_float2(__uint_as_float(xb[e] << 16), __uint_as_float(xb[e] & 0xFFFF0000u));
+          }
+        }
+        if (kind < 2 && w) {
+          float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s2 = __ffma2_rn(a[e], a[e], s2);
+            s2 = __ffma2_rn(b[e], b[e], s2);
+          }
+          float ss = s2.x + s2.y;
+#pragma unroll
+          for (int off = R / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+          const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = __fmul2_rn(__fmul2_rn(a[e], rs2), wa[e]);
+            b[e] = __fmul2_rn(__fmul2_rn(b[e], rs2), wb[e]);
+          }
+        }
+        if (kind < 2 && p.rot) {
+          if (split) {
+            if (paired) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = a[e], y = b[e];
+                if constexpr (CACHE == kCacheFp4 && kind == 1) {
+                  // Scalar: packed products and sums get contracted, whatever their rounding.
+                  a[e] = make_float2(__fsub_rn(__fmul_rn(x.x, cs[e].x), __fmul_rn(y.x, sn[e].x)),
+                                     __fsub_rn(__fmul_rn(x.y, cs[e].y), __fmul_rn(y.y, sn[e].y)));
+                  b[e] = make_float2(__fadd_rn(__fmul_rn(y.x, cs[e].x), __fmul_rn(x.x, sn[e].x)),
+                                     __fadd_rn(__fmul_rn(y.y, cs[e].y), __fmul_rn(x.y, sn[e].y)));
+                } else {
+                  a[e] = __ffma2_rn(x, cs[e], __fmul2_rn(y, ns[e]));
+                  b[e] = __ffma2_rn(y, cs[e], __fmul2_rn(x, sn[e]));
+                }
+              }
             }
-            if (turn_b) {
-              const float x = b[2 * e], y = b[2 * e + 1];
-              b[2 * e] = __fsub_rn(__fmul_rn(x, cs[4 + e]), __fmul_rn(y, sn[4 + e]));
-              b[2 * e + 1] = __fadd_rn(__fmul_rn(y, cs[4 + e]), __fmul_rn(x, sn[4 + e]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              auto turn = [](float2& v, float c, float s) {
+                v = make_float2(__fsub_rn(__fmul_rn(v.x, c), __fmul_rn(v.y, s)),
+                                __fadd_rn(__fmul_rn(v.y, c), __fmul_rn(v.x, s)));
+              };
+              const int h = e >> 1;
+              if (turn_a) turn(a[e], e & 1 ? cs[h].y : cs[h].x, e & 1 ? sn[h].y : sn[h].x);
+              if (turn_b)
+                turn(b[e], e & 1 ? cs[2 + h].y : cs[2 + h].x, e & 1 ? sn[2 + h].y : sn[2 + h].x);
             }
           }
         }
-      }
-      if (CACHE == kCacheFp4 && kind >= 1) {
-        // 16-channel blocks: this lane's chunk a with the partner lane's (chunk a ^ 1), and b
-        // with its; past the rotated channels of a half-split, a with b.
-        const float inv = p.inv_scale[kind - 1];
-        float ma = 0.f, mb = 0.f;
+        if constexpr (CACHE == kCacheFp4 && kind >= 1) {
+          // 16-channel blocks: this lane's chunk a with the partner lane's (chunk a ^ 1), and
+          // b with its; past the rotated channels of a half-split, a with b.
+          const float2 inv = make_float2(p.inv_scale[kind - 1], p.inv_scale[kind - 1]);
+          float ma = 0.f, mb = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] *= inv, b[e] *= inv;
-          ma = fmaxf(ma, fabsf(a[e]));
-          mb = fmaxf(mb, fabsf(b[e]));
-        }
-        const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
-        const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
-        if (paired) {
-          ma = fmaxf(ma, oa), mb = fmaxf(mb, ob);
-        } else {
-          ma = mb = fmaxf(ma, mb);
-        }
-        const uint32_t sa = f32_to_e4m3(__fdiv_rn(ma, 6.f)), sb = f32_to_e4m3(__fdiv_rn(mb, 6.f));
-        const float fa = e4m3_to_f32(sa), fb = e4m3_to_f32(sb);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] = fa > 0.f ? __fdiv_rn(a[e], fa) : 0.f;
-          b[e] = fb > 0.f ? __fdiv_rn(b[e], fb) : 0.f;
-        }
-        if (phys >= 0 && head >= 0) {
-          const int P = 1 << p.page_shift, slot = pos & (P - 1);
-          uint8_t* blk = p.pool[kind - 1] +
-                         (static_cast<size_t>(phys) * p.heads[1] + head) *
-                             static_cast<size_t>(P * fp4_row_bytes(D));
-          uint32_t* codes = reinterpret_cast<uint32_t*>(blk + slot * fp4_code_bytes(D));
-          uint8_t* scales = blk + P * fp4_code_bytes(D) + slot * fp4_scale_bytes(D);
-          codes[ca] = f32x8_to_e2m1(a);
-          codes[cb] = f32x8_to_e2m1(b);
-          if (!(ca & 1)) scales[ca >> 1] = static_cast<uint8_t>(sa);
-          if (!(cb & 1)) scales[cb >> 1] = static_cast<uint8_t>(sb);
-        }
-      } else if (head >= 0) {
-        uint4* dst = nullptr;
-        if (CACHE == kCacheBf16 && kind >= 1) {
-          const int slot = pos & ((1 << p.page_shift) - 1);
-          if (phys >= 0)
-            dst = reinterpret_cast<uint4*>(
-                p.pool[kind - 1] +
-                (((static_cast<size_t>(phys) * p.heads[1] + head) << p.page_shift) + slot) *
-                    (2 * D));
-        } else {
-          const int blk = t / p.N, row = t % p.N;
-          dst = reinterpret_cast<uint4*>(
-              p.out[kind] +
-              ((static_cast<size_t>(blk) * p.heads[kind] + head) * p.N + row) * (2 * D));
-        }
-        if (dst) {
-          dst[ca] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                               pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
-          dst[cb] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]),
-                               pack_bf16x2(b[4], b[5]), pack_bf16x2(b[6], b[7]));
+          for (int e = 0; e < 4; ++e) {
+            a[e] = __fmul2_rn(a[e], inv);
+            b[e] = __fmul2_rn(b[e], inv);
+            ma = fmaxf(ma, fmaxf(fabsf(a[e].x), fabsf(a[e].y)));
+            mb = fmaxf(mb, fmaxf(fabsf(b[e].x), fabsf(b[e].y)));
+          }
+          const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
+          const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+          if (paired) {
+            ma = fmaxf(ma, oa), mb = fmaxf(mb, ob);
+          } else {
+            ma = mb = fmaxf(ma, mb);
+          }
+          // max / 6, correctly rounded as in divide8, then to E4M3.
+          constexpr float kSixth = 1.f / 6.f;
+          const float qa = ma * kSixth, qm = mb * kSixth;
+          const float da = fmaf(fmaf(qa, -6.f, ma), kSixth, qa);
+          const float db = fmaf(fmaf(qm, -6.f, mb), kSixth, qm);
+          const uint32_t sf = f32x2_to_e4m3(da, db);
+          const uint32_t sh = e4m3x2_to_f16(sf);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sh));
+          // A zero scale: zeros, not quotients.
+          divide8(a, f.x, f.x > 0.f ? __frcp_rn(f.x) : 0.f);
+          divide8(b, f.y, f.y > 0.f ? __frcp_rn(f.y) : 0.f);
+          if (live) {
+            uint32_t* codes = reinterpret_cast<uint32_t*>(to + slot * fp4_code_bytes(D));
+            uint8_t* scales = to + (fp4_code_bytes(D) << p.page_shift) + slot * fp4_scale_bytes(D);
+            codes[ca] = f.x > 0.f ? f32x8_to_e2m1(a) : 0u;
+            codes[cb] = f.y > 0.f ? f32x8_to_e2m1(b) : 0u;
+            if (!(ca & 1)) scales[ca >> 1] = static_cast<uint8_t>(sf);
+            if (!(cb & 1)) scales[cb >> 1] = static_cast<uint8_t>(sf >> 8);
+          }
+        } else if (live) {
+          reinterpret_cast<uint4*>(to)[ca] =
+              make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y),
+                         pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[3].x, a[3].y));
+          reinterpret_cast<uint4*>(to)[cb] =
+              make_uint4(pack_bf16x2(b[0].x, b[0].y), pack_bf16x2(b[1].x, b[1].y),
+                         pack_bf16x2(b[2].x, b[2].y), pack_bf16x2(b[3].x, b[3].y));
         }
       }
     }
-  }
+  };
+  // This warp's share of the token's row groups: [g0, g1) of q's, then k's, then v's.
+  const int g0 = static_cast<int>(blockIdx.y) * p.groups_per_task;
+  const int g1 = g0 + p.groups_per_task;
+  const int nq = p.groups[0], nk = p.groups[1], nv = p.groups[2];
+  if (g0 < nq) rows(std::integral_constant<int, 0>{}, g0, imin(g1, nq));
+  if (g1 > nq && g0 < nq + nk)
+    rows(std::integral_constant<int, 1>{}, imax(g0 - nq, 0), imin(g1 - nq, nk));
+  if (CACHE != kCacheNone && g1 > nq + nk && g0 < nq + nk + nv)
+    rows(std::integral_constant<int, 2>{}, imax(g0 - nq - nk, 0), imin(g1 - nq - nk, nv));
 }
 
 // 4-bit pages -> bf16 pages: page p of sequence b, as the table lists it, goes to dst page
-// b * max_pages + p. One CTA per page; a thread turns 4 bytes of codes into 16 bytes. Slots
-// past the sequence's length get zeros (a reader multiplies them by zero, so they have to be
-// finite), pages past it are left alone.
+// b * max_pages + p. A thread turns 4 bytes of codes into 16 bytes and has kUnpackBatch such
+// loads in flight; a CTA takes 256 * kUnpackBatch of a page, so that a few pages of many heads
+// still fill the GPU. Slots past the sequence's length get zeros (a reader multiplies them by
+// zero, so they have to be finite), pages past it are left alone.
+constexpr int kUnpackBatch = 8;
+
 struct UnpackParams {
   const uint8_t* pool;
   uint4* dst;
@@ -321,41 +373,55 @@ template <int D>
 __global__ void __launch_bounds__(256) unpack_fp4_kernel(const UnpackParams p) {
   const int pg = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
   const int P = 1 << p.page_shift;
-  const int len = p.lens[b];
+  const int len = __ldg(p.lens + b);
+  const int phys = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + pg);
   if (len < 0 || len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
-    if (pg == 0 && threadIdx.x == 0) report_status(p.status, -7);
+    if (pg == 0 && blockIdx.z == 0 && threadIdx.x == 0) report_status(p.status, -7);
     return;
   }
   const int here = imin(len - (pg << p.page_shift), P);  // valid tokens of this page
   if (here <= 0) return;
-  const int phys = p.table[static_cast<size_t>(b) * p.max_pages + pg];
   if (phys < 0 || phys >= p.num_pages) {
-    if (threadIdx.x == 0) report_status(p.status, -5);
+    if (blockIdx.z == 0 && threadIdx.x == 0) report_status(p.status, -5);
     return;
   }
-  constexpr int kChunks = D / 8;  // 8-channel chunks of a row
+  constexpr int kChunks = D / 8;             // 8-channel chunks of a row
+  constexpr int kRowsPer = 256 / kChunks;    // rows the CTA's threads cover at once
+  const int c = static_cast<int>(threadIdx.x) % kChunks;
+  const int row0 = static_cast<int>(blockIdx.z) * (kRowsPer * kUnpackBatch) +
+                   static_cast<int>(threadIdx.x) / kChunks;
+  const int rows = p.Hkv << p.page_shift;    // (head, token) rows of the page
   const size_t blk = static_cast<size_t>(P * fp4_row_bytes(D));
   const uint8_t* src = p.pool + static_cast<size_t>(phys) * p.Hkv * blk;
-  uint4* dst = p.dst + (static_cast<size_t>(b) * p.max_pages + pg) * p.Hkv *
-                           (static_cast<size_t>(P) * kChunks);
-  const int n = p.Hkv * P * kChunks;
-  for (int i = static_cast<int>(threadIdx.x); i < n; i += blockDim.x) {
-    const int c = i % kChunks, row = i / kChunks, tok = row & (P - 1), h = row >> p.page_shift;
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (tok < here) {
-      const uint8_t* q = src + h * blk;
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + tok * kChunks + c);
-      const float s = e4m3_to_f32(__ldg(q + P * fp4_code_bytes(D) + tok * (kChunks / 2) + c / 2));
-      uint32_t v[4], o[4];
-      e2m1x8_to_f16(w, v);
+  uint4* dst = p.dst + (static_cast<size_t>(b) * p.max_pages + pg) * rows * kChunks + c;
+  uint32_t w[kUnpackBatch];
+  uint8_t sf[kUnpackBatch];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
-        o[e] = pack_bf16x2(f.x * s * p.scale, f.y * s * p.scale);
-      }
-      out = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < kUnpackBatch; ++i) {
+    const int row = row0 + i * kRowsPer, tok = row & (P - 1);
+    w[i] = 0, sf[i] = 0;
+    if (row < rows && tok < here) {
+      const uint8_t* q = src + static_cast<size_t>(row >> p.page_shift) * blk;
+      w[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + tok * kChunks + c);
+      sf[i] = __ldg(q + (fp4_code_bytes(D) << p.page_shift) + tok * (kChunks / 2) + c / 2);
     }
-    dst[i] = out;
+  }
+  const float2 scale = make_float2(p.scale, p.scale);
+#pragma unroll
+  for (int i = 0; i < kUnpackBatch; ++i) {
+    const int row = row0 + i * kRowsPer;
+    if (row >= rows) break;
+    uint32_t v[4], o[4];
+    e2m1x8_to_f16(w[i], v);
+    const __half2 s = __half2half2(__ushort_as_half(e4m3x2_to_f16(sf[i]) & 0xFFFFu));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // code * scale is exact in f16; one product in fp32, one rounding to bf16.
+      const float2 f =
+          __fmul2_rn(__half22float2(__hmul2(*reinterpret_cast<const __half2*>(&v[e]), s)), scale);
+      o[e] = pack_bf16x2(f.x, f.y);
+    }
+    dst[static_cast<size_t>(row) * kChunks] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

@@ -44,28 +44,24 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
   return h;
 }
 
-// fp32 -> E4M3 code, round to nearest even, saturating at 448.
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+// Two fp32 -> two E4M3 codes (lo in the low byte), round to nearest even, saturating at 448.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
-  return r & 0xFFu;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
-  const uint32_t h = e4m3x2_to_f16(code);
-  return __low2float(*reinterpret_cast<const __half2*>(&h));
-}
-
-// Eight fp32 -> eight E2M1 codes, round to nearest even, saturating at 6; x[0] in the low
+// Eight fp32 -> eight E2M1 codes, round to nearest even, saturating at 6; x[0].x in the low
 // nibble of the low byte.
-__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float2 (&x)[4]) {
   uint32_t r;
   asm("{\n .reg .b8 b0, b1, b2, b3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
       " mov.b32 %0, {b0, b1, b2, b3};\n}"
       : "=r"(r)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y),
+        "f"(x[3].x), "f"(x[3].y));
   return r;
 }
 
