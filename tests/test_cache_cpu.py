@@ -20,11 +20,14 @@ def library():
 class _Ptr:
     """Stands in for a device tensor in calls that fail validation: never dereferenced."""
 
-    def __init__(self, addr=1 << 20):
-        self.addr = addr
+    def __init__(self, addr=1 << 20, device=0):
+        self.addr, self.device = addr, device
 
     def data_ptr(self):
         return self.addr
+
+    def get_device(self):
+        return self.device
 
 
 T = _Ptr()
@@ -219,6 +222,16 @@ def test_decode_fp4_workspace():
     assert attn.attn_workspace_bytes_fp4(32, 64, 8, 16384, 128) > need
     assert attn.attn_workspace_bytes_fp4(0, 32, 8, 128, 128) == 0
     assert attn.attn_workspace_bytes_fp4(1, 32, 8, 128, 96) == 0
+
+
+def test_tensors_of_two_devices_are_refused():
+    far = _Ptr(device=1)
+    for call in (lambda: _norm_rope(k_out=far), lambda: _append(False, block_table=far),
+                 lambda: _append(True, v_pool=far), lambda: _unpack(seqlens=far),
+                 lambda: _decode(lse=far)):
+        with pytest.raises(attn.AttnError) as e:
+            call()
+        assert e.value.code == INVALID and "device" in str(e.value)
 
 
 # ------------------------------------------------------------------ the oracle's own pins

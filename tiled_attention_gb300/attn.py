@@ -107,16 +107,45 @@ def declared_functions():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = None  # (the current device's index, the handle of a device's current stream)
+
+
+def _current():
+    """(index, current stream's handle) of the current device, without building a
+    torch.cuda.Stream (which costs more than a small kernel's launch)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(device):
+                return torch.cuda.current_stream(device).cuda_stream
+        _raw_stream = torch.cuda.current_device, raw
+    device = _raw_stream[0]()
+    return device, _raw_stream[1](device)
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _current()[1]
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _place(stream, *tensors):
+    """(stream handle, addresses of the tensors; None: NULL). The tensors must share one device,
+    the current one if the call goes to the current stream."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    if stream is None:
+        device, handle = _current()
+        devices.add(device)
+    else:
+        handle = _stream(stream)
+    if len(devices) > 1:
+        raise AttnError(ATTN_ERR_INVALID, f"tensors and call on devices {sorted(devices)}")
+    return handle, [None if t is None else t.data_ptr() for t in tensors]
 
 
 def last_error() -> str:
@@ -187,10 +216,10 @@ def attn_norm_rope(q, k, q_out, k_out, total, N, Hq, Hkv, d, q_stride, k_stride,
                    interleaved=False, positions=None, stream=None) -> int:
     """Per-head RMS norm and rotation of q and k token rows (strides in elements, so q and k may
     be views into one projection) into attention's layouts."""
-    return lib().attn_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), total, N, Hq, Hkv, d,
-                                q_stride, k_stride, _ptr(q_weight), _ptr(k_weight), eps,
-                                _ptr(cos_sin), max_pos, rot_dim, interleaved, _ptr(positions),
-                                _stream(stream))
+    handle, (q, k, qo, ko, qw, kw, cs, pos) = _place(stream, q, k, q_out, k_out, q_weight,
+                                                     k_weight, cos_sin, positions)
+    return lib().attn_norm_rope(q, k, qo, ko, total, N, Hq, Hkv, d, q_stride, k_stride, qw, kw,
+                                eps, cs, max_pos, rot_dim, interleaved, pos, handle)
 
 
 def attn_append_paged(q, k, v, q_out, k_pool, v_pool, B, Hq, Hkv, total_q, N, d, q_stride,
@@ -198,12 +227,13 @@ def attn_append_paged(q, k, v, q_out, k_pool, v_pool, B, Hq, Hkv, total_q, N, d,
                       interleaved, cu_seqlens_q, seqlens_k, block_table, max_pages, page_size,
                       num_pages, stream=None) -> int:
     """New tokens' K / V into bf16 page pools, normed and rotated, with their queries."""
-    return lib().attn_append_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool),
-                                   _ptr(v_pool), B, Hq, Hkv, total_q, N, d, q_stride, k_stride,
-                                   v_stride, _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin),
-                                   max_pos, rot_dim, interleaved, _ptr(cu_seqlens_q),
-                                   _ptr(seqlens_k), _ptr(block_table), max_pages, page_size,
-                                   num_pages, _stream(stream))
+    handle, (q, k, v, qo, kp, vp, qw, kw, cs, cu, lk, table) = _place(
+        stream, q, k, v, q_out, k_pool, v_pool, q_weight, k_weight, cos_sin, cu_seqlens_q,
+        seqlens_k, block_table)
+    return lib().attn_append_paged(q, k, v, qo, kp, vp, B, Hq, Hkv, total_q, N, d, q_stride,
+                                   k_stride, v_stride, qw, kw, eps, cs, max_pos, rot_dim,
+                                   interleaved, cu, lk, table, max_pages, page_size, num_pages,
+                                   handle)
 
 
 def attn_append_paged_fp4(q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, B, Hq, Hkv, total_q,
@@ -211,21 +241,21 @@ def attn_append_paged_fp4(q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, B, H
                           max_pos, rot_dim, interleaved, cu_seqlens_q, seqlens_k, block_table,
                           max_pages, page_size, num_pages, stream=None) -> int:
     """attn_append_paged into 4-bit pools (uint8 [num_pages, Hkv, page_size * (d/2 + d/16)])."""
-    return lib().attn_append_paged_fp4(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool),
-                                       _ptr(v_pool), k_scale, v_scale, B, Hq, Hkv, total_q, N, d,
-                                       q_stride, k_stride, v_stride, _ptr(q_weight),
-                                       _ptr(k_weight), eps, _ptr(cos_sin), max_pos, rot_dim,
-                                       interleaved, _ptr(cu_seqlens_q), _ptr(seqlens_k),
-                                       _ptr(block_table), max_pages, page_size, num_pages,
-                                       _stream(stream))
+    handle, (q, k, v, qo, kp, vp, qw, kw, cs, cu, lk, table) = _place(
+        stream, q, k, v, q_out, k_pool, v_pool, q_weight, k_weight, cos_sin, cu_seqlens_q,
+        seqlens_k, block_table)
+    return lib().attn_append_paged_fp4(q, k, v, qo, kp, vp, k_scale, v_scale, B, Hq, Hkv, total_q,
+                                       N, d, q_stride, k_stride, v_stride, qw, kw, eps, cs,
+                                       max_pos, rot_dim, interleaved, cu, lk, table, max_pages,
+                                       page_size, num_pages, handle)
 
 
 def attn_unpack_pages_fp4(pool, dst, pool_scale, block_table, seqlens, B, max_pages, Hkv,
                           page_size, d, num_pages, stream=None) -> int:
     """4-bit pages, as the table lists them, to bf16 pages [B * max_pages, Hkv, page_size, d]."""
-    return lib().attn_unpack_pages_fp4(_ptr(pool), _ptr(dst), pool_scale, _ptr(block_table),
-                                       _ptr(seqlens), B, max_pages, Hkv, page_size, d, num_pages,
-                                       _stream(stream))
+    handle, (pool, dst, table, lens) = _place(stream, pool, dst, block_table, seqlens)
+    return lib().attn_unpack_pages_fp4(pool, dst, pool_scale, table, lens, B, max_pages, Hkv,
+                                       page_size, d, num_pages, handle)
 
 
 def attn_fwd_paged_decode_fp4(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, k_scale, v_scale,
@@ -233,10 +263,11 @@ def attn_fwd_paged_decode_fp4(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, k_scale,
                               stream=None) -> int:
     """Paged decode over 4-bit pools (torch tensors in device memory)."""
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return lib().attn_fwd_paged_decode_fp4(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq,
-                                           Hkv, N, d, scale, k_scale, v_scale, _ptr(cu_seqlens),
-                                           _ptr(block_table), page_size, num_pages,
-                                           _ptr(workspace), ws_bytes, _stream(stream))
+    handle, (q, k, v, o, lse, cu, table, ws) = _place(stream, q, k, v, o, lse, cu_seqlens,
+                                                      block_table, workspace)
+    return lib().attn_fwd_paged_decode_fp4(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, k_scale,
+                                           v_scale, cu, table, page_size, num_pages, ws, ws_bytes,
+                                           handle)
 
 
 def attn_workspace_bytes_fp4(B, Hq, Hkv, N, d) -> int:
