@@ -100,7 +100,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
   if (num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
-  if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || N > (1 << 30))
+  if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 65535 || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
   if (B > 65535 ||
       static_cast<long long>(B) * Hkv >= (1ll << 31) / ((static_cast<long long>(N) + 127) / 128))

@@ -35,7 +35,7 @@
 // The second kernel starts under programmatic dependent launch: it finds its parts while the
 // first still runs. No counters, so no memset.
 //
-// CTA: four warps; warp w takes 64-token stages w, w + 4, ... of a segment, through a ring of its
+// CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64), through a ring of its
 // own in shared memory: it brings the next stages in with bulk copies while it works on one, so
 // no warp waits for another before a segment's end.
 #pragma once
@@ -70,26 +70,26 @@ struct DecodeFp4Params {
 template <int D, int NT>  // NT: 8-head column tiles (1 or 2)
 struct DecodeFp4Cfg {
   static constexpr int kTok = 32;     // tokens per slice: two 16-row tiles
-  static constexpr int kStage = 64;    // tokens per ring stage
+  static constexpr int kStage = 64 * 128 / D;  // tokens per ring stage
   static constexpr int kWarps = 4;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kCtas = 3;  // per SM
   static constexpr int kCode = D / 2, kScale = D / 16;
   // A stage in shared memory: K codes, K scales, V codes, V scales.
   static constexpr int kOffKs = kStage * kCode, kOffV = kOffKs + kStage * kScale;
-  static constexpr int kStageBytes = 2 * kOffV;      // 9216 (D = 128), 4608 (D = 64)
-  static constexpr int kStages = 2 * 128 / D;     // of one warp's ring
+  static constexpr int kStageBytes = 2 * kOffV;      // 9216
+  static constexpr int kStages = 2;                  // of one warp's ring
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kSteps = D / 16;              // k-steps of S^T, m-tiles of O^T
   static constexpr int kMiscBytes = 256 + 2 * kWarps * 16 * 4;
   static constexpr int kSmemBytes = kWarps * kRingBytes + kMiscBytes + 128;
   static_assert(kWarps * kHeads * D * 4 <= kWarps * kRingBytes, "the O rows reuse the rings");
-  static_assert(kWarps * kStages <= 24, "barriers");
+  static_assert(kWarps * kStages <= 8, "barriers");
 };
 
 struct DecodeFp4Ctrl {
-  uint64_t full[24];  // [warps][stages]
+  uint64_t full[8];  // [warps][stages]
   int abort_flag;
   int seq, seq_before;
   int warp_sum[4];
@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     decode_fp4_kernel(const DecodeFp4Params p) {
   using C = DecodeFp4Cfg<D, NT>;
   constexpr int S = C::kStages;
+  static_assert(S == 2, "two slots a ring");
   const int G = p.group;  // 1 <= G <= 8 NT
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5;
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 16);
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 32);
     if (warp == 0) ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -409,9 +410,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
-  // Copies of one stage: lane 4 sub + part < 16 brings K codes, K scales, V codes or V scales
-  // (part 0..3) of the stage's tokens in its page `sub` (four pages of 16 tokens, two of 32, else
-  // one), and arrives on the stage's barrier with the bytes it asked for. A warp's stages all
+  // Copies of one stage: lane 4 sub + part brings K codes, K scales, V codes or V scales (part
+  // 0..3) of the stage's tokens in its page `sub` (up to eight pages of 16 tokens), and arrives
+  // on the stage's barrier with the bytes it asked for. A warp's stages all
   // lie at the same place of their pages. Pages past the context are not copied. A page whose
   // entry lies outside the pool is never addressed: the status word reports it and it reads as
   // zeros. A stage's table entries are read one stage ahead of its copies.
@@ -421,17 +422,21 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const bool copies = sub * run < C::kStage;
   const int tok0 = warp * C::kStage + sub * run;  // this lane's first token in the warp's stage 0
   const uint32_t bytes = static_cast<uint32_t>(run) * ((part & 1) ? C::kScale : C::kCode);
-  uint8_t* const dst0 = ring + ((part & 2) ? C::kOffV : 0) + ((part & 1) ? C::kOffKs : 0) +
-                        sub * static_cast<int>(bytes);
+  // Shared-memory addresses of this lane's copy and of its barrier, for the next stage; the
+  // other slot's follow by adding, then subtracting, the distance.
+  uint32_t dst = smem_u32(ring) + ((part & 2) ? C::kOffV : 0) + ((part & 1) ? C::kOffKs : 0) +
+                 sub * bytes;
+  uint32_t bar = smem_u32(full);
+  int step = 1;
   const int in_page = tok0 & ((1 << lp) - 1);
   const uint8_t* const src0 =
       ((part & 2) ? p.v : p.k) +
       ((part & 1) ? (C::kCode << lp) + in_page * C::kScale : in_page * C::kCode);
   const uint32_t blk_bytes = static_cast<uint32_t>(C::kCode + C::kScale) << lp;
-  const uint64_t page_bytes = static_cast<uint64_t>(p.Hkv) * blk_bytes;
+  const uint32_t page_bytes = static_cast<uint32_t>(p.Hkv) * blk_bytes;  // the host checks it
 
   const int r = lane >> 2, q = lane & 3;
-  int st_in = 0, st_out = 0;   // ring slots of the next copy and the next slice
+  int st_out = 0;              // ring slot of the next stage
   uint32_t parity = 0;         // of slot st_out
   bool aborted = false;
 
@@ -454,30 +459,35 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 
     const int* const row = p.table + static_cast<size_t>(b) * p.max_pages;
     const uint8_t* const src_g = src0 + static_cast<size_t>(g) * blk_bytes;
-    auto entry = [&](int i) {  // -2: nothing to copy, -1: bad entry
-      const int tok = t0 + tok0 + i * (C::kWarps * C::kStage);
-      if (!copies || i >= n || tok >= t1) return -2;
-      const int e = __ldg(row + (tok >> lp));
+    // Table entry of this lane's page of stage i: -2 nothing to copy, -1 outside the pool.
+    const int last = copies ? t1 - t0 - tok0 : 0;  // tokens from this lane's first on
+    const int first_page = (t0 + tok0) >> lp;      // a warp's stages are whole pages apart
+    auto entry = [&](int i) {
+      const int tok = i * (C::kWarps * C::kStage);
+      if (i >= n || tok >= last) return -2;
+      const int e = __ldg(row + first_page + (tok >> lp));
       return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
     };
     auto issue = [&](int phys) {
-      if (lane < 16) {
-        uint8_t* dst = dst0 + st_in * C::kStageBytes;
-        if (phys >= 0) {
-          mbar_arrive_expect_tx(&full[st_in], bytes);
-          bulk_load(dst, src_g + static_cast<uint64_t>(phys) * page_bytes, bytes,
-                    &full[st_in]);
-        } else {
-          if (phys == -1) {
-            report_status(p.status, -5);
-            for (uint32_t x = 0; x < bytes; x += 16)
-              *reinterpret_cast<uint4*>(dst + x) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
-          mbar_arrive(&full[st_in]);
+      if (phys >= 0) {
+        asm volatile(
+            "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+            "[%3];" ::"r"(dst),
+            "l"(src_g + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * page_bytes),
+            "r"(bytes), "r"(bar)
+            : "memory");
+      } else {
+        if (phys == -1) {
+          report_status(p.status, -5);
+          for (uint32_t x = 0; x < bytes; x += 16) st_shared_v4(dst + x, 0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
       }
-      st_in = st_in + 1 == S ? 0 : st_in + 1;
+      dst += step * C::kStageBytes;
+      bar += step * 8;
+      step = -step;
     };
     int issued = 0;
     for (; issued < S - 1 && issued < n; ++issued) issue(entry(issued));
