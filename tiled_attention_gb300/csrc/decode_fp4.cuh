@@ -61,6 +61,7 @@ struct DecodeFp4Params {
   int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
   int slots;             // CTAs of the decode kernel
   int min_blocks;        // least blocks a CTA takes
+  int join_heads;        // query heads a CTA of the joining kernel takes
   float scale_log2;      // softmax scale * K tensor scale * log2 e
   float v_scale;
   int* status;
@@ -198,20 +199,26 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, in
   bool live[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) live[x] = !EDGE || r + 8 * x < left;
-  float y[2][NT][4];
-  float top = -INFINITY;
+  // Weights 2^(x - mref) and their sums. A weight above 2^15 (a score past the reference max by
+  // more than 8) shows in the sums, which are needed anyway; a sum may also pass it without one,
+  // and the slow path then finds nothing to move, or moves early.
+  float e[2][NT][4], sum[NT][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[u][nt][e] = fmaf(s[u][nt][e], sc[nt][e & 1], -mref[nt][e & 1]);
-        if (EDGE && !live[2 * u + (e >> 1)]) y[u][nt][e] = -INFINITY;
-        top = fmaxf(top, y[u][nt][e]);
+      for (int i = 0; i < 4; ++i) {
+        e[u][nt][i] = fast_exp2(fmaf(s[u][nt][i], sc[nt][i & 1], -mref[nt][i & 1]));
+        if (EDGE && !live[2 * u + (i >> 1)]) e[u][nt][i] = 0.f;
       }
-  if (__any_sync(0xffffffffu, top > 15.f)) {
-    // Some score passed the reference max by more than 8: move that head's.
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      sum[nt][c] = (e[0][nt][c] + e[0][nt][c + 2]) + (e[1][nt][c] + e[1][nt][c + 2]);
+  }
+  float all = sum[0][0] + sum[0][1];
+  if (NT == 2) all += sum[NT - 1][0] + sum[NT - 1][1];
+  if (__any_sync(0xffffffffu, !(all <= 32768.f))) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -223,8 +230,8 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, in
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if (mx > mref[nt][c] + 15.f) {
-          const float mn = mx - 7.f;
+        const float mn = mx - 7.f;
+        if (mn > mref[nt][c]) {
           const float f = fast_exp2(mref[nt][c] - mn);
           mref[nt][c] = mn;
           l[nt][c] *= f;
@@ -232,26 +239,25 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, in
           for (int i = 0; i < C::kSteps; ++i) o[nt][i][c] *= f, o[nt][i][c + 2] *= f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int u = x >> 1, e = c + 2 * (x & 1);
-            y[u][nt][e] = live[x] ? fmaf(s[u][nt][e], sc[nt][c], -mn) : -INFINITY;
+            const int u = x >> 1, i = c + 2 * (x & 1);
+            e[u][nt][i] = live[x] ? fast_exp2(fmaf(s[u][nt][i], sc[nt][c], -mn)) : 0.f;
           }
+          sum[nt][c] = (e[0][nt][c] + e[0][nt][c + 2]) + (e[1][nt][c] + e[1][nt][c + 2]);
         }
       }
   }
   uint32_t pb[2][NT][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int nt = 0; nt < NT; ++nt) {
+    l[nt][0] += sum[nt][0];
+    l[nt][1] += sum[nt][1];
+    // The weights' fragment, transposed, is the B operand of O^T: k = tokens.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float e[4];
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = fast_exp2(y[u][nt][i]);
-      l[nt][0] += e[0] + e[2];
-      l[nt][1] += e[1] + e[3];
-      // The scores' fragment, transposed, is the B operand of O^T: k = tokens.
-      pb[u][nt][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
-      pb[u][nt][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
-    }
+      for (int i = 0; i < 2; ++i)
+        pb[u][nt][i] = movmatrix_trans(pack_f16x2(e[u][nt][2 * i], e[u][nt][2 * i + 1]));
+  }
   // ---- O^T += V^T P^T
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -315,16 +321,17 @@ __device__ __forceinline__ int fp4_length(const DecodeFp4Params& p, int b, bool 
 
 __device__ __forceinline__ int fp4_blocks(int L) { return (L + kFp4Block128 - 1) / kFp4Block128; }
 
-// The work list as every CTA (of 128 threads) sees it: thread t sums the blocks of sequences
+// The work list as every CTA (of T threads) sees it: thread t sums the blocks of sequences
 // [t c, (t + 1) c), a scan over the threads gives `before` (blocks of the sequences before its
 // own) and `total`. The host has checked that all blocks of all heads fit an int.
 struct Fp4Plan {
   int first, count, before, mine, total;
 };
+template <int T>
 __device__ __forceinline__ Fp4Plan fp4_plan(const DecodeFp4Params& p, int* warp_sum, bool report) {
   Fp4Plan w;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
-  const int c = (p.B + 127) / 128;
+  const int c = (p.B + T - 1) / T;
   w.first = imin(tid * c, p.B);
   w.count = imin(c, p.B - w.first);
   int sum = 0;
@@ -339,7 +346,7 @@ __device__ __forceinline__ Fp4Plan fp4_plan(const DecodeFp4Params& p, int* warp_
   __syncthreads();
   int before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < T / 32; ++i) {
     if (i < (tid >> 5)) before += warp_sum[i];
     total += warp_sum[i];
   }
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     if (warp == 0) ctl->abort_flag = 0;
     fence_mbar_init();
   }
-  const Fp4Plan plan = fp4_plan(p, ctl->warp_sum, blockIdx.x == 0);
+  const Fp4Plan plan = fp4_plan<C::kThreads>(p, ctl->warp_sum, blockIdx.x == 0);
   const int U = plan.total * p.Hkv;
   const int nn = fp4_ctas(p, U);
   const int cta = static_cast<int>(blockIdx.x);
@@ -641,18 +648,23 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 }
 
 // Joins the parts of contexts that several CTAs share, and writes the rows of empty ones. One
-// CTA per (query head, sequence): four threads a four-column group, thread s of them the parts
-// s, s + 4, ...; the four sums are added in order.
+// CTA per (kv head, sequence), or per query head; a thread takes four columns of one head, and where that leaves
+// threads over, set s of them takes the parts s, s + sets, ...; the sets' sums are added in
+// order.
+constexpr int kCombineThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(128) combine_fp4_kernel(const DecodeFp4Params p) {
-  constexpr int kQuads = D / 4, kSets = 128 / kQuads, kBatch = 8;
-  __shared__ int warp_sum[4];
+__global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const DecodeFp4Params p) {
+  constexpr int kQuads = D / 4, kBatch = 8;
+  __shared__ int warp_sum[kCombineThreads / 32];
   __shared__ int seq_before;
-  __shared__ float sm[kSets], sl[kSets];
-  __shared__ float4 so[kSets][kQuads];
-  const int h = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
+  __shared__ float2 sml[kCombineThreads];
+  __shared__ float4 so[kCombineThreads];
+  const int H = p.join_heads, G = p.group;
+  const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
+  const int g = h0 / G, hg = h0 % G;  // kv head, first query head of its group
   const int tid = static_cast<int>(threadIdx.x);
-  const Fp4Plan plan = fp4_plan(p, warp_sum, false);
+  const Fp4Plan plan = fp4_plan<kCombineThreads>(p, warp_sum, false);
   if (plan.first <= b && b < plan.first + plan.count) {
     int x = plan.before;
     for (int i = plan.first; i < b; ++i) x += fp4_blocks(fp4_length(p, i, false));
@@ -660,74 +672,83 @@ __global__ void __launch_bounds__(128) combine_fp4_kernel(const DecodeFp4Params 
   }
   __syncthreads();
   const int nb = fp4_blocks(fp4_length(p, b, false));
-  const size_t orow = static_cast<size_t>(b) * p.Hq + h;
+  const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
+  // Every CTA waits, those without work too: this kernel must not end before the first one.
   if (nb == 0) {  // empty context: O = 0, LSE = -inf
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < D / 2) reinterpret_cast<uint32_t*>(p.o + orow * D)[tid] = 0;
-    if (tid == 0) p.lse[orow] = -INFINITY;
+    for (int i = tid; i < H * kQuads; i += kCombineThreads)
+      reinterpret_cast<uint2*>(p.o + head0 * D)[i] = make_uint2(0, 0);
+    if (tid < H) p.lse[head0 + tid] = -INFINITY;
     return;
   }
-  const int G = p.group, g = h / G, hh = h % G;
   const int U = plan.total * p.Hkv, nn = fp4_ctas(p, U);
   const int u0 = seq_before * p.Hkv + g * nb;
   const int c0 = fp4_cta_of(u0, U, nn), c1 = fp4_cta_of(u0 + nb - 1, U, nn);
-  // Every CTA waits, those without work too: this kernel must not end before the first one.
-  if (c0 == c1) {  // one CTA held the whole context
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;  // one CTA held the whole context
   // The first part is its CTA's first segment only if the CTA starts with this context.
   const int slot0 = 2 * c0 + (fp4_start(c0, U, nn) == u0 ? 0 : 1);
   const int parts = c1 - c0 + 1;
-  const int quad = tid % kQuads, set = tid / kQuads;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float M = -INFINITY, Ls = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x0 = set; x0 < parts; x0 += kSets * kBatch) {
-    float2 ml[kBatch];
-    float4 ov[kBatch];
+  const int items = H * kQuads;
+  const int sets = imax(1, kCombineThreads / items);
+  const int set = items < kCombineThreads ? tid / items : 0;
+  for (int it0 = 0; it0 < items; it0 += kCombineThreads) {
+    const int item = it0 + (items < kCombineThreads ? tid % items : tid);
+    const bool here = item < items && set < sets;
+    const int hh = item / kQuads, quad = item % kQuads;
+    float M = -INFINITY, Ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = here ? set : parts; x0 < parts; x0 += sets * kBatch) {
+      float2 ml[kBatch];
+      float4 ov[kBatch];
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int x = imin(x0 + t * kSets, parts - 1);
-      const size_t at = static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * G + hh;
-      ml[t] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
-      ov[t] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * quad));
-    }
-    float Mn = M;
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, ml[t].x);
-    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-    M = Mn;
-    Ls *= f;
-    a.x *= f, a.y *= f, a.z *= f, a.w *= f;
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t)
-      if (x0 + t * kSets < parts) {
-        const float wt = exp2f(ml[t].x - M);
-        Ls += ml[t].y * wt;
-        a.x += ov[t].x * wt, a.y += ov[t].y * wt, a.z += ov[t].z * wt, a.w += ov[t].w * wt;
+      for (int t = 0; t < kBatch; ++t) {
+        const int x = imin(x0 + t * sets, parts - 1);
+        const size_t at = static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * G + hg + hh;
+        ml[t] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
+        ov[t] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * quad));
       }
-  }
-  so[set][quad] = a;
-  if (quad == 0) sm[set] = M, sl[set] = Ls;
-  __syncthreads();
-  if (set) return;
+      float Mn = M;
 #pragma unroll
-  for (int i = 1; i < kSets; ++i) M = fmaxf(M, sm[i]);
-  Ls = 0.f;
-  a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, ml[t].x);
+      const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+      M = Mn;
+      Ls *= f;
+      a.x *= f, a.y *= f, a.z *= f, a.w *= f;
 #pragma unroll
-  for (int i = 0; i < kSets; ++i)
-    if (sm[i] != -INFINITY) {
-      const float f = exp2f(sm[i] - M);
-      const float4 x = so[i][quad];
-      Ls += sl[i] * f;
-      a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+      for (int t = 0; t < kBatch; ++t)
+        if (x0 + t * sets < parts) {
+          const float wt = exp2f(ml[t].x - M);
+          Ls += ml[t].y * wt;
+          a.x += ov[t].x * wt, a.y += ov[t].y * wt, a.z += ov[t].z * wt, a.w += ov[t].w * wt;
+        }
     }
-  const float inv = p.v_scale / Ls;
-  *reinterpret_cast<uint2*>(p.o + orow * D + 4 * quad) =
-      make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-  if (quad == 0) p.lse[orow] = (M + log2f(Ls)) * 0.69314718055994530942f;
+    if (sets > 1) {
+      so[tid] = a;
+      sml[tid] = make_float2(M, Ls);
+      __syncthreads();
+      if (set == 0) {
+        for (int i = 1; i < sets; ++i) M = fmaxf(M, sml[tid + i * items].x);
+        Ls = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < sets; ++i) {
+          const float2 ml = sml[tid + i * items];
+          if (ml.x == -INFINITY) continue;  // more sets than parts
+          const float f = exp2f(ml.x - M);
+          const float4 x = so[tid + i * items];
+          Ls += ml.y * f;
+          a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+        }
+      }
+    }
+    if (here && set == 0) {
+      const float inv = p.v_scale / Ls;
+      const size_t orow = head0 + hh;
+      *reinterpret_cast<uint2*>(p.o + orow * D + 4 * quad) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      if (quad == 0) p.lse[orow] = (M + log2f(Ls)) * 0.69314718055994530942f;
+    }
+  }
 }
 
 }  // namespace ta
