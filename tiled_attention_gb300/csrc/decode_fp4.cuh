@@ -74,10 +74,11 @@ struct DecodeFp4Cfg {
   static constexpr int kStage = 64 * 128 / D;  // tokens per ring stage
   static constexpr int kWarps = 4;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kCtas = 3;  // per SM
+  static constexpr int kCtas = D == 128 && NT == 2 ? 2 : 3;  // per SM
   static constexpr int kCode = D / 2, kScale = D / 16;
-  // A stage in shared memory: K codes, K scales, V codes, V scales.
-  static constexpr int kOffKs = kStage * kCode, kOffV = kOffKs + kStage * kScale;
+  // A stage in shared memory: K, then V, each as blocks of min(page, stage) tokens laid out like
+  // the pool's: codes, then scales.
+  static constexpr int kOffV = kStage * (kCode + kScale);
   static constexpr int kStageBytes = 2 * kOffV;      // 9216
   static constexpr int kStages = 2;                  // of one warp's ring
   static constexpr int kRingBytes = kStages * kStageBytes;
@@ -144,15 +145,25 @@ __device__ __forceinline__ uint32_t hmul2_dup(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 
-// One slice: S^T, the softmax step and O^T of 32 tokens, of which the first `left` belong to
-// the context. EDGE: some do not; the others run without a mask.
+// Slice h of stage `sl` (blocks of `run` tokens): S^T, the softmax step and O^T of 32 tokens, of
+// which the first `left` belong to the context. EDGE: some do not; the others run without a
+// mask.
 template <int D, int NT, bool EDGE>
-__device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, int r, int q,
+__device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int left, int r, int q,
                                           const uint32_t (&qb)[NT][D / 16][2],
                                           const float (&sc)[NT][2], float (&o)[NT][D / 16][4],
                                           float (&mref)[NT][2], float (&l)[NT][2]) {
   using C = DecodeFp4Cfg<D, NT>;
   constexpr int kWords = D / 64;  // 32-bit words of V codes per lane and token; K: 2 kWords
+  // Codes and scales of the two 16-token tiles (K; V lies kOffV further): tile token tb is token
+  // tb - first of the block that starts with token `first`.
+  const uint8_t *codes[2], *scales[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int tb = 32 * h + 16 * u, first = tb & -run;
+    codes[u] = sl + tb * C::kCode + first * C::kScale;
+    scales[u] = sl + tb * C::kScale + (first + run) * C::kCode;
+  }
   // ---- S^T = K Q^T, tiles of 16 tokens
   float s[2][NT][4];
 #pragma unroll
@@ -160,16 +171,16 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, in
     uint32_t w[2][2 * kWords], sf[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int row = 16 * u + r + 8 * x;
+      const int row = r + 8 * x;
       if constexpr (D == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sl + (32 * h + row) * C::kCode + 16 * q);
+        const uint4 v = *reinterpret_cast<const uint4*>(codes[u] + row * C::kCode + 16 * q);
         w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
         sf[x] = e4m3x2_to_f16(
-            *reinterpret_cast<const uint16_t*>(sl + C::kOffKs + (32 * h + row) * C::kScale + 2 * q));
+            *reinterpret_cast<const uint16_t*>(scales[u] + row * C::kScale + 2 * q));
       } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(sl + (32 * h + row) * C::kCode + 8 * q);
+        const uint2 v = *reinterpret_cast<const uint2*>(codes[u] + row * C::kCode + 8 * q);
         w[x][0] = v.x, w[x][1] = v.y;
-        sf[x] = e4m3x2_to_f16(sl[C::kOffKs + (32 * h + row) * C::kScale + q]);
+        sf[x] = e4m3x2_to_f16(scales[u][row * C::kScale + q]);
       }
     }
 #pragma unroll
@@ -264,24 +275,24 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int left, in
     uint32_t w[4][kWords], sv[2];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int tok = 16 * u + 2 * q + (x & 1) + 8 * (x >> 1);
+      const int tok = 2 * q + (x & 1) + 8 * (x >> 1);
       if constexpr (D == 128) {
-        const uint2 v = *reinterpret_cast<const uint2*>(sl + C::kOffV + (32 * h + tok) * C::kCode + 8 * r);
+        const uint2 v = *reinterpret_cast<const uint2*>(codes[u] + C::kOffV + tok * C::kCode + 8 * r);
         w[x][0] = v.x, w[x][1] = v.y;
       } else {
-        w[x][0] = *reinterpret_cast<const uint32_t*>(sl + C::kOffV + (32 * h + tok) * C::kCode + 4 * r);
+        w[x][0] = *reinterpret_cast<const uint32_t*>(codes[u] + C::kOffV + tok * C::kCode + 4 * r);
       }
     }
     constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int tok = 16 * u + 2 * q + 8 * x;
-      const uint8_t* at = sl + C::kOffV + C::kOffKs + (32 * h + tok) * C::kScale + r / kPer;
+      const int tok = 2 * q + 8 * x;
+      const uint8_t* at = scales[u] + C::kOffV + tok * C::kScale + r / kPer;
       uint32_t two = __byte_perm(at[0], at[C::kScale], 0x5540);
       if (EDGE) {
         // Slots past the context may hold anything; a NaN scale would survive p = 0.
-        if (tok >= left) two &= 0xFF00u;
-        if (tok + 1 >= left) two &= 0x00FFu;
+        if (16 * u + tok >= left) two &= 0xFF00u;
+        if (16 * u + tok + 1 >= left) two &= 0x00FFu;
       }
       sv[x] = e4m3x2_to_f16(two);
     }
@@ -417,22 +428,25 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
-  // Copies of one stage: lane 4 sub + part brings K codes, K scales, V codes or V scales (part
-  // 0..3) of the stage's tokens in its page `sub` (up to eight pages of 16 tokens), and arrives
-  // on the stage's barrier with the bytes it asked for. A warp's stages all
-  // lie at the same place of their pages. Pages past the context are not copied. A page whose
-  // entry lies outside the pool is never addressed: the status word reports it and it reads as
-  // zeros. A stage's table entries are read one stage ahead of its copies.
+  // Copies of one stage: lane 4 sub + part brings K (part 0) or V (part 2) of the stage's tokens
+  // in its page `sub` (up to eight pages of 16 tokens), a whole (page, head) block in one
+  // copy; where a page is longer than a stage, parts 0 and 2 bring its codes and parts 1 and 3
+  // its scales. Every lane arrives on the stage's barrier with the bytes it asked for. A warp's
+  // stages all lie at the same place of their pages. Pages past the context are not copied. A
+  // page whose entry lies outside the pool is never addressed: the status word reports it and
+  // it reads as zeros. A stage's table entries are read one stage ahead of its copies.
   const int lp = p.page_shift;
   const int sub = lane >> 2, part = lane & 3;
   const int run = imin(C::kStage, 1 << lp);  // tokens of the stage in one page
-  const bool copies = sub * run < C::kStage;
+  const bool whole_pages = (1 << lp) == run;
+  const bool copies = sub * run < C::kStage && !(whole_pages && (part & 1));
   const int tok0 = warp * C::kStage + sub * run;  // this lane's first token in the warp's stage 0
-  const uint32_t bytes = static_cast<uint32_t>(run) * ((part & 1) ? C::kScale : C::kCode);
+  const uint32_t bytes = static_cast<uint32_t>(run) *
+                         (whole_pages ? C::kCode + C::kScale : (part & 1) ? C::kScale : C::kCode);
   // Shared-memory addresses of this lane's copy and of its barrier, for the next stage; the
   // other slot's follow by adding, then subtracting, the distance.
-  uint32_t dst = smem_u32(ring) + ((part & 2) ? C::kOffV : 0) + ((part & 1) ? C::kOffKs : 0) +
-                 sub * bytes;
+  uint32_t dst = smem_u32(ring) + ((part & 2) ? C::kOffV : 0) +
+                 ((part & 1) ? run * C::kCode : 0) + sub * run * (C::kCode + C::kScale);
   uint32_t bar = smem_u32(full);
   int step = 1;
   const int in_page = tok0 & ((1 << lp) - 1);
@@ -563,11 +577,11 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
       if (left >= C::kStage) {
 #pragma unroll 1
         for (int h = 0; h < C::kStage / C::kTok; ++h)
-          fp4_slice<D, NT, false>(sl, h, C::kTok, r, q, qb, sc, o, mref, l);
+          fp4_slice<D, NT, false>(sl, h, run, C::kTok, r, q, qb, sc, o, mref, l);
       } else {
 #pragma unroll 1
         for (int h = 0; h * C::kTok < left; ++h)
-          fp4_slice<D, NT, true>(sl, h, left - h * C::kTok, r, q, qb, sc, o, mref, l);
+          fp4_slice<D, NT, true>(sl, h, run, left - h * C::kTok, r, q, qb, sc, o, mref, l);
       }
       if (++st_out == S) st_out = 0, parity ^= 1;
       __syncwarp();
