@@ -263,13 +263,13 @@ size_t attn_noalloc_scratch_bytes(void);
  *           where q, k and v share one buffer. q or k may be NULL (not both): it is left out.
  * q_out, k_out bf16 [total / N, H, N, d]: token t is row t % N of block t / N. N = 1 gives
  *           decode's [B, H, 1, d]; N = total the packed [1, H, total, d]; a prompt length N
- *           the dense [B, H, N, d]. Must not overlap q or k.
+ *           the dense [B, H, N, d]. Must not overlap q or k (ATTN_ERR_INVALID).
  * total     tokens, a multiple of N. Hq, Hkv: any counts; d 64 or 128.
  * q_weight, k_weight fp32 [d], each may be NULL. eps >= 0 (read if a weight is given).
  * cos_sin   fp32 [max_pos, rot_dim]: of every position rot_dim/2 cosines, then rot_dim/2 sines.
  * rot_dim   0 or a multiple of 16 up to d.
- * positions int32 [total]; NULL: t % N. A position outside [0, max_pos) sets ATTN_ERR_BOUNDS
- *           and its token's rows are not written.
+ * positions int32 [total]; NULL: t % N (then N <= max_pos). A position outside [0, max_pos)
+ *           sets ATTN_ERR_BOUNDS and its token's rows are not written.
  * Every tensor is 16-byte aligned (positions 4). No workspace; asynchronous on `stream`.
  */
 int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int total, int N,
@@ -292,7 +292,7 @@ int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int t
  * q, k, v   bf16 token rows with strides q_stride, k_stride, v_stride, as for attn_norm_rope. q
  *           may be NULL (then q_out, Hq and q_weight are not used).
  * q_out     bf16 [total_q / N, Hq, N, d]: N = 1 for decode's [B, Hq, 1, d], N = total_q for
- *           chunked prefill's [1, Hq, total_q, d].
+ *           chunked prefill's [1, Hq, total_q, d]. Must not overlap q, k or v.
  * k_pool, v_pool bf16 [num_pages, Hkv, page_size, d].
  * cu_seqlens_q int32 [B+1]: cu[0] = 0, nondecreasing, cu[B] <= total_q. Rows from cu[B] on belong
  *           to no sequence and nothing is written for them (a padded batch of a captured graph).

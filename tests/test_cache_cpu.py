@@ -31,11 +31,12 @@ class _Ptr:
 
 
 T = _Ptr()
+OUT, OUT2 = _Ptr(1 << 24), _Ptr(1 << 25)  # outputs apart from the inputs
 ODD = _Ptr((1 << 20) | 8)
 
 
 def _norm_rope(**kw):
-    a = dict(q=T, k=T, q_out=T, k_out=T, total=8, N=4, Hq=4, Hkv=2, d=128, q_stride=512,
+    a = dict(q=T, k=T, q_out=OUT, k_out=OUT2, total=8, N=4, Hq=4, Hkv=2, d=128, q_stride=512,
              k_stride=256, q_weight=None, k_weight=None, eps=1e-6, cos_sin=T, max_pos=16,
              rot_dim=128, interleaved=False, positions=None, stream=0)
     a.update(kw)
@@ -62,6 +63,8 @@ ROW_REFUSALS = [
     (dict(k_weight=T, eps=float("nan")), INVALID),
     (dict(q_weight=T, eps=-1.0), INVALID),
     (dict(N=0), INVALID),
+    (dict(q_out=T), INVALID),  # in place
+    (dict(q_out=_Ptr((1 << 20) + 7 * 1024)), INVALID),  # into the last row
 ]
 
 
@@ -73,6 +76,8 @@ ROW_REFUSALS = [
     (dict(q=None, k=None), INVALID),
     (dict(Hq=-1), INVALID),
     (dict(Hq=0, Hkv=0), INVALID),
+    (dict(k_out=_Ptr((1 << 20) + 256)), INVALID),
+    (dict(max_pos=3), INVALID),  # rows of 4 positions, a table of 3
 ])
 def test_norm_rope_refusals(kw, code):
     assert _norm_rope(**kw) == code
@@ -85,7 +90,7 @@ def test_norm_rope_without_tokens_is_a_no_op():
 
 
 def _append(fp4, **kw):
-    a = dict(q=T, k=T, v=T, q_out=T, k_pool=T, v_pool=T, B=2, Hq=4, Hkv=2, total_q=8, N=8, d=128,
+    a = dict(q=T, k=T, v=T, q_out=OUT, k_pool=T, v_pool=T, B=2, Hq=4, Hkv=2, total_q=8, N=8, d=128,
              q_stride=512, k_stride=256, v_stride=256, q_weight=None, k_weight=None, eps=1e-6,
              cos_sin=T, max_pos=64, rot_dim=128, interleaved=False, cu_seqlens_q=T, seqlens_k=T,
              block_table=T, max_pages=4, page_size=16, num_pages=8, stream=0)

@@ -368,9 +368,21 @@ def test_append_device_checks(fp4, fault):
             continue
         sl = slice(bt.cu[b], bt.cu[b + 1])
         assert np.array_equal(vgot[bt.phys[sl], :, bt.slot[sl]], vwant[sl])
-    if hurt == [1]:
-        sl = slice(bt.cu[1], bt.cu[2])
-        assert not vgot[bt.phys[sl], :, bt.slot[sl]].any()
+    if fault in ("long", "short", "page", "negative page", "position"):
+        sl = slice(bt.cu[hurt[0]], bt.cu[hurt[0] + 1])
+        wrong = vgot[bt.phys[sl], :, bt.slot[sl]]
+        if fault == "position":  # the other tokens of that sequence are fine
+            assert not wrong[-1].any() and np.array_equal(wrong[:-1], vwant[sl][:-1])
+        elif "page" in fault:  # one of its two tokens sits on the good page 1 or both do
+            on = bt.pos[sl] // 16 == 1
+            assert not wrong[on].any() and np.array_equal(wrong[~on], vwant[sl][~on])
+        else:
+            assert not wrong.any()
+    elif fault in ("start", "past"):  # nothing of the sequence anywhere: zeros but the others'
+        keep = np.concatenate([np.arange(bt.cu[b], bt.cu[b + 1]) for b in range(3)
+                               if b not in hurt])
+        vgot[bt.phys[keep], :, bt.slot[keep]] = 0
+        assert not vgot.any()
 
 
 # ------------------------------------------------------------------ append in 4 bits

@@ -10,6 +10,17 @@
 namespace ta {
 namespace {
 
+// Bytes from the first to the last element of token rows.
+size_t rows_bytes(int total, int heads, int d, int64_t stride) {
+  return total > 0 ? (static_cast<size_t>(total - 1) * stride + static_cast<size_t>(heads) * d) * 2
+                   : 0;
+}
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an && bn && x < y + bn && y < x + an;
+}
+
 // Checks and fields common to the row entry points. Sizes of absent tensors (null q or k) are
 // passed as 0 heads.
 int row_params(RowParams* p, const void* q, const void* k, const void* v, void* q_out, int Hq,
@@ -41,6 +52,11 @@ int row_params(RowParams* p, const void* q, const void* k, const void* v, void* 
     return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
   if (rot_dim > 0 && total > 0 && !cos_sin) return fail(ATTN_ERR_INVALID, "cos_sin is required");
   if (q && total > 0 && !q_out) return fail(ATTN_ERR_INVALID, "null pointer");
+  // q_out must not touch the rows that other warps may still read.
+  const size_t out_bytes = static_cast<size_t>(total) * Hq * d * 2;
+  for (const auto& i : in)
+    if (q && total > 0 && overlap(q_out, out_bytes, i.x, rows_bytes(total, i.heads, d, i.stride)))
+      return fail(ATTN_ERR_INVALID, "an output overlaps an input");
   p->in[0] = static_cast<const uint8_t*>(q);
   p->in[1] = static_cast<const uint8_t*>(k);
   p->in[2] = static_cast<const uint8_t*>(v);
@@ -144,6 +160,14 @@ int attn_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int t
   if ((!q && !k) || (k && !k_out)) return fail(ATTN_ERR_INVALID, "null pointer");
   if (p.heads[0] + p.heads[1] == 0) return fail(ATTN_ERR_INVALID, "no heads");
   if (!aligned16(k_out)) return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
+  if (!positions && rot_dim > 0 && N > max_pos)
+    return fail(ATTN_ERR_INVALID, "positions of %d rows, a table of %d", N, max_pos);
+  if (k) {
+    const size_t n = static_cast<size_t>(total) * Hkv * d * 2;
+    if (overlap(k_out, n, q, rows_bytes(total, Hq, d, q_stride)) ||
+        overlap(k_out, n, k, rows_bytes(total, Hkv, d, k_stride)))
+      return fail(ATTN_ERR_INVALID, "an output overlaps an input");
+  }
   p.out[1] = static_cast<uint8_t*>(k_out);
   p.positions = positions;
   return launch_rows<kCacheNone>(p, d, stream);

@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
       start = __ldg(p.cu + b);
       n = __ldg(p.cu + b + 1) - start;
       len = __ldg(p.lens + b);
-      ok = start >= 0 && len >= n && len <= (static_cast<long long>(p.max_pages) << p.page_shift);
+      ok = start >= 0 && n <= p.total - start && len >= n &&
+           len <= (static_cast<long long>(p.max_pages) << p.page_shift);
     }
     if (!ok) {
       if (lane == 0) report_status(p.status, -7);
