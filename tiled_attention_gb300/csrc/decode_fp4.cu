@@ -102,8 +102,8 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   if (num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 65535 || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
-  if (B > 65535 ||
-      static_cast<long long>(B) * Hkv >= (1ll << 31) / ((static_cast<long long>(N) + 127) / 128))
+  const long long units = (static_cast<long long>(N) + 127) / 128 + 8;  // of one context, at most
+  if (B > 65535 || static_cast<long long>(B) * Hkv >= (1ll << 31) / units)
     return fail(ATTN_ERR_UNSUPPORTED, "decode batch too large");
   const Fp4Layout L = fp4_layout(Hq, Hkv, d);
   if (!workspace || workspace_bytes < L.total || !aligned16(workspace))

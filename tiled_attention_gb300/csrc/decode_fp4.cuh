@@ -24,9 +24,10 @@
 //     max by less than 8; f16 keeps 11 bits of it where bf16 would keep 8.
 //
 // Work: the contexts are cut into 128-token blocks, numbered over sequence, kv head and
-// position, and CTA i of nn takes blocks [i U / nn, (i + 1) U / nn): every CTA streams the same
-// number of bytes whatever the lengths are, and finds its range from cu_seqlens alone. A range
-// is one or more segments, each of one (sequence, kv head). A segment that is the whole
+// position, with a few units more at each context's start for the cost of beginning it, and
+// shared out evenly over the CTAs in that order: every CTA has the same work whatever the
+// lengths are, and finds its range from cu_seqlens alone. A range is one or more segments, each of one
+// (sequence, kv head). A segment that is the whole
 // context writes O and LSE itself; the others (a CTA's first and last at most) leave the
 // unnormalised O, the reference max and the sum in the workspace, two slots a CTA, and a
 // second kernel joins them in CTA order, so results do not depend on timing:
@@ -68,6 +69,16 @@ struct DecodeFp4Params {
   unsigned long long timeout_ns;
 };
 
+// Units of work that beginning a context costs a CTA, in 128-token blocks. Measured: a CTA that
+// begins one context more ends about 2.5 us later, and a block takes it 1.35 us (d = 128) or
+// 0.9 us. With 0, 1, 2, 3 and 4 units 32 sequences of 1K-16K take 68.3, 65.7, 63.7, 63.2 and
+// 63.8 us; with 0, 2, 3, 4 and 6 units 48 sequences of up to 32K at d = 64 take 81, 75.0, 74.5,
+// 73.6 and 74.6 us.
+template <int D>
+struct DecodeFp4Start {
+  static constexpr int kUnits = D == 128 ? 3 : 4;
+};
+
 template <int D, int NT>  // NT: 8-head column tiles (1 or 2)
 struct DecodeFp4Cfg {
   static constexpr int kTok = 32;     // tokens per slice: two 16-row tiles
@@ -86,15 +97,14 @@ struct DecodeFp4Cfg {
   static constexpr int kSteps = D / 16;              // k-steps of S^T, m-tiles of O^T
   static constexpr int kMiscBytes = 256 + 2 * kWarps * 16 * 4;
   static constexpr int kSmemBytes = kWarps * kRingBytes + kMiscBytes + 128;
-  static_assert(kWarps * kHeads * D * 4 <= kWarps * kRingBytes, "the O rows reuse the rings");
+  static_assert(kHeads * D * 4 <= kStageBytes, "a warp's O rows reuse one slot");
   static_assert(kWarps * kStages <= 8, "barriers");
 };
 
 struct DecodeFp4Ctrl {
   uint64_t full[8];  // [warps][stages]
   int abort_flag;
-  int seq, seq_before;
-  int warp_sum[4];
+  int idle[4];       // ring slot each warp's rows are merged in
 };
 
 // D(16x8, fp32) += A(16x16, f16, row-major) * B(16x8, f16, column-major).
@@ -332,51 +342,74 @@ __device__ __forceinline__ int fp4_length(const DecodeFp4Params& p, int b, bool 
 
 __device__ __forceinline__ int fp4_blocks(int L) { return (L + kFp4Block128 - 1) / kFp4Block128; }
 
-// The work list as every CTA (of T threads) sees it: thread t sums the blocks of sequences
-// [t c, (t + 1) c), a scan over the threads gives `before` (blocks of the sequences before its
-// own) and `total`. The host has checked that all blocks of all heads fit an int.
-struct Fp4Plan {
-  int first, count, before, mine, total;
-};
-template <int T>
-__device__ __forceinline__ Fp4Plan fp4_plan(const DecodeFp4Params& p, int* warp_sum, bool report) {
-  Fp4Plan w;
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
-  const int c = (p.B + T - 1) / T;
-  w.first = imin(tid * c, p.B);
-  w.count = imin(c, p.B - w.first);
-  int sum = 0;
-  for (int i = 0; i < w.count; ++i) sum += fp4_blocks(fp4_length(p, w.first + i, report));
-  w.mine = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, sum, off);
-    if (lane >= off) sum += x;
-  }
-  if (lane == 31) warp_sum[tid >> 5] = sum;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < T / 32; ++i) {
-    if (i < (tid >> 5)) before += warp_sum[i];
-    total += warp_sum[i];
-  }
-  w.before = before + sum - w.mine;
-  w.total = total;
-  return w;
+// Units of work of a context of nb blocks: its blocks, after kStart units for what a CTA spends
+// on beginning it (its query, its first copies, its merge). A range of units that ends among
+// the kStart ones holds none of the context.
+template <int D>
+__device__ __forceinline__ int fp4_units(int nb) {
+  constexpr int kStart = DecodeFp4Start<D>::kUnits;
+  return nb > 0 ? nb + kStart : 0;
 }
 
-// CTAs that share U blocks: all, unless that leaves them fewer than min_blocks each.
-__device__ __forceinline__ int fp4_ctas(const DecodeFp4Params& p, int U) {
-  return imax(1, imin(p.slots, U / p.min_blocks));
+// Units of all sequences (of one kv head), and of those before sequence `upto`: the whole warp
+// sums them. The host has checked that the units of all heads fit an int.
+template <int D>
+__device__ __forceinline__ void fp4_total(const DecodeFp4Params& p, int upto, bool report,
+                                          int& total, int& before) {
+  int all = 0, ahead = 0;
+  for (int b = static_cast<int>(threadIdx.x) & 31; b < p.B; b += 32) {
+    const int w = fp4_units<D>(fp4_blocks(fp4_length(p, b, report)));
+    all += w;
+    if (b < upto) ahead += w;
+  }
+  total = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, ahead);
 }
-__device__ __forceinline__ int fp4_start(int i, int U, int nn) {
-  return static_cast<int>(static_cast<long long>(i) * U / nn);
+
+// The sequence whose heads hold unit u, and the units before it (of one kv head).
+template <int D>
+__device__ __forceinline__ void fp4_find(const DecodeFp4Params& p, int u, int& seq, int& before) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  int run = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int w = b < p.B ? fp4_units<D>(fp4_blocks(fp4_length(p, b, false))) : 0;
+    int sum = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += x;
+    }
+    sum += run;
+    const unsigned past = __ballot_sync(0xffffffffu, u < sum * p.Hkv);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      seq = b0 + l;
+      before = __shfl_sync(0xffffffffu, sum - w, l);
+      return;
+    }
+    run = __shfl_sync(0xffffffffu, sum, 31);
+  }
+  seq = p.B - 1;  // not reached: u lies below the total
+  before = run;
 }
-// The CTA that takes block u.
-__device__ __forceinline__ int fp4_cta_of(int u, int U, int nn) {
-  return static_cast<int>(((static_cast<long long>(u) + 1) * nn - 1) / U);
-}
+
+// How U units are shared out: over n CTAs (all, unless that leaves them fewer than min_blocks
+// each), q or q + 1 each, the first r CTAs the larger share.
+struct Fp4Share {
+  int n, q, r;
+  __device__ __forceinline__ Fp4Share(const DecodeFp4Params& p, int U) {
+    n = imax(1, imin(p.slots, U / p.min_blocks));
+    q = U / n;
+    r = U - q * n;
+  }
+  // First unit of CTA i, and the CTA that takes unit u.
+  __device__ __forceinline__ int start(int i) const { return i * q + imin(i, r); }
+  __device__ __forceinline__ int cta_of(int u) const {
+    const int large = r * (q + 1);
+    return u < large ? u / (q + 1) : r + (u - large) / q;
+  }
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
@@ -405,26 +438,19 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     if (warp == 0) ctl->abort_flag = 0;
     fence_mbar_init();
   }
-  const Fp4Plan plan = fp4_plan<C::kThreads>(p, ctl->warp_sum, blockIdx.x == 0);
-  const int U = plan.total * p.Hkv;
-  const int nn = fp4_ctas(p, U);
+  // Every warp works out the CTA's range by itself.
+  constexpr int kStart = DecodeFp4Start<D>::kUnits;
   const int cta = static_cast<int>(blockIdx.x);
-  if (U == 0 || cta >= nn) return;
-  int u = fp4_start(cta, U, nn);
-  const int end = fp4_start(cta + 1, U, nn);
-  if (plan.before * p.Hkv <= u && u < (plan.before + plan.mine) * p.Hkv) {
-    int x = plan.before, b = plan.first;
-    for (;; ++b) {
-      const int nb = fp4_blocks(fp4_length(p, b, false));
-      if (u < (x + nb) * p.Hkv) break;
-      x += nb;
-    }
-    ctl->seq = b;
-    ctl->seq_before = x;
-  }
-  __syncthreads();
-  int b = ctl->seq;
-  int seq_u = ctl->seq_before * p.Hkv;  // first block of sequence b
+  int total, b, seq_u;
+  fp4_total<D>(p, 0, cta == 0 && warp == 0, total, seq_u);
+  const int U = total * p.Hkv;
+  const Fp4Share share(p, U);
+  if (U == 0 || cta >= share.n) return;
+  int u = share.start(cta);
+  const int end = share.start(cta + 1);
+  fp4_find<D>(p, u, b, seq_u);
+  seq_u *= p.Hkv;  // first unit of sequence b
+  __syncthreads();  // barriers and flag
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
@@ -461,59 +487,75 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   uint32_t parity = 0;         // of slot st_out
   bool aborted = false;
 
-  for (bool first = true; u < end; first = false) {
-    int L = fp4_length(p, b, false), nb = fp4_blocks(L);
-    while (u >= seq_u + nb * p.Hkv) {  // the sequence is done: on to the next that has blocks
-      seq_u += nb * p.Hkv;
+  // The segment that starts at block u, and its first stage on the way.
+  int g, n, t0, t1, next;
+  bool whole;
+  const int* row;
+  const uint8_t* src_g;
+  // Table entry of this lane's page of stage i: -2 nothing to copy, -1 outside the pool.
+  auto entry = [&](int i) {
+    const int tok = t0 + tok0 + i * (C::kWarps * C::kStage);
+    if (!copies || i >= n || tok >= t1) return -2;
+    const int e = __ldg(row + (tok >> lp));
+    return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
+  };
+  auto issue = [&](int phys) {
+    if (phys >= 0) {
+      asm volatile(
+          "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+          "[%3];" ::"r"(dst),
+          "l"(src_g + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * page_bytes),
+          "r"(bytes), "r"(bar)
+          : "memory");
+    } else {
+      if (phys == -1) {
+        report_status(p.status, -5);
+        for (uint32_t x = 0; x < bytes; x += 16) st_shared_v4(dst + x, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    }
+    dst += step * C::kStageBytes;
+    bar += step * 8;
+    step = -step;
+  };
+  auto open = [&]() {  // false: the range holds no more blocks
+    if (u >= end) return false;
+    int L = fp4_length(p, b, false), nb = fp4_blocks(L), w = fp4_units<D>(nb);
+    while (u >= seq_u + w * p.Hkv) {  // the sequence is done: on to the next that has blocks
+      seq_u += w * p.Hkv;
       L = fp4_length(p, ++b, false);
       nb = fp4_blocks(L);
+      w = fp4_units<D>(nb);
     }
-    const int g = (u - seq_u) / nb;
-    const int blk0 = (u - seq_u) % nb;
+    g = (u - seq_u) / w;
+    int pos = u - seq_u - g * w;
+    if (pos < kStart) {
+      u += kStart - pos;
+      pos = kStart;
+      if (u >= end) return false;
+    }
+    const int blk0 = pos - kStart;
     const int nblk = imin(nb - blk0, end - u);
-    const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
+    whole = nblk == nb;
+    u += nblk;
     // Stages of the segment's tokens [t0, t1): this warp takes stage warp, warp + 4, ...
-    const int t0 = blk0 * kFp4Block128;
-    const int t1 = imin(t0 + nblk * kFp4Block128, L);
-    const int n = aborted ? 0 : (t1 - t0 + (C::kWarps - 1 - warp) * C::kStage + C::kStage - 1) /
-                                    (C::kWarps * C::kStage);
-
-    const int* const row = p.table + static_cast<size_t>(b) * p.max_pages;
-    const uint8_t* const src_g = src0 + static_cast<size_t>(g) * blk_bytes;
-    // Table entry of this lane's page of stage i: -2 nothing to copy, -1 outside the pool.
-    const int last = copies ? t1 - t0 - tok0 : 0;  // tokens from this lane's first on
-    const int first_page = (t0 + tok0) >> lp;      // a warp's stages are whole pages apart
-    auto entry = [&](int i) {
-      const int tok = i * (C::kWarps * C::kStage);
-      if (i >= n || tok >= last) return -2;
-      const int e = __ldg(row + first_page + (tok >> lp));
-      return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
-    };
-    auto issue = [&](int phys) {
-      if (phys >= 0) {
-        asm volatile(
-            "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-            "[%3];" ::"r"(dst),
-            "l"(src_g + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * page_bytes),
-            "r"(bytes), "r"(bar)
-            : "memory");
-      } else {
-        if (phys == -1) {
-          report_status(p.status, -5);
-          for (uint32_t x = 0; x < bytes; x += 16) st_shared_v4(dst + x, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-      }
-      dst += step * C::kStageBytes;
-      bar += step * 8;
-      step = -step;
-    };
-    int issued = 0;
-    for (; issued < S - 1 && issued < n; ++issued) issue(entry(issued));
-    int next = entry(issued);
-
+    t0 = blk0 * kFp4Block128;
+    t1 = imin(t0 + nblk * kFp4Block128, L);
+    n = aborted ? 0 : (t1 - t0 + (C::kWarps - 1 - warp) * C::kStage + C::kStage - 1) /
+                          (C::kWarps * C::kStage);
+    row = p.table + static_cast<size_t>(b) * p.max_pages;
+    src_g = src0 + static_cast<size_t>(g) * blk_bytes;
+    if (n > 0) {
+      issue(entry(0));
+      next = entry(1);
+    }
+    return true;
+  };
+  bool more = open();
+  for (bool first = true; more; first = false) {
+    const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
     // Q as the B operand: column (head) r, k-step kk = channels D/4 q + 4 kk + {0, 1 | 2, 3}.
     uint32_t qb[NT][C::kSteps][2];
     float sc[NT][2];  // scale of heads 8 nt + 2 q, + 1
@@ -565,9 +607,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 
     int left = t1 - t0 - warp * C::kStage;  // tokens from the stage's first on
     for (int i = 0; i < n; ++i, left -= C::kWarps * C::kStage) {
-      if (issued < n) {  // into the slot of stage i - 1, which the whole warp has left
+      if (i + 1 < n) {  // into the slot of stage i - 1, which the whole warp has left
         issue(next);
-        next = entry(++issued);
+        next = entry(i + 2);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&full[st_out], parity, wc))) {
         aborted = true;
@@ -586,11 +628,17 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
       if (++st_out == S) st_out = 0, parity ^= 1;
       __syncwarp();
     }
-    // After a timeout, let copies still in flight land (with a limit) before the rings are used
-    // again.
+    // After a timeout, let the copies still in flight land (with a limit) before the slots are
+    // used again; there are no more after that.
     if (aborted)
-      for (int s = 0; s < S - 1; ++s)
-        mbar_wait(&full[(st_out + s) % S], parity ^ (st_out + s >= S ? 1 : 0), wc_drain);
+      for (int x = 0; x < S; ++x)
+        mbar_wait(&full[(st_out + x) % S], parity ^ (st_out + x >= S ? 1 : 0), wc_drain);
+    // The next segment's first stage goes into slot st_out, while this one's rows are merged in
+    // the other slot: the copy's latency hides behind the merge.
+    const bool was_whole = whole;
+    float* const mine =
+        reinterpret_cast<float*>(ring + (st_out ^ 1) * C::kStageBytes);
+    more = open();
 
     // ---------------------------------------------------------------- merge the four warps
 #pragma unroll
@@ -600,10 +648,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
-    __syncthreads();  // every warp is past its last ring read
-    // [warp][head][D] fp32 in the idle rings. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
+    // [head][D] fp32 in each warp's idle slot. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
     // m-tile i holds channels 2i and 2i + 1 of them.
-    float* buf = reinterpret_cast<float*>(base);
+    if (lane == 0) ctl->idle[warp] = st_out ^ 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -614,7 +661,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
           red_l[warp * 16 + h] = l[nt][c];
         }
         if (h < G) {
-          float* to = buf + (warp * C::kHeads + h) * D + r * (D / 8);
+          float* to = mine + h * D + r * (D / 8);
 #pragma unroll
           for (int i = 0; i < C::kSteps; i += 2)
             *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
@@ -622,7 +669,6 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
         }
       }
     __syncthreads();
-    const bool whole = nblk == nb;
     const size_t slot = 2 * static_cast<size_t>(cta) + (first ? 0 : 1);
     constexpr int kQuads = D / 4;  // four-column groups of one head's row
     for (int idx = tid; idx < G * kQuads; idx += C::kThreads) {
@@ -637,12 +683,13 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
         const float mw = red_m[w * 16 + hh];
         if (mw != -INFINITY) {
           const float f = fast_exp2(mw - M);
-          const float4 x = *reinterpret_cast<const float4*>(buf + (w * C::kHeads + hh) * D + d0);
+          const float4 x = *reinterpret_cast<const float4*>(
+              base + w * C::kRingBytes + ctl->idle[w] * C::kStageBytes + (hh * D + d0) * 4);
           Ls += red_l[w * 16 + hh] * f;
           a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
         }
       }
-      if (whole) {
+      if (was_whole) {
         const size_t orow = head0 + hh;
         const float inv = Ls > 0.f ? p.v_scale / Ls : 0.f;
         *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
@@ -655,36 +702,28 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
           *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * G + hh)) = make_float2(M, Ls);
       }
     }
-    u += nblk;
     fence_proxy_async_smem();  // the merge's plain writes, before the next segment's copies
     __syncthreads();
   }
 }
 
 // Joins the parts of contexts that several CTAs share, and writes the rows of empty ones. One
-// CTA per (kv head, sequence), or per query head; a thread takes four columns of one head, and where that leaves
-// threads over, set s of them takes the parts s, s + sets, ...; the sets' sums are added in
-// order.
+// CTA per (kv head, sequence), or per query head; a thread takes four columns of one head, and
+// where that leaves threads over, set s of them takes the parts s, s + sets, ...; the sets'
+// sums are added in order.
 constexpr int kCombineThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const DecodeFp4Params p) {
   constexpr int kQuads = D / 4, kBatch = 8;
-  __shared__ int warp_sum[kCombineThreads / 32];
-  __shared__ int seq_before;
   __shared__ float2 sml[kCombineThreads];
   __shared__ float4 so[kCombineThreads];
   const int H = p.join_heads, G = p.group;
   const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
   const int g = h0 / G, hg = h0 % G;  // kv head, first query head of its group
   const int tid = static_cast<int>(threadIdx.x);
-  const Fp4Plan plan = fp4_plan<kCombineThreads>(p, warp_sum, false);
-  if (plan.first <= b && b < plan.first + plan.count) {
-    int x = plan.before;
-    for (int i = plan.first; i < b; ++i) x += fp4_blocks(fp4_length(p, i, false));
-    seq_before = x;
-  }
-  __syncthreads();
+  int total, before;
+  fp4_total<D>(p, b, false, total, before);
   const int nb = fp4_blocks(fp4_length(p, b, false));
   const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
   // Every CTA waits, those without work too: this kernel must not end before the first one.
@@ -695,13 +734,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const Deco
     if (tid < H) p.lse[head0 + tid] = -INFINITY;
     return;
   }
-  const int U = plan.total * p.Hkv, nn = fp4_ctas(p, U);
-  const int u0 = seq_before * p.Hkv + g * nb;
-  const int c0 = fp4_cta_of(u0, U, nn), c1 = fp4_cta_of(u0 + nb - 1, U, nn);
+  constexpr int kStart = DecodeFp4Start<D>::kUnits;
+  const Fp4Share share(p, total * p.Hkv);
+  const int u0 = before * p.Hkv + g * fp4_units<D>(nb);
+  const int c0 = share.cta_of(u0 + kStart), c1 = share.cta_of(u0 + kStart + nb - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // one CTA held the whole context
-  // The first part is its CTA's first segment only if the CTA starts with this context.
-  const int slot0 = 2 * c0 + (fp4_start(c0, U, nn) == u0 ? 0 : 1);
+  // The first part is its CTA's first segment only if the CTA has no block of the context before.
+  const int slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
   const int parts = c1 - c0 + 1;
   const int items = H * kQuads;
   const int sets = imax(1, kCombineThreads / items);
