@@ -2,6 +2,7 @@
 // 8-head column tiles) and its entry points.
 #include "decode_fp4.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/attn.h"
@@ -10,10 +11,6 @@
 
 namespace ta {
 namespace {
-
-// Least 128-token blocks a CTA takes. One 16K-token sequence of 8 kv heads (1024 blocks): 4
-// blocks 12.1 us, 2 blocks 12.2, 1 block 12.4.
-constexpr int kFp4MinBlocks = 4;
 
 // CTAs of the decode kernel: as many as the GPU holds at once.
 int fp4_slots(int d, int group) {
@@ -127,7 +124,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.max_pages = (N + page_size - 1) / page_size;
   p.num_pages = num_pages;
   p.slots = L.slots;
-  p.min_blocks = kFp4MinBlocks;
+  p.fine = static_cast<int>(std::min<long long>(32ll * B * Hkv, L.slots));
   // The joining kernel: a CTA a group once the groups fill the GPU (48 sequences x 4 kv heads of 16
   // query heads: 83 us against 87 with a CTA a head), else a CTA a head, with four threads a
   // column to share the parts (one sequence x 8 kv heads: 12.5 us against 13.7).
