@@ -658,6 +658,26 @@ def test_decode_fp4_splits(d, group):
         assert torch.equal(first[1], w.lse)
 
 
+@pytest.mark.parametrize("B,most,d,Hkv", [(333, 200, 64, 1), (97, 700, 128, 2), (33, 130, 128, 3),
+                                          (32, 128, 64, 1), (700, 3, 128, 1)])
+def test_decode_fp4_many_sequences(B, most, d, Hkv):
+    """More sequences than a warp has lanes, empty ones among them: how the blocks are shared out,
+    contexts of one block, shares that end between a context's start and its first block."""
+    rng = np.random.default_rng(3000 + B)
+    w = Decode(rng, rng.integers(0, most + 1, B), 2 * Hkv, Hkv, d, 16)
+    w.run()
+    assert status() == 0
+    w.check()
+
+
+def test_decode_fp4_all_empty():
+    rng = np.random.default_rng(3100)
+    w = Decode(rng, [0, 0, 0], 4, 2, 128, 16)
+    w.run()
+    assert status() == 0
+    w.check()
+
+
 @pytest.mark.parametrize("q_amp,ks,vs", [(0.0, 1.0, 1.0), (2.0 ** -60, 1.0, 1.0), (2.0 ** 60, 2.0 ** -60, 1.0),
                                          (30.0, 0.25, 3e-20), (1.0, 1e-20, 1e20), (8.0, 0.25, 1.0)])
 def test_decode_fp4_magnitudes(q_amp, ks, vs):
