@@ -358,6 +358,46 @@ def suite(args):
                     torch.equal(lse_na, dp.lse))
             emit(w, ms_na, {"workload": w.name + " (allocation-free entry point)",
                             "bit_identical_to_attn_fwd": bool(same)})
+        if cfg in (5, "5b1", "5b4"):
+            # The same batch on a 4-bit cache: random codes and scales (the arithmetic does not
+            # depend on them), and one new token a sequence appended with its norm and rotation.
+            pages, rng4 = dp.num_pages, torch.Generator(device=dev).manual_seed(1)
+            blk = w.page_size * (w.d // 2 + w.d // 16)
+            pools = [torch.randint(0, 0x78, (pages, w.Hkv, blk), generator=rng4, device=dev,
+                                   dtype=torch.uint8) for _ in range(2)]
+            ws4 = torch.empty(attn.attn_workspace_bytes_fp4(w.B, w.Hq, w.Hkv, w.N, w.d),
+                              dtype=torch.uint8, device=dev)
+            o4, lse4 = torch.empty_like(dp.o), torch.empty_like(dp.lse)
+            width = (w.Hq + 2 * w.Hkv) * w.d
+            qkv = torch.randn((w.B, width), generator=rng4, device=dev).to(torch.bfloat16)
+            q_in, k_in, v_in = qkv.split([w.Hq * w.d, w.Hkv * w.d, w.Hkv * w.d], dim=1)
+            norm_w = torch.ones(w.d, device=dev)
+            cos_sin = torch.rand((w.N, w.d), generator=rng4, device=dev)
+            cu_new = torch.arange(w.B + 1, dtype=torch.int32, device=dev)
+            lens = dp.cu.diff().contiguous()
+
+            def decode4():
+                return attn.attn_fwd_paged_decode_fp4(dp.q, *pools, o4, lse4, w.B, w.Hq, w.Hkv,
+                                                      w.N, w.d, w.scale, 1.0, 1.0, dp.cu, dp.table,
+                                                      w.page_size, pages, ws4, stream)
+
+            def append4():
+                return attn.attn_append_paged_fp4(q_in, k_in, v_in, o4, *pools, 1.0, 1.0, w.B,
+                                                  w.Hq, w.Hkv, w.B, 1, w.d, width, width, width,
+                                                  norm_w, norm_w, 1e-6, cos_sin, w.N, w.d, False,
+                                                  cu_new, lens, dp.table, dp.table.shape[1],
+                                                  w.page_size, pages, stream)
+
+            d4_ms, a4_ms = timed(decode4, args.steps), timed(append4, args.steps)
+            bytes4 = (dec_bytes(w) - w.kv_bytes_valid() +
+                      w.kv_bytes_valid() * (w.d // 2 + w.d // 16) // (2 * w.d))
+            gbs4 = bytes4 / (d4_ms * 1e-3) / 1e9
+            print(json.dumps({
+                "suite": True, "workload": w.name + " (4-bit cache)", "d": w.d, "ms": d4_ms,
+                "launches_timed": args.steps, "value": gbs4, "unit": "GB/s",
+                "frac": gbs4 / peaks["hbm_gbs"], "peak": f"HBM copy {tag}", "bytes": bytes4,
+                "append_ms": a4_ms}), flush=True)
+            del pools, ws4
         if cfg == 5:
             # Two-stage path of the paged-KV pattern: gather K and V pages into dense caches,
             # then the decode kernel reads the caches.

@@ -951,3 +951,27 @@ def test_two_graphs_share_a_workspace_and_a_stream_of_their_own():
     assert attn.attn_get_status(side) == 0
     a.check()
     b.check()
+
+
+def test_two_decodes_at_once():
+    """Two decodes on two streams at the same time, each with its own workspace, and an append into
+    a third pool beside them."""
+    rng = np.random.default_rng(33)
+    a = Decode(rng, list(rng.integers(500, 6000, 20)), 16, 4, 128, 64)
+    b = Decode(rng, list(rng.integers(1, 4000, 9)), 32, 2, 64, 16)
+    bt = Batch(rng, [400, 90], [400, 50], 16)
+    r = Rows(rng, bt.total, 8, 4, 128, 128, max_pos=400, norm=True)
+    _, kp, vp = pools_bf16(rng, bt, 4, 128)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a.run(streams[0])
+        b.run(streams[1])
+        with torch.cuda.stream(streams[2]):
+            append_bf16(r, bt, kp, vp, bt.total)
+    torch.cuda.synchronize()
+    assert attn.attn_get_status() == 0
+    a.check()
+    b.check()
+    want, mag = r.want("k", bt.pos)
+    close(f64(kp)[bt.phys, :, bt.slot], want, mag)
