@@ -26,19 +26,26 @@
 // Work: the contexts are cut into 128-token blocks, numbered over sequence, kv head and
 // position, with a few units more at each context's start for the cost of beginning it, and
 // shared out evenly over the CTAs in that order: every CTA has the same work whatever the
-// lengths are, and finds its range from cu_seqlens alone. A range is one or more segments, each of one
-// (sequence, kv head). A segment that is the whole
-// context writes O and LSE itself; the others (a CTA's first and last at most) leave the
-// unnormalised O, the reference max and the sum in the workspace, two slots a CTA, and a
-// second kernel joins them in CTA order, so results do not depend on timing:
+// lengths are, and finds its range from cu_seqlens alone. A range is one or more segments, each
+// of one (sequence, kv head). A segment that is the whole context writes O and LSE itself; the
+// others (a CTA's first and last at most) leave the unnormalised O, the reference max and the
+// sum in the workspace, two slots a CTA, and a second kernel joins them in CTA order, so
+// results do not depend on timing:
 //   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  O = sum_c O_c 2^(m_c - M) / L,
 //   LSE = (M + log2 L) ln 2.
 // The second kernel starts under programmatic dependent launch: it finds its parts while the
 // first still runs. No counters, so no memset.
 //
-// CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64), through a ring of its
-// own in shared memory: it brings the next stages in with bulk copies while it works on one, so
-// no warp waits for another before a segment's end.
+// CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64),
+// through a ring of its own in shared memory: it brings the next stage in with bulk copies while
+// it works on one, so no warp waits for another before a segment's end.
+//
+// Measured (GB300, device time): 32 sequences of 1K-16K tokens, 8 kv heads of 4 query heads,
+// d = 128, 313 MB: 61 us, 5.1 TB/s, 76 % of the copy rate; 48 sequences of 1-32K, 4 kv heads of
+// 16, d = 64, pages of 16, 216 MB: 73 us; one sequence of 16K: 13 us. Bound by issue: 224
+// instructions of a warp per 16 tokens at d = 128, of which 64 convert and 64 scale at half
+// rate; computing alone takes 55 us on the first, streaming alone 54, ~11 of each start-up
+// and joining.
 #pragma once
 
 #include "fp4.cuh"
@@ -178,18 +185,18 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
   float s[2][NT][4];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    uint32_t w[2][2 * kWords], sf[2];
+    uint32_t kw[2][2 * kWords], sf[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int row = r + 8 * x;
       if constexpr (D == 128) {
         const uint4 v = *reinterpret_cast<const uint4*>(codes[u] + row * C::kCode + 16 * q);
-        w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+        kw[x][0] = v.x, kw[x][1] = v.y, kw[x][2] = v.z, kw[x][3] = v.w;
         sf[x] = e4m3x2_to_f16(
             *reinterpret_cast<const uint16_t*>(scales[u] + row * C::kScale + 2 * q));
       } else {
         const uint2 v = *reinterpret_cast<const uint2*>(codes[u] + row * C::kCode + 8 * q);
-        w[x][0] = v.x, w[x][1] = v.y;
+        kw[x][0] = v.x, kw[x][1] = v.y;
         sf[x] = e4m3x2_to_f16(scales[u][row * C::kScale + q]);
       }
     }
@@ -198,7 +205,7 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
       uint32_t a[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        e2m1x8_to_f16(w[x][i], a[x]);
+        e2m1x8_to_f16(kw[x][i], a[x]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           a[x][e] = i < 2 ? hmul2_dup<false>(a[x][e], sf[x]) : hmul2_dup<true>(a[x][e], sf[x]);
@@ -214,6 +221,28 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
         mma_f16_16816(s[u][nt], a[0][2], a[1][2], a[0][3], a[1][3], qb[nt][2 * i + 1][0],
                       qb[nt][2 * i + 1][1]);
       }
+    }
+  }
+  // V's codes and scale pairs of both tiles, asked for before the softmax step, whose branch the
+  // loads would not pass (32 sequences: 63.0 us without, 60.8 with).
+  constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
+  uint32_t w[2][4][kWords], two[2][2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint8_t* at = codes[u] + C::kOffV + (2 * q + (x & 1) + 8 * (x >> 1)) * C::kCode;
+      if constexpr (D == 128) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at + 8 * r);
+        w[u][x][0] = v.x, w[u][x][1] = v.y;
+      } else {
+        w[u][x][0] = *reinterpret_cast<const uint32_t*>(at + 4 * r);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* at = scales[u] + C::kOffV + (2 * q + 8 * x) * C::kScale + r / kPer;
+      two[u][x] = __byte_perm(at[0], at[C::kScale], 0x5540);
     }
   }
   // ---- softmax: columns are heads 2q, 2q + 1, rows tokens r and r + 8 of each tile
@@ -282,29 +311,16 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
   // ---- O^T += V^T P^T
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    uint32_t w[4][kWords], sv[2];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int tok = 2 * q + (x & 1) + 8 * (x >> 1);
-      if constexpr (D == 128) {
-        const uint2 v = *reinterpret_cast<const uint2*>(codes[u] + C::kOffV + tok * C::kCode + 8 * r);
-        w[x][0] = v.x, w[x][1] = v.y;
-      } else {
-        w[x][0] = *reinterpret_cast<const uint32_t*>(codes[u] + C::kOffV + tok * C::kCode + 4 * r);
-      }
-    }
-    constexpr int kPer = D == 128 ? 1 : 2;  // lanes r of one scale block
+    uint32_t sv[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int tok = 2 * q + 8 * x;
-      const uint8_t* at = scales[u] + C::kOffV + tok * C::kScale + r / kPer;
-      uint32_t two = __byte_perm(at[0], at[C::kScale], 0x5540);
       if (EDGE) {
         // Slots past the context may hold anything; a NaN scale would survive p = 0.
-        if (16 * u + tok >= left) two &= 0xFF00u;
-        if (16 * u + tok + 1 >= left) two &= 0x00FFu;
+        const int tok = 16 * u + 2 * q + 8 * x;
+        if (tok >= left) two[u][x] &= 0xFF00u;
+        if (tok + 1 >= left) two[u][x] &= 0x00FFu;
       }
-      sv[x] = e4m3x2_to_f16(two);
+      sv[x] = e4m3x2_to_f16(two[u][x]);
     }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
@@ -313,7 +329,7 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
       uint32_t lo[2][4], hi[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t w0 = w[2 * x][i], w1 = w[2 * x + 1][i];
+        const uint32_t w0 = w[u][2 * x][i], w1 = w[u][2 * x + 1][i];
         e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), lo[x]);
         e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), hi[x]);
 #pragma unroll
