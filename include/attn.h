@@ -326,8 +326,8 @@ int attn_append_paged(const void *q, const void *k, const void *v, void *q_out, 
  *   xs    = y * (1 / k_scale)                       (the reciprocal rounded to fp32)
  *   scale = E4M3(max over the 16 channels |xs| / 6) (to nearest even, saturating at 448)
  *   code  = E2M1(xs / scale)                        (to nearest even, saturating; 0 if scale is 0)
- * with IEEE fp32 products, sums and divisions throughout (the rotation's too). y must be
- * finite.
+ * with IEEE fp32 products, sums and divisions throughout (the rotation's too). Infinities
+ * saturate; a NaN makes its block's scale NaN (0x7F) and its codes 0.
  * k_scale, v_scale > 0, finite, with finite reciprocals: one scale a tensor. About
  * max |y| / 2688 uses the scales' whole range; 1 serves values between about 0.05 and 2688.
  * rot_dim   a multiple of 32, or of 16 if interleaved (else ATTN_ERR_UNSUPPORTED).
@@ -367,7 +367,8 @@ int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
  * cu_seqlens, block_table, num_pages, page_size, Hq, Hkv, scale as for attn_fwd's PAGED_DECODE:
  *           at most 16 query heads per kv head; a bad length gives O = 0, LSE = -inf and
  *           ATTN_ERR_SEQLENS; a table entry outside the pool sets ATTN_ERR_BOUNDS and its page
- *           reads as zeros. L_b = 0 gives O = 0 and LSE = -inf.
+ *           reads as zeros. L_b = 0 gives O = 0 and LSE = -inf. A NaN in a query, or a NaN
+ *           scale of a key in the context, makes the rows it meets NaN.
  * workspace of at least attn_workspace_bytes_fp4(...) bytes (may be NULL when that is 0); contents
  *           need not be initialised; concurrent calls need separate ones.
  */

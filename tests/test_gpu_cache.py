@@ -468,6 +468,51 @@ def test_append_fp4_edges():
             assert np.array_equal(gc[bt.phys, :, bt.slot], codes)
 
 
+@pytest.mark.parametrize("d,rot,interleaved", [(64, 32, False), (128, 0, False), (128, 64, True),
+                                               (128, 128, False)])
+def test_append_fp4_infinities_and_nan(d, rot, interleaved):
+    """Infinite values, and finite ones whose quotient by the tensor scale overflows, saturate:
+    scale 448, codes of 6. A NaN makes its own block's scale NaN and its codes zero."""
+    rng = np.random.default_rng(104)
+    bt = Batch(rng, [16], [16], 16)
+    r = Rows(rng, 16, 1, 2, d, rot, interleaved=interleaved)
+    x = np.array(r.x, np.float32)
+    inf, nan = np.float32(np.inf), np.float32(np.nan)
+    x[1, 5::40] = inf
+    x[2, 3::24] = -inf
+    x[3] = np.where(np.arange(x.shape[1]) % 2, inf, -inf)
+    x[4] = np.float32(3e38) * np.sign(x[4])
+    x[5, ::37] = np.float32(-2e38)
+    x[6, 9::50] = nan
+    x[7] = nan
+    x[8, 4::48], x[8, 20::48] = inf, nan
+    x[9, ::8] = np.float32(4200.0)
+    bits = I.f32_to_bf16_bits(np.where(np.isfinite(x), x, 0).astype(np.float32))
+    top = (np.ascontiguousarray(x).view(np.uint32) >> 16).astype(np.uint16)
+    bits = np.where(np.isfinite(x), bits, top)
+    r.x = I.bf16_bits_to_f32(bits).astype(np.float64)
+    r.buf = bf16_tensor(bits, "cuda")
+    for ks, vs in ((1.0, 1.0), (0.003, 2.0 ** -20)):
+        kp, vp = pools_fp4(rng, bt.num, 2, 16, d)
+        append_fp4(r, bt, kp, vp, 16, ks, vs, q=False)
+        assert status() == 0
+        with np.errstate(all="ignore"):
+            k32 = cache.rotate(r.part("k")[1], r.cs, bt.pos, rot, interleaved, np.float32)
+        for pool, rows, scale in ((kp, k32, ks), (vp, r.part("v")[1], vs)):
+            y = rows.astype(np.float32)
+            with np.errstate(over="ignore"):
+                xs = y * (np.float32(1) / np.float32(scale))
+            lost = np.isnan(xs.reshape(16, 2, d // 16, 16)).any(-1)
+            y = np.where(np.repeat(lost, 16, -1), np.float32(0), y)
+            with np.errstate(all="ignore"):
+                codes, sf = cache.quantize(y, scale)
+            assert lost[6:9].any() and not lost[1].all() and (sf == 0x7E).any()
+            sf[lost] = 0x7F
+            gc, gs = cache.split_block(pool.cpu().numpy(), 16, d)
+            assert np.array_equal(gs[bt.phys, :, bt.slot], sf)
+            assert np.array_equal(gc[bt.phys, :, bt.slot], codes)
+
+
 def test_append_fp4_normed_within_a_step():
     """|value - y| is at most half the widest step (1 * scale, or 0.4 * scale where 6 saturates),
     the scale at most max |y| / 6 * (1 + 2^-4)."""
@@ -711,6 +756,52 @@ def test_decode_fp4_rising_scores(d):
         w.run()
         assert status() == 0
         w.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [2, 16])
+def test_decode_fp4_nan_is_not_hidden(d, group):
+    """A NaN query channel makes its own row NaN, a NaN key scale the rows of its kv head, a NaN
+    value scale its 16 channels; contexts of one token, of one slice and of many splits."""
+    rng = np.random.default_rng(21)
+    lens = [1, 20, 9000, 1, 20, 9000, 1, 9000, 40]
+    Hkv, page = 2, 32
+    w = Decode(rng, lens, group * Hkv, Hkv, d, page)
+    codes, sf = (a.copy() for a in cache.split_block(w.pools[0], page, d))
+    for b, tok in ((3, 0), (4, 11), (5, 8999)):  # keys of kv head 1
+        f, s = cache.slots([tok], w.table[b], page)
+        sf[f, 1, s, 1] = 0x7F
+    w.k = dev(np.concatenate([codes.reshape(w.bt.num, Hkv, -1), sf.reshape(w.bt.num, Hkv, -1)], 2))
+    codes, sf = (a.copy() for a in cache.split_block(w.pools[1], page, d))
+    for b, tok in ((6, 0), (7, 4500)):  # values of kv head 0
+        f, s = cache.slots([tok], w.table[b], page)
+        sf[f, 0, s, 2] = 0x7F
+    w.v = dev(np.concatenate([codes.reshape(w.bt.num, Hkv, -1), sf.reshape(w.bt.num, Hkv, -1)], 2))
+    q = w.q.clone()
+    q[:3, 1, 0, 17] = float("nan")
+    w.q = q
+    w.run()
+    assert status() == 0
+    o, lse = w.o.float().cpu().numpy()[:, :, 0], w.lse.cpu().numpy()
+    hurt = np.zeros(o.shape, bool)
+    hurt[:3, 1] = True
+    hurt[3:6, group:] = True
+    assert np.array_equal(np.isnan(lse), hurt[:, :, 0])
+    hurt[6:8, :group, 32:48] = True
+    assert np.array_equal(np.isnan(o), hurt)
+    # The rest is right, as all of it is without them.
+    first = w.o.clone(), w.lse.clone()
+    w.q = torch.where(torch.isnan(q), torch.zeros_like(q), q)
+    w.k, w.v = (dev(p) for p in w.pools)
+    w.run()
+    w.qv[:3, 1, 17] = 0.0
+    w.check()
+    # Not bit for bit: a NaN score sends its warp through the branch that moves the reference
+    # max of all its heads, and a weight 2^(x - m), m not an integer, rounds to f16 by its own m.
+    # The bound of check() holds for any m.
+    w.o = torch.where(dev(hurt)[:, :, None], w.o, first[0])
+    w.lse = torch.where(torch.isnan(first[1]), w.lse, first[1])
+    w.check()
 
 
 def test_decode_fp4_bad_entries():

@@ -92,6 +92,10 @@ __device__ __forceinline__ void divide8(float2 (&x)[4], float s, float rc) {
   }
 }
 
+__device__ __forceinline__ float2 clamp2(float2 x, float m) {
+  return make_float2(fminf(fmaxf(x.x, -m), m), fminf(fmaxf(x.y, -m), m));
+}
+
 template <int D, int CACHE>
 __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p) {
   constexpr int R = D / 16;          // lanes per row
@@ -315,15 +319,28 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
           for (int e = 0; e < 4; ++e) {
             a[e] = __fmul2_rn(a[e], inv);
             b[e] = __fmul2_rn(b[e], inv);
-            ma = fmaxf(ma, fmaxf(fabsf(a[e].x), fabsf(a[e].y)));
-            mb = fmaxf(mb, fmaxf(fabsf(b[e].x), fabsf(b[e].y)));
+            ma = fmax_nan(ma, fmax_nan(fabsf(a[e].x), fabsf(a[e].y)));
+            mb = fmax_nan(mb, fmax_nan(fabsf(b[e].x), fabsf(b[e].y)));
           }
           const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
           const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
           if (paired) {
-            ma = fmaxf(ma, oa), mb = fmaxf(mb, ob);
+            ma = fmax_nan(ma, oa), mb = fmax_nan(mb, ob);
           } else {
-            ma = mb = fmaxf(ma, mb);
+            ma = mb = fmax_nan(ma, mb);
+          }
+          // From kFp4Large on scale and codes saturate (448 * 6 < kFp4Large); infinities would
+          // not go through the divisions below. A NaN stays, gives its block the scale NaN and,
+          // as that is not > 0, zero codes.
+          if (ma >= kFp4Large) {
+            ma = kFp4Large;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = clamp2(a[e], kFp4Large);
+          }
+          if (mb >= kFp4Large) {
+            mb = kFp4Large;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = clamp2(b[e], kFp4Large);
           }
           // max / 6, correctly rounded as in divide8, then to E4M3.
           constexpr float kSixth = 1.f / 6.f;

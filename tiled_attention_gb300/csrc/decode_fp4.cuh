@@ -694,22 +694,22 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
-        const float mw = red_m[w * 16 + hh];
-        if (mw != -INFINITY) {
-          const float f = fast_exp2(mw - M);
+        const float lw = red_l[w * 16 + hh];
+        if (lw != 0.f) {  // the warp had tokens; a NaN among their scores is a sum of NaN
+          const float f = fast_exp2(red_m[w * 16 + hh] - M);
           const float4 x = *reinterpret_cast<const float4*>(
               base + w * C::kRingBytes + ctl->idle[w] * C::kStageBytes + (hh * D + d0) * 4);
-          Ls += red_l[w * 16 + hh] * f;
+          Ls += lw * f;
           a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
         }
       }
       if (was_whole) {
         const size_t orow = head0 + hh;
-        const float inv = Ls > 0.f ? p.v_scale / Ls : 0.f;
+        const float inv = Ls != 0.f ? p.v_scale / Ls : 0.f;
         *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
         if (d0 == 0)
-          p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
+          p.lse[orow] = Ls != 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(p.part_o + (slot * G + hh) * D + d0) = a;
         if (d0 == 0)
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const Deco
         a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = 0; i < sets; ++i) {
           const float2 ml = sml[tid + i * items];
-          if (ml.x == -INFINITY) continue;  // more sets than parts
+          if (ml.y == 0.f) continue;  // more sets than parts
           const float f = exp2f(ml.x - M);
           const float4 x = so[tid + i * items];
           Ls += ml.y * f;

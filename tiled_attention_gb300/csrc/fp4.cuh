@@ -18,12 +18,20 @@
 namespace ta {
 
 constexpr int kFp4Block = 16;  // channels per scale
+constexpr float kFp4Large = 4096.f;  // past every value of code * scale (448 * 6 = 2688)
 
 __host__ __device__ constexpr int fp4_code_bytes(int d) { return d / 2; }
 __host__ __device__ constexpr int fp4_scale_bytes(int d) { return d / kFp4Block; }
 // Bytes of one token of one kv head: 72 at d = 128, 36 at d = 64.
 __host__ __device__ constexpr int fp4_row_bytes(int d) {
   return fp4_code_bytes(d) + fp4_scale_bytes(d);
+}
+
+// The larger one, or NaN if either is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 // Four E2M1 pairs (the bytes of w, low nibble first) to f16 pairs.
