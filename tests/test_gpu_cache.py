@@ -715,6 +715,70 @@ def test_decode_fp4_many_sequences(B, most, d, Hkv):
     w.check()
 
 
+def many(rng, Hkv, most, *some):
+    """Lengths of enough sequences that contexts outnumber the CTAs of any variant (three an SM),
+    `some` among them, in random order."""
+    B = 3 * torch.cuda.get_device_properties(0).multi_processor_count // Hkv + 40
+    lens = np.concatenate([rng.integers(0, most + 1, B), some]).astype(int)
+    rng.shuffle(lens)
+    return lens
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 7, 16])
+def test_decode_fp4_many_contexts(page, d, group):
+    """More contexts than CTAs, so that warps take them by themselves: odd lengths, empty ones,
+    one over many warps; the same bits again on the second run."""
+    rng = np.random.default_rng(3200 + page + d + group)
+    lens = many(rng, 3, 200, *EDGE_LENS, 700, 1025, 5000)
+    w = Decode(rng, lens, 3 * group, 3, d, page)
+    w.run()
+    assert status() == 0
+    w.check()
+    first = w.o.clone(), w.lse.clone()
+    w.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0].view(torch.int16), w.o.view(torch.int16))
+    assert torch.equal(first[1], w.lse)
+
+
+@pytest.mark.parametrize("lens", [[0] * 700, [0] * 699 + [1], [1] * 700, [0] * 350 + [900] + [0] * 350,
+                                  [128] * 600, [129] * 500])
+def test_decode_fp4_many_contexts_few_tokens(lens):
+    """Fewer blocks than warps, down to none."""
+    rng = np.random.default_rng(3300)
+    w = Decode(rng, lens, 2, 1, 128, 16)
+    w.run()
+    assert status() == 0
+    w.check()
+
+
+def test_decode_fp4_many_contexts_device_checks():
+    """A NaN query, a page outside the pool, bad lengths among many contexts: each hurts its own
+    rows only."""
+    rng = np.random.default_rng(3400)
+    lens = many(rng, 2, 300)
+    lens[:8] = [200, 90, 77, 1, 128, 250, 40, 300]
+    w = Decode(rng, lens, 8, 2, 128, 32, N=300)
+    w.table[1, 2] = w.bt.num  # the third page of sequence 1: reads as zeros
+    w.d_table = dev(w.table)
+    w.q[3, 5, 0, 3] = float("nan")
+    w.run()
+    assert status() == attn.ATTN_ERR_BOUNDS
+    assert np.isnan(w.lse[3, 5].item()) and torch.isnan(w.o[3, 5]).all()
+    assert not torch.isnan(w.lse[3, :5]).any()
+    w.check(skip=(1, 3))
+    cu = w.cu.cpu().numpy().copy()
+    w.alloc()
+    cu[10] = cu[11] + 5  # sequence 10: negative; sequence 9 too long or as it is
+    w.cu = dev(cu, np.int32)
+    w.run()
+    assert status() in (attn.ATTN_ERR_SEQLENS, attn.ATTN_ERR_BOUNDS)
+    assert not f64(w.o)[10].any() and torch.all(w.lse[10] == -np.inf)
+    w.check(skip=(1, 3, 9, 10))
+
+
 def test_decode_fp4_all_empty():
     rng = np.random.default_rng(3100)
     w = Decode(rng, [0, 0, 0], 4, 2, 128, 16)

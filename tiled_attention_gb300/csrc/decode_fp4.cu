@@ -19,26 +19,30 @@ int fp4_slots(int d, int group) {
   return per * sms_or_default();
 }
 
+constexpr int kWorkers = DecodeFp4Cfg<64, 1>::kWarps;  // of a CTA, at most
+
 struct Fp4Layout {
-  size_t part_ml, total;
+  size_t part_ml, joins, total;
   int slots;
 };
 
-// Two partial rows of every query head of a group a CTA: O, then (max, sum).
+// Of every worker (up to four a CTA) two partial rows of each query head of a group: O, then
+// (max, sum); then what it has to have joined.
 Fp4Layout fp4_layout(int Hq, int Hkv, int d) {
   Fp4Layout L{};
   const int group = Hq / Hkv;
   L.slots = fp4_slots(d, group);
-  const size_t rows = 2 * static_cast<size_t>(L.slots) * group;
+  const size_t rows = 2 * static_cast<size_t>(kWorkers * L.slots) * group;
   L.part_ml = align256(rows * d * sizeof(float));
-  L.total = L.part_ml + align256(rows * 2 * sizeof(float));
+  L.joins = L.part_ml + align256(rows * 2 * sizeof(float));
+  L.total = L.joins + align256(static_cast<size_t>(kWorkers * L.slots) * sizeof(int4));
   return L;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SOLO>
 cudaError_t launch_one(const DecodeFp4Params& p, cudaStream_t stream) {
   static unsigned long long done = 0;
-  auto kern = decode_fp4_kernel<D, NT>;
+  auto kern = decode_fp4_kernel<D, NT, SOLO>;
   using C = DecodeFp4Cfg<D, NT>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
@@ -46,15 +50,25 @@ cudaError_t launch_one(const DecodeFp4Params& p, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // The joining kernel may start before the decode kernel has ended (it waits for it).
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.Hq / p.join_heads, p.B);
-  cfg.blockDim = dim3(kCombineThreads);
+  cfg.gridDim = SOLO ? dim3(kWorkers * p.slots) : dim3(p.Hq / p.join_heads, p.B);
+  // By contexts: eight sets of threads a column for one head, and as many threads for several
+  // (48 sequences x 4 kv heads: 73 us, with 128 threads 75); by workers, which have few parts
+  // each: 128 (256 sequences x 4 kv heads of 16 at d = 64: 37.7 us, with 256 threads 38.5).
+  cfg.blockDim = dim3(SOLO || p.join_heads * D < 128 ? 128 : 256);
   cfg.stream = stream;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_fp4_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, combine_fp4_kernel<D, SOLO>, p);
+}
+
+template <bool SOLO>
+cudaError_t launch(const DecodeFp4Params& p, int d, cudaStream_t stream) {
+  if (d == 64)
+    return p.group <= 8 ? launch_one<64, 1, SOLO>(p, stream) : launch_one<64, 2, SOLO>(p, stream);
+  return p.group <= 8 ? launch_one<128, 1, SOLO>(p, stream) : launch_one<128, 2, SOLO>(p, stream);
 }
 
 }  // namespace
@@ -118,6 +132,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
+  p.joins = reinterpret_cast<int4*>(ws + L.joins);
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -136,11 +151,12 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.v_scale = v_scale;
   p.timeout_ns = kTimeoutNs;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  cudaError_t e;
-  if (d == 64)
-    e = group <= 8 ? launch_one<64, 1>(p, stream) : launch_one<64, 2>(p, stream);
-  else
-    e = group <= 8 ? launch_one<128, 1>(p, stream) : launch_one<128, 2>(p, stream);
+  // From as many contexts (a sequence and kv head each) on as the GPU holds CTAs, a warp is a
+  // worker; below, a CTA. Measured with warps and with CTAs: 64 sequences of 1K-8K tokens x 8 kv
+  // heads 66 and 68 us, 256 of 1K 64 and 76, 1000 of 20-400 81 and 169; 24 of 1K-16K 51 and 49,
+  // one of 16K 33 and 13.
+  const bool solo = static_cast<long long>(B) * Hkv >= L.slots;
+  const cudaError_t e = solo ? launch<true>(p, d, stream) : launch<false>(p, d, stream);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   return ATTN_OK;
 }

@@ -25,19 +25,23 @@
 //
 // Work: the contexts are cut into 128-token blocks, numbered over sequence, kv head and
 // position, with a few units more at each context's start for the cost of beginning it, and
-// shared out evenly over the CTAs in that order: every CTA has the same work whatever the
-// lengths are, and finds its range from cu_seqlens alone. A range is one or more segments, each
-// of one (sequence, kv head). A segment that is the whole context writes O and LSE itself; the
-// others (a CTA's first and last at most) leave the unnormalised O, the reference max and the
-// sum in the workspace, two slots a CTA, and a second kernel joins them in CTA order, so
-// results do not depend on timing:
+// shared out evenly over the workers in that order: every worker has the same work whatever the
+// lengths are, and finds its range from cu_seqlens alone. A worker is a CTA where contexts are
+// few, so that they fall into few parts, and a single warp where they are many (SOLO), which
+// then begins and ends contexts without waiting for three others. A range is one or more
+// segments, each of one (sequence, kv head). A segment that is the whole context writes O and
+// LSE itself; the others (a worker's first and last at most) leave the unnormalised O, the
+// reference max and the sum in the workspace, two slots a worker, and a second kernel joins them
+// in the workers' order, so results do not depend on timing:
 //   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  O = sum_c O_c 2^(m_c - M) / L,
 //   LSE = (M + log2 L) ln 2.
-// The second kernel starts under programmatic dependent launch: it finds its parts while the
-// first still runs. No counters, so no memset.
+// The second kernel starts under programmatic dependent launch: with CTAs as workers it takes a
+// context a CTA and finds the parts from cu_seqlens while the first still runs; with warps a
+// worker a CTA, and each warp leaves word of the context that it begins and others end (going
+// by contexts there, 1000 sequences x 8 kv heads took 31 us longer). No counters, so no memset.
 //
-// CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64),
-// through a ring of its own in shared memory: it brings the next stage in with bulk copies while
+// CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64), or
+// all stages of its own segments, through a ring of its own in shared memory: it brings the next stage in with bulk copies while
 // it works on one, so no warp waits for another before a segment's end.
 //
 // Measured (GB300, device time): 32 sequences of 1K-16K tokens, 8 kv heads of 4 query heads,
@@ -66,6 +70,8 @@ struct DecodeFp4Params {
   float* lse;            // [B, Hq]
   float* part_o;         // [2 * slots, group, D]
   float* part_ml;        // [2 * slots, group, 2]
+  int4* joins;           // [workers], SOLO: the context that a worker begins and others end:
+                         // its number, first part's slot, parts (0: none)
   int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
   int slots;             // CTAs of the decode kernel
   int fine;              // CTAs that units smaller than four may go to
@@ -360,14 +366,16 @@ __device__ __forceinline__ int fp4_blocks(int L) { return (L + kFp4Block128 - 1)
 
 // How the blocks are shared out. Every warp of both kernels works it out by itself, from
 // cu_seqlens alone: a context counts its blocks and kStart units before them for what beginning
-// it costs, and CTA i of n takes an even share of the units, the first r CTAs q + 1, the others
-// q. A share that ends among a context's kStart units holds none of it. Cutting small batches
-// into equal parts of whole rounds of the four warps instead, a CTA a part, so that no CTA begins
-// two contexts, gained 0.6 us on one sequence of 16K tokens (13.7 us) and lost 0.5 to 1 us on one
-// of 700, one of 4K and four of 1K to 16K.
-template <int D>
+// it costs, and worker i of n takes an even share of the units, the first r workers q + 1, the
+// others q. A share that ends among a context's kStart units holds none of it. Cutting small
+// batches into equal parts of whole rounds of the four warps instead, a CTA a part, so that no
+// CTA begins two contexts, gained 0.6 us on one sequence of 16K tokens (13.7 us) and lost 0.5 to
+// 1 us on one of 700, one of 4K and four of 1K to 16K. Warps as workers: with 0, 1 and 2 units
+// 1000 sequences of 20-400 tokens x 8 kv heads take 87, 83 and 88 us, 256 of 1K 64.3, 65.0 and
+// 64.8.
+template <int D, bool SOLO>
 struct Fp4Share {
-  static constexpr int kStart = DecodeFp4Start<D>::kUnits;
+  static constexpr int kStart = SOLO ? 1 : DecodeFp4Start<D>::kUnits;
   int total;    // units of one kv head, all sequences
   int before;   // those of the sequences before `upto`
   int n, q, r;
@@ -379,23 +387,26 @@ struct Fp4Share {
     const int lane = static_cast<int>(threadIdx.x) & 31;
     w0 = lane < p.B ? units(fp4_blocks(fp4_length(p, lane, report))) : 0;
     int all = w0, ahead = lane < upto ? w0 : 0;
-    for (int b = lane + 32; b < p.B; b += 32) {
-      const int w = units(fp4_blocks(fp4_length(p, b, report)));
-      all += w;
-      if (b < upto) ahead += w;
+    for (int b0 = lane + 32; b0 < p.B; b0 += 128) {
+#pragma unroll
+      for (int b = b0; b < b0 + 128; b += 32) {  // four loads at a time
+        const int w = b < p.B ? units(fp4_blocks(fp4_length(p, b, report))) : 0;
+        all += w;
+        if (b < upto) ahead += w;
+      }
     }
     total = __reduce_add_sync(0xffffffffu, all);
     before = __reduce_add_sync(0xffffffffu, ahead);
     const int U = total * p.Hkv;
-    // As many CTAs as the GPU holds, but over 32 parts a context only at four units or more a
-    // CTA: the joining kernel reads 32 parts in one round.
-    n = imin(p.slots, imin(U, imax(p.fine, U / 4)));
+    // As many workers as the GPU holds, but CTAs over 32 parts a context only at four units or
+    // more each: the joining kernel reads 32 parts in one round.
+    n = SOLO ? imin(DecodeFp4Cfg<D, 1>::kWarps * p.slots, U) : imin(p.slots, imin(U, imax(p.fine, U / 4)));
     q = n ? U / n : 0;
     r = U - q * n;
   }
-  // First unit of CTA i, and the CTA that takes unit u.
+  // First unit of worker i, and the worker that takes unit u.
   __device__ __forceinline__ int start(int i) const { return i * q + imin(i, r); }
-  __device__ __forceinline__ int cta_of(int u) const {
+  __device__ __forceinline__ int worker_of(int u) const {
     const int large = r * (q + 1);
     return u < large ? u / (q + 1) : r + (u - large) / q;
   }
@@ -404,10 +415,9 @@ struct Fp4Share {
                                        int& ahead) const {
     const int lane = static_cast<int>(threadIdx.x) & 31;
     int run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
+    for (int b0 = 0; b0 < p.B;) {
       const int b = b0 + lane;
-      const int w =
-          b0 == 0 ? w0 : b < p.B ? units(fp4_blocks(fp4_length(p, b, false))) : 0;
+      const int w = b0 == 0 ? w0 : b < p.B ? units(fp4_blocks(fp4_length(p, b, false))) : 0;
       int sum = w;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -423,13 +433,22 @@ struct Fp4Share {
         return;
       }
       run = __shfl_sync(0xffffffffu, sum, 31);
+      for (b0 += 32; b0 < p.B; b0 += 128) {  // past four times 32 sequences at once
+        int four = 0;
+#pragma unroll
+        for (int c = b0 + lane; c < b0 + lane + 128; c += 32)
+          four += units(c < p.B ? fp4_blocks(fp4_length(p, c, false)) : 0);
+        four = run + __reduce_add_sync(0xffffffffu, four);
+        if (u < four * p.Hkv) break;
+        run = four;
+      }
     }
     seq = p.B - 1;  // not reached: u lies below the total
     ahead = run;
   }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool SOLO>
 __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     decode_fp4_kernel(const DecodeFp4Params p) {
   using C = DecodeFp4Cfg<D, NT>;
@@ -457,22 +476,24 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     fence_mbar_init();
   }
   const int cta = static_cast<int>(blockIdx.x);
-  const Fp4Share<D> share(p, 0, cta == 0 && warp == 0);
-  if (cta >= share.n) return;
-  int u = share.start(cta);
-  const int end = share.start(cta + 1);
+  const Fp4Share<D, SOLO> share(p, 0, cta == 0 && warp == 0);
+  const int worker = SOLO ? C::kWarps * cta + warp : cta;
+  if (SOLO && lane == 0) p.joins[worker] = make_int4(0, 0, 0, 0);  // so far
+  __syncthreads();  // barriers and flag
+  if (worker >= share.n) return;
+  int u = share.start(worker);
+  const int end = share.start(worker + 1);
   int b, seq_u;
   share.find(p, u, b, seq_u);
   seq_u *= p.Hkv;  // first unit of sequence b
-  __syncthreads();  // barriers and flag
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
   // Copies of one stage: lane 4 sub + part brings K (part 0) or V (part 2) of the stage's tokens
   // in its page `sub` (up to eight pages of 16 tokens), a whole (page, head) block in one
   // copy; where a page is longer than a stage, parts 0 and 2 bring its codes and parts 1 and 3
-  // its scales. Every lane arrives on the stage's barrier with the bytes it asked for. A warp's
-  // stages all lie at the same place of their pages. Pages past the context are not copied. A
+  // its scales. Every lane arrives on the stage's barrier with the bytes it asked for. Stages
+  // lie at the same place of their pages, but for `flip` below. Pages past the context are not copied. A
   // page whose entry lies outside the pool is never addressed: the status word reports it and
   // it reads as zeros. A stage's table entries are read one stage ahead of its copies.
   const int lp = p.page_shift;
@@ -480,7 +501,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const int run = imin(C::kStage, 1 << lp);  // tokens of the stage in one page
   const bool whole_pages = (1 << lp) == run;
   const bool copies = sub * run < C::kStage && !(whole_pages && (part & 1));
-  const int tok0 = warp * C::kStage + sub * run;  // this lane's first token in the warp's stage 0
+  constexpr int kHop = (SOLO ? 1 : C::kWarps) * C::kStage;  // tokens from stage to stage
+  const int tok_w = SOLO ? 0 : warp * C::kStage;  // the warp's first token in a segment
+  const int tok0 = tok_w + sub * run;             // this lane's first token in the warp's stage 0
   const uint32_t bytes = static_cast<uint32_t>(run) *
                          (whole_pages ? C::kCode + C::kScale : (part & 1) ? C::kScale : C::kCode);
   // Shared-memory addresses of this lane's copy and of its barrier, for the next stage; the
@@ -493,6 +516,12 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   const uint8_t* const src0 =
       ((part & 2) ? p.v : p.k) +
       ((part & 1) ? (C::kCode << lp) + in_page * C::kScale : in_page * C::kCode);
+  // A page of 128 tokens at d = 128 holds two stages; a warp that takes all goes to and fro
+  // between the halves.
+  const uint32_t flip = SOLO && (C::kStage << 1) == (1 << lp)
+                            ? static_cast<uint32_t>(run * ((part & 1) ? C::kScale : C::kCode))
+                            : 0;
+  uint32_t half = 0;
   const uint32_t blk_bytes = static_cast<uint32_t>(C::kCode + C::kScale) << lp;
   const uint32_t page_bytes = static_cast<uint32_t>(p.Hkv) * blk_bytes;  // the host checks it
 
@@ -503,12 +532,13 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 
   // The segment that starts at block u, and its first stage on the way.
   int g, n, t0, t1, next;
-  bool whole;
+  bool whole;         // the segment is its whole context
+  int begins;         // the context's last unit, if others end it; else -1
   const int* row;
   const uint8_t* src_g;
   // Table entry of this lane's page of stage i: -2 nothing to copy, -1 outside the pool.
   auto entry = [&](int i) {
-    const int tok = t0 + tok0 + i * (C::kWarps * C::kStage);
+    const int tok = t0 + tok0 + i * kHop;
     if (!copies || i >= n || tok >= t1) return -2;
     const int e = __ldg(row + (tok >> lp));
     return static_cast<unsigned>(e) < static_cast<unsigned>(p.num_pages) ? e : -1;
@@ -519,7 +549,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
           "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
           "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
           "[%3];" ::"r"(dst),
-          "l"(src_g + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * page_bytes),
+          "l"(src_g + half + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * page_bytes),
           "r"(bytes), "r"(bar)
           : "memory");
     } else {
@@ -530,6 +560,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
       }
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     }
+    half ^= flip;
     dst += step * C::kStageBytes;
     bar += step * 8;
     step = -step;
@@ -554,11 +585,12 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     const int nblk = imin(nb - blk0, end - u);
     u += nblk;
     whole = nblk == nb;
+    begins = blk0 || whole ? -1 : seq_u + (g + 1) * w - 1;
     // Stages of the segment's tokens [t0, t1): this warp takes stage warp, warp + 4, ...
     t0 = blk0 * kFp4Block128;
     t1 = imin(t0 + nblk * kFp4Block128, L);
-    n = aborted ? 0 : (t1 - t0 + (C::kWarps - 1 - warp) * C::kStage + C::kStage - 1) /
-                          (C::kWarps * C::kStage);
+    n = aborted ? 0 : (t1 - t0 - tok_w + kHop - 1) / kHop;
+    half = 0;
     row = p.table + static_cast<size_t>(b) * p.max_pages;
     src_g = src0 + static_cast<size_t>(g) * blk_bytes;
     if (n > 0) {
@@ -569,7 +601,8 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   };
   bool more = open();
   for (bool first = true; more; first = false) {
-    const size_t head0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * G;
+    const int ctx = b * p.Hkv + g;
+    const size_t head0 = static_cast<size_t>(ctx) * G;
     // Q as the B operand: column (head) r, k-step kk = channels D/4 q + 4 kk + {0, 1 | 2, 3}.
     uint32_t qb[NT][C::kSteps][2];
     float sc[NT][2];  // scale of heads 8 nt + 2 q, + 1
@@ -619,15 +652,31 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     for (int nt = 0; nt < NT; ++nt)
       mref[nt][0] = mref[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-    int left = t1 - t0 - warp * C::kStage;  // tokens from the stage's first on
-    for (int i = 0; i < n; ++i, left -= C::kWarps * C::kStage) {
-      if (i + 1 < n) {  // into the slot of stage i - 1, which the whole warp has left
+    int left = t1 - t0 - tok_w;  // tokens from the stage's first on
+    const bool was_whole = whole;
+    const int begun = begins;
+    int stages = aborted ? 0 : n;
+    for (int i = 0;; ++i, left -= kHop) {
+      // Into the slot of stage i - 1, which the whole warp has left: the next stage, or the next
+      // segment's first one.
+      if (i + 1 < stages) {
         issue(next);
         next = entry(i + 2);
+      } else if (i == imax(stages - 1, 0)) {
+        more = open();
       }
+      if (i >= stages) break;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[st_out], parity, wc))) {
+        // Let the copies in flight land (with a limit) before their slots are used again; there
+        // are no more after that. The rest of the range is walked without stages.
         aborted = true;
-        break;
+        mbar_wait(&full[st_out], parity, wc_drain);
+        if (i + 1 < stages || (more && n > 0))
+          mbar_wait(&full[st_out ^ 1], parity ^ static_cast<uint32_t>(st_out), wc_drain);
+        if (i + 1 >= stages) break;  // the next segment is open already
+        stages = 0;
+        i = -1;
+        continue;
       }
       const uint8_t* sl = ring + st_out * C::kStageBytes;
       if (left >= C::kStage) {
@@ -642,19 +691,7 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
       if (++st_out == S) st_out = 0, parity ^= 1;
       __syncwarp();
     }
-    // After a timeout, let the copies still in flight land (with a limit) before the slots are
-    // used again; there are no more after that.
-    if (aborted)
-      for (int x = 0; x < S; ++x)
-        mbar_wait(&full[(st_out + x) % S], parity ^ (st_out + x >= S ? 1 : 0), wc_drain);
-    // The next segment's first stage goes into slot st_out, while this one's rows are merged in
-    // the other slot: the copy's latency hides behind the merge.
-    const bool was_whole = whole;
-    float* const mine =
-        reinterpret_cast<float*>(ring + (st_out ^ 1) * C::kStageBytes);
-    more = open();
-
-    // ---------------------------------------------------------------- merge the four warps
+    // ---------------------------------------------------------------- the segment's rows
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -662,105 +699,163 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
-    // [head][D] fp32 in each warp's idle slot. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
-    // m-tile i holds channels 2i and 2i + 1 of them.
-    if (lane == 0) ctl->idle[warp] = st_out ^ 1;
+    const size_t slot = 2 * static_cast<size_t>(worker) + (first ? 0 : 1);
+    if constexpr (SOLO) {
+      if (begun >= 0 && lane == 0)
+        p.joins[worker] = make_int4(ctx, static_cast<int>(slot),
+                                    share.worker_of(begun) - worker + 1, 0);
+      // Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..; m-tile i holds channels 2i and 2i + 1.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int h = 8 * nt + 2 * q + c;
-        if (r == 0) {
-          red_m[warp * 16 + h] = mref[nt][c];
-          red_l[warp * 16 + h] = l[nt][c];
+        for (int c = 0; c < 2; ++c) {
+          const int h = 8 * nt + 2 * q + c;
+          if (h >= G) continue;
+          const float Ls = l[nt][c];
+          if (was_whole) {
+            const float inv = Ls != 0.f ? p.v_scale / Ls : 0.f;
+            uint16_t* to = p.o + (head0 + h) * D + r * (D / 8);
+#pragma unroll
+            for (int i = 0; i < C::kSteps; i += 4)
+              *reinterpret_cast<uint4*>(to + 2 * i) =
+                  make_uint4(pack_bf16x2(o[nt][i][c] * inv, o[nt][i][c + 2] * inv),
+                             pack_bf16x2(o[nt][i + 1][c] * inv, o[nt][i + 1][c + 2] * inv),
+                             pack_bf16x2(o[nt][i + 2][c] * inv, o[nt][i + 2][c + 2] * inv),
+                             pack_bf16x2(o[nt][i + 3][c] * inv, o[nt][i + 3][c + 2] * inv));
+            if (r == 0)
+              p.lse[head0 + h] =
+                  Ls != 0.f ? (mref[nt][c] + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
+          } else {
+            float* to = p.part_o + (slot * G + h) * D + r * (D / 8);
+#pragma unroll
+            for (int i = 0; i < C::kSteps; i += 2)
+              *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
+                  o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+            if (r == 0)
+              *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * G + h)) =
+                  make_float2(mref[nt][c], Ls);
+          }
         }
-        if (h < G) {
-          float* to = mine + h * D + r * (D / 8);
+    } else {
+      // The slot of the stage just used; the next segment's first stage is on its way into the
+      // other one, and its latency hides behind the merge.
+      float* const mine =
+          reinterpret_cast<float*>(ring + (st_out ^ 1) * C::kStageBytes);
+      // [head][D] fp32 in each warp's idle slot. Lane (r, q): heads 2q, 2q + 1, channels D/8 r ..;
+      // m-tile i holds channels 2i and 2i + 1 of them.
+      if (lane == 0) ctl->idle[warp] = st_out ^ 1;
 #pragma unroll
-          for (int i = 0; i < C::kSteps; i += 2)
-            *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
-                o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int h = 8 * nt + 2 * q + c;
+          if (r == 0) {
+            red_m[warp * 16 + h] = mref[nt][c];
+            red_l[warp * 16 + h] = l[nt][c];
+          }
+          if (h < G) {
+            float* to = mine + h * D + r * (D / 8);
+#pragma unroll
+            for (int i = 0; i < C::kSteps; i += 2)
+              *reinterpret_cast<float4*>(to + 2 * i) = make_float4(
+                  o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+          }
+        }
+      __syncthreads();
+      constexpr int kQuads = D / 4;  // four-column groups of one head's row
+      for (int idx = tid; idx < G * kQuads; idx += C::kThreads) {
+        const int hh = idx / kQuads, d0 = (idx % kQuads) * 4;
+        float M = red_m[hh];
+#pragma unroll
+        for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * 16 + hh]);
+        float Ls = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+          const float lw = red_l[w * 16 + hh];
+          if (lw != 0.f) {  // the warp had tokens; a NaN among their scores is a sum of NaN
+            const float f = fast_exp2(red_m[w * 16 + hh] - M);
+            const float4 x = *reinterpret_cast<const float4*>(
+                base + w * C::kRingBytes + ctl->idle[w] * C::kStageBytes + (hh * D + d0) * 4);
+            Ls += lw * f;
+            a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
+          }
+        }
+        if (was_whole) {
+          const size_t orow = head0 + hh;
+          const float inv = Ls != 0.f ? p.v_scale / Ls : 0.f;
+          *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          if (d0 == 0)
+            p.lse[orow] = Ls != 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + (slot * G + hh) * D + d0) = a;
+          if (d0 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * G + hh)) = make_float2(M, Ls);
         }
       }
-    __syncthreads();
-    const size_t slot = 2 * static_cast<size_t>(cta) + (first ? 0 : 1);
-    constexpr int kQuads = D / 4;  // four-column groups of one head's row
-    for (int idx = tid; idx < G * kQuads; idx += C::kThreads) {
-      const int hh = idx / kQuads, d0 = (idx % kQuads) * 4;
-      float M = red_m[hh];
-#pragma unroll
-      for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * 16 + hh]);
-      float Ls = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float lw = red_l[w * 16 + hh];
-        if (lw != 0.f) {  // the warp had tokens; a NaN among their scores is a sum of NaN
-          const float f = fast_exp2(red_m[w * 16 + hh] - M);
-          const float4 x = *reinterpret_cast<const float4*>(
-              base + w * C::kRingBytes + ctl->idle[w] * C::kStageBytes + (hh * D + d0) * 4);
-          Ls += lw * f;
-          a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
-        }
-      }
-      if (was_whole) {
-        const size_t orow = head0 + hh;
-        const float inv = Ls != 0.f ? p.v_scale / Ls : 0.f;
-        *reinterpret_cast<uint2*>(p.o + orow * D + d0) =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (d0 == 0)
-          p.lse[orow] = Ls != 0.f ? (M + log2f(Ls)) * 0.69314718055994530942f : -INFINITY;
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * G + hh) * D + d0) = a;
-        if (d0 == 0)
-          *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * G + hh)) = make_float2(M, Ls);
-      }
+      fence_proxy_async_smem();  // the merge's plain writes, before the next segment's copies
+      __syncthreads();
     }
-    fence_proxy_async_smem();  // the merge's plain writes, before the next segment's copies
-    __syncthreads();
   }
 }
 
-// Joins the parts of contexts that several CTAs share, and writes the rows of empty ones. One
-// CTA per (kv head, sequence), or per query head; a thread takes four columns of one head, and
+// Joins the parts of contexts that several workers share, and writes the rows of empty ones. One
+// CTA per (kv head, sequence), per query head, or per worker (SOLO); a thread takes four columns of one head, and
 // where that leaves threads over, set s of them takes the parts s, s + sets, ...; the sets'
 // sums are added in order.
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256;  // at most
 
-template <int D>
+template <int D, bool SOLO>
 __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const DecodeFp4Params p) {
-  constexpr int kQuads = D / 4, kBatch = 8;
+  constexpr int kQuads = D / 4, kBatch = 4;
   __shared__ float2 sml[kCombineThreads];
   __shared__ float4 so[kCombineThreads];
-  const int H = p.join_heads, G = p.group;
-  const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
-  const int g = h0 / G, hg = h0 % G;  // kv head, first query head of its group
-  const int tid = static_cast<int>(threadIdx.x);
-  const Fp4Share<D> share(p, b, false);
-  const int nb = fp4_blocks(fp4_length(p, b, false));
-  const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
+  const int G = p.group, H = SOLO ? G : p.join_heads;
+  const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
+  size_t head0;  // first query head's row
+  int hg, slot0, c0, parts;  // its place in the group; first part's slot and worker; parts
+  auto empty = [&](size_t row, int heads) {  // O = 0, LSE = -inf
+    for (int i = tid; i < heads * kQuads; i += threads)
+      reinterpret_cast<uint2*>(p.o + row * D)[i] = make_uint2(0, 0);
+    for (int i = tid; i < heads; i += threads) p.lse[row + i] = -INFINITY;
+  };
   // Every CTA waits, those without work too: this kernel must not end before the first one.
-  if (nb == 0) {  // empty context: O = 0, LSE = -inf
+  if constexpr (SOLO) {
+    for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x))
+      if (fp4_length(p, b, false) == 0) empty(static_cast<size_t>(b) * p.Hq, p.Hq);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < H * kQuads; i += kCombineThreads)
-      reinterpret_cast<uint2*>(p.o + head0 * D)[i] = make_uint2(0, 0);
-    if (tid < H) p.lse[head0 + tid] = -INFINITY;
-    return;
+    const int4 join = __ldcg(p.joins + blockIdx.x);
+    if (join.z == 0) return;
+    head0 = static_cast<size_t>(join.x) * G, hg = 0, slot0 = join.y, parts = join.z;
+    c0 = slot0 >> 1;
+  } else {
+    const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
+    const int g = h0 / G;  // kv head
+    hg = h0 % G;
+    const Fp4Share<D, SOLO> share(p, b, false);
+    const int nb = fp4_blocks(fp4_length(p, b, false));
+    head0 = static_cast<size_t>(b) * p.Hq + h0;
+    if (nb == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      empty(head0, H);
+      return;
+    }
+    // The context's first unit, and those of its first and last block.
+    const int w = share.units(nb), u0 = share.before * p.Hkv + g * w;
+    c0 = share.worker_of(u0 + share.kStart);
+    parts = share.worker_of(u0 + w - 1) - c0 + 1;
+    // The first part is its worker's first segment only if that has no block of the context
+    // before.
+    slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (parts == 1) return;  // one worker held the whole context
   }
-  // The context's first unit, and those of its first and last block.
-  const int w = share.units(nb), u0 = share.before * p.Hkv + g * w;
-  const int c0 = share.cta_of(u0 + share.kStart);
-  const int c1 = share.cta_of(u0 + w - 1);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 == c1) return;  // one CTA held the whole context
-  // The first part is its CTA's first segment only if the CTA has no block of the context before.
-  const int slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
-  const int parts = c1 - c0 + 1;
   const int items = H * kQuads;
-  const int sets = imax(1, kCombineThreads / items);
-  const int set = items < kCombineThreads ? tid / items : 0;
-  for (int it0 = 0; it0 < items; it0 += kCombineThreads) {
-    const int item = it0 + (items < kCombineThreads ? tid % items : tid);
+  const int sets = imax(1, imin(threads / items, parts));
+  const int set = items < threads ? tid / items : 0;
+  for (int it0 = 0; it0 < items; it0 += threads) {
+    const int item = it0 + (items < threads ? tid % items : tid);
     const bool here = item < items && set < sets;
     const int hh = item / kQuads, quad = item % kQuads;
     float M = -INFINITY, Ls = 0.f;
