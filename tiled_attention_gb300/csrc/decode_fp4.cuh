@@ -41,14 +41,15 @@
 // by contexts there, 1000 sequences x 8 kv heads took 31 us longer). No counters, so no memset.
 //
 // CTA: four warps; warp w takes stages w, w + 4, ... of a segment (64 tokens, 128 at d = 64), or
-// all stages of its own segments, through a ring of its own in shared memory: it brings the next stage in with bulk copies while
-// it works on one, so no warp waits for another before a segment's end.
+// all stages of its own segments, through a ring of its own in shared memory: it brings the next
+// stage in with bulk copies while it works on one, so no warp waits for another before a
+// segment's end.
 //
 // Measured (GB300, device time): 32 sequences of 1K-16K tokens, 8 kv heads of 4 query heads,
 // d = 128, 313 MB: 61 us, 5.1 TB/s, 76 % of the copy rate; 48 sequences of 1-32K, 4 kv heads of
 // 16, d = 64, pages of 16, 216 MB: 73 us; one sequence of 16K: 13 us. Bound by issue: 224
 // instructions of a warp per 16 tokens at d = 128, of which 64 convert and 64 scale at half
-// rate; computing alone takes 55 us on the first, streaming alone 54, ~11 of each start-up
+// rate; computing alone takes 54 us on the first, streaming alone 53, ~10 of each start-up
 // and joining.
 #pragma once
 
