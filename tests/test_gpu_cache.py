@@ -1130,3 +1130,33 @@ def test_two_decodes_at_once():
     b.check()
     want, mag = r.want("k", bt.pos)
     close(f64(kp)[bt.phys, :, bt.slot], want, mag)
+
+
+def test_many_contexts_at_once_and_replayed():
+    """Two decodes of many contexts on two streams at once, each with its own workspace; then one
+    captured, its lengths halved in place (some to nothing) and replayed."""
+    rng = np.random.default_rng(34)
+    a = Decode(rng, many(rng, 4, 300, 4000), 16, 4, 128, 128)
+    b = Decode(rng, many(rng, 2, 200, 900), 32, 2, 64, 16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a.run(streams[0])
+        b.run(streams[1])
+    torch.cuda.synchronize()
+    assert attn.attn_get_status() == 0
+    a.check()
+    b.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        a.run(streams[0])
+    a.lens = np.where(rng.random(len(a.lens)) < 0.2, 0, a.lens // 2)
+    a.cu.copy_(dev(np.concatenate([[0], np.cumsum(a.lens)]), np.int32))
+    a.o.fill_(float("nan"))
+    a.ws.fill_(0x5A)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert attn.attn_get_status() == 0
+    a.check()
