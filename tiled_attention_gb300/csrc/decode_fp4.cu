@@ -113,7 +113,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   if (num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 65535 || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
-  const long long units = (static_cast<long long>(N) + 127) / 128 + 8;  // of one context, at most
+  const long long units = (static_cast<long long>(N) + 63) / 64 + 8;  // of one context, at most
   if (B > 65535 || static_cast<long long>(B) * Hkv >= (1ll << 31) / units)
     return fail(ATTN_ERR_UNSUPPORTED, "decode batch too large");
   const Fp4Layout L = fp4_layout(Hq, Hkv, d);
@@ -153,7 +153,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   // From as many contexts (a sequence and kv head each) on as the GPU holds CTAs, a warp is a
   // worker; below, a CTA. Measured with warps and with CTAs: 64 sequences of 1K-8K tokens x 8 kv
-  // heads 66 and 68 us, 256 of 1K 64 and 76, 1000 of 20-400 81 and 169; 24 of 1K-16K 51 and 49,
+  // heads 66 and 68 us, 256 of 1K 64 and 76, 1000 of 20-400 79 and 169; 24 of 1K-16K 51 and 49,
   // one of 16K 33 and 13.
   const bool solo = static_cast<long long>(B) * Hkv >= L.slots;
   const cudaError_t e = solo ? launch<true>(p, d, stream) : launch<false>(p, d, stream);

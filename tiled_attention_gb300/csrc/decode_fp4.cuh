@@ -23,7 +23,7 @@
 //     the head's scale. P in f16: 2^(s - m + 7), at most 2^15, where m trails the running
 //     max by less than 8; f16 keeps 11 bits of it where bf16 would keep 8.
 //
-// Work: the contexts are cut into 128-token blocks, numbered over sequence, kv head and
+// Work: the contexts are cut into blocks (of 128 tokens; of a stage where SOLO), numbered over sequence, kv head and
 // position, with a few units more at each context's start for the cost of beginning it, and
 // shared out evenly over the workers in that order: every worker has the same work whatever the
 // lengths are, and finds its range from cu_seqlens alone. A worker is a CTA where contexts are
@@ -58,8 +58,6 @@
 #include "sched.h"
 
 namespace ta {
-
-constexpr int kFp4Block128 = 128;  // tokens per block of the work list
 
 struct DecodeFp4Params {
   const uint4* q;        // bf16 [B, Hq, 1, D]
@@ -363,35 +361,35 @@ __device__ __forceinline__ int fp4_length(const DecodeFp4Params& p, int b, bool 
   return 0;
 }
 
-__device__ __forceinline__ int fp4_blocks(int L) { return (L + kFp4Block128 - 1) / kFp4Block128; }
-
 // How the blocks are shared out. Every warp of both kernels works it out by itself, from
 // cu_seqlens alone: a context counts its blocks and kStart units before them for what beginning
 // it costs, and worker i of n takes an even share of the units, the first r workers q + 1, the
 // others q. A share that ends among a context's kStart units holds none of it. Cutting small
 // batches into equal parts of whole rounds of the four warps instead, a CTA a part, so that no
 // CTA begins two contexts, gained 0.6 us on one sequence of 16K tokens (13.7 us) and lost 0.5 to
-// 1 us on one of 700, one of 4K and four of 1K to 16K. Warps as workers: with 0, 1 and 2 units
-// 1000 sequences of 20-400 tokens x 8 kv heads take 87, 83 and 88 us, 256 of 1K 64.3, 65.0 and
-// 64.8.
+// 1 us on one of 700, one of 4K and four of 1K to 16K. Warps as workers, with blocks of a stage:
+// with 1, 2 and 3 units 1000 sequences of 20-400 tokens x 8 kv heads take 78.7, 79.3 and 80.2 us,
+// 512 of 200-1000 81.0, 82.1 and 84.4 (blocks of 128 tokens at d = 128 and one unit: 81.9, 83.4).
 template <int D, bool SOLO>
 struct Fp4Share {
   static constexpr int kStart = SOLO ? 1 : DecodeFp4Start<D>::kUnits;
+  static constexpr int kTok = SOLO ? DecodeFp4Cfg<D, 1>::kStage : 128;  // tokens of a block
   int total;    // units of one kv head, all sequences
   int before;   // those of the sequences before `upto`
   int n, q, r;
   int w0;       // units of sequence `lane`
 
+  __device__ __forceinline__ static int blocks(int L) { return (L + kTok - 1) / kTok; }
   __device__ __forceinline__ static int units(int nb) { return nb > 0 ? nb + kStart : 0; }
 
   __device__ __forceinline__ Fp4Share(const DecodeFp4Params& p, int upto, bool report) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    w0 = lane < p.B ? units(fp4_blocks(fp4_length(p, lane, report))) : 0;
+    w0 = lane < p.B ? units(blocks(fp4_length(p, lane, report))) : 0;
     int all = w0, ahead = lane < upto ? w0 : 0;
     for (int b0 = lane + 32; b0 < p.B; b0 += 128) {
 #pragma unroll
       for (int b = b0; b < b0 + 128; b += 32) {  // four loads at a time
-        const int w = b < p.B ? units(fp4_blocks(fp4_length(p, b, report))) : 0;
+        const int w = b < p.B ? units(blocks(fp4_length(p, b, report))) : 0;
         all += w;
         if (b < upto) ahead += w;
       }
@@ -418,7 +416,7 @@ struct Fp4Share {
     int run = 0;
     for (int b0 = 0; b0 < p.B;) {
       const int b = b0 + lane;
-      const int w = b0 == 0 ? w0 : b < p.B ? units(fp4_blocks(fp4_length(p, b, false))) : 0;
+      const int w = b0 == 0 ? w0 : b < p.B ? units(blocks(fp4_length(p, b, false))) : 0;
       int sum = w;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -438,7 +436,7 @@ struct Fp4Share {
         int four = 0;
 #pragma unroll
         for (int c = b0 + lane; c < b0 + lane + 128; c += 32)
-          four += units(c < p.B ? fp4_blocks(fp4_length(p, c, false)) : 0);
+          four += units(c < p.B ? blocks(fp4_length(p, c, false)) : 0);
         four = run + __reduce_add_sync(0xffffffffu, four);
         if (u < four * p.Hkv) break;
         run = four;
@@ -568,11 +566,11 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   };
   auto open = [&]() {  // false: the range holds no more blocks
     if (u >= end) return false;
-    int L = fp4_length(p, b, false), nb = fp4_blocks(L), w = share.units(nb);
+    int L = fp4_length(p, b, false), nb = share.blocks(L), w = share.units(nb);
     while (u >= seq_u + w * p.Hkv) {  // the sequence is done: on to the next that has blocks
       seq_u += w * p.Hkv;
       L = fp4_length(p, ++b, false);
-      nb = fp4_blocks(L);
+      nb = share.blocks(L);
       w = share.units(nb);
     }
     g = (u - seq_u) / w;
@@ -588,10 +586,10 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
     whole = nblk == nb;
     begins = blk0 || whole ? -1 : seq_u + (g + 1) * w - 1;
     // Stages of the segment's tokens [t0, t1): this warp takes stage warp, warp + 4, ...
-    t0 = blk0 * kFp4Block128;
-    t1 = imin(t0 + nblk * kFp4Block128, L);
+    t0 = blk0 * share.kTok;
+    t1 = imin(t0 + nblk * share.kTok, L);
     n = aborted ? 0 : (t1 - t0 - tok_w + kHop - 1) / kHop;
-    half = 0;
+    half = t0 & C::kStage ? flip : 0;  // flip is 0 where the page holds one stage
     row = p.table + static_cast<size_t>(b) * p.max_pages;
     src_g = src0 + static_cast<size_t>(g) * blk_bytes;
     if (n > 0) {
@@ -835,7 +833,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const Deco
     const int g = h0 / G;  // kv head
     hg = h0 % G;
     const Fp4Share<D, SOLO> share(p, b, false);
-    const int nb = fp4_blocks(fp4_length(p, b, false));
+    const int nb = share.blocks(fp4_length(p, b, false));
     head0 = static_cast<size_t>(b) * p.Hq + h0;
     if (nb == 0) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
