@@ -263,7 +263,7 @@ size_t attn_noalloc_scratch_bytes(void);
  *           where q, k and v share one buffer. q or k may be NULL (not both): it is left out.
  * q_out, k_out bf16 [total / N, H, N, d]: token t is row t % N of block t / N. N = 1 gives
  *           decode's [B, H, 1, d]; N = total the packed [1, H, total, d]; a prompt length N
- *           the dense [B, H, N, d]. Must not overlap q or k (ATTN_ERR_INVALID).
+ *           the dense [B, H, N, d]. Must not overlap q, k or one another (ATTN_ERR_INVALID).
  * total     tokens, a multiple of N. Hq, Hkv: any counts; d 64 or 128.
  * q_weight, k_weight fp32 [d], each may be NULL. eps >= 0 (read if a weight is given).
  * cos_sin   fp32 [max_pos, rot_dim]: of every position rot_dim/2 cosines, then rot_dim/2 sines.
@@ -293,7 +293,8 @@ int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int t
  *           may be NULL (then q_out, Hq and q_weight are not used).
  * q_out     bf16 [total_q / N, Hq, N, d]: N = 1 for decode's [B, Hq, 1, d], N = total_q for
  *           chunked prefill's [1, Hq, total_q, d]. Must not overlap q, k or v.
- * k_pool, v_pool bf16 [num_pages, Hkv, page_size, d].
+ * k_pool, v_pool bf16 [num_pages, Hkv, page_size, d]. Must not overlap one another, q, k, v or
+ *           q_out (ATTN_ERR_INVALID).
  * cu_seqlens_q int32 [B+1]: cu[0] = 0, nondecreasing, cu[B] <= total_q. Rows from cu[B] on belong
  *           to no sequence and nothing is written for them (a padded batch of a captured graph).
  * seqlens_k int32 [B]: Lq_b <= seqlens_k[b] <= max_pages * page_size.
@@ -350,7 +351,7 @@ int attn_append_paged_fp4(const void *q, const void *k, const void *v, void *q_o
  * max_pages * page_size, else ATTN_ERR_SEQLENS and sequence b is skipped): slots of the last
  * page past it are written as zeros, whatever the pool holds there; pages past it are neither
  * read nor written. An entry outside [0, num_pages) sets ATTN_ERR_BOUNDS and its page is
- * skipped. pool and dst 16-byte aligned; B <= 65535. Asynchronous on `stream`.
+ * skipped. pool and dst 16-byte aligned and apart; B <= 65535. Asynchronous on `stream`.
  */
 int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
                           const int32_t *block_table, const int32_t *seqlens, int B,

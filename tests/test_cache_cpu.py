@@ -84,6 +84,29 @@ def test_norm_rope_refusals(kw, code):
     assert attn.last_error()
 
 
+FAR = _Ptr(1 << 30)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _norm_rope(k_out=_Ptr((1 << 24) + 4096)),  # outputs into one another
+    lambda: _append(False, k_pool=FAR, v_pool=FAR),
+    lambda: _append(True, k_pool=FAR, v_pool=FAR),
+    # K's pool: 8 pages x 2 heads x 16 tokens of 256 or 72 bytes; V's begins in its last row
+    lambda: _append(False, k_pool=FAR, v_pool=_Ptr((1 << 30) + 256 * 255)),
+    lambda: _append(True, k_pool=FAR, v_pool=_Ptr((1 << 30) + 72 * 254)),
+    lambda: _append(False, k_pool=OUT, v_pool=FAR),  # q_out
+    lambda: _append(True, k_pool=FAR, v_pool=OUT),
+    lambda: _append(False, k_pool=T, v_pool=FAR),  # an input
+    lambda: _append(True, k_pool=FAR, v_pool=T),
+    lambda: _unpack(),
+    lambda: _unpack(dst=FAR, pool=_Ptr((1 << 30) + 2 * 4 * 2 * 16 * 256 - 16)),
+    lambda: _unpack(pool=FAR, dst=_Ptr((1 << 30) + 8 * 2 * 16 * 72 - 16)),
+])
+def test_overlapping_outputs_are_refused(call):
+    assert call() == INVALID
+    assert "overlap" in attn.last_error()
+
+
 def test_norm_rope_without_tokens_is_a_no_op():
     assert _norm_rope(total=0) == attn.ATTN_OK
     assert _norm_rope(total=0, q=None, k=None, cos_sin=None) == attn.ATTN_OK

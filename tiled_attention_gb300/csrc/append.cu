@@ -79,9 +79,11 @@ int row_params(RowParams* p, const void* q, const void* k, const void* v, void* 
   return ATTN_OK;
 }
 
+// row_bytes: of one token of one kv head in a pool.
 int cache_params(RowParams* p, const void* k, const void* v, void* k_pool, void* v_pool, int B,
                  const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
-                 const int32_t* block_table, int max_pages, int page_size, int num_pages) {
+                 const int32_t* block_table, int max_pages, int page_size, int num_pages, int d,
+                 int row_bytes) {
   if (B < 0) return fail(ATTN_ERR_INVALID, "need B >= 0");
   if (!page_size_ok(page_size))
     return fail(ATTN_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128)", page_size);
@@ -95,6 +97,15 @@ int cache_params(RowParams* p, const void* k, const void* v, void* k_pool, void*
   if (static_cast<long long>(num_pages) * p->heads[1] >= (1ll << 31) ||
       static_cast<long long>(max_pages) * page_size >= (1ll << 31))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or block table too large");
+  const size_t n = static_cast<size_t>(num_pages) * p->heads[1] * page_size * row_bytes;
+  const size_t out_bytes = p->in[0] ? static_cast<size_t>(p->total) * p->heads[0] * d * 2 : 0;
+  bool shared = overlap(k_pool, n, v_pool, n);
+  for (const void* pool : {k_pool, v_pool}) {
+    shared |= overlap(pool, n, p->out[0], out_bytes);
+    for (int i = 0; i < 3; ++i)
+      shared |= overlap(pool, n, p->in[i], rows_bytes(p->total, p->heads[i], d, p->stride[i] / 2));
+  }
+  if (shared) return fail(ATTN_ERR_INVALID, "a pool overlaps the other or a tensor of rows");
   p->pool[0] = static_cast<uint8_t*>(k_pool);
   p->pool[1] = static_cast<uint8_t*>(v_pool);
   p->cu = cu_seqlens_q;
@@ -167,6 +178,8 @@ int attn_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int t
     if (overlap(k_out, n, q, rows_bytes(total, Hq, d, q_stride)) ||
         overlap(k_out, n, k, rows_bytes(total, Hkv, d, k_stride)))
       return fail(ATTN_ERR_INVALID, "an output overlaps an input");
+    if (q && overlap(k_out, n, q_out, static_cast<size_t>(total) * Hq * d * 2))
+      return fail(ATTN_ERR_INVALID, "q_out and k_out overlap");
   }
   p.out[1] = static_cast<uint8_t*>(k_out);
   p.positions = positions;
@@ -188,7 +201,7 @@ int attn_append_paged(const void* q, const void* k, const void* v, void* q_out, 
                       q_weight, k_weight, eps, cos_sin, max_pos, rot_dim, interleaved, 16);
   if (rc) return rc;
   rc = cache_params(&p, k, v, k_pool, v_pool, B, cu_seqlens_q, seqlens_k, block_table, max_pages,
-                    page_size, num_pages);
+                    page_size, num_pages, d, 2 * d);
   if (rc) return rc;
   if (B == 0 || total_q == 0) return ATTN_OK;  // no new tokens
   return launch_rows<kCacheBf16>(p, d, stream);
@@ -214,7 +227,7 @@ int attn_append_paged_fp4(const void* q, const void* k, const void* v, void* q_o
                       interleaved ? 16 : 32);
   if (rc) return rc;
   rc = cache_params(&p, k, v, k_pool, v_pool, B, cu_seqlens_q, seqlens_k, block_table, max_pages,
-                    page_size, num_pages);
+                    page_size, num_pages, d, fp4_row_bytes(d));
   if (rc) return rc;
   if (B == 0 || total_q == 0) return ATTN_OK;
   p.inv_scale[0] = 1.f / k_scale;
@@ -241,6 +254,10 @@ int attn_unpack_pages_fp4(const void* pool, void* dst, float pool_scale,
   if (B > 65535 || static_cast<long long>(max_pages) * page_size >= (1ll << 31) ||
       static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 32768)
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or block table too large");
+  const size_t rows = static_cast<size_t>(Hkv) * page_size;
+  if (overlap(pool, rows * num_pages * fp4_row_bytes(d), dst,
+              rows * B * static_cast<size_t>(max_pages) * d * 2))
+    return fail(ATTN_ERR_INVALID, "dst overlaps the pool");
   UnpackParams p{};
   int rc = status_ptr(&p.status);
   if (rc) return rc;
