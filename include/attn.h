@@ -372,6 +372,7 @@ int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
  *           scale of a key in the context, makes the rows it meets NaN.
  * workspace of at least attn_workspace_bytes_fp4(...) bytes (may be NULL when that is 0); contents
  *           need not be initialised; concurrent calls need separate ones.
+ * o, lse and workspace must not overlap one another or an input, q among them (ATTN_ERR_INVALID).
  */
 int attn_fwd_paged_decode_fp4(const void *q, const void *k, const void *v, void *o, float *lse,
                               int B, int Hq, int Hkv, int N, int d, float scale, float k_scale,

@@ -241,6 +241,54 @@ def test_decode_fp4_empty_is_a_no_op():
     assert _decode(N=0) == attn.ATTN_OK
 
 
+class _Bytes(_Ptr):
+    """A stand-in with a size, for the workspace."""
+
+    def __init__(self, addr, n):
+        super().__init__(addr)
+        self.n = n
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
+
+
+def _decode_apart(**kw):
+    """A decode whose tensors lie apart: q, K, V, o, lse, cu, table and the workspace at 1 to 8
+    times 4 GB. B = 2, Hq = 4, Hkv = 2, d = 128, 8 pages of 64: q and o 2048 bytes, lse 32,
+    pools 73728, cu 12, the table's 1563 columns 12504."""
+    ws = attn.attn_workspace_bytes_fp4(2, 4, 2, 100000, 128)
+    a = {n: _Ptr(i << 32) for i, n in enumerate(("q", "k", "v", "o", "lse", "cu_seqlens",
+                                                 "block_table"), 1)}
+    a["workspace"] = _Bytes(8 << 32, ws)
+    a.update(kw)
+    return _decode(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(o=_Ptr(1 << 32)),  # q's place
+    dict(o=_Ptr((1 << 32) + 2032)),  # the end of q
+    dict(lse=_Ptr((1 << 32) + 1024)),
+    dict(lse=_Ptr((1 << 32) - 16)),
+    dict(o=_Ptr((2 << 32) + 73712)),  # the end of K
+    dict(lse=_Ptr(3 << 32)),
+    dict(lse=_Ptr((4 << 32) + 2032)),  # the end of o
+    dict(o=_Ptr(5 << 32)),
+    dict(o=_Ptr((6 << 32) - 2032)),  # cu_seqlens
+    dict(lse=_Ptr((7 << 32) + 12496)),  # the end of the table
+    dict(q=_Ptr((8 << 32) + 4096)),  # the workspace
+    dict(o=_Ptr((8 << 32) + 4096)),
+    dict(lse=_Ptr((8 << 32) - 16)),
+    dict(v=_Ptr((8 << 32) - 73712)),
+    dict(block_table=_Ptr((8 << 32) - 12496)),
+])
+def test_decode_fp4_overlaps_are_refused(kw):
+    assert _decode_apart(**kw) == INVALID
+    assert "overlap" in attn.last_error()
+
+
 def test_decode_fp4_workspace():
     need = attn.attn_workspace_bytes_fp4(32, 32, 8, 16384, 128)
     # two partial rows of 4 heads a resident CTA, O and (max, sum): the batch and the contexts

@@ -787,6 +787,38 @@ def test_decode_fp4_all_empty():
     w.check()
 
 
+def test_decode_fp4_overlaps_are_refused_and_neighbours_are_not():
+    """Outputs into queries, one another or the workspace are refused and nothing is written;
+    tensors that end where the next begins, as in one arena, are served."""
+    rng = np.random.default_rng(3500)
+    w = Decode(rng, [300, 0, 77], 8, 2, 128, 64)
+    q, n = w.q, w.q.numel() * 2  # bytes, a multiple of 16; lse: 3 x 8 floats
+    arena = torch.full((n + n + 96 + w.ws.numel(),), 0x5A, dtype=torch.uint8, device="cuda")
+
+    def rows(at):
+        return arena[at:at + n].view(torch.bfloat16).view(q.shape)
+
+    def lse(at):
+        return arena[at:at + 96].view(torch.float32).view(3, 8)
+
+    ws = arena[2 * n + 96:]
+    w.q, w.o, w.lse, w.ws = rows(0), rows(n), lse(2 * n), ws
+    w.q.copy_(q)
+    w.run()
+    assert status() == 0
+    w.check()
+    assert torch.equal(w.q, q)
+    was = arena.clone()
+    for bad in (dict(o=rows(0)), dict(o=rows(n - 16)), dict(lse=lse(0)), dict(lse=lse(2 * n - 16)),
+                dict(o=rows(2 * n)), dict(lse=lse(2 * n + 16)), dict(ws=arena[2 * n + 80:])):
+        a = dict(o=w.o, lse=w.lse, ws=ws) | bad
+        rc = attn.attn_fwd_paged_decode_fp4(w.q, w.k, w.v, a["o"], a["lse"], 3, 8, 2, w.N, 128,
+                                            w.scale, w.ks, w.vs, w.cu, w.d_table, 64, w.bt.num,
+                                            a["ws"])
+        assert rc == attn.ATTN_ERR_INVALID and "overlap" in attn.last_error()
+    assert status() == 0 and torch.equal(arena, was)
+
+
 @pytest.mark.parametrize("q_amp,ks,vs", [(0.0, 1.0, 1.0), (2.0 ** -60, 1.0, 1.0), (2.0 ** 60, 2.0 ** -60, 1.0),
                                          (30.0, 0.25, 3e-20), (1.0, 1e-20, 1e20), (8.0, 0.25, 1.0)])
 def test_decode_fp4_magnitudes(q_amp, ks, vs):

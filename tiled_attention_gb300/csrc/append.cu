@@ -16,11 +16,6 @@ size_t rows_bytes(int total, int heads, int d, int64_t stride) {
                    : 0;
 }
 
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && an && bn && x < y + bn && y < x + an;
-}
-
 // Checks and fields common to the row entry points. Sizes of absent tensors (null q or k) are
 // passed as 0 heads.
 int row_params(RowParams* p, const void* q, const void* k, const void* v, void* q_out, int Hq,

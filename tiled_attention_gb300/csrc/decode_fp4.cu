@@ -119,6 +119,19 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   const Fp4Layout L = fp4_layout(Hq, Hkv, d);
   if (!workspace || workspace_bytes < L.total || !aligned16(workspace))
     return fail(ATTN_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned)", L.total);
+  // Rows are written while other workers still read queries, lengths and pages.
+  const int max_pages = (N + page_size - 1) / page_size;
+  const size_t rows = static_cast<size_t>(B) * Hq;
+  const size_t pool = static_cast<size_t>(num_pages) * Hkv * page_size * fp4_row_bytes(d);
+  const struct { const void* x; size_t bytes; } out[3] = {
+      {o, rows * d * 2}, {lse, rows * sizeof(float)}, {workspace, L.total}}, in[5] = {
+      {q, rows * d * 2}, {k, pool}, {v, pool}, {cu_seqlens, sizeof(int32_t) * (B + size_t(1))},
+      {block_table, sizeof(int32_t) * B * static_cast<size_t>(max_pages)}};
+  for (int i = 0; i < 3; ++i) {
+    bool shared = overlap(out[i].x, out[i].bytes, out[(i + 1) % 3].x, out[(i + 1) % 3].bytes);
+    for (const auto& t : in) shared |= overlap(out[i].x, out[i].bytes, t.x, t.bytes);
+    if (shared) return fail(ATTN_ERR_INVALID, "o, lse or workspace overlaps another tensor");
+  }
   DecodeFp4Params p{};
   int rc = status_ptr(&p.status);
   if (rc) return rc;
@@ -136,7 +149,7 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.max_pages = (N + page_size - 1) / page_size;
+  p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.slots = L.slots;
   p.fine = static_cast<int>(std::min<long long>(32ll * B * Hkv, L.slots));
