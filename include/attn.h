@@ -364,7 +364,9 @@ int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
  * (v_scale); products accumulate in fp32, softmax weights enter the second product in f16.
  * q, o      bf16 [B, Hq, 1, d]; lse fp32 [B, Hq], natural log.
  * k, v      4-bit pools (16-byte aligned). Slots past a sequence's context may hold anything.
- * N         the longest context (block_table has ceil(N / page_size) columns); N <= 2^30.
+ * N         the longest context (block_table has ceil(N / page_size) columns); N <= 2^30. With
+ *           N = 0 every context is empty: O = 0, LSE = -inf. q, k, v, block_table and workspace
+ *           are not used then and may be NULL.
  * cu_seqlens, block_table, num_pages, page_size, Hq, Hkv, scale as for attn_fwd's PAGED_DECODE:
  *           at most 16 query heads per kv head; a bad length gives O = 0, LSE = -inf and
  *           ATTN_ERR_SEQLENS; a table entry outside the pool sets ATTN_ERR_BOUNDS and its page

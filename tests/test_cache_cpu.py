@@ -289,6 +289,13 @@ def test_decode_fp4_overlaps_are_refused(kw):
     assert "overlap" in attn.last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(o=None), dict(lse=None), dict(cu_seqlens=None), dict(o=ODD)])
+def test_decode_fp4_without_keys_still_has_rows_to_write(kw):
+    """N = 0: the sequences are empty, but their rows and lengths are there."""
+    assert _decode(N=0, **kw) == INVALID
+    assert attn.last_error()
+
+
 def test_decode_fp4_workspace():
     need = attn.attn_workspace_bytes_fp4(32, 32, 8, 16384, 128)
     # two partial rows of 4 heads a resident CTA, O and (max, sum): the batch and the contexts

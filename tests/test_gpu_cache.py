@@ -819,6 +819,56 @@ def test_decode_fp4_overlaps_are_refused_and_neighbours_are_not():
     assert status() == 0 and torch.equal(arena, was)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(3, 4, 2, 128), (700, 2, 1, 64), (40, 64, 4, 128),
+                                        (200, 32, 8, 64)])
+def test_decode_fp4_without_keys(B, Hq, Hkv, d):
+    """N = 0: every sequence of the batch is empty, and its rows are written all the same, eagerly
+    and in a replayed graph, without pools, table or workspace; a length that is not 0 is
+    reported."""
+    assert attn.attn_workspace_bytes_fp4(B, Hq, Hkv, 0, d) == 0
+    o = torch.full((B, Hq, 1, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, Hq), float("nan"), device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+
+    def run():
+        rc = attn.attn_fwd_paged_decode_fp4(None, None, None, o, lse, B, Hq, Hkv, 0, d, 0.1, 1.0,
+                                            1.0, cu, None, 16, 0)
+        assert rc == 0, attn.last_error()
+
+    def check():
+        assert not o.view(torch.int16).any() and (lse == -np.inf).all()
+
+    run()
+    assert status() == 0
+    check()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        run()
+    o.fill_(float("nan")), lse.fill_(float("nan"))
+    g.replay()
+    assert status() == 0
+    check()
+    cu[B] = 5
+    o.fill_(float("nan")), lse.fill_(float("nan"))
+    run()
+    assert status() == attn.ATTN_ERR_SEQLENS
+    check()
+
+
+def test_decode_fp4_without_keys_takes_the_tensors_of_a_batch():
+    """The same with the tensors that a serving loop passes anyway: neither q nor the workspace is
+    touched."""
+    rng = np.random.default_rng(3150)
+    w = Decode(rng, [0] * 500, 4, 2, 128, 16)
+    q, ws = w.q.clone(), w.ws.clone()
+    w.N = 0
+    w.run()
+    assert status() == 0
+    w.check()
+    assert torch.equal(w.q, q) and torch.equal(w.ws, ws)
+
+
 @pytest.mark.parametrize("q_amp,ks,vs", [(0.0, 1.0, 1.0), (2.0 ** -60, 1.0, 1.0), (2.0 ** 60, 2.0 ** -60, 1.0),
                                          (30.0, 0.25, 3e-20), (1.0, 1e-20, 1e20), (8.0, 0.25, 1.0)])
 def test_decode_fp4_magnitudes(q_amp, ks, vs):

@@ -21,6 +21,14 @@ int fp4_slots(int d, int group) {
 
 constexpr int kWorkers = DecodeFp4Cfg<64, 1>::kWarps;  // of a CTA, at most
 
+// Whether this host sees no device at all.
+bool no_device() {
+  int n = 0;
+  const cudaError_t e = cudaGetDeviceCount(&n);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver;
+}
+
 struct Fp4Layout {
   size_t part_ml, joins, total;
   int slots;
@@ -105,27 +113,33 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   if (group > kMaxDecodeGroup)
     return fail(ATTN_ERR_UNSUPPORTED, "query heads per kv head %d (at most %d)", group,
                 kMaxDecodeGroup);
-  if (B == 0 || N == 0) return ATTN_OK;  // nothing to compute
-  if (!q || !k || !v || !o || !lse || !cu_seqlens || !block_table)
+  if (B == 0) return ATTN_OK;  // no rows
+  // N = 0: every context is empty, and its rows are still the caller's to have: O = 0, LSE =
+  // -inf. They come of the lengths alone; q, the pools, the table and the workspace are not used.
+  const bool keys = N > 0;
+  if (!o || !lse || !cu_seqlens || (keys && (!q || !k || !v || !block_table)))
     return fail(ATTN_ERR_INVALID, "null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
-  if (num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
+  if (keys && num_pages <= 0) return fail(ATTN_ERR_INVALID, "num_pages %d", num_pages);
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 65535 || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
   const long long units = (static_cast<long long>(N) + 63) / 64 + 8;  // of one context, at most
   if (B > 65535 || static_cast<long long>(B) * Hkv >= (1ll << 31) / units)
     return fail(ATTN_ERR_UNSUPPORTED, "decode batch too large");
+  if (!keys && no_device()) return ATTN_OK;  // nor are there device rows to fill
   const Fp4Layout L = fp4_layout(Hq, Hkv, d);
-  if (!workspace || workspace_bytes < L.total || !aligned16(workspace))
+  if (keys && (!workspace || workspace_bytes < L.total || !aligned16(workspace)))
     return fail(ATTN_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned)", L.total);
   // Rows are written while other workers still read queries, lengths and pages.
   const int max_pages = (N + page_size - 1) / page_size;
   const size_t rows = static_cast<size_t>(B) * Hq;
-  const size_t pool = static_cast<size_t>(num_pages) * Hkv * page_size * fp4_row_bytes(d);
+  const size_t pool =
+      keys ? static_cast<size_t>(num_pages) * Hkv * page_size * fp4_row_bytes(d) : 0;
   const struct { const void* x; size_t bytes; } out[3] = {
-      {o, rows * d * 2}, {lse, rows * sizeof(float)}, {workspace, L.total}}, in[5] = {
-      {q, rows * d * 2}, {k, pool}, {v, pool}, {cu_seqlens, sizeof(int32_t) * (B + size_t(1))},
+      {o, rows * d * 2}, {lse, rows * sizeof(float)}, {workspace, keys ? L.total : 0}}, in[5] = {
+      {q, keys ? rows * d * 2 : 0}, {k, pool}, {v, pool},
+      {cu_seqlens, sizeof(int32_t) * (B + size_t(1))},
       {block_table, sizeof(int32_t) * B * static_cast<size_t>(max_pages)}};
   for (int i = 0; i < 3; ++i) {
     bool shared = overlap(out[i].x, out[i].bytes, out[(i + 1) % 3].x, out[(i + 1) % 3].bytes);
@@ -135,7 +149,6 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   DecodeFp4Params p{};
   int rc = status_ptr(&p.status);
   if (rc) return rc;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const uint4*>(q);
   p.k = static_cast<const uint8_t*>(k);
   p.v = static_cast<const uint8_t*>(v);
@@ -143,9 +156,12 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.table = block_table;
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
-  p.joins = reinterpret_cast<int4*>(ws + L.joins);
+  if (keys) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
+    p.joins = reinterpret_cast<int4*>(ws + L.joins);
+  }
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -168,7 +184,8 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   // worker; below, a CTA. Measured with warps and with CTAs: 64 sequences of 1K-8K tokens x 8 kv
   // heads 66 and 68 us, 256 of 1K 64 and 76, 1000 of 20-400 79 and 169; 24 of 1K-16K 51 and 49,
   // one of 16K 33 and 13.
-  const bool solo = static_cast<long long>(B) * Hkv >= L.slots;
+  // Without keys CTAs: they find no work and leave the workspace alone, warps would clear `joins`.
+  const bool solo = keys && static_cast<long long>(B) * Hkv >= L.slots;
   const cudaError_t e = solo ? launch<true>(p, d, stream) : launch<false>(p, d, stream);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   return ATTN_OK;
