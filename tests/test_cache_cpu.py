@@ -317,6 +317,44 @@ def test_tensors_of_two_devices_are_refused():
         assert e.value.code == INVALID and "device" in str(e.value)
 
 
+CALLS = [lambda t, **kw: _norm_rope(q=t, k=t, q_out=t, k_out=t, cos_sin=t, **kw),
+         lambda t, **kw: _append(False, **_rows_on(t), **kw),
+         lambda t, **kw: _append(True, **_rows_on(t), **kw),
+         lambda t, **kw: _unpack(pool=t, dst=t, block_table=t, seqlens=t, **kw),
+         lambda t, **kw: _decode(q=t, k=t, v=t, o=t, lse=t, cu_seqlens=t, block_table=t, **kw)]
+
+
+def _rows_on(t):
+    return {n: t for n in ("q", "k", "v", "q_out", "k_pool", "v_pool", "cos_sin", "cu_seqlens_q",
+                           "seqlens_k", "block_table")}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_host_tensors_are_refused_on_a_given_stream_too(call):
+    """All of a call's tensors in host memory are of one device, but not of one to launch on."""
+    with pytest.raises(attn.AttnError) as e:
+        call(_Ptr(device=-1), stream=0)
+    assert e.value.code == INVALID and "host memory" in str(e.value)
+
+
+class _Stream:
+    cuda_stream = 0
+
+    def __init__(self, device_index):
+        self.device_index = device_index
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("tensors,stream", [(1, 0), (1, _Stream(1)), (1, _Stream(0)),
+                                            (0, _Stream(1))])
+def test_another_device_than_the_current_one_is_refused(call, tensors, stream, monkeypatch):
+    """The library launches on the current device, here 0, whatever the stream is."""
+    monkeypatch.setattr(attn, "_launch_device", lambda: 0)
+    with pytest.raises(attn.AttnError) as e:
+        call(_Ptr(device=tensors), stream=stream)
+    assert e.value.code == INVALID and "[0, 1]" in str(e.value)
+
+
 # ------------------------------------------------------------------ the oracle's own pins
 
 def test_e2m1_rounding():

@@ -1029,6 +1029,32 @@ def test_far_pages():
     assert np.array_equal(f64(vp[num - 1]).transpose(1, 0, 2), r.part("v")[1])
 
 
+def test_host_tensors_are_refused():
+    """Before any launch, on the current stream and on a given one, alone or among device tensors."""
+    rng = np.random.default_rng(22)
+    w = Decode(rng, [20], 2, 1, 128, 16)
+    side = torch.cuda.Stream()
+    o, lse = w.o.clone(), w.lse.clone()
+    names = ("q", "k", "v", "o", "lse", "cu", "d_table", "ws")
+    there = {n: getattr(w, n) for n in names}
+    for some in (("q",), ("d_table",), ("o", "lse"), names):
+        for n in names:
+            setattr(w, n, there[n].cpu() if n in some else there[n])
+        for stream in (None, 0, side, side.cuda_stream):
+            with pytest.raises(attn.AttnError) as e:
+                w.run(stream)
+            assert e.value.code == attn.ATTN_ERR_INVALID
+    for n in names:
+        setattr(w, n, there[n])
+    for stream in (0, side, side.cuda_stream):  # device tensors are served on each
+        torch.cuda.synchronize()
+        w.o.copy_(o), w.lse.copy_(lse)
+        torch.cuda.synchronize()
+        w.run(stream)
+        assert status() == 0
+        w.check()
+
+
 # ------------------------------------------------------------------ a run of them together
 
 def test_serving_run_bf16():

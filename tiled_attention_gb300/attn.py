@@ -134,17 +134,27 @@ def _stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _launch_device():
+    """The current device's index, which kernels are launched on; None before CUDA is
+    initialised (there are no device tensors then)."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else None
+
+
 def _place(stream, *tensors):
-    """(stream handle, addresses of the tensors; None: NULL). The tensors must share one device,
-    the current one if the call goes to the current stream."""
+    """(stream handle, addresses of the tensors; None: NULL). The tensors and the stream must be of
+    the current device, on which the library launches."""
     devices = {t.get_device() for t in tensors if t is not None}
     if stream is None:
         device, handle = _current()
-        devices.add(device)
     else:
-        handle = _stream(stream)
-    if len(devices) > 1:
-        raise AttnError(ATTN_ERR_INVALID, f"tensors and call on devices {sorted(devices)}")
+        device, handle = _launch_device(), _stream(stream)
+        devices.add(getattr(stream, "device_index", device))
+    devices.add(device)
+    devices.discard(None)
+    if len(devices) > 1 or -1 in devices:
+        raise AttnError(ATTN_ERR_INVALID,
+                        f"tensors and call on devices {sorted(devices)} (-1: host memory)")
     return handle, [None if t is None else t.data_ptr() for t in tensors]
 
 
