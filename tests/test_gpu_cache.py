@@ -819,6 +819,44 @@ def test_decode_fp4_overlaps_are_refused_and_neighbours_are_not():
     assert status() == 0 and torch.equal(arena, was)
 
 
+@pytest.mark.parametrize("lens", [[5000], [16384], [900, 3000]])
+@pytest.mark.parametrize("d,group", [(64, 4), (64, 16), (128, 4), (128, 16)])
+def test_decode_fp4_padding_changes_nothing(lens, d, group):
+    """Sequences without tokens take no share of the work: a padded batch gives its live rows the
+    bits that they have alone."""
+    rng = np.random.default_rng(3600 + d + group)
+    at = [20 + 9 * i for i in range(len(lens))]
+    padded = np.zeros(50, int)
+    padded[at] = lens
+    w = Decode(rng, padded, 2 * group, 2, d, 64)
+    w.run()
+    assert status() == 0
+    w.check()
+    alone = Decode(rng, lens, 2 * group, 2, d, 64)
+    alone.q, alone.k, alone.v = w.q[at].contiguous(), w.k, w.v
+    alone.d_table, alone.bt.num = w.d_table[at].contiguous(), w.bt.num
+    alone.run()
+    assert status() == 0
+    assert torch.equal(alone.o.view(torch.int16), w.o[at].view(torch.int16))
+    assert torch.equal(alone.lse, w.lse[at])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_fp4_padded_many_contexts_are_joined_in_few_parts(d):
+    """Warps as workers, all but two of the batch's contexts empty: neither is cut into more than
+    64 parts of an even share (65 with their ends), as what each warp leaves word of, the last
+    region of the workspace, shows."""
+    rng = np.random.default_rng(3700 + d)
+    w = Decode(rng, [0] * 300 + [16000] + [0] * 300, 8, 2, d, 64)
+    w.run()
+    assert status() == 0
+    w.check()
+    workers = 4 * 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    left = w.ws[-(-workers * 16 // 256) * -256:].view(torch.int32).view(-1, 4)[:workers].cpu()
+    assert sorted(left[:, 0][left[:, 2] > 0].tolist()) == [600, 601]
+    assert 2 <= left[:, 2].max() <= 65
+
+
 @pytest.mark.parametrize("B,Hq,Hkv,d", [(3, 4, 2, 128), (700, 2, 1, 64), (40, 64, 4, 128),
                                         (200, 32, 8, 64)])
 def test_decode_fp4_without_keys(B, Hq, Hkv, d):

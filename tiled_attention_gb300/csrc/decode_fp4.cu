@@ -2,7 +2,6 @@
 // 8-head column tiles) and its entry points.
 #include "decode_fp4.cuh"
 
-#include <algorithm>
 #include <cmath>
 
 #include "../../include/attn.h"
@@ -168,7 +167,6 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.slots = L.slots;
-  p.fine = static_cast<int>(std::min<long long>(32ll * B * Hkv, L.slots));
   // The joining kernel: a CTA a group once the groups fill the GPU (48 sequences x 4 kv heads of 16
   // query heads: 4 us less than with a CTA a head), else a CTA a head, with eight threads a
   // column to share the parts (one sequence x 8 kv heads: 12.7 us, with four 13.6).

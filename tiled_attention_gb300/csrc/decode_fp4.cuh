@@ -73,7 +73,6 @@ struct DecodeFp4Params {
                          // its number, first part's slot, parts (0: none)
   int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
   int slots;             // CTAs of the decode kernel
-  int fine;              // CTAs that units smaller than four may go to
   int join_heads;        // query heads a CTA of the joining kernel takes
   float scale_log2;      // softmax scale * K tensor scale * log2 e
   float v_scale;
@@ -374,6 +373,9 @@ template <int D, bool SOLO>
 struct Fp4Share {
   static constexpr int kStart = SOLO ? 1 : DecodeFp4Start<D>::kUnits;
   static constexpr int kTok = SOLO ? DecodeFp4Cfg<D, 1>::kStage : 128;  // tokens of a block
+  // Parts of a context that join well: with CTAs as workers the joining kernel reads 32 in one
+  // round. Warps: one sequence of 16K tokens among 63 empty ones takes 26 us, in 128 parts 28.
+  static constexpr int kParts = SOLO ? 64 : 32;
   int total;    // units of one kv head, all sequences
   int before;   // those of the sequences before `upto`
   int n, q, r;
@@ -397,9 +399,12 @@ struct Fp4Share {
     total = __reduce_add_sync(0xffffffffu, all);
     before = __reduce_add_sync(0xffffffffu, ahead);
     const int U = total * p.Hkv;
-    // As many workers as the GPU holds, but CTAs over 32 parts a context only at four units or
-    // more each: the joining kernel reads 32 parts in one round.
-    n = SOLO ? imin(DecodeFp4Cfg<D, 1>::kWarps * p.slots, U) : imin(p.slots, imin(U, imax(p.fine, U / 4)));
+    // As many workers as the GPU holds, but over kParts a context only at four units or more each.
+    // Contexts are counted by the lanes that have any, up to 32 x kv heads (enough for every
+    // worker), and a padded batch's empty ones are none: with B counted instead, one sequence of
+    // 16K tokens x 8 kv heads took 18 us among 55 empty ones and 54 among 63, now 15.6 and 26.
+    const int live = __popc(__ballot_sync(0xffffffffu, all > 0)) * p.Hkv;
+    n = imin((SOLO ? DecodeFp4Cfg<D, 1>::kWarps : 1) * p.slots, imin(U, imax(live * kParts, U / 4)));
     q = n ? U / n : 0;
     r = U - q * n;
   }
