@@ -269,7 +269,8 @@ size_t attn_noalloc_scratch_bytes(void);
  * cos_sin   fp32 [max_pos, rot_dim]: of every position rot_dim/2 cosines, then rot_dim/2 sines.
  * rot_dim   0 or a multiple of 16 up to d.
  * positions int32 [total]; NULL: t % N (then N <= max_pos). A position outside [0, max_pos)
- *           sets ATTN_ERR_BOUNDS and its token's rows are not written.
+ *           sets ATTN_ERR_BOUNDS and its token's rows are not written. Without a rotation neither
+ *           positions nor max_pos is looked at.
  * Every tensor is 16-byte aligned (positions 4). No workspace; asynchronous on `stream`.
  */
 int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int total, int N,
@@ -303,8 +304,8 @@ int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int t
  * block_table int32 [B, max_pages]. Only the new tokens' entries are read; one outside
  *           [0, num_pages) sets ATTN_ERR_BOUNDS and that token's key and value are not written.
  * cos_sin, max_pos, rot_dim, interleaved, q_weight, k_weight, eps, d as for attn_norm_rope.
- *           A position outside [0, max_pos) sets ATTN_ERR_BOUNDS; nothing of its token is
- *           written.
+ *           With a rotation a position outside [0, max_pos) sets ATTN_ERR_BOUNDS; nothing of its
+ *           token is written.
  * page_size 16, 32, 64 or 128. No workspace; asynchronous on `stream`.
  */
 int attn_append_paged(const void *q, const void *k, const void *v, void *q_out, void *k_pool,
@@ -327,7 +328,8 @@ int attn_append_paged(const void *q, const void *k, const void *v, void *q_out, 
  *   xs    = y * (1 / k_scale)                       (the reciprocal rounded to fp32)
  *   scale = E4M3(max over the 16 channels |xs| / 6) (to nearest even, saturating at 448)
  *   code  = E2M1(xs / scale)                        (to nearest even, saturating; 0 if scale is 0)
- * with IEEE fp32 products, sums and divisions throughout (the rotation's too). Infinities
+ * with IEEE fp32 products, sums and divisions throughout (the rotation's too). A norm's reciprocal
+ * root may be 2 ulp off, and a normed key's code then a step, next to a midpoint. Infinities
  * saturate; a NaN makes its block's scale NaN (0x7F) and its codes 0.
  * k_scale, v_scale > 0, finite, with finite reciprocals: one scale a tensor. About
  * max |y| / 2688 uses the scales' whole range; 1 serves values between about 0.05 and 2688.
@@ -361,7 +363,9 @@ int attn_unpack_pages_fp4(const void *pool, void *dst, float pool_scale,
 /*
  * attn_fwd_paged_decode_fp4 — paged decode over a 4-bit cache: attn_fwd's PAGED_DECODE with pools
  * in attn_append_paged_fp4's format. K and V are their exact values code * scale * k_scale
- * (v_scale); products accumulate in fp32, softmax weights enter the second product in f16.
+ * (v_scale); products accumulate in fp32. Two operands are rounded to f16: softmax weights (11
+ * bits; their sum stays fp32), and queries over the power of two of their head's largest channel
+ * (exact down to 2^-14 of that power, off by at most 2^-25 of it below).
  * q, o      bf16 [B, Hq, 1, d]; lse fp32 [B, Hq], natural log.
  * k, v      4-bit pools (16-byte aligned). Slots past a sequence's context may hold anything.
  * N         the longest context (block_table has ceil(N / page_size) columns); N <= 2^30. With

@@ -919,6 +919,40 @@ def test_decode_fp4_magnitudes(q_amp, ks, vs):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,B", [(1, 2), (12, 2), (4, 240)])
+def test_decode_fp4_small_query_channels(d, group, B):
+    """Scores that come from channels 2^16 below their head's largest, where f16 is not exact: a
+    channel is off by at most 2^-25 of the largest one's power of two, a score by that times
+    scale * sum |k|. (Dropped, they would leave all weights alike.)"""
+    rng = np.random.default_rng(23 + d + group)
+    lens = rng.integers(1, 90, B)
+    lens[:2] = 700, 45
+    Hkv, page = 2, 32
+    w = Decode(rng, lens, group * Hkv, Hkv, d, page, ks=512.0)
+    q = np.array(w.qv, np.float32) * np.float32(2.0 ** -6)
+    q[:, :, 5] = 2.0 ** 10
+    bits = I.f32_to_bf16_bits(q)
+    w.q = bf16_tensor(bits[:, :, None], "cuda")
+    w.qv = I.bf16_bits_to_f32(bits).astype(np.float64)
+    codes, sf = (a.copy() for a in cache.split_block(w.pools[0], page, d))
+    codes[..., 2] &= 0x0F  # channel 5 of every key: zero
+    w.pools[0] = np.concatenate([codes.reshape(w.bt.num, Hkv, -1), sf.reshape(w.bt.num, Hkv, -1)], 2)
+    w.k = dev(w.pools[0])
+    w.run()
+    assert status() == 0
+    o, lse = f64(w.o)[:, :, 0], w.lse.cpu().numpy().astype(np.float64)
+    for b in range(B):
+        k, v = w.context(0, b), w.context(1, b)
+        want, wl, wa, big = cache.decode(w.qv[b], k, v, w.scale)
+        off = 2.0 ** -15 * w.scale * np.abs(k).sum(-1).max(-1).repeat(group)
+        e = 2.0 ** -18 * big + off
+        tol = (BF16_HALF * np.abs(want) + (2.0 ** -11 + np.expm1(2 * e))[:, None] * wa
+               + 2.0 ** -18 * np.abs(v).max())
+        assert np.all(np.abs(o[b] - want) <= tol)
+        assert np.all(np.abs(lse[b] - wl) <= e + 2.0 ** -17 + 2.0 ** -22 * np.abs(wl))
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_decode_fp4_rising_scores(d):
     """Scores that grow along the context move the running max again and again; falling ones
     leave most weights at zero."""

@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
         const int head = (gb + i) * kRows + rr;
         va[i] = vb[i] = make_uint4(0, 0, 0, 0);
         if (gb + i < g1 && head < heads) {
-          const uint4* from = reinterpret_cast<const uint4*>(src + static_cast<size_t>(head) * (2 * D));
+          const uint4* from =
+              reinterpret_cast<const uint4*>(src + static_cast<size_t>(head) * (2 * D));
           va[i] = __ldg(from + ca);
           vb[i] = __ldg(from + cb);
         }

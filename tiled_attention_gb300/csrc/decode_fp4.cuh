@@ -23,9 +23,9 @@
 //     the head's scale. P in f16: 2^(s - m + 7), at most 2^15, where m trails the running
 //     max by less than 8; f16 keeps 11 bits of it where bf16 would keep 8.
 //
-// Work: the contexts are cut into blocks (of 128 tokens; of a stage where SOLO), numbered over sequence, kv head and
-// position, with a few units more at each context's start for the cost of beginning it, and
-// shared out evenly over the workers in that order: every worker has the same work whatever the
+// Work: the contexts are cut into blocks (of 128 tokens; of a stage where SOLO), numbered over
+// sequence, kv head and position, with a few units more at each context's start for the cost of
+// beginning it, and shared out evenly over the workers in that order: every worker has the same work whatever the
 // lengths are, and finds its range from cu_seqlens alone. A worker is a CTA where contexts are
 // few, so that they fall into few parts, and a single warp where they are many (SOLO), which
 // then begins and ends contexts without waiting for three others. A range is one or more
@@ -67,8 +67,8 @@ struct DecodeFp4Params {
   const int* table;      // [B, max_pages]
   uint16_t* o;           // bf16 [B, Hq, 1, D]
   float* lse;            // [B, Hq]
-  float* part_o;         // [2 * slots, group, D]
-  float* part_ml;        // [2 * slots, group, 2]
+  float* part_o;         // [2 * workers, group, D]: two rows a worker; room for four workers a CTA
+  float* part_ml;        // [2 * workers, group, 2]
   int4* joins;           // [workers], SOLO: the context that a worker begins and others end:
                          // its number, first part's slot, parts (0: none)
   int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
@@ -497,9 +497,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   // in its page `sub` (up to eight pages of 16 tokens), a whole (page, head) block in one
   // copy; where a page is longer than a stage, parts 0 and 2 bring its codes and parts 1 and 3
   // its scales. Every lane arrives on the stage's barrier with the bytes it asked for. Stages
-  // lie at the same place of their pages, but for `flip` below. Pages past the context are not copied. A
-  // page whose entry lies outside the pool is never addressed: the status word reports it and
-  // it reads as zeros. A stage's table entries are read one stage ahead of its copies.
+  // lie at the same place of their pages, but for `flip` below. Pages past the context are not
+  // copied. A page whose entry lies outside the pool is never addressed: the status word reports it
+  // and it reads as zeros. A stage's table entries are read one stage ahead of its copies.
   const int lp = p.page_shift;
   const int sub = lane >> 2, part = lane & 3;
   const int run = imin(C::kStage, 1 << lp);  // tokens of the stage in one page
@@ -805,9 +805,9 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
 }
 
 // Joins the parts of contexts that several workers share, and writes the rows of empty ones. One
-// CTA per (kv head, sequence), per query head, or per worker (SOLO); a thread takes four columns of one head, and
-// where that leaves threads over, set s of them takes the parts s, s + sets, ...; the sets'
-// sums are added in order.
+// CTA per (kv head, sequence), per query head, or per worker (SOLO); a thread takes four columns of
+// one head, and where that leaves threads over, set s of them takes the parts s, s + sets, ...;
+// the sets' sums are added in order.
 constexpr int kCombineThreads = 256;  // at most
 
 template <int D, bool SOLO>
