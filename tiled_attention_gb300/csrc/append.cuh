@@ -52,7 +52,7 @@ struct RowParams {
 };
 
 // Two CTAs of eight warps an SM and four row groups in flight a warp, measured on 16384 tokens of
-// 32 + 8 heads (norm and rotation) and on 17756 tokens of 32 + 8 + 8 appended to 16-token
+// 32 + 8 heads (norm and rotation) and on 17754 tokens of 32 + 8 + 8 appended to 16-token
 // pages: 60.0 and 80.6 us; three CTAs with two groups 58.4 and 74.5, but spilling; 128 threads,
 // five CTAs, four groups 57.5 and 76.7, spilling; three CTAs of 128 with six groups 67 and 94.
 // With the rows prefetched (below) the first takes 55.5 and 75.0.

@@ -180,8 +180,10 @@ int attn_fwd_paged_decode_fp4(const void* q, const void* k, const void* v, void*
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   // From as many contexts (a sequence and kv head each) on as the GPU holds CTAs, a warp is a
   // worker; below, a CTA. Measured with warps and with CTAs: 64 sequences of 1K-8K tokens x 8 kv
-  // heads 66 and 68 us, 256 of 1K 64 and 76, 1000 of 20-400 79 and 169; 24 of 1K-16K 51 and 49,
-  // one of 16K 33 and 13.
+  // heads 66 and 68 us, 256 of 1K 65 and 76, 1000 of 20-400 79 and 169; 24 of 1K-16K 50 and 48,
+  // one of 16K 25 and 13. The lengths are not known here, so a batch of that size with its tokens
+  // in a few sequences gets warps too: 63 empty ones and one of 16K 26 and 16, 63 of 256 tokens
+  // and one of 128K 77 and 46.
   // Without keys CTAs: they find no work and leave the workspace alone, warps would clear `joins`.
   const bool solo = keys && static_cast<long long>(B) * Hkv >= L.slots;
   const cudaError_t e = solo ? launch<true>(p, d, stream) : launch<false>(p, d, stream);

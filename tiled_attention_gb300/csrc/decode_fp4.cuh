@@ -46,11 +46,11 @@
 // segment's end.
 //
 // Measured (GB300, device time): 32 sequences of 1K-16K tokens, 8 kv heads of 4 query heads,
-// d = 128, 313 MB: 61 us, 5.1 TB/s, 76 % of the copy rate; 48 sequences of 1-32K, 4 kv heads of
-// 16, d = 64, pages of 16, 216 MB: 73 us; one sequence of 16K: 13 us. Bound by issue: 224
-// instructions of a warp per 16 tokens at d = 128, of which 64 convert and 64 scale at half
-// rate; computing alone takes 54 us on the first, streaming alone 53, ~10 of each start-up
-// and joining.
+// d = 128, 313 MB: 62 us, 5.1 TB/s, 75 % of the copy rate; 48 sequences of 1-32K, 4 kv heads of
+// 16, d = 64, pages of 16, 216 MB: 73 us (pages of 64: 67; 8 heads a kv head: 60 and 53); one
+// sequence of 16K: 13 us. Bound by issue: 224 instructions of a warp per 16 tokens at d = 128, of
+// which 64 convert and 64 scale at half rate; computing alone takes 54 us on the first, streaming
+// alone 53, ~10 of each start-up and joining. At d = 64 with two head tiles 217 instructions.
 #pragma once
 
 #include "fp4.cuh"
