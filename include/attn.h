@@ -280,6 +280,30 @@ int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int t
                    const int32_t *positions, void *stream);
 
 /*
+ * attn_norm_rope_axes — attn_norm_rope for tokens with a position on each of several axes (time,
+ * height and width of a video's patches, say), and for heads that hold two rows.
+ *
+ *  - Pair i of a row turns by the angle cos_sin[positions[a][t]][i], where a = pair_axis[i] is the
+ *    axis that the pair goes by. Runs of pairs an axis, axes in turns and any other order are
+ *    tables of pair_axis; the table's frequencies are the caller's, pair by pair.
+ *  - maps = 2: a head's d channels are two rows of d / 2, side by side, each normed over its own
+ *    d / 2 channels and turned on its own: the maps of differential attention (attn_fwd_diff). The
+ *    weights then have d / 2 channels, and rot_dim is at most d / 2. maps = 1: one row of d.
+ * axes      1 to 4.
+ * pair_axis HOST array of rot_dim / 2 bytes, each below axes (else ATTN_ERR_INVALID), read during
+ *           the call; may be NULL where axes is 1 or there is no rotation.
+ * positions int32 device array [axes, total], required with a rotation. A token with a position
+ *           outside [0, max_pos) on any axis sets ATTN_ERR_BOUNDS and its rows are not written.
+ * Everything else as for attn_norm_rope: with axes = 1, maps = 1 and the same positions, the same
+ * bits.
+ */
+int attn_norm_rope_axes(const void *q, const void *k, void *q_out, void *k_out, int total, int N,
+                        int Hq, int Hkv, int d, int maps, int64_t q_stride, int64_t k_stride,
+                        const float *q_weight, const float *k_weight, float eps,
+                        const float *cos_sin, int max_pos, int rot_dim, int interleaved, int axes,
+                        const uint8_t *pair_axis, const int32_t *positions, void *stream);
+
+/*
  * attn_append_paged — new tokens' keys and values into a paged cache, normed and rotated on the
  * way, and their queries made ready in the same launch. The block-table layout is that of
  * attn_fwd's PAGED_DECODE and attn_fwd_paged_prefill, which read the pools next.
@@ -316,6 +340,24 @@ int attn_append_paged(const void *q, const void *k, const void *v, void *q_out, 
                       const int32_t *cu_seqlens_q, const int32_t *seqlens_k,
                       const int32_t *block_table, int max_pages, int page_size, int num_pages,
                       void *stream);
+
+/*
+ * attn_append_paged_axes — attn_append_paged with attn_norm_rope_axes' rotation and maps: a token's
+ * slot still goes by its place in the context (seqlens_k[b] - Lq_b + t), its angles by its
+ * positions. With maps = 2 the pools are those that attn_fwd_diff_paged_prefill and
+ * attn_fwd_diff_paged_decode read: [num_pages, Hkv, page_size, d] with the two maps' keys side by
+ * side, and values as they are. positions [axes, total_q] are looked at for the tokens of sequences
+ * alone; one outside [0, max_pos) sets ATTN_ERR_BOUNDS and nothing of its token is written.
+ */
+int attn_append_paged_axes(const void *q, const void *k, const void *v, void *q_out, void *k_pool,
+                           void *v_pool, int B, int Hq, int Hkv, int total_q, int N, int d,
+                           int maps, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const float *q_weight, const float *k_weight, float eps,
+                           const float *cos_sin, int max_pos, int rot_dim, int interleaved,
+                           int axes, const uint8_t *pair_axis, const int32_t *positions,
+                           const int32_t *cu_seqlens_q, const int32_t *seqlens_k,
+                           const int32_t *block_table, int max_pages, int page_size,
+                           int num_pages, void *stream);
 
 /*
  * attn_append_paged_fp4 — attn_append_paged into a cache held in 4 bits.
@@ -388,6 +430,74 @@ int attn_fwd_paged_decode_fp4(const void *q, const void *k, const void *v, void 
 
 /* Bytes of workspace attn_fwd_paged_decode_fp4 needs for these arguments. */
 size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d);
+
+/*
+ * attn_fwd_diff — differential attention: the difference of two softmax maps over one set of
+ * values, with its per-head norm, in one pass over K and V. (No counterpart on the pages.)
+ *
+ * A head's d channels of q and k are two maps of d / 2, side by side (channels [0, d/2) and
+ * [d/2, d)); a value row is d channels. For every query row of head h
+ *   A_m = softmax(scale * q_m k_m^T + mask),  m = 1, 2
+ *   y   = A_1 v - lam[h] * A_2 v
+ *   o   = out_scale * y * norm_weight / sqrt(mean_c y_c^2 + eps)   (norm_weight NULL:
+ *                                                                   o = out_scale * y)
+ * in fp32 from the accumulators on, rounded to bf16 once; the softmax weights enter the product
+ * with v in bf16, their sums stay fp32. A row that sees no key gets o = 0.
+ * q, o      bf16 [B,Hq,N,d] (document kinds [1,Hq,N,d]); k, v bf16 [B,Hkv,N,d]; layouts, masks,
+ *           window, cu_seqlens, B, Hq, Hkv and N as for attn_fwd's prefill kinds (NONE, CAUSAL,
+ *           SLIDING, SLIDING_BIDIR, DOCUMENT, DOCUMENT_BIDIR, PREFIX_LM; others: ATTN_ERR_INVALID).
+ *           Values at masked places have to be finite, as for attn_fwd.
+ * lse       fp32 [B,Hq,2,N] (document kinds [1,Hq,2,N]): each map's natural log-sum-exp; -inf where
+ *           a row sees no key.
+ * lam       fp32 [Hq]: the second map's factor, of either sign.
+ * norm_weight fp32 [d] or NULL: no norm. eps finite and >= 0 (read if there is a norm). out_scale
+ *           finite (1 - lambda_init, usually).
+ * d         64 or 128: maps of 32 or 64 channels.
+ * scale     > 0, usually 1/sqrt(d/2).
+ * o and lse must not overlap one another, q, k or v (ATTN_ERR_INVALID). Tensors are 16-byte aligned
+ * (lam 4). No workspace; asynchronous on `stream`.
+ */
+int attn_fwd_diff(const void *q, const void *k, const void *v, void *o, float *lse,
+                  const float *lam, int B, int Hq, int Hkv, int N, int d, float scale,
+                  int mask_kind, int window, const int32_t *cu_seqlens, const float *norm_weight,
+                  float eps, float out_scale, void *stream);
+
+/*
+ * attn_fwd_diff_paged_prefill — differential attention of chunks of new tokens over a paged cache:
+ * attn_fwd_paged_prefill's chunks, lengths, table and pools with attn_fwd_diff's rows.
+ * q, o bf16 [1, Hq, total_q, d]; lse fp32 [1, Hq, 2, total_q]; k, v bf16 pools [num_pages, Hkv,
+ * page_size, d], the two maps' keys side by side (attn_append_paged_axes with maps = 2 fills them).
+ * Slots of a sequence's last page past its context may hold anything.
+ */
+int attn_fwd_diff_paged_prefill(const void *q, const void *k, const void *v, void *o, float *lse,
+                                const float *lam, int B, int Hq, int Hkv, int total_q, int d,
+                                float scale, const float *norm_weight, float eps,
+                                float out_scale, const int32_t *cu_seqlens_q,
+                                const int32_t *seqlens_k, const int32_t *block_table,
+                                int max_pages, int page_size, int num_pages, void *stream);
+
+/*
+ * attn_fwd_diff_paged_decode — differential attention of one new token a sequence over a paged
+ * cache: attn_fwd's PAGED_DECODE with attn_fwd_diff's rows.
+ * q, o bf16 [B, Hq, 1, d]; lse fp32 [B, Hq, 2]; k, v as for attn_fwd_diff_paged_prefill, slots past
+ * a context included. N, cu_seqlens, block_table, page_size and num_pages as for PAGED_DECODE: at
+ * most 16 query heads per kv head; a bad length gives o = 0, lse = -inf and ATTN_ERR_SEQLENS; a
+ * table entry outside the pool sets ATTN_ERR_BOUNDS and its page reads as zeros; L_b = 0 gives
+ * o = 0 and lse = -inf. N <= 2^30. With N = 0 every context is empty; k, v, block_table and
+ * workspace are not used then and may be NULL, nor are q, lam and norm_weight.
+ * workspace of at least attn_workspace_bytes_diff(...) bytes (may be NULL when that is 0); contents
+ * need not be initialised; concurrent calls need separate ones. o, lse and workspace must not
+ * overlap one another or an input (ATTN_ERR_INVALID). Results do not depend on timing.
+ */
+int attn_fwd_diff_paged_decode(const void *q, const void *k, const void *v, void *o, float *lse,
+                               const float *lam, int B, int Hq, int Hkv, int N, int d,
+                               float scale, const float *norm_weight, float eps,
+                               float out_scale, const int32_t *cu_seqlens,
+                               const int32_t *block_table, int page_size, int num_pages,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace attn_fwd_diff_paged_decode needs for these arguments. */
+size_t attn_workspace_bytes_diff(int B, int Hq, int Hkv, int N, int d);
 
 /* Synchronises `stream`, then returns and clears the device status word (ATTN_OK or one of
  * ATTN_ERR_TIMEOUT / ATTN_ERR_BOUNDS / ATTN_ERR_SEQLENS), or ATTN_ERR_CUDA if the stream

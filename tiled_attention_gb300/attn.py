@@ -40,6 +40,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _l = ctypes.c_int64
 _f = ctypes.c_float
+_b = ctypes.c_char_p  # host bytes
 _SIGS = {
     "attn_fwd": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _p, _p, _i,
                       _i, _p, ctypes.c_size_t, _p]),
@@ -74,6 +75,18 @@ _SIGS = {
     "attn_fwd_paged_decode_fp4": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _f, _p, _p,
                                        _i, _i, _p, ctypes.c_size_t, _p]),
     "attn_workspace_bytes_fp4": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
+    "attn_norm_rope_axes": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _l, _l, _p, _p, _f, _p, _i,
+                                 _i, _i, _i, _b, _p, _p]),
+    "attn_append_paged_axes": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _l, _l, _l,
+                                    _p, _p, _f, _p, _i, _i, _i, _i, _b, _p, _p, _p, _p, _i, _i, _i,
+                                    _p]),
+    "attn_fwd_diff": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _i, _i, _p, _p, _f, _f,
+                           _p]),
+    "attn_fwd_diff_paged_prefill": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _p, _f, _f,
+                                         _p, _p, _p, _i, _i, _i, _p]),
+    "attn_fwd_diff_paged_decode": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _p, _f, _f,
+                                        _p, _p, _i, _i, _p, ctypes.c_size_t, _p]),
+    "attn_workspace_bytes_diff": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
 }
 
 
@@ -282,6 +295,83 @@ def attn_fwd_paged_decode_fp4(q, k, v, o, lse, B, Hq, Hkv, N, d, scale, k_scale,
 
 def attn_workspace_bytes_fp4(B, Hq, Hkv, N, d) -> int:
     return lib().attn_workspace_bytes_fp4(B, Hq, Hkv, N, d)
+
+
+def _pair_bytes(pair_axis, rot_dim):
+    """Axis of every rotated pair as host bytes: bytes, or whole numbers below 256."""
+    if pair_axis is None:
+        return None
+    pair_axis = bytes(pair_axis)
+    if len(pair_axis) != rot_dim // 2:
+        raise AttnError(ATTN_ERR_INVALID,
+                        f"pair_axis of {len(pair_axis)} pairs, rot_dim {rot_dim}")
+    return pair_axis
+
+
+def attn_norm_rope_axes(q, k, q_out, k_out, total, N, Hq, Hkv, d, maps, q_stride, k_stride,
+                        q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, max_pos=0, rot_dim=0,
+                        interleaved=False, axes=1, pair_axis=None, positions=None,
+                        stream=None) -> int:
+    """attn_norm_rope with a position on each of several axes (positions [axes, total], pair_axis
+    the axis of every rotated pair, on the host) and heads of one or two rows."""
+    pairs = _pair_bytes(pair_axis, rot_dim)
+    handle, (q, k, qo, ko, qw, kw, cs, pos) = _place(stream, q, k, q_out, k_out, q_weight,
+                                                     k_weight, cos_sin, positions)
+    return lib().attn_norm_rope_axes(q, k, qo, ko, total, N, Hq, Hkv, d, maps, q_stride, k_stride,
+                                     qw, kw, eps, cs, max_pos, rot_dim, interleaved, axes, pairs,
+                                     pos, handle)
+
+
+def attn_append_paged_axes(q, k, v, q_out, k_pool, v_pool, B, Hq, Hkv, total_q, N, d, maps,
+                           q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, max_pos,
+                           rot_dim, interleaved, axes, pair_axis, positions, cu_seqlens_q,
+                           seqlens_k, block_table, max_pages, page_size, num_pages,
+                           stream=None) -> int:
+    """attn_append_paged with attn_norm_rope_axes' positions and rows."""
+    pairs = _pair_bytes(pair_axis, rot_dim)
+    handle, (q, k, v, qo, kp, vp, qw, kw, cs, pos, cu, lk, table) = _place(
+        stream, q, k, v, q_out, k_pool, v_pool, q_weight, k_weight, cos_sin, positions,
+        cu_seqlens_q, seqlens_k, block_table)
+    return lib().attn_append_paged_axes(q, k, v, qo, kp, vp, B, Hq, Hkv, total_q, N, d, maps,
+                                        q_stride, k_stride, v_stride, qw, kw, eps, cs, max_pos,
+                                        rot_dim, interleaved, axes, pairs, pos, cu, lk, table,
+                                        max_pages, page_size, num_pages, handle)
+
+
+def attn_fwd_diff(q, k, v, o, lse, lam, B, Hq, Hkv, N, d, scale, mask_kind, window=0,
+                  cu_seqlens=None, norm_weight=None, eps=1e-5, out_scale=1.0, stream=None) -> int:
+    """Differential attention, dense or packed (torch tensors in device memory)."""
+    handle, (q, k, v, o, lse, lam, cu, w) = _place(stream, q, k, v, o, lse, lam, cu_seqlens,
+                                                   norm_weight)
+    return lib().attn_fwd_diff(q, k, v, o, lse, lam, B, Hq, Hkv, N, d, scale, mask_kind, window,
+                               cu, w, eps, out_scale, handle)
+
+
+def attn_fwd_diff_paged_prefill(q, k, v, o, lse, lam, B, Hq, Hkv, total_q, d, scale, norm_weight,
+                                eps, out_scale, cu_seqlens_q, seqlens_k, block_table, max_pages,
+                                page_size, num_pages, stream=None) -> int:
+    """Differential attention of chunks of new tokens over a paged cache."""
+    handle, (q, k, v, o, lse, lam, w, cu, lk, table) = _place(
+        stream, q, k, v, o, lse, lam, norm_weight, cu_seqlens_q, seqlens_k, block_table)
+    return lib().attn_fwd_diff_paged_prefill(q, k, v, o, lse, lam, B, Hq, Hkv, total_q, d, scale,
+                                             w, eps, out_scale, cu, lk, table, max_pages,
+                                             page_size, num_pages, handle)
+
+
+def attn_fwd_diff_paged_decode(q, k, v, o, lse, lam, B, Hq, Hkv, N, d, scale, norm_weight, eps,
+                               out_scale, cu_seqlens, block_table, page_size, num_pages,
+                               workspace=None, stream=None) -> int:
+    """Differential attention of one new token a sequence over a paged cache."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    handle, (q, k, v, o, lse, lam, w, cu, table, ws) = _place(
+        stream, q, k, v, o, lse, lam, norm_weight, cu_seqlens, block_table, workspace)
+    return lib().attn_fwd_diff_paged_decode(q, k, v, o, lse, lam, B, Hq, Hkv, N, d, scale, w, eps,
+                                            out_scale, cu, table, page_size, num_pages, ws,
+                                            ws_bytes, handle)
+
+
+def attn_workspace_bytes_diff(B, Hq, Hkv, N, d) -> int:
+    return lib().attn_workspace_bytes_diff(B, Hq, Hkv, N, d)
 
 
 def attn_selftest_wait_timeout(timeout_ns: int, stream=None) -> int:

@@ -117,22 +117,26 @@ int get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   return ATTN_OK;
 }
 
-// 3-D bf16 view [planes][rows][inner] with a 64-column x box_rows box, 128-byte swizzle.
+}  // namespace
+
 int encode_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
-              uint32_t box_rows) {
+              uint32_t box_rows, uint32_t box_cols) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   int rc = get_encoder(&enc);
   if (rc) return rc;
   cuuint64_t dims[3] = {inner, rows, planes};
   cuuint64_t strides[2] = {inner * 2, inner * 2 * rows};
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return ATTN_OK;
 }
+
+namespace {
 
 // 3-D E4M3 (byte) view [planes][rows][inner] with a 128-column x box_rows box, 128-byte
 // swizzle: one box row is one 128-byte swizzle row, as for the bf16 maps' 64 columns.
@@ -152,7 +156,8 @@ int encode_3d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
   return ATTN_OK;
 }
 
-// Mask kinds served by the prefill kernel.
+}  // namespace
+
 bool prefill_kind(int m) {
   return m == ATTN_MASK_NONE || m == ATTN_MASK_CAUSAL || m == ATTN_MASK_SLIDING ||
          m == ATTN_MASK_DOCUMENT || m == ATTN_MASK_SLIDING_BIDIR ||
@@ -169,6 +174,8 @@ bool window_ok(int m, int window) {
   return true;
 }
 
+namespace {
+
 constexpr int kDecodeStage = 64;       // tokens per decode ring stage
 
 struct DecodeLayout {
@@ -177,6 +184,13 @@ struct DecodeLayout {
 };
 
 }  // namespace
+
+bool no_device() {
+  int n = 0;
+  const cudaError_t e = cudaGetDeviceCount(&n);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver;
+}
 
 // Streaming multiprocessors of the current device, or 152 (GB300's count) when no device is
 // visible, so that host-only callers size workspaces the same way. Sets no error message.

@@ -2,6 +2,7 @@
 // messages, the device status word and argument checks. Defined in api.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -16,8 +17,21 @@ void clear_error();
 
 // Address of the current device's status word.
 int status_ptr(int** out);
+// Whether this host sees no device at all.
+bool no_device();
 // Streaming multiprocessors of the current device, or 152 when no device is visible.
 int sms_or_default();
+
+// 3-D bf16 tensor map [planes][rows][inner], boxes of box_cols columns (64: 128-byte swizzle, 32:
+// 64-byte) x box_rows.
+int encode_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
+              uint32_t box_rows, uint32_t box_cols = 64);
+
+// Mask kinds served by the prefill kernels, those of packed segments among them, and whether the
+// window argument suits a kind.
+bool prefill_kind(int mask_kind);
+bool document_kind(int mask_kind);
+bool window_ok(int mask_kind, int window);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Whether two tensors of an and bn bytes share any (a null one shares none).

@@ -1,7 +1,8 @@
-// append.cu — entry points of the token-row kernels (append.cuh): norm and rotation, append to
-// a bf16 or 4-bit paged cache, and 4-bit pages back to bf16.
+// append.cu — entry points of the token-row kernels (append.cuh): norm and rotation by one or
+// several positions a token, append to a bf16 or 4-bit paged cache, and 4-bit pages back to bf16.
 #include "append.cuh"
 
+#include <climits>
 #include <cmath>
 
 #include "../../include/attn.h"
@@ -17,17 +18,18 @@ size_t rows_bytes(int total, int heads, int d, int64_t stride) {
 }
 
 // Checks and fields common to the row entry points. Sizes of absent tensors (null q or k) are
-// passed as 0 heads.
+// passed as 0 heads. A head is `maps` rows of d / maps channels, normed and turned apart.
 int row_params(RowParams* p, const void* q, const void* k, const void* v, void* q_out, int Hq,
                int Hkv, int total, int N, int d, int64_t q_stride, int64_t k_stride,
                int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
-               const float* cos_sin, int max_pos, int rot_dim, int interleaved, int rot_unit) {
+               const float* cos_sin, int max_pos, int rot_dim, int interleaved, int rot_unit,
+               int maps = 1) {
   if (total < 0 || N < 1) return fail(ATTN_ERR_INVALID, "need total >= 0 and N >= 1");
   if (Hq < 0 || Hkv < 0 || Hq + static_cast<long long>(Hkv) == 0)
     return fail(ATTN_ERR_INVALID, "Hq %d, Hkv %d", Hq, Hkv);
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d (64 or 128)", d);
   if (total % N != 0) return fail(ATTN_ERR_INVALID, "%d tokens are not rows of %d", total, N);
-  if (rot_dim < 0 || rot_dim > d) return fail(ATTN_ERR_INVALID, "rot_dim %d", rot_dim);
+  if (rot_dim < 0 || rot_dim > d / maps) return fail(ATTN_ERR_INVALID, "rot_dim %d", rot_dim);
   if (rot_dim % rot_unit != 0)
     return fail(ATTN_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of %d", rot_dim, rot_unit);
   if (rot_dim > 0 && max_pos < 1) return fail(ATTN_ERR_INVALID, "max_pos %d", max_pos);
@@ -63,9 +65,9 @@ int row_params(RowParams* p, const void* q, const void* k, const void* v, void* 
   p->weight[1] = k_weight;
   p->cos_sin = rot_dim ? cos_sin : nullptr;
   p->eps = eps;
-  p->heads[0] = q ? Hq : 0;
-  p->heads[1] = k ? Hkv : 0;
-  p->heads[2] = v ? Hkv : 0;
+  p->heads[0] = q ? Hq * maps : 0;
+  p->heads[1] = k ? Hkv * maps : 0;
+  p->heads[2] = v ? Hkv * maps : 0;
   p->total = total;
   p->N = N;
   p->max_pos = max_pos;
@@ -113,8 +115,10 @@ int cache_params(RowParams* p, const void* k, const void* v, void* k_pool, void*
   return ATTN_OK;
 }
 
-template <int CACHE>
-int launch_rows(RowParams& p, int d, void* stream) {
+// d: channels of a row.
+template <int CACHE, class Params>
+int launch_rows(Params& p, int d, void* stream) {
+  constexpr bool kAxes = std::is_same_v<Params, AxesRowParams>;
   int rc = status_ptr(&p.status);
   if (rc) return rc;
   const int rows = 512 / d;  // rows a warp takes at once: 32 lanes over d / 16 lanes a row
@@ -134,12 +138,62 @@ int launch_rows(RowParams& p, int d, void* stream) {
                   static_cast<unsigned>(parts));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    rows_kernel<64, CACHE><<<grid, kRowThreads, 0, s>>>(p);
-  else
-    rows_kernel<128, CACHE><<<grid, kRowThreads, 0, s>>>(p);
+    rows_kernel<64, CACHE, kAxes><<<grid, kRowThreads, 0, s>>>(p);
+  else if (d == 128)
+    rows_kernel<128, CACHE, kAxes><<<grid, kRowThreads, 0, s>>>(p);
+  else if constexpr (kAxes)
+    rows_kernel<32, CACHE, true><<<grid, kRowThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "row kernel launch");
   return ATTN_OK;
+}
+
+// Rows of a head, and the axes and positions of the rotation.
+int maps_ok(int maps, int Hq, int Hkv, int d) {
+  if (maps != 1 && maps != 2) return fail(ATTN_ERR_INVALID, "maps %d (1 or 2)", maps);
+  if ((Hq > 0 || Hkv > 0) && (Hq > INT_MAX / 2 / 128 || Hkv > INT_MAX / 2 / 128))
+    return fail(ATTN_ERR_UNSUPPORTED, "too many heads");
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d (64 or 128)", d);
+  return ATTN_OK;
+}
+
+int axes_params(AxesRowParams* p, int maps, int axes, const uint8_t* pair_axis,
+                const int32_t* positions) {
+  if (axes < 1 || axes > 4) return fail(ATTN_ERR_INVALID, "axes %d (1 to 4)", axes);
+  if (p->rot > 0 && axes > 1 && !pair_axis) return fail(ATTN_ERR_INVALID, "pair_axis is required");
+  if (p->rot > 0 && p->total > 0 && !positions)
+    return fail(ATTN_ERR_INVALID, "positions are required");
+  p->axes = axes;
+  p->map_shift = maps - 1;
+  p->positions = positions;
+  p->quads = 1;
+  for (int i = 0; axes > 1 && i < p->rot / 2; ++i) {
+    if (pair_axis[i] >= axes)
+      return fail(ATTN_ERR_INVALID, "pair %d goes by axis %d of %d", i, pair_axis[i], axes);
+    p->axis_bits[i / 32] |= static_cast<uint64_t>(pair_axis[i]) << (2 * (i % 32));
+    if (pair_axis[i] != pair_axis[i & ~3]) p->quads = 0;
+  }
+  return ATTN_OK;
+}
+
+// Checks of norm and rotation that go by q, k and their outputs. Returns 1 if all is well and
+// there is work.
+int norm_rope_outputs(const RowParams& p, const void* q, const void* k, const void* q_out,
+                      const void* k_out, int total, int Hq, int Hkv, int d, int64_t q_stride,
+                      int64_t k_stride) {
+  if (total == 0) return ATTN_OK;
+  if ((!q && !k) || (k && !k_out)) return fail(ATTN_ERR_INVALID, "null pointer");
+  if (p.heads[0] + p.heads[1] == 0) return fail(ATTN_ERR_INVALID, "no heads");
+  if (!aligned16(k_out)) return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
+  if (k) {
+    const size_t n = static_cast<size_t>(total) * Hkv * d * 2;
+    if (overlap(k_out, n, q, rows_bytes(total, Hq, d, q_stride)) ||
+        overlap(k_out, n, k, rows_bytes(total, Hkv, d, k_stride)))
+      return fail(ATTN_ERR_INVALID, "an output overlaps an input");
+    if (q && overlap(k_out, n, q_out, static_cast<size_t>(total) * Hq * d * 2))
+      return fail(ATTN_ERR_INVALID, "q_out and k_out overlap");
+  }
+  return 1;
 }
 
 // The 4-bit pools' tensor scales: finite, > 0, with a finite reciprocal.
@@ -162,23 +216,32 @@ int attn_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int t
   int rc = row_params(&p, q, k, nullptr, q_out, Hq, Hkv, total, N, d, q_stride, k_stride, 0,
                       q_weight, k_weight, eps, cos_sin, max_pos, rot_dim, interleaved, 16);
   if (rc) return rc;
-  if (total == 0) return ATTN_OK;
-  if ((!q && !k) || (k && !k_out)) return fail(ATTN_ERR_INVALID, "null pointer");
-  if (p.heads[0] + p.heads[1] == 0) return fail(ATTN_ERR_INVALID, "no heads");
-  if (!aligned16(k_out)) return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned");
+  rc = norm_rope_outputs(p, q, k, q_out, k_out, total, Hq, Hkv, d, q_stride, k_stride);
+  if (rc != 1) return rc;
   if (!positions && rot_dim > 0 && N > max_pos)
     return fail(ATTN_ERR_INVALID, "positions of %d rows, a table of %d", N, max_pos);
-  if (k) {
-    const size_t n = static_cast<size_t>(total) * Hkv * d * 2;
-    if (overlap(k_out, n, q, rows_bytes(total, Hq, d, q_stride)) ||
-        overlap(k_out, n, k, rows_bytes(total, Hkv, d, k_stride)))
-      return fail(ATTN_ERR_INVALID, "an output overlaps an input");
-    if (q && overlap(k_out, n, q_out, static_cast<size_t>(total) * Hq * d * 2))
-      return fail(ATTN_ERR_INVALID, "q_out and k_out overlap");
-  }
   p.out[1] = static_cast<uint8_t*>(k_out);
   p.positions = positions;
   return launch_rows<kCacheNone>(p, d, stream);
+}
+
+int attn_norm_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int total, int N,
+                        int Hq, int Hkv, int d, int maps, int64_t q_stride, int64_t k_stride,
+                        const float* q_weight, const float* k_weight, float eps,
+                        const float* cos_sin, int max_pos, int rot_dim, int interleaved, int axes,
+                        const uint8_t* pair_axis, const int32_t* positions, void* stream) {
+  clear_error();
+  AxesRowParams p{};
+  int rc = maps_ok(maps, Hq, Hkv, d);
+  if (rc) return rc;
+  rc = row_params(&p, q, k, nullptr, q_out, Hq, Hkv, total, N, d, q_stride, k_stride, 0, q_weight,
+                  k_weight, eps, cos_sin, max_pos, rot_dim, interleaved, 16, maps);
+  if (rc) return rc;
+  if ((rc = axes_params(&p, maps, axes, pair_axis, positions))) return rc;
+  rc = norm_rope_outputs(p, q, k, q_out, k_out, total, Hq, Hkv, d, q_stride, k_stride);
+  if (rc != 1) return rc;
+  p.out[1] = static_cast<uint8_t*>(k_out);
+  return launch_rows<kCacheNone>(p, d / maps, stream);
 }
 
 int attn_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_pool,
@@ -200,6 +263,31 @@ int attn_append_paged(const void* q, const void* k, const void* v, void* q_out, 
   if (rc) return rc;
   if (B == 0 || total_q == 0) return ATTN_OK;  // no new tokens
   return launch_rows<kCacheBf16>(p, d, stream);
+}
+
+int attn_append_paged_axes(const void* q, const void* k, const void* v, void* q_out,
+                           void* k_pool, void* v_pool, int B, int Hq, int Hkv, int total_q, int N,
+                           int d, int maps, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const float* q_weight, const float* k_weight, float eps,
+                           const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                           int axes, const uint8_t* pair_axis, const int32_t* positions,
+                           const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                           const int32_t* block_table, int max_pages, int page_size,
+                           int num_pages, void* stream) {
+  clear_error();
+  AxesRowParams p{};
+  if (Hkv <= 0) return fail(ATTN_ERR_INVALID, "Hkv %d", Hkv);
+  int rc = maps_ok(maps, Hq, Hkv, d);
+  if (rc) return rc;
+  rc = row_params(&p, q, k, v, q_out, Hq, Hkv, total_q, N, d, q_stride, k_stride, v_stride,
+                  q_weight, k_weight, eps, cos_sin, max_pos, rot_dim, interleaved, 16, maps);
+  if (rc) return rc;
+  if ((rc = axes_params(&p, maps, axes, pair_axis, positions))) return rc;
+  rc = cache_params(&p, k, v, k_pool, v_pool, B, cu_seqlens_q, seqlens_k, block_table, max_pages,
+                    page_size, num_pages, d / maps, 2 * (d / maps));
+  if (rc) return rc;
+  if (B == 0 || total_q == 0) return ATTN_OK;  // no new tokens
+  return launch_rows<kCacheBf16>(p, d / maps, stream);
 }
 
 int attn_append_paged_fp4(const void* q, const void* k, const void* v, void* q_out, void* k_pool,

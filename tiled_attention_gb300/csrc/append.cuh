@@ -8,6 +8,9 @@
 //             a' = a cos - b sin,  b' = b cos + a sin                       (optional)
 //             for keys that go to 4 bits each product and sum is rounded on its own (no FMA):
 //             the codes then depend on the inputs alone, not on how a compiler contracts
+//             with several axes (AXES) a token has a position on each and pair i goes by
+//             the one that pair_axis names; a head may hold two rows that are normed and turned
+//             apart (the maps of differential attention, D channels each)
 //   bf16 out  round to nearest even, once
 //   4-bit out xs = y * RN(1 / tensor scale); s = E4M3(max over 16 channels |xs| / 6);
 //             code = E2M1(xs / s), the division rounded as IEEE does; 0 where s is 0
@@ -49,6 +52,14 @@ struct RowParams {
   int total, N, B, max_pos, rot, interleaved, max_pages, page_shift, num_pages;
   int groups_per_task;       // row groups a warp takes of its token; the grid's y picks which
   int* status;
+};
+
+// Rows whose tokens have several positions, or whose heads hold two rows.
+struct AxesRowParams : RowParams {  // positions: [axes, total]; heads and groups count rows
+  int axes;                // 1 .. 4
+  int map_shift;           // log2 of the rows of a head
+  int quads;               // every four pairs 4 i .. 4 i + 3 go by one axis
+  uint64_t axis_bits[2];   // axis of pair i: bits 2 (i % 32) of word i / 32
 };
 
 // Two CTAs of eight warps an SM and four row groups in flight a warp, measured on 16384 tokens of
@@ -96,8 +107,10 @@ __device__ __forceinline__ float2 clamp2(float2 x, float m) {
   return make_float2(fminf(fmaxf(x.x, -m), m), fminf(fmaxf(x.y, -m), m));
 }
 
-template <int D, int CACHE>
-__global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p) {
+template <int D, int CACHE, bool AXES = false>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    rows_kernel(const std::conditional_t<AXES, AxesRowParams, RowParams> p) {
+  static_assert(!AXES || CACHE != kCacheFp4, "the 4-bit cache takes one position a token");
   constexpr int R = D / 16;          // lanes per row
   constexpr int kRows = 32 / R;      // rows per warp
   constexpr int kBatch = 4;             // row groups in flight
@@ -129,8 +142,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
                                                                    t * p.stride[lane]),
                  "r"(p.heads[lane] * 2 * D));
 
-  int pos, phys = -1;
-  if constexpr (CACHE == kCacheNone) {
+  int pos = 0, phys = -1;  // pos with AXES: the place in the context alone
+  if constexpr (AXES && CACHE == kCacheNone) {
+  } else if constexpr (CACHE == kCacheNone) {
     pos = p.positions ? __ldg(p.positions + t) : t % p.N;
   } else {
     const int b = find_sequence(p.cu, p.B, t, lane);
@@ -155,7 +169,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
       phys = -1;
     }
   }
-  if (p.rot && (pos < 0 || pos >= p.max_pos)) {
+  int on_axis[4];
+  bool off_table = p.rot && (pos < 0 || pos >= p.max_pos);
+  if constexpr (AXES) {
+    off_table = false;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      on_axis[a] = p.rot && a < p.axes
+                       ? __ldg(p.positions + static_cast<size_t>(a) * p.total + t)
+                       : 0;
+      off_table |= p.rot && (on_axis[a] < 0 || on_axis[a] >= p.max_pos);
+    }
+  }
+  if (off_table) {
     if (lane == 0) report_status(p.status, -5);
     return;
   }
@@ -181,7 +207,37 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
       const float4 v = __ldg(reinterpret_cast<const float4*>(from));
       to[0] = make_float2(v.x, v.y), to[1] = make_float2(v.z, v.w);
     };
-    if (split) {
+    if constexpr (AXES) {
+      // Cosines and sines of pairs i .. i + 3: two loads where they go by one axis, else eight.
+      auto row_of = [&](uint32_t axis) {
+        const int x = (axis & 2) ? ((axis & 1) ? on_axis[3] : on_axis[2])
+                                 : ((axis & 1) ? on_axis[1] : on_axis[0]);
+        return p.cos_sin + static_cast<size_t>(x) * p.rot;
+      };
+      auto four_axes = [&](int i, float2* c, float2* s) {
+        const uint32_t bits =
+            static_cast<uint32_t>((i & 32 ? p.axis_bits[1] : p.axis_bits[0]) >> (2 * (i & 31)));
+        if (p.quads) {
+          const float* at = row_of(bits & 3) + i;
+          four(at, c), four(at + p.rot / 2, s);
+        } else {
+          float cv[4], sv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* at = row_of((bits >> (2 * e)) & 3) + i + e;
+            cv[e] = __ldg(at), sv[e] = __ldg(at + p.rot / 2);
+          }
+          c[0] = make_float2(cv[0], cv[1]), c[1] = make_float2(cv[2], cv[3]);
+          s[0] = make_float2(sv[0], sv[1]), s[1] = make_float2(sv[2], sv[3]);
+        }
+      };
+      if (split) {
+        if (paired) four_axes(8 * l, cs, sn), four_axes(8 * l + 4, cs + 2, sn + 2);
+      } else {
+        if (turn_a) four_axes(4 * ca, cs, sn);
+        if (turn_b) four_axes(4 * cb, cs + 2, sn + 2);
+      }
+    } else if (split) {
       if (paired) {
         four(row + 8 * l, cs), four(row + 8 * l + 4, cs + 2);
         four(srow + 8 * l, sn), four(srow + 8 * l + 4, sn + 2);
@@ -213,17 +269,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
     uint8_t* dst = nullptr;   // of head 0; null: this token has no page
     size_t dst_step = 0;      // from head to head
     const int slot = pos & ((1 << p.page_shift) - 1);
+    int ms = 0;               // log2 of the rows of a head
+    if constexpr (AXES) ms = p.map_shift;
     if (CACHE == kCacheNone || kind == 0) {
       const unsigned blk = static_cast<unsigned>(t) / static_cast<unsigned>(p.N);
       const unsigned row = static_cast<unsigned>(t) - blk * static_cast<unsigned>(p.N);
-      dst_step = static_cast<size_t>(p.N) * (2 * D);
-      dst = p.out[kind == 0 ? 0 : 1] + static_cast<size_t>(blk) * heads * dst_step +
-            static_cast<size_t>(row) * (2 * D);
+      dst_step = static_cast<size_t>(p.N) * (2 * D) << ms;
+      dst = p.out[kind == 0 ? 0 : 1] + static_cast<size_t>(blk) * (heads >> ms) * dst_step +
+            (static_cast<size_t>(row) * (2 * D) << ms);
     } else if (phys >= 0) {
       const size_t tok = CACHE == kCacheFp4 ? fp4_row_bytes(D) : 2 * D;
-      dst_step = tok << p.page_shift;
-      dst = p.pool[kind - 1] + static_cast<size_t>(phys) * heads * dst_step;
-      if (CACHE == kCacheBf16) dst += static_cast<size_t>(slot) * (2 * D);
+      dst_step = tok << p.page_shift << ms;
+      dst = p.pool[kind - 1] + static_cast<size_t>(phys) * (heads >> ms) * dst_step;
+      if (CACHE == kCacheBf16) dst += static_cast<size_t>(slot) * (2 * D) << ms;
     }
     for (int gb = g0; gb < g1; gb += kBatch) {
       uint4 va[kBatch], vb[kBatch];
@@ -243,7 +301,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rows_kernel(const RowParams p)
         if (gb + i >= g1) break;  // the same for the whole warp
         const int head = (gb + i) * kRows + rr;
         const bool live = head < heads && dst != nullptr;
-        uint8_t* to = dst + static_cast<size_t>(head) * dst_step;
+        uint8_t* to = dst + static_cast<size_t>(head >> ms) * dst_step;
+        if constexpr (AXES) to += (head & ((1 << ms) - 1)) * (2 * D);
         if constexpr (kind == 2 && CACHE == kCacheBf16) {
           if (live) {
             reinterpret_cast<uint4*>(to)[ca] = va[i];

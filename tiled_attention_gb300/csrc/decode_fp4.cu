@@ -20,14 +20,6 @@ int fp4_slots(int d, int group) {
 
 constexpr int kWorkers = DecodeFp4Cfg<64, 1>::kWarps;  // of a CTA, at most
 
-// Whether this host sees no device at all.
-bool no_device() {
-  int n = 0;
-  const cudaError_t e = cudaGetDeviceCount(&n);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver;
-}
-
 struct Fp4Layout {
   size_t part_ml, joins, total;
   int slots;

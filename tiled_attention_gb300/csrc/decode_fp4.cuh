@@ -56,6 +56,7 @@
 #include "fp4.cuh"
 #include "ptx.cuh"
 #include "sched.h"
+#include "share.cuh"
 
 namespace ta {
 
@@ -352,105 +353,20 @@ __device__ __forceinline__ void fp4_slice(const uint8_t* sl, int h, int run, int
   }
 }
 
-// Context length of sequence b; 0 (and a report, if asked) where cu_seqlens is malformed.
-__device__ __forceinline__ int fp4_length(const DecodeFp4Params& p, int b, bool report) {
-  const int L = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
-  if (L >= 0 && L <= p.max_len) return L;
-  if (report) report_status(p.status, -7);
-  return 0;
-}
-
-// How the blocks are shared out. Every warp of both kernels works it out by itself, from
-// cu_seqlens alone: a context counts its blocks and kStart units before them for what beginning
-// it costs, and worker i of n takes an even share of the units, the first r workers q + 1, the
-// others q. A share that ends among a context's kStart units holds none of it. Cutting small
-// batches into equal parts of whole rounds of the four warps instead, a CTA a part, so that no
-// CTA begins two contexts, gained 0.6 us on one sequence of 16K tokens (13.7 us) and lost 0.5 to
-// 1 us on one of 700, one of 4K and four of 1K to 16K. Warps as workers, with blocks of a stage:
-// with 1, 2 and 3 units 1000 sequences of 20-400 tokens x 8 kv heads take 78.7, 79.3 and 80.2 us,
-// 512 of 200-1000 81.0, 82.1 and 84.4 (blocks of 128 tokens at d = 128 and one unit: 81.9, 83.4).
+// How the blocks are shared out (share.cuh). Cutting small batches into equal parts of whole rounds
+// of the four warps instead, a CTA a part, so that no CTA begins two contexts, gained 0.6 us on one
+// sequence of 16K tokens (13.7 us) and lost 0.5 to 1 us on one of 700, one of 4K and four of 1K to
+// 16K. Warps as workers, with blocks of a stage: with 1, 2 and 3 units at a context's start 1000
+// sequences of 20-400 tokens x 8 kv heads take 78.7, 79.3 and 80.2 us, 512 of 200-1000 81.0, 82.1
+// and 84.4 (blocks of 128 tokens at d = 128 and one unit: 81.9, 83.4). Parts of a context that join
+// well: with CTAs as workers the joining kernel reads 32 in one round. Warps: one sequence of 16K
+// tokens among 63 empty ones takes 26 us, in 128 parts 28. Empty contexts are not counted: with B
+// counted instead, one sequence of 16K tokens x 8 kv heads took 18 us among 55 empty ones and 54
+// among 63, now 15.6 and 26.
 template <int D, bool SOLO>
-struct Fp4Share {
-  static constexpr int kStart = SOLO ? 1 : DecodeFp4Start<D>::kUnits;
-  static constexpr int kTok = SOLO ? DecodeFp4Cfg<D, 1>::kStage : 128;  // tokens of a block
-  // Parts of a context that join well: with CTAs as workers the joining kernel reads 32 in one
-  // round. Warps: one sequence of 16K tokens among 63 empty ones takes 26 us, in 128 parts 28.
-  static constexpr int kParts = SOLO ? 64 : 32;
-  int total;    // units of one kv head, all sequences
-  int before;   // those of the sequences before `upto`
-  int n, q, r;
-  int w0;       // units of sequence `lane`
-
-  __device__ __forceinline__ static int blocks(int L) { return (L + kTok - 1) / kTok; }
-  __device__ __forceinline__ static int units(int nb) { return nb > 0 ? nb + kStart : 0; }
-
-  __device__ __forceinline__ Fp4Share(const DecodeFp4Params& p, int upto, bool report) {
-    const int lane = static_cast<int>(threadIdx.x) & 31;
-    w0 = lane < p.B ? units(blocks(fp4_length(p, lane, report))) : 0;
-    int all = w0, ahead = lane < upto ? w0 : 0;
-    for (int b0 = lane + 32; b0 < p.B; b0 += 128) {
-#pragma unroll
-      for (int b = b0; b < b0 + 128; b += 32) {  // four loads at a time
-        const int w = b < p.B ? units(blocks(fp4_length(p, b, report))) : 0;
-        all += w;
-        if (b < upto) ahead += w;
-      }
-    }
-    total = __reduce_add_sync(0xffffffffu, all);
-    before = __reduce_add_sync(0xffffffffu, ahead);
-    const int U = total * p.Hkv;
-    // As many workers as the GPU holds, but over kParts a context only at four units or more each.
-    // Contexts are counted by the lanes that have any, up to 32 x kv heads (enough for every
-    // worker), and a padded batch's empty ones are none: with B counted instead, one sequence of
-    // 16K tokens x 8 kv heads took 18 us among 55 empty ones and 54 among 63, now 15.6 and 26.
-    const int live = __popc(__ballot_sync(0xffffffffu, all > 0)) * p.Hkv;
-    n = imin((SOLO ? DecodeFp4Cfg<D, 1>::kWarps : 1) * p.slots, imin(U, imax(live * kParts, U / 4)));
-    q = n ? U / n : 0;
-    r = U - q * n;
-  }
-  // First unit of worker i, and the worker that takes unit u.
-  __device__ __forceinline__ int start(int i) const { return i * q + imin(i, r); }
-  __device__ __forceinline__ int worker_of(int u) const {
-    const int large = r * (q + 1);
-    return u < large ? u / (q + 1) : r + (u - large) / q;
-  }
-  // The sequence whose heads hold unit u, and the units (of one kv head) before it.
-  __device__ __forceinline__ void find(const DecodeFp4Params& p, int u, int& seq,
-                                       int& ahead) const {
-    const int lane = static_cast<int>(threadIdx.x) & 31;
-    int run = 0;
-    for (int b0 = 0; b0 < p.B;) {
-      const int b = b0 + lane;
-      const int w = b0 == 0 ? w0 : b < p.B ? units(blocks(fp4_length(p, b, false))) : 0;
-      int sum = w;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += x;
-      }
-      sum += run;
-      const unsigned past = __ballot_sync(0xffffffffu, u < sum * p.Hkv);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        seq = b0 + l;
-        ahead = __shfl_sync(0xffffffffu, sum - w, l);
-        return;
-      }
-      run = __shfl_sync(0xffffffffu, sum, 31);
-      for (b0 += 32; b0 < p.B; b0 += 128) {  // past four times 32 sequences at once
-        int four = 0;
-#pragma unroll
-        for (int c = b0 + lane; c < b0 + lane + 128; c += 32)
-          four += units(c < p.B ? blocks(fp4_length(p, c, false)) : 0);
-        four = run + __reduce_add_sync(0xffffffffu, four);
-        if (u < four * p.Hkv) break;
-        run = four;
-      }
-    }
-    seq = p.B - 1;  // not reached: u lies below the total
-    ahead = run;
-  }
-};
+using Fp4Share = Share<DecodeFp4Params, SOLO ? DecodeFp4Cfg<D, 1>::kStage : 128,
+                       SOLO ? 1 : DecodeFp4Start<D>::kUnits, SOLO ? 64 : 32,
+                       SOLO ? DecodeFp4Cfg<D, 1>::kWarps : 1>;
 
 template <int D, int NT, bool SOLO>
 __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
@@ -571,10 +487,10 @@ __global__ void __launch_bounds__(128, DecodeFp4Cfg<D, NT>::kCtas)
   };
   auto open = [&]() {  // false: the range holds no more blocks
     if (u >= end) return false;
-    int L = fp4_length(p, b, false), nb = share.blocks(L), w = share.units(nb);
+    int L = context_length(p, b, false), nb = share.blocks(L), w = share.units(nb);
     while (u >= seq_u + w * p.Hkv) {  // the sequence is done: on to the next that has blocks
       seq_u += w * p.Hkv;
-      L = fp4_length(p, ++b, false);
+      L = context_length(p, ++b, false);
       nb = share.blocks(L);
       w = share.units(nb);
     }
@@ -827,7 +743,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const Deco
   // Every CTA waits, those without work too: this kernel must not end before the first one.
   if constexpr (SOLO) {
     for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x))
-      if (fp4_length(p, b, false) == 0) empty(static_cast<size_t>(b) * p.Hq, p.Hq);
+      if (context_length(p, b, false) == 0) empty(static_cast<size_t>(b) * p.Hq, p.Hq);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 join = __ldcg(p.joins + blockIdx.x);
     if (join.z == 0) return;
@@ -838,7 +754,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_fp4_kernel(const Deco
     const int g = h0 / G;  // kv head
     hg = h0 % G;
     const Fp4Share<D, SOLO> share(p, b, false);
-    const int nb = share.blocks(fp4_length(p, b, false));
+    const int nb = share.blocks(context_length(p, b, false));
     head0 = static_cast<size_t>(b) * p.Hq + h0;
     if (nb == 0) {
       asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -1,0 +1,209 @@
+// diff.cu — differential attention's prefill instantiations (head dim 64 / 128; dense, document and
+// paged) and their entry points.
+#include "diff.cuh"
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "api.h"
+#include "diff.h"
+#include "launch.h"
+
+namespace ta {
+namespace {
+
+template <int D, int PACK>
+cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
+  static unsigned long long done = 0;
+  auto kern = diff_prefill_kernel<D, PACK>;
+  using C = DiffCfg<D>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(q, k, v, o, p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(int mask, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
+  if (mask == kMaskPagedPrefill)
+    return launch_one<D, kMaskPagedPrefill>(q, k, v, o, p, grid, stream);
+  if (is_packed(mask)) return launch_one<D, kMaskDocument>(q, k, v, o, p, grid, stream);
+  return launch_one<D, kMaskNone>(q, k, v, o, p, grid, stream);
+}
+
+// Fields and checks the two prefill entry points share; o and lse are written while other CTAs
+// still read the inputs.
+int diff_outputs(const void* q, size_t q_bytes, const void* k, const void* v, size_t kv_bytes,
+                 const void* o, const float* lse, size_t lse_bytes) {
+  const struct { const void* x; size_t n; } out[2] = {{o, q_bytes}, {lse, lse_bytes}};
+  bool shared = overlap(o, q_bytes, lse, lse_bytes);
+  for (const auto& t : out)
+    shared |= overlap(t.x, t.n, q, q_bytes) || overlap(t.x, t.n, k, kv_bytes) ||
+              overlap(t.x, t.n, v, kv_bytes);
+  if (shared) return fail(ATTN_ERR_INVALID, "o or lse overlaps another tensor");
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int diff_checks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                const float* lam, const float* weight, float eps, float out_scale) {
+  if (!q || !k || !v || !o || !lse || !lam) return fail(ATTN_ERR_INVALID, "null pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      !aligned16(weight) || (reinterpret_cast<uintptr_t>(lam) & 3u))
+    return fail(ATTN_ERR_INVALID, "tensors must be 16-byte aligned, lam 4-byte aligned");
+  return diff_numbers(weight, eps, out_scale);
+}
+
+int diff_numbers(const float* weight, float eps, float out_scale) {
+  if (!std::isfinite(out_scale)) return fail(ATTN_ERR_INVALID, "out_scale is not finite");
+  if (weight && !(std::isfinite(eps) && eps >= 0.f))
+    return fail(ATTN_ERR_INVALID, "eps must be finite and >= 0");
+  return ATTN_OK;
+}
+
+int diff_sizes(int B, int Hq, int Hkv, int n, int d, float scale) {
+  if (B < 0 || n < 0 || Hq <= 0 || Hkv <= 0)
+    return fail(ATTN_ERR_INVALID, "need B >= 0, N >= 0, Hq > 0, Hkv > 0");
+  if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID, "Hq (%d) %% Hkv (%d) != 0", Hq, Hkv);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d (64 or 128)", d);
+  if (!std::isfinite(scale)) return fail(ATTN_ERR_INVALID, "scale is not finite");
+  if (!(scale > 0.f)) return fail(ATTN_ERR_UNSUPPORTED, "scale must be > 0");
+  return ATTN_OK;
+}
+
+}  // namespace ta
+
+using namespace ta;
+
+extern "C" {
+
+int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* lse,
+                  const float* lam, int B, int Hq, int Hkv, int N, int d, float scale,
+                  int mask_kind, int window, const int32_t* cu_seqlens, const float* norm_weight,
+                  float eps, float out_scale, void* stream) {
+  clear_error();
+  int rc = diff_sizes(B, Hq, Hkv, N, d, scale);
+  if (rc) return rc;
+  if (!prefill_kind(mask_kind))
+    return fail(ATTN_ERR_INVALID, "mask_kind %d is not a prefill kind", mask_kind);
+  if (!window_ok(mask_kind, window))
+    return fail(ATTN_ERR_INVALID, "window %d out of range for mask_kind %d", window, mask_kind);
+  const bool doc = document_kind(mask_kind);
+  if (doc && !cu_seqlens) return fail(ATTN_ERR_INVALID, "cu_seqlens is required");
+  if ((rc = diff_numbers(norm_weight, eps, out_scale))) return rc;
+  if (B == 0 || N == 0) return ATTN_OK;  // nothing to compute
+  if ((rc = diff_checks(q, k, v, o, lse, lam, norm_weight, eps, out_scale))) return rc;
+  const long long planes = doc ? Hq : static_cast<long long>(B) * Hq;
+  const long long planes_kv = doc ? Hkv : static_cast<long long>(B) * Hkv;
+  const long long units =
+      doc ? 2ll * Hq * (N / kUnitRows + static_cast<long long>(B)) : planes * tiles_for_rows(N);
+  if (planes >= (1ll << 31) || units >= (1ll << 31) - 1 || N > INT32_MAX - 512)
+    return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
+  rc = diff_outputs(q, static_cast<size_t>(planes) * N * d * 2, k, v,
+                    static_cast<size_t>(planes_kv) * N * d * 2, o, lse,
+                    static_cast<size_t>(planes) * N * 2 * sizeof(float));
+  if (rc) return rc;
+  DiffParams p{};
+  if ((rc = status_ptr(&p.base.status))) return rc;
+  CUtensorMap tq, tk, tv, to;
+  if ((rc = encode_3d(&tq, q, d, N, planes, 128))) return rc;
+  if ((rc = encode_3d(&to, o, d, N, planes, 32, d / 2))) return rc;
+  if ((rc = encode_3d(&tk, k, d, N, planes_kv, 128))) return rc;
+  if ((rc = encode_3d(&tv, v, d, N, planes_kv, 128))) return rc;
+  p.base.o = o;
+  p.base.lse = lse;
+  p.base.cu_seqlens = cu_seqlens;
+  p.base.B = B;
+  p.base.Hq = Hq;
+  p.base.Hkv = Hkv;
+  p.base.N = N;
+  p.base.group = Hq / Hkv;
+  p.base.num_units = static_cast<int>(units);
+  p.base.window = window;
+  p.base.scale_log2 = scale * kLog2e;
+  p.base.timeout_ns = kTimeoutNs;
+  p.lam = lam;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.out_scale = out_scale;
+  p.mask = mask_kind;
+  const int sms = sms_or_default();
+  const int grid = p.base.num_units < sms ? p.base.num_units : sms;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = d == 64 ? launch<64>(mask_kind, tq, tk, tv, to, p, grid, st)
+                                : launch<128>(mask_kind, tq, tk, tv, to, p, grid, st);
+  if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+  return ATTN_OK;
+}
+
+int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, void* o, float* lse,
+                                const float* lam, int B, int Hq, int Hkv, int total_q, int d,
+                                float scale, const float* norm_weight, float eps,
+                                float out_scale, const int32_t* cu_seqlens_q,
+                                const int32_t* seqlens_k, const int32_t* block_table,
+                                int max_pages, int page_size, int num_pages, void* stream) {
+  clear_error();
+  int rc = diff_sizes(B, Hq, Hkv, total_q, d, scale);
+  if (rc) return rc;
+  if (!page_size_ok(page_size))
+    return fail(ATTN_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128)", page_size);
+  if ((rc = diff_numbers(norm_weight, eps, out_scale))) return rc;
+  if (B == 0 || total_q == 0) return ATTN_OK;  // no query rows
+  if (!cu_seqlens_q || !seqlens_k || !block_table) return fail(ATTN_ERR_INVALID, "null pointer");
+  if ((rc = diff_checks(q, k, v, o, lse, lam, norm_weight, eps, out_scale))) return rc;
+  if (max_pages <= 0 || num_pages <= 0)
+    return fail(ATTN_ERR_INVALID, "max_pages %d, num_pages %d", max_pages, num_pages);
+  const long long keys = static_cast<long long>(max_pages) * page_size;
+  if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || keys >= (1ll << 30))
+    return fail(ATTN_ERR_UNSUPPORTED, "page pool or block table too large");
+  const long long units = 2ll * Hq * (total_q / kUnitRows + static_cast<long long>(B));
+  if (units >= (1ll << 31) - 1 || total_q >= (1 << 30))
+    return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
+  const size_t q_bytes = static_cast<size_t>(Hq) * total_q * d * 2;
+  rc = diff_outputs(q, q_bytes, k, v, static_cast<size_t>(num_pages) * Hkv * page_size * d * 2, o,
+                    lse, static_cast<size_t>(Hq) * total_q * 2 * sizeof(float));
+  if (rc) return rc;
+  DiffParams p{};
+  if ((rc = status_ptr(&p.base.status))) return rc;
+  CUtensorMap tq, tk, tv, to;
+  if ((rc = encode_3d(&tq, q, d, total_q, Hq, 128))) return rc;
+  if ((rc = encode_3d(&to, o, d, total_q, Hq, 32, d / 2))) return rc;
+  const uint64_t planes = static_cast<uint64_t>(num_pages) * Hkv;
+  if ((rc = encode_3d(&tk, k, d, page_size, planes, page_size))) return rc;
+  if ((rc = encode_3d(&tv, v, d, page_size, planes, page_size))) return rc;
+  p.base.o = o;
+  p.base.lse = lse;
+  p.base.cu_seqlens = cu_seqlens_q;
+  p.base.seqlens_k = seqlens_k;
+  p.base.table = block_table;
+  p.base.max_pages = max_pages;
+  p.base.page_size = page_size;
+  p.base.page_shift = log2_exact(page_size);
+  p.base.num_pages = num_pages;
+  p.base.B = B;
+  p.base.Hq = Hq;
+  p.base.Hkv = Hkv;
+  p.base.N = total_q;
+  p.base.group = Hq / Hkv;
+  p.base.num_units = static_cast<int>(units);
+  p.base.scale_log2 = scale * kLog2e;
+  p.base.timeout_ns = kTimeoutNs;
+  p.lam = lam;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.out_scale = out_scale;
+  p.mask = kMaskPagedPrefill;
+  const int sms = sms_or_default();
+  const int grid = p.base.num_units < sms ? p.base.num_units : sms;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = d == 64 ? launch<64>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st)
+                                : launch<128>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st);
+  if (e != cudaSuccess) return cuda_fail(e, "differential paged prefill launch");
+  return ATTN_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,561 @@
+// diff_decode.cuh — differential attention's paged decode: one query token a sequence, the
+// difference of two softmax maps over one set of values (diff.cuh has the formulas).
+//
+// K and V are read once for both maps, and both maps' products cost as many MMAs as one map of
+// ordinary attention with up to 16 heads a kv head: rows r < 8 of an m16n8k16 tile are head r's
+// first map, rows r + 8 its second. K holds the maps' channels side by side, so the queries enter
+// block-diagonally, (q_1, 0) in rows r and (0, q_2) in rows r + 8: one chain of k-steps over all D
+// channels leaves S_1 and S_2 in the two halves of one accumulator, and P of both maps is one A
+// fragment for V. Decode reads 512 bytes a token and kv head at D = 128 and is bound by HBM.
+//
+// Work: contexts are cut into 64-token blocks and shared out evenly over two CTAs an SM (share.cuh),
+// each of which walks its range of (sequence, kv head, block), one or more segments of one
+// (sequence, kv head). A producer warp brings 64-token stages into a ring by TMA, page by page
+// through the block table, and runs ahead over the segments' ends. Each of four consumer warps owns
+// a 16-token slice of every stage with its own running max, sum and O; at a segment's end the four
+// are merged in the slot of its last stage. A segment that is its whole context writes O and LSE
+// itself, normed; the others (a CTA's first and last at most) leave O, max and sum of both maps in
+// the workspace, two slots a CTA, and a second kernel, under programmatic dependent launch, joins
+// them in the workers' order: results do not depend on timing.
+#pragma once
+
+#include "decode.cuh"
+#include "ptx.cuh"
+#include "sched.h"
+#include "share.cuh"
+
+namespace ta {
+
+struct DiffDecodeParams {
+  const uint32_t* q;     // bf16 [B, Hq, 1, D]
+  const int* cu;         // [B+1] cumulative context lengths
+  const int* table;      // [B, max_pages]
+  uint16_t* o;           // bf16 [B, Hq, 1, D]
+  float* lse;            // [B, Hq, 2]
+  const float* lam;      // [Hq]
+  const float* weight;   // [D] or null
+  float* part_o;         // [2 * slots, 2 maps, group, D]
+  float* part_ml;        // [2 * slots, 2 maps, group, 2]
+  int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
+  int slots;             // CTAs of the decode kernel
+  int join_heads;        // query heads a CTA of the joining kernel takes
+  float scale_log2, eps, out_scale;
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+constexpr int kDiffDecodeCtas = 2;  // per SM
+
+using DiffShare = Share<DiffDecodeParams, 64, 2, 32, 1>;
+
+template <int D>
+struct DiffDecodeCfg {
+  static constexpr int kTok = 64;  // tokens per ring stage; consumer warp w owns 16 w .. 16 w + 15
+  static constexpr int kWarps = 4;
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanelBytes = kTok * 128;
+  static constexpr int kHalfBytes = kTok * D * 2;            // K or V of a stage
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kStages = (96 * 1024) / kStageBytes;  // 3 (D = 128), 6 (D = 64)
+  static constexpr int kSteps = D / 16;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kMiscBytes = 1280;
+  static constexpr int kSmemBytes = 1024 + kRingBytes + kMiscBytes;
+  static_assert(kWarps * 16 * D * 4 <= kStageBytes, "a tile's rows are merged in one slot");
+  static_assert(kDiffDecodeCtas * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+struct DiffDecodeCtrl {
+  uint64_t full[8], empty[8];
+  int abort_flag;
+};
+
+// A worker's walk over its range of blocks, segment by segment.
+template <class S, class P>
+struct SegmentWalk {
+  int u, end, b, seq_u;           // next unit, the range's end, sequence and its first unit
+  int g, L, nb, blk0, nblk;       // the segment: kv head, context, its blocks, first and count
+  __device__ __forceinline__ SegmentWalk(const S& share, const P& p, int worker) {
+    u = share.start(worker);
+    end = share.start(worker + 1);
+    share.find(p, u, b, seq_u);
+    seq_u *= p.Hkv;
+  }
+  __device__ __forceinline__ bool next(const P& p) {  // false: the range holds no more blocks
+    if (u >= end) return false;
+    L = context_length(p, b, false);
+    nb = S::blocks(L);
+    int w = S::units(nb);
+    while (u >= seq_u + w * p.Hkv) {  // on to the next sequence that has blocks
+      seq_u += w * p.Hkv;
+      L = context_length(p, ++b, false);
+      nb = S::blocks(L);
+      w = S::units(nb);
+    }
+    g = (u - seq_u) / w;
+    int pos = u - seq_u - g * w;
+    if (pos < S::kStart) {
+      u += S::kStart - pos;
+      pos = S::kStart;
+      if (u >= end) return false;
+    }
+    blk0 = pos - S::kStart;
+    nblk = imin(nb - blk0, end - u);
+    u += nblk;
+    return true;
+  }
+};
+
+// Four columns of one head's row from both maps' sums: the difference, its norm over the `quads`
+// lanes that hold the row (a power of two, side by side), and the store.
+template <int D>
+__device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, int head, int quad,
+                                            float4 a0, float4 a1, float2 ml0, float2 ml1,
+                                            unsigned lanes) {
+  const bool some = ml0.y != 0.f;  // an empty context has its rows zero whatever eps is
+  const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? __ldg(p.lam + head) / ml1.y : 0.f;
+  float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
+                         a0.w * f0 - a1.w * f1);
+  float rs = p.out_scale;
+  float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (p.weight) {
+    float ss = (y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w);
+#pragma unroll
+    for (int off = D / 8; off; off >>= 1) ss += __shfl_xor_sync(lanes, ss, off);
+    w = __ldg(reinterpret_cast<const float4*>(p.weight) + quad);
+    if (some) rs *= rsqrtf(ss * (1.f / D) + p.eps);
+  }
+  *reinterpret_cast<uint2*>(p.o + row * D + 4 * quad) =
+      make_uint2(pack_bf16x2(y.x * rs * w.x, y.y * rs * w.y),
+                 pack_bf16x2(y.z * rs * w.z, y.w * rs * w.w));
+  if (quad == 0)
+    *reinterpret_cast<float2*>(p.lse + 2 * row) =
+        some ? make_float2((ml0.x + log2f(ml0.y)) * 0.69314718055994530942f,
+                           (ml1.x + log2f(ml1.y)) * 0.69314718055994530942f)
+             : make_float2(-INFINITY, -INFINITY);
+}
+
+// NT: tiles of eight query heads (1 or 2).
+template <int D, int NT>
+__global__ void __launch_bounds__(160, kDiffDecodeCtas)
+    diff_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const DiffDecodeParams p) {
+  using C = DiffDecodeCfg<D>;
+  constexpr int S = C::kStages;
+  const int G = p.group;  // 1 <= G <= 8 NT
+  const int tid = static_cast<int>(threadIdx.x);
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  DiffDecodeCtrl* ctl = reinterpret_cast<DiffDecodeCtrl*>(ring + C::kRingBytes);
+  float* red_m = reinterpret_cast<float*>(ring + C::kRingBytes + 256);  // [warps][NT][16]
+  float* red_l = red_m + C::kWarps * 32;
+  static_assert(256 + 2 * C::kWarps * 32 * 4 <= C::kMiscBytes, "misc area");
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == C::kConsumers) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], C::kWarps);
+    }
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  const int worker = static_cast<int>(blockIdx.x);
+  const DiffShare share(p, 0, worker == 0 && warp == 0);
+  __syncthreads();
+  if (worker >= share.n) return;
+  SegmentWalk<DiffShare, DiffDecodeParams> seg(share, p, worker);
+  const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
+  const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
+
+  if (warp == C::kWarps) {
+    // ---------------------------------------------------------------- TMA producer
+    // A stage is one box a panel of a page of 64 tokens or of half a page of 128, or whole pages of
+    // 16 or 32, lane sb issuing page sb's boxes. Its table entry is read a stage ahead. A page past
+    // the context, or whose entry lies outside the pool (never addressed; the status word
+    // reports it), comes from the plane past the pool, which TMA fills with zeros.
+    const int lp = p.page_shift;
+    const int run = imin(C::kTok, 1 << lp), nbox = C::kTok / run;
+    int e = 0;  // stages issued
+    bool ok = true;
+    while (ok && seg.next(p)) {
+      const int* row = p.table + static_cast<size_t>(seg.b) * p.max_pages;
+      auto plane_of = [&](int i) {
+        const int tok = (seg.blk0 + i) * C::kTok + lane * run;
+        int pl = p.num_pages * p.Hkv;
+        if (lane < nbox && tok < seg.L) {
+          const int raw = __ldg(row + (tok >> lp));
+          if (raw < 0 || raw >= p.num_pages)
+            report_status(p.status, -5);
+          else
+            pl = raw * p.Hkv + seg.g;
+        }
+        return pl;
+      };
+      int pl_next = plane_of(0);
+      for (int i = 0; i < seg.nblk; ++i, ++e) {
+        const int st = e % S;
+        if (lane == 0) ok = mbar_wait(&ctl->empty[st], ((e / S) & 1) ^ 1, wc);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        uint8_t* dst = ring + st * C::kStageBytes + lane * run * 128;
+        const int pl = pl_next;
+        const int row0 = ((seg.blk0 + i) * C::kTok) & ((1 << lp) - 1);  // 64: the page's second half
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], C::kStageBytes);
+        __syncwarp();
+        if (lane < nbox) {
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+            tma_load_3d(dst + pn * C::kPanelBytes, &tm_k, &ctl->full[st], pn * 64, row0, pl);
+            tma_load_3d(dst + C::kHalfBytes + pn * C::kPanelBytes, &tm_v, &ctl->full[st], pn * 64,
+                        row0, pl);
+          }
+        }
+        if (i + 1 < seg.nblk) pl_next = plane_of(i + 1);
+      }
+    }
+    if (lane == 0)
+      for (int x = imax(0, e - S); x < e; ++x)
+        mbar_wait(&ctl->full[x % S], (x / S) & 1, wc_drain);
+    return;  // the producer takes no part in the consumer barriers below
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int r = lane >> 2;  // tile rows r (map 0) and r + 8 (map 1) of head r of a tile
+  const int q = lane & 3;
+  const float c = p.scale_log2;
+  const int tok_w = warp * 16;
+  // ldmatrix row addresses: lane -> (matrix, row).
+  const int mrow = lane & 7, msel = lane >> 3;
+  const int k_token = tok_w + 8 * (msel >> 1) + mrow;  // K: matrices (n-tile, k half)
+  const int k_half = (msel & 1) * 8;
+  const int v_token = tok_w + 8 * (msel & 1) + mrow;   // V: matrices (n-tile, token half)
+  const int v_sub = (msel >> 1) * 8;
+  int e = 0;
+  bool ok = true;
+  for (bool first = true; seg.next(p); first = false) {
+    const size_t head0 = (static_cast<size_t>(seg.b) * p.Hkv + seg.g) * G;
+    // Q as the A operand: k-step kk lies in map 2 kk / kSteps, whose rows alone are not zero.
+    uint32_t qa[NT][C::kSteps][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int kk = 0; kk < C::kSteps; ++kk) {
+        const bool here = 8 * nt + r < G;
+        const uint32_t* from = p.q + (head0 + 8 * nt + r) * (D / 2) + kk * 8 + q;
+        qa[nt][kk][0] = here ? __ldg(from) : 0u;
+        qa[nt][kk][1] = here ? __ldg(from + 4) : 0u;
+      }
+    float o[NT][D / 8][4];
+    float mx[NT][2], l[NT][2];  // of rows r and r + 8; the max in log2 units, trailing by < 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      mx[nt][0] = mx[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    int last_st = 0;
+    for (int i = 0; i < seg.nblk; ++i, ++e) {
+      const int st = e % S;
+      last_st = st;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (e / S) & 1, wc));
+      if (ok) {
+        const uint32_t kp = smem_u32(ring + st * C::kStageBytes);
+        const uint32_t vp = kp + C::kHalfBytes;
+        float s[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[nt][0][x] = s[nt][1][x] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < C::kSteps; ++kk) {
+          uint32_t kb[4];
+          ldmatrix_x4(kb, kp + page_chunk(k_token, kk * 16 + k_half));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const bool lo = kk < C::kSteps / 2;
+            const uint32_t a[4] = {lo ? qa[nt][kk][0] : 0u, lo ? 0u : qa[nt][kk][0],
+                                   lo ? qa[nt][kk][1] : 0u, lo ? 0u : qa[nt][kk][1]};
+            mma_bf16_16816(s[nt][0], a, kb[0], kb[1]);
+            mma_bf16_16816(s[nt][1], a, kb[2], kb[3]);
+          }
+        }
+        const int left = seg.L - (seg.blk0 + i) * C::kTok - tok_w;  // of the context, from this slice
+        if (left < 16) {
+          // Slots past the context may hold anything: their scores are dropped below, and their
+          // values cleared, since a NaN would survive a weight of zero.
+          for (int x = lane; x < 16 * (D / 8); x += 32) {
+            const int tok = x / (D / 8);
+            if (tok >= left)
+              st_shared_v4(vp + page_chunk(tok_w + tok, (x % (D / 8)) * 8), 0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+        uint32_t pa[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // Element x of n-tile y: row r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the slice.
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              s[nt][y][x] = 8 * y + 2 * q + (x & 1) < left ? s[nt][y][x] * c : -INFINITY;
+              top[x >> 1] = fmaxf(top[x >> 1], s[nt][y][x]);
+            }
+          float al[2] = {1.f, 1.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+            // Move the reference max only when it grows by more than 8.
+            if (top[h] > mx[nt][h] + 8.f) {
+              al[h] = fast_exp2(mx[nt][h] - top[h]);
+              mx[nt][h] = top[h];
+            }
+          }
+          if (__any_sync(0xffffffffu, al[0] < 1.f || al[1] < 1.f)) {
+#pragma unroll
+            for (int t = 0; t < D / 8; ++t) {
+              o[nt][t][0] *= al[0];
+              o[nt][t][1] *= al[0];
+              o[nt][t][2] *= al[1];
+              o[nt][t][3] *= al[1];
+            }
+            l[nt][0] *= al[0];
+            l[nt][1] *= al[1];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float sub = mx[nt][h] == -INFINITY ? 0.f : mx[nt][h];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              s[nt][y][2 * h] = fast_exp2(s[nt][y][2 * h] - sub);
+              s[nt][y][2 * h + 1] = fast_exp2(s[nt][y][2 * h + 1] - sub);
+            }
+            l[nt][h] += (s[nt][0][2 * h] + s[nt][0][2 * h + 1]) +
+                        (s[nt][1][2 * h] + s[nt][1][2 * h + 1]);
+          }
+          // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P.
+          pa[nt][0] = pack_bf16x2(s[nt][0][0], s[nt][0][1]);
+          pa[nt][1] = pack_bf16x2(s[nt][0][2], s[nt][0][3]);
+          pa[nt][2] = pack_bf16x2(s[nt][1][0], s[nt][1][1]);
+          pa[nt][3] = pack_bf16x2(s[nt][1][2], s[nt][1][3]);
+        }
+#pragma unroll
+        for (int pair = 0; pair < D / 16; ++pair) {
+          uint32_t vb[4];
+          ldmatrix_x4_trans(vb, vp + page_chunk(v_token, pair * 16 + v_sub));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(o[nt][2 * pair], pa[nt], vb[0], vb[1]);
+            mma_bf16_16816(o[nt][2 * pair + 1], pa[nt], vb[2], vb[3]);
+          }
+        }
+      }
+      __syncwarp();
+      // The segment's last slot is kept for the merge.
+      if (lane == 0 && i + 1 < seg.nblk) mbar_arrive(&ctl->empty[st]);
+    }
+    // ---------------------------------------------------------------- the segment's rows
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 1);
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 2);
+        if (q == 0) {
+          red_m[(warp * NT + nt) * 16 + 8 * h + r] = mx[nt][h];
+          red_l[(warp * NT + nt) * 16 + 8 * h + r] = l[nt][h];
+        }
+      }
+    named_barrier_sync(1, C::kConsumers);  // and every consumer is past its last read of the slot
+    // Each warp's rows, rescaled to the common max: [warp][16][D] fp32, columns rotated by eight a
+    // row against bank conflicts.
+    float* buf = reinterpret_cast<float*>(ring + last_st * C::kStageBytes);
+    const bool whole = seg.nblk == seg.nb;
+    const size_t slot = 2 * static_cast<size_t>(worker) + (first ? 0 : 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt) named_barrier_sync(1, C::kConsumers);  // the tile before has been read
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = nt * 16 + 8 * h + r;
+        float M = red_m[at];
+#pragma unroll
+        for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * NT * 16 + at]);
+        const float f = l[nt][h] != 0.f ? fast_exp2(mx[nt][h] - M) : 0.f;
+        if (8 * nt + r < G) {
+          float* to = buf + (warp * 16 + 8 * h + r) * D;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t)
+            *reinterpret_cast<float2*>(to + ((8 * t + 2 * q + 8 * r) & (D - 1))) =
+                make_float2(o[nt][t][2 * h] * f, o[nt][t][2 * h + 1] * f);
+        }
+      }
+      named_barrier_sync(1, C::kConsumers);
+      constexpr int kQuads = D / 4;
+      const int heads = imin(8, G - 8 * nt);
+      for (int idx = tid; idx < heads * kQuads; idx += C::kConsumers) {
+        const int hh = idx / kQuads, quad = idx % kQuads;
+        const int col = (4 * quad + 8 * hh) & (D - 1);
+        float4 a[2];
+        float2 ml[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float* from = buf + (8 * h + hh) * D + col;
+          float4 w[C::kWarps];
+#pragma unroll
+          for (int x = 0; x < C::kWarps; ++x)
+            w[x] = *reinterpret_cast<const float4*>(from + x * 16 * D);
+          a[h] = make_float4((w[0].x + w[2].x) + (w[1].x + w[3].x),
+                             (w[0].y + w[2].y) + (w[1].y + w[3].y),
+                             (w[0].z + w[2].z) + (w[1].z + w[3].z),
+                             (w[0].w + w[2].w) + (w[1].w + w[3].w));
+          const int at = nt * 16 + 8 * h + hh;
+          float M = red_m[at], Ls = 0.f;
+#pragma unroll
+          for (int x = 1; x < C::kWarps; ++x) M = fmaxf(M, red_m[x * NT * 16 + at]);
+#pragma unroll
+          for (int x = 0; x < C::kWarps; ++x) {
+            const float lw = red_l[x * NT * 16 + at];
+            if (lw != 0.f) Ls += lw * fast_exp2(red_m[x * NT * 16 + at] - M);
+          }
+          ml[h] = make_float2(M, Ls);
+        }
+        const int hg = 8 * nt + hh;
+        if (whole) {
+          const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+          diff_finish<D>(p, head0 + hg, seg.g * G + hg, quad, a[0], a[1], ml[0], ml[1], lanes);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const size_t at = (slot * 2 + h) * G + hg;
+            *reinterpret_cast<float4*>(p.part_o + at * D + 4 * quad) = a[h];
+            if (quad == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = ml[h];
+          }
+        }
+      }
+    }
+    fence_proxy_async_smem();  // the merge's plain accesses, before the slot's next copy
+    named_barrier_sync(1, C::kConsumers);
+    if (lane == 0) mbar_arrive(&ctl->empty[last_st]);
+  }
+}
+
+// Joins the parts of contexts that several workers share, and writes the rows of empty ones. A CTA
+// takes join_heads heads of a (kv head, sequence); a thread four columns of both maps of one head,
+// and where that leaves threads over, set s of them takes the parts s, s + sets, ...; the sets' sums
+// are added in order.
+constexpr int kDiffJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kDiffJoinThreads) diff_join_kernel(const DiffDecodeParams p) {
+  constexpr int kQuads = D / 4, kBatch = 4;
+  __shared__ float2 sml[2][kDiffJoinThreads];
+  __shared__ float4 so[2][kDiffJoinThreads];
+  const int G = p.group, H = p.join_heads;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
+  const int g = h0 / G, hg = h0 % G;
+  // Without keys this kernel runs alone, and reports what is wrong with the lengths.
+  const DiffShare share(p, b, p.max_len == 0 && blockIdx.x == 0 && b == 0 && tid < 32);
+  const int nb = share.blocks(context_length(p, b, false));
+  const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
+  // Every CTA waits, those without work too: this kernel must not end before the first one.
+  if (nb == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < H * kQuads; i += kDiffJoinThreads)
+      reinterpret_cast<uint2*>(p.o + head0 * D)[i] = make_uint2(0, 0);
+    for (int i = tid; i < 2 * H; i += kDiffJoinThreads) p.lse[2 * head0 + i] = -INFINITY;
+    return;
+  }
+  // The context's first unit, and the workers of its first and last block; the first part is its
+  // worker's first segment only if that has no block of a context before.
+  const int w = share.units(nb), u0 = share.before * p.Hkv + g * w;
+  const int c0 = share.worker_of(u0 + share.kStart);
+  const int parts = share.worker_of(u0 + w - 1) - c0 + 1;
+  const int slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (parts == 1) return;  // one worker held the whole context
+  const int items = H * kQuads;
+  const int sets = imax(1, imin(kDiffJoinThreads / items, parts));
+  const int set = items < kDiffJoinThreads ? tid / items : 0;
+  for (int it0 = 0; it0 < items; it0 += kDiffJoinThreads) {
+    const int item = it0 + (items < kDiffJoinThreads ? tid % items : tid);
+    const bool here = item < items && set < sets;
+    const int hh = item / kQuads, quad = item % kQuads;
+    float2 ml[2];
+    float4 a[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float M = -INFINITY, Ls = 0.f;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x0 = here ? set : parts; x0 < parts; x0 += sets * kBatch) {
+        float2 pm[kBatch];
+        float4 po[kBatch];
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+          const int x = imin(x0 + t * sets, parts - 1);
+          const size_t at =
+              (static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * 2 + h) * G + hg + hh;
+          pm[t] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
+          po[t] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * quad));
+        }
+        float Mn = M;
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, pm[t].x);
+        const float f = Ls != 0.f ? exp2f(M - Mn) : 0.f;
+        M = Mn;
+        Ls *= f;
+        s.x *= f, s.y *= f, s.z *= f, s.w *= f;
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+          if (x0 + t * sets < parts) {
+            const float wt = exp2f(pm[t].x - M);
+            Ls += pm[t].y * wt;
+            s.x += po[t].x * wt, s.y += po[t].y * wt, s.z += po[t].z * wt, s.w += po[t].w * wt;
+          }
+      }
+      a[h] = s;
+      ml[h] = make_float2(M, Ls);
+    }
+    if (sets > 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) so[h][tid] = a[h], sml[h][tid] = ml[h];
+      __syncthreads();
+      if (set == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float M = ml[h].x, Ls = 0.f;
+          for (int i = 1; i < sets; ++i) M = fmaxf(M, sml[h][tid + i * items].x);
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < sets; ++i) {
+            const float2 z = sml[h][tid + i * items];
+            if (z.y == 0.f) continue;  // more sets than parts
+            const float f = exp2f(z.x - M);
+            const float4 x = so[h][tid + i * items];
+            Ls += z.y * f;
+            s.x += x.x * f, s.y += x.y * f, s.z += x.z * f, s.w += x.w * f;
+          }
+          a[h] = s;
+          ml[h] = make_float2(M, Ls);
+        }
+      }
+    }
+    if (here && set == 0) {
+      const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (tid & 16);
+      diff_finish<D>(p, head0 + hh, h0 + hh, quad, a[0], a[1], ml[0], ml[1], lanes);
+    }
+  }
+}
+
+}  // namespace ta
