@@ -365,6 +365,13 @@ __global__ void __launch_bounds__(384, 1)
       if (rng.hi <= rng.lo) continue;
       const int k_org = un.k_org, k_end = un.k_end, bh = un.bh;
       const int row = un.q_row0 + r;
+      // Keys that every row of the tile sees, and those that this row sees, from the range's first
+      // key on.
+      const int key0 = k_org + rng.lo * BN;
+      const int full_lo = vis_lo(mask, p.window, k_org, imin(un.q_row0 + BM, k_end) - 1) - key0;
+      const int full_hi = vis_hi(mask, p.window, k_end, un.q_row0) - key0 - (BN - 1);
+      const int see_lo = vis_lo(mask, p.window, k_org, row) - key0;
+      const int see_hi = vis_hi(mask, p.window, k_end, row) - key0;
       float m_run = -INFINITY;  // running max in log2 units (may trail the true max by < 8)
       float l_run = 0.f;
       for (int j = rng.lo; j < rng.hi && ok; ++j) {
@@ -384,11 +391,9 @@ __global__ void __launch_bounds__(384, 1)
         float* f1 = reinterpret_cast<float*>(s1);
         float* f2 = reinterpret_cast<float*>(s2);
         float* f3 = reinterpret_cast<float*>(s3);
-        if (tile_kind(mask, p.window, un.q_row0, BM, k_end, k_org, k_end, BN, j) ==
-            kTileBoundary) {
-          const int key0 = k_org + j * BN;
-          const int lo_k = vis_lo(mask, p.window, k_org, row) - key0;
-          const int hi_k = vis_hi(mask, p.window, k_end, row) - key0;
+        const int at = (j - rng.lo) * BN;
+        if (at < full_lo || at > full_hi) {
+          const int lo_k = see_lo - at, hi_k = see_hi - at;
           const uint32_t b0 = vis_bits32(lo_k, hi_k), b1 = vis_bits32(lo_k - 32, hi_k - 32);
           const uint32_t b2 = vis_bits32(lo_k - 64, hi_k - 64);
           const uint32_t b3 = vis_bits32(lo_k - 96, hi_k - 96);
