@@ -18,7 +18,7 @@ cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
                        const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
   static unsigned long long done = 0;
   auto kern = diff_prefill_kernel<D, PACK>;
-  using C = DiffCfg<D>;
+  using C = DiffCfg<D, PACK>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(q, k, v, o, p);
@@ -112,8 +112,9 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   CUtensorMap tq, tk, tv, to;
   if ((rc = encode_3d(&tq, q, d, N, planes, 128))) return rc;
   if ((rc = encode_3d(&to, o, d, N, planes, 32, d / 2))) return rc;
-  if ((rc = encode_3d(&tk, k, d, N, planes_kv, 128))) return rc;
-  if ((rc = encode_3d(&tv, v, d, N, planes_kv, 128))) return rc;
+  const uint32_t tile = d == 64 ? DiffCfg<64, kMaskNone>::BN : DiffCfg<128, kMaskNone>::BN;
+  if ((rc = encode_3d(&tk, k, d, N, planes_kv, tile))) return rc;
+  if ((rc = encode_3d(&tv, v, d, N, planes_kv, tile))) return rc;
   p.base.o = o;
   p.base.lse = lse;
   p.base.cu_seqlens = cu_seqlens;
@@ -173,8 +174,9 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   if ((rc = encode_3d(&tq, q, d, total_q, Hq, 128))) return rc;
   if ((rc = encode_3d(&to, o, d, total_q, Hq, 32, d / 2))) return rc;
   const uint64_t planes = static_cast<uint64_t>(num_pages) * Hkv;
-  if ((rc = encode_3d(&tk, k, d, page_size, planes, page_size))) return rc;
-  if ((rc = encode_3d(&tv, v, d, page_size, planes, page_size))) return rc;
+  const uint32_t box = page_size < 64 ? page_size : 64;  // rows of a page in one 64-key tile
+  if ((rc = encode_3d(&tk, k, d, page_size, planes, box))) return rc;
+  if ((rc = encode_3d(&tv, v, d, page_size, planes, box))) return rc;
   p.base.o = o;
   p.base.lse = lse;
   p.base.cu_seqlens = cu_seqlens_q;

@@ -45,38 +45,150 @@ struct DiffParams {
   int mask;              // of the dense and document kinds
 };
 
-template <int D>
+constexpr float kDiffRaise = 18446744073709551616.f;  // 2^64
+
+constexpr int imin_c(int a, int b) { return a < b ? a : b; }
+
+template <int D, int PACK>
 struct DiffCfg {
-  static constexpr int BM = 128, BN = 128;
+  static constexpr int BM = 128;
+  static constexpr int BN = D == 64 && PACK != kMaskPagedPrefill ? 96 : 64;
   static constexpr int kThreads = 384;
   static constexpr int kPanels = D / 64;
-  static constexpr int kChunkBytes = 128 * 128;      // 64 columns of 128 rows
-  static constexpr int kTileBytes = 128 * D * 2;     // Q, K or V
+  static constexpr int kQPanelBytes = BM * 128;      // 64 columns of a Q tile
+  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kPanelBytes = BN * 128;       // 64 columns of a K or V tile
+  static constexpr int kTileBytes = BN * D * 2;
+  static constexpr int kStageBytes = 2 * kTileBytes; // K, then V
   static constexpr int kQBufs = 2;                   // this unit's and the next one's
-  static constexpr int kStages = D == 128 ? 5 : 12;
   static constexpr int kCtrlBytes = 2048;
-  static constexpr int kSmemBytes = 1024 + (kQBufs + kStages) * kTileBytes + kCtrlBytes;
+  static constexpr int kStages =
+      imin_c((232448 - 1024 - kCtrlBytes - kQBufs * kQBytes) / kStageBytes, 8);
+  static constexpr int kSmemBytes = 1024 + kQBufs * kQBytes + kStages * kStageBytes + kCtrlBytes;
   static constexpr int kTmemCols = 512;
-  static constexpr int kOCol = 256;
+  static constexpr int kOCol = 4 * BN;
   static constexpr int kSteps = D / 32;              // 16-channel k-steps of one map
   static constexpr int kHalf = D / 2;                // columns of O a softmax warp writes
   static constexpr uint32_t kRegsControl = 88, kRegsSoftmax = 208;
   static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
   static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kOCol + 2 * D <= kTmemCols, "TMEM columns");
   static constexpr uint32_t kIdescS = idesc_bf16(BM, BN, false, false);
   static constexpr uint32_t kIdescO = idesc_bf16(BM, D, false, true);
 };
 
 struct DiffCtrl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[12], kv_empty[12];
-  uint64_t s_ready[2], p_ready[2], o_done, drain;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_ready[2][2], p_ready[2][2];  // of map m, buffer b
+  uint64_t o_done, drain[2];
   uint64_t both[4];          // warps q of the two softmax warpgroups
   uint32_t tmem_base;
   int abort_flag;
   float coef[2][128];        // 1 / l of map 0's rows, lam / l of map 1's
   float weight[128];         // out_scale * w
 };
+
+// Waits and commits by a barrier's shared-memory address. A wait looks at the clock every 64 polls
+// only.
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
+                                          int* status, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t polls = 0; polls < (1u << 20); ++polls) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_at(bar, parity)) return true;
+    if (*abort_flag) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > timeout_ns) break;
+  }
+  *abort_flag = 1;
+  report_status(status, -4);
+  return false;
+}
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  return __all_sync(0xffffffffu, try_wait_at(bar, parity)) ||
+         __all_sync(0xffffffffu, wait_at_slow(bar, parity, w.timeout_ns, w.status, w.abort_flag));
+}
+// One lane's commit: `lead` is set in the lane that issues the MMAs.
+__device__ __forceinline__ void commit_at(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
+// N SS MMAs of one accumulator from the lane where `lead` is set: k-steps of 16 columns, 32 bytes apart in both
+// operands; the first overwrites D.
+template <int N>
+__device__ __forceinline__ void mma_ss_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t lead) {
+  static_assert(N == 2 || N == 4, "k-steps");
+  if constexpr (N == 4)
+    asm volatile(
+        "{\n .reg .pred e, t, f;\n .reg .b64 a1, b1, a2, b2, a3, b3;\n"
+        " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n"
+        " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+        " add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+        " setp.ne.b32 e, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e, t, f;\n .reg .b64 a1, b1;\n"
+        " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n"
+        " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
+        " setp.ne.b32 e, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+}
+
+// N TS MMAs of one accumulator from the lane where `lead` is set: A from TMEM, 8 columns a 16-key step, B an
+// MN-major operand whose steps are 2048 bytes apart; the first accumulates iff acc0.
+template <int N>
+__device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t acc0, uint32_t lead) {
+  static_assert(N == 4 || N == 6, "k-steps");
+  asm volatile(
+      "{\n .reg .pred e, t, p;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+      " setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc0), "r"(lead)
+      : "memory");
+  if constexpr (N == 6)
+    asm volatile(
+        "{\n .reg .pred e, t;\n .reg .b64 b1;\n .reg .b32 a1;\n setp.ne.b32 t, 1, 0;\n"
+        " add.s32 a1, %1, 8;\n add.s64 b1, %2, 128;\n"
+        " setp.ne.b32 e, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n}" ::"r"(d),
+        "r"(a + 32), "l"(b + 512), "r"(idesc), "r"(lead)
+        : "memory");
+}
 
 // Work unit u in launch order: 128-row tiles from the last one down, then batch and head; packed
 // kinds take the two halves of prefill.cuh's 256-row units, the later (longer) one first. q_row0
@@ -108,7 +220,7 @@ __global__ void __launch_bounds__(384, 1)
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_o, const DiffParams dp) {
-  using C = DiffCfg<D>;
+  using C = DiffCfg<D, PACK>;
   constexpr int BM = C::BM, BN = C::BN, STAGES = C::kStages, QB = C::kQBufs;
   constexpr bool kPaged = PACK == kMaskPagedPrefill;
   constexpr unsigned kFull = 0xffffffffu;
@@ -118,8 +230,8 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = smem;
-  uint8_t* kv_s = smem + QB * C::kTileBytes;
-  DiffCtrl* ctl = reinterpret_cast<DiffCtrl*>(kv_s + STAGES * C::kTileBytes);
+  uint8_t* kv_s = smem + QB * C::kQBytes;
+  DiffCtrl* ctl = reinterpret_cast<DiffCtrl*>(kv_s + STAGES * C::kStageBytes);
   static_assert(sizeof(DiffCtrl) <= C::kCtrlBytes, "control block");
 
   const int warp = static_cast<int>(threadIdx.x >> 5);
@@ -132,15 +244,17 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(&ctl->q_empty[q], 8);  // one arrival per softmax warp
       }
       for (int s = 0; s < STAGES; ++s) {
-        mbar_init(&ctl->kv_full[s], 1);
-        mbar_init(&ctl->kv_empty[s], 1);
+        mbar_init(&ctl->kv_full[s], kPaged ? 2 : 1);  // an arrival for K, one for V
+        mbar_init(&ctl->kv_empty[s], 2);  // one release per issuing warp
       }
       for (int m = 0; m < 2; ++m) {
-        mbar_init(&ctl->s_ready[m], 1);
-        mbar_init(&ctl->p_ready[m], 128);
+        for (int x = 0; x < 2; ++x) {
+          mbar_init(&ctl->s_ready[m][x], 1);
+          mbar_init(&ctl->p_ready[m][x], 4);  // one arrival per warp
+        }
+        mbar_init(&ctl->drain[m], 1);
       }
-      mbar_init(&ctl->o_done, 1);
-      mbar_init(&ctl->drain, 1);
+      mbar_init(&ctl->o_done, 2);
       for (int q = 0; q < 4; ++q) mbar_init(&ctl->both[q], 2);
       fence_mbar_init();
       prefetch_tensormap(&tm_q);
@@ -174,7 +288,7 @@ __global__ void __launch_bounds__(384, 1)
     const bool split_v = kPaged && p.page_shift < 6;
     if (warp == 0 || (split_v && warp == 3)) {
       // -------------------------------------------------------------- TMA producer
-      int e = 0;   // K/V ring entries
+      int e = 0;   // K/V stages
       int qn = 0;  // Q loads issued
       bool ok = true;
       for (int k = 0; ok; ++k) {
@@ -191,34 +305,37 @@ __global__ void __launch_bounds__(384, 1)
             ok = mbar_wait(&ctl->q_empty[qb], ((qn / QB) & 1) ^ 1, wc);
             if (ok) {
               ++qn;
-              mbar_arrive_expect_tx(&ctl->q_full[qb], C::kTileBytes);
+              mbar_arrive_expect_tx(&ctl->q_full[qb], C::kQBytes);
               for (int c = 0; c < C::kPanels; ++c)
-                tma_load_3d(q_s + qb * C::kTileBytes + c * C::kChunkBytes, &tm_q,
+                tma_load_3d(q_s + qb * C::kQBytes + c * C::kQPanelBytes, &tm_q,
                             &ctl->q_full[qb], c * 64, un.q_row0, un.bh);
             }
           }
-          // Ring entry: K (even x) or V of the key tile at position x / 2.
-          for (int x = 0; !kPaged && x < 2 * npos && ok; ++x, ++e) {
+          for (int x = 0; !kPaged && x < npos && ok; ++x, ++e) {
             const int st = e % STAGES;
             ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
             if (!ok) break;
-            mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
+            mbar_arrive_expect_tx(&ctl->kv_full[st], C::kStageBytes);
+            uint8_t* dst = kv_s + st * C::kStageBytes;
+            const int key = un.k_org + (rng.lo + x) * BN;
             for (int c = 0; c < C::kPanels; ++c)
-              tma_load_3d(kv_s + st * C::kTileBytes + c * C::kChunkBytes, (x & 1) ? &tm_v : &tm_k,
-                          &ctl->kv_full[st], c * 64, un.k_org + (rng.lo + x / 2) * BN, un.kvh);
+              tma_load_3d(dst + c * C::kPanelBytes, &tm_k, &ctl->kv_full[st], c * 64, key, un.kvh);
+            for (int c = 0; c < C::kPanels; ++c)
+              tma_load_3d(dst + C::kTileBytes + c * C::kPanelBytes, &tm_v, &ctl->kv_full[st], c * 64,
+                          key, un.kvh);
           }
         }
         ok = __shfl_sync(kFull, ok, 0);
         if constexpr (kPaged) {
-          // Lane sb owns page sb of every key tile, as in prefill.cuh: it reads the page's entry a
-          // tile ahead and issues its boxes; pages past the context or outside the pool come
-          // from the zero-filled plane past it.
+          // Lane sb owns page sb of every key tile (one half of a page of 128), as in prefill.cuh: it
+          // reads the page's entry a tile ahead and issues its boxes; pages past the context or
+          // outside the pool come from the zero-filled plane past it.
           const int lp = p.page_shift;
-          const int nb = BN >> lp;
+          const int run = imin(BN, 1 << lp), nb = BN / run;
           const int lk = un.k_end - un.k_org;
           const int* trow = p.table + static_cast<size_t>(un.seq) * p.max_pages;
           auto plane_of = [&](int j) {
-            const int tok = j * BN + (lane << lp);
+            const int tok = j * BN + lane * run;
             int pl = p.num_pages * p.Hkv;
             if (lane < nb && tok < lk) {
               const int raw = __ldg(trow + (tok >> lp));
@@ -229,38 +346,65 @@ __global__ void __launch_bounds__(384, 1)
             }
             return pl;
           };
-          int pl_next = plane_of(rng.lo), pl = 0;
-          for (int x = 0; x < 2 * npos && ok; ++x, ++e) {
-            if (split_v && (x & 1) != (warp == 3 ? 1 : 0)) continue;  // the other warp's entry
+          // With pages under 64 tokens warp 0 brings K and warp 3 V, else warp 0 both.
+          const int first = warp == 3 ? 1 : 0, last = split_v && warp == 0 ? 0 : 1;
+          int pl_next = plane_of(rng.lo);
+          for (int x = 0; x < npos && ok; ++x, ++e) {
             const int st = e % STAGES;
             if (lane == 0) ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
             ok = __shfl_sync(kFull, ok, 0);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
+            if (lane == 0)
+              for (int y = first; y <= last; ++y)
+                mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
             __syncwarp();
-            if (split_v || !(x & 1)) pl = pl_next;  // the first entry of its tile this warp issues
+            const int pl = pl_next;
             if (lane < nb) {
-              for (int c = 0; c < C::kPanels; ++c)
-                tma_load_3d(kv_s + st * C::kTileBytes + c * C::kChunkBytes + (lane << lp) * 128,
-                            (x & 1) ? &tm_v : &tm_k, &ctl->kv_full[st], c * 64, 0, pl);
+              const int row0 = nb > 1 ? 0 : ((rng.lo + x) * BN) & ((1 << lp) - 1);
+              uint8_t* dst = kv_s + st * C::kStageBytes + lane * run * 128;
+              for (int y = first; y <= last; ++y)
+                for (int c = 0; c < C::kPanels; ++c)
+                  tma_load_3d(dst + y * C::kTileBytes + c * C::kPanelBytes, y ? &tm_v : &tm_k,
+                              &ctl->kv_full[st], c * 64, row0, pl);
             }
-            if ((split_v || !(x & 1)) && x / 2 + 1 < npos) pl_next = plane_of(rng.lo + x / 2 + 1);
+            if (x + 1 < npos) pl_next = plane_of(rng.lo + x + 1);
           }
         }
       }
       if (lane == 0) {
         // Let copies still in flight land before the CTA can exit (no-op on the normal path).
         for (int x = imax(0, e - STAGES); x < e; ++x)
-          if (!split_v || (x & 1) == (warp == 3 ? 1 : 0))
-            mbar_wait(&ctl->kv_full[x % STAGES], (x / STAGES) & 1, wc_drain);
+          mbar_wait(&ctl->kv_full[x % STAGES], (x / STAGES) & 1, wc_drain);
         for (int x = imax(0, qn - QB); x < qn; ++x)
           mbar_wait(&ctl->q_full[x % QB], (x / QB) & 1, wc_drain);
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------------- MMA issuer
-      int e = 0;   // ring entry of the unit's first K
-      int qn = 0;  // Q tiles used
-      int pn = 0;  // P tiles consumed, of each map
+    } else if (warp == 1 || warp == 2) {
+      // -------------------------------------------------------------- MMA issuers
+      // Warp 1 issues map 0's MMAs, warp 2 map 1's. S of positions 0 and 1 go first; step x is P V of
+      // position x, then S of x + 2 into the buffer that P V has just read (MMAs of one thread run
+      // in order), so the map's next S is there when its softmax is done with this one. Every ring
+      // entry takes one release from each issuer.
+      const int m = warp - 1;
+      uint32_t lead;
+      asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}"
+                   : "=r"(lead));
+      const uint32_t full0 = smem_u32(ctl->kv_full), empty0 = smem_u32(ctl->kv_empty);
+      const uint32_t s_bar = smem_u32(ctl->s_ready[m]), p_bar = smem_u32(ctl->p_ready[m]);
+      // Operands of map m in stage 0 and the Q tiles: a map's k-steps are 32 bytes apart inside a
+      // 128-byte swizzle row, four steps a panel.
+      constexpr int kPer = 4 / C::kSteps;  // maps of a panel
+      const uint64_t k_desc0 =
+          sw128_desc(smem_u32(kv_s), 16, 1024) +
+          ((m / kPer * C::kPanelBytes + m % kPer * C::kSteps * 32) >> 4);
+      const uint64_t v_desc0 = sw128_desc(smem_u32(kv_s) + C::kTileBytes, C::kPanelBytes, 1024);
+      const uint64_t q_desc0 =
+          sw128_desc(smem_u32(q_s), 16, 1024) +
+          ((m / kPer * C::kQPanelBytes + m % kPer * C::kSteps * 32) >> 4);
+      const uint32_t d_s = tmem + 2 * m * BN, d_o = tmem + C::kOCol + m * D;
+      // Stage of the next S and of the next P V, the parity of the former's, and of Q's and P's.
+      int st_s = 0, st_v = 0, qn = 0;
+      uint32_t ph_s = 0, ph_p = 0;
+      uint32_t buf = 0;  // S buffer of the next P
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int u = unit_of(k);
@@ -270,67 +414,49 @@ __global__ void __launch_bounds__(384, 1)
         const KvRange rng = range_of(un);
         const int npos = rng.hi - rng.lo;
         if (npos <= 0) continue;
-        const uint64_t q_desc = sw128_desc(smem_u32(q_s + (qn % QB) * C::kTileBytes), 16, 1024);
-        // Step x: P V of the key tile at position x - 1, then S of the one at x, map by map.
-        for (int x = 0; x <= npos && ok; ++x) {
-          const bool have_v = x > 0, have_k = x < npos;
-          const int ev = e + 2 * x - 1, ek = e + 2 * x;
-          {
-            const bool rv = !have_v || mbar_try_wait(&ctl->kv_full[ev % STAGES], (ev / STAGES) & 1);
-            const bool rk = !have_k || mbar_try_wait(&ctl->kv_full[ek % STAGES], (ek / STAGES) & 1);
-            if (!__all_sync(kFull, rv && rk)) {
-              if (have_v)
-                ok = __all_sync(kFull,
-                                mbar_wait(&ctl->kv_full[ev % STAGES], (ev / STAGES) & 1, wc));
-              if (have_k && ok)
-                ok = __all_sync(kFull,
-                                mbar_wait(&ctl->kv_full[ek % STAGES], (ek / STAGES) & 1, wc));
-            }
-            if (ok && x == 0)
-              ok = __all_sync(kFull, mbar_wait(&ctl->q_full[qn % QB], (qn / QB) & 1, wc));
-          }
+        const uint64_t q_desc = q_desc0 + (qn % QB) * (C::kQBytes >> 4);
+        auto issue_s = [&](uint32_t b) {
+          mma_ss_steps<C::kSteps>(d_s + b * BN, q_desc, k_desc0 + st_s * (C::kStageBytes >> 4),
+                                  C::kIdescS, lead);
+          commit_at(s_bar + 8 * b, lead);
+          if (++st_s == STAGES) st_s = 0, ph_s ^= 1;
+        };
+        ok = wait_at(smem_u32(&ctl->q_full[qn % QB]), (qn / QB) & 1, wc);
+        for (int x = 0; x < 2 && x < npos && ok; ++x) {
+          ok = wait_at(full0 + 8 * st_s, ph_s, wc);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v_desc =
-              sw128_desc(smem_u32(kv_s + (ev % STAGES) * C::kTileBytes), C::kChunkBytes, 1024);
-          const uint64_t k_desc =
-              sw128_desc(smem_u32(kv_s + (ek % STAGES) * C::kTileBytes), 16, 1024);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (have_v) {
-              const int ph = (pn + x - 1) & 1;
-              if (!__all_sync(kFull, mbar_try_wait(&ctl->p_ready[m], ph)))
-                ok = __all_sync(kFull, mbar_wait(&ctl->p_ready[m], ph, wc));
-              if (!ok) break;
-              tc_fence_after();
-              // The unit's first P V overwrites O_m: both warps of every row published this P
-              // after they had read O of the unit before.
-              mma_ts_chain8(tmem + C::kOCol + m * D, tmem + m * 128, v_desc, C::kIdescO, x > 1);
-              if (m == 1) {
-                mma_commit(&ctl->kv_empty[ev % STAGES]);
-                if (!have_k) mma_commit(&ctl->o_done);
-              }
-            }
-            if (have_k) {
-#pragma unroll
-              for (int s = 0; s < C::kSteps; ++s) {
-                // 32 bytes a step inside a 128-byte swizzle row, four steps a panel.
-                const int at = m * C::kSteps + s;
-                const uint32_t off16 = ((at >> 2) * C::kChunkBytes + (at & 3) * 32) >> 4;
-                mma_ss(tmem + m * 128, q_desc + off16, k_desc + off16, C::kIdescS, s > 0);
-              }
-              mma_commit(&ctl->s_ready[m]);
-              if (m == 1) mma_commit(&ctl->kv_empty[ek % STAGES]);
-            }
-          }
+          issue_s(buf ^ x);
         }
-        e += 2 * npos;
-        pn += npos;
+        if (!ok) break;
+        for (int x = 0; x < npos; ++x) {
+          // P and the next K together: looking at a barrier takes 80 cycles, and the tensor core may
+          // run dry meanwhile.
+          const bool more = x + 2 < npos;
+          const bool rp = try_wait_at(p_bar + 8 * buf, ph_p);
+          const bool rk = !more || try_wait_at(full0 + 8 * st_s, ph_s);
+          if (!__all_sync(kFull, rp && rk)) {
+            ok = wait_at(p_bar + 8 * buf, ph_p, wc) &&
+                 (!more || wait_at(full0 + 8 * st_s, ph_s, wc));
+            if (!ok) break;
+          }
+          tc_fence_after();
+          // The unit's first P V overwrites O_m: both warps of every row published this P after they
+          // had read O of the unit before.
+          mma_ts_steps<BN / 16>(d_o, d_s + buf * BN, v_desc0 + st_v * (C::kStageBytes >> 4),
+                                C::kIdescO, x > 0, lead);
+          if (more) issue_s(buf);
+          commit_at(empty0 + 8 * st_v, lead);  // K and V of the stage are done with
+          if (++st_v == STAGES) st_v = 0;
+          ph_p ^= buf;
+          buf ^= 1;
+        }
+        commit_at(smem_u32(&ctl->o_done), lead);
         ++qn;
       }
       // Every MMA this warp issued has completed before TMEM can be released.
-      mma_commit(&ctl->drain);
-      mbar_wait(&ctl->drain, 0, wc_drain);
+      commit_at(smem_u32(&ctl->drain[m]), lead);
+      mbar_wait(&ctl->drain[m], 0, wc_drain);
     }
   } else {
     regs_increase<C::kRegsSoftmax>();
@@ -339,11 +465,11 @@ __global__ void __launch_bounds__(384, 1)
     const int quarter = warp & 3;           // TMEM lanes [32*quarter, 32*quarter + 32)
     const int r = quarter * 32 + lane;      // row inside the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_col = lane_base + m * 128;
+    const uint32_t s_bar = smem_u32(ctl->s_ready[m]);
     const float c = p.scale_log2;
     int sc = 0;          // S tiles consumed
     int un_done = 0;     // units with work finished
-    int e = 0;           // ring entry of the unit's first K
+    int e = 0;           // stage of the unit's first key tile
     int pending_q = -1;  // Q buffer whose O store may still be reading it
     auto release_pending = [&]() {
       if (pending_q >= 0) {
@@ -374,83 +500,100 @@ __global__ void __launch_bounds__(384, 1)
       const int see_hi = vis_hi(mask, p.window, k_end, row) - key0;
       float m_run = -INFINITY;  // running max in log2 units (may trail the true max by < 8)
       float l_run = 0.f;
+      constexpr int kParts = BN / 32;
+      const float2 cc2 = make_float2(c, c);
       for (int j = rng.lo; j < rng.hi && ok; ++j) {
-        ok = __all_sync(kFull, mbar_wait(&ctl->s_ready[m], (sc++) & 1, wc));
+        const int buf = sc & 1;
+        ok = wait_at(s_bar + 8 * buf, (sc >> 1) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s0[32], s1[32], s2[32], s3[32];
-        tmem_ld_x32(s_col + 0, s0);
-        tmem_ld_x32(s_col + 32, s1);
-        tmem_ld_x32(s_col + 64, s2);
-        tmem_ld_x32(s_col + 96, s3);
-        tmem_wait_ld_x32(s0);
-        tmem_wait_ld_x32(s1);
-        tmem_wait_ld_x32(s2);
-        tmem_wait_ld_x32(s3);
-        float* f0 = reinterpret_cast<float*>(s0);
-        float* f1 = reinterpret_cast<float*>(s1);
-        float* f2 = reinterpret_cast<float*>(s2);
-        float* f3 = reinterpret_cast<float*>(s3);
+        const uint32_t s_col = lane_base + (2 * m + buf) * BN;
         const int at = (j - rng.lo) * BN;
-        if (at < full_lo || at > full_hi) {
-          const int lo_k = see_lo - at, hi_k = see_hi - at;
-          const uint32_t b0 = vis_bits32(lo_k, hi_k), b1 = vis_bits32(lo_k - 32, hi_k - 32);
-          const uint32_t b2 = vis_bits32(lo_k - 64, hi_k - 64);
-          const uint32_t b3 = vis_bits32(lo_k - 96, hi_k - 96);
+        // Weights 2^(c s - m_run) against the reference max that the row has so far: weights are
+        // floating-point, so that a score far above it costs no accuracy, only range, and a sum above
+        // 2^64 tells of one. A row's first tile, such a one and boundary tiles take the longer way
+        // below, which finds the max and hides what a row does not see; S is still in TMEM then.
+        bool slow = j == rng.lo || at < full_lo || at > full_hi;
+        if (!slow) {
+          uint32_t s[kParts][32], pk[kParts][16];
 #pragma unroll
-          for (int t = 0; t < 32; ++t) {
-            if (!(b0 & (1u << t))) f0[t] = -INFINITY;
-            if (!(b1 & (1u << t))) f1[t] = -INFINITY;
-            if (!(b2 & (1u << t))) f2[t] = -INFINITY;
-            if (!(b3 & (1u << t))) f3[t] = -INFINITY;
+          for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
+#pragma unroll
+          for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
+          const float2 mm = make_float2(-m_run, -m_run);  // of a row yet without keys: +inf
+#pragma unroll
+          for (int y = 0; y < kParts; ++y)
+            exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, mm, sa, sb, pk[y]);
+          sa = __fadd2_rn(sa, sb);
+          const float sum = sa.x + sa.y;
+          slow = __any_sync(kFull, !(sum <= kDiffRaise));
+          if (!slow) {
+            l_run += sum;
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
           }
         }
-        // Row max: four independent chains of 3-input max over the 128 scores.
-        float mx0 = fmax3(f0[0], f0[1], f0[2]), mx1 = fmax3(f1[0], f1[1], f1[2]);
-        float mx2 = fmax3(f2[0], f2[1], f2[2]), mx3 = fmax3(f3[0], f3[1], f3[2]);
+        if (slow) {
+          uint32_t f[32];
+          auto load = [&](int y) {
+            tmem_ld_x32(s_col + 32 * y, f);
+            tmem_wait_ld_x32(f);
+            if (at < full_lo || at > full_hi) {
+              const uint32_t bits = vis_bits32(see_lo - at - 32 * y, see_hi - at - 32 * y);
 #pragma unroll
-        for (int t = 3; t < 31; t += 2) {
-          mx0 = fmax3(mx0, f0[t], f0[t + 1]);
-          mx1 = fmax3(mx1, f1[t], f1[t + 1]);
-          mx2 = fmax3(mx2, f2[t], f2[t + 1]);
-          mx3 = fmax3(mx3, f3[t], f3[t + 1]);
-        }
-        mx0 = fmax3(mx0, f0[31], f1[31]);
-        mx2 = fmax3(mx2, f2[31], f3[31]);
-        const float m_tile = fmax3(fmaxf(mx0, mx1), mx2, mx3) * c;
-        float alpha = 1.f;
-        // Move the reference max only when it grows by more than 8 (a factor 256).
-        if (m_tile > m_run + 8.f) {
-          alpha = fast_exp2(m_run - m_tile);  // 0 when m_run is -inf
-          m_run = m_tile;
-        }
-        if (j > rng.lo && __any_sync(kFull, alpha < 1.f)) {
-          const uint32_t o_col = lane_base + C::kOCol + m * D;
+              for (int t = 0; t < 32; ++t)
+                if (!(bits & (1u << t))) f[t] = 0xff800000u;  // -inf
+            }
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int y = 0; y < kParts; ++y) {
+            load(y);
 #pragma unroll
-          for (int cc = 0; cc < D / 16; ++cc) {
-            uint32_t ov[16];
-            tmem_ld_x16(o_col + cc * 16, ov);
-            tmem_wait_ld_x16(ov);
-#pragma unroll
-            for (int t = 0; t < 16; ++t)
-              ov[t] = __float_as_uint(__uint_as_float(ov[t]) * alpha);
-            tmem_st_x16(o_col + cc * 16, ov);
+            for (int t = 0; t < 32; t += 2)
+              mx = fmax3(mx, __uint_as_float(f[t]), __uint_as_float(f[t + 1]));
           }
+          // Move the reference only when it grows by more than 8 (a factor of 256).
+          float alpha = 1.f;
+          if (mx * c > m_run + 8.f) {
+            alpha = fast_exp2(m_run - mx * c);  // 0 when m_run is -inf
+            m_run = mx * c;
+          }
+          l_run *= alpha;
+          if (j > rng.lo && __any_sync(kFull, alpha < 1.f)) {
+            // This tile's S was issued before the P V of the one before, which ends with its stage's
+            // release.
+            const int ep = e + j - 1 - rng.lo;
+            ok = wait_at(smem_u32(&ctl->kv_empty[ep % STAGES]), (ep / STAGES) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t o_col = lane_base + C::kOCol + m * D;
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 16) {
+              uint32_t ov[16];
+              tmem_ld_x16(o_col + cc, ov);
+              tmem_wait_ld_x16(ov);
+#pragma unroll
+              for (int t = 0; t < 16; ++t)
+                ov[t] = __float_as_uint(__uint_as_float(ov[t]) * alpha);
+              tmem_st_x16(o_col + cc, ov);
+            }
+          }
+          const float msub = (m_run == -INFINITY) ? 0.f : m_run;
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
+          // P of part y takes the place of columns whose S has been read.
+#pragma unroll 1
+          for (int y = 0; y < kParts; ++y) {
+            uint32_t pk[16];
+            load(y);
+            exp2_pack_32(reinterpret_cast<const float*>(f), cc2, make_float2(-msub, -msub), sa, sb,
+                         pk);
+            tmem_st_x16(s_col + 16 * y, pk);
+          }
+          sa = __fadd2_rn(sa, sb);
+          l_run += sa.x + sa.y;
         }
-        const float msub = (m_run == -INFINITY) ? 0.f : m_run;
-        const float2 cc2 = make_float2(c, c);
-        const float2 mm = make_float2(-msub, -msub);
-        float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
-        uint32_t pk[16];
-        exp2_pack_32(f0, cc2, mm, sa, sb, pk);
-        tmem_st_x16(s_col + 0, pk);
-        exp2_pack_32(f1, cc2, mm, sa, sb, pk);
-        tmem_st_x16(s_col + 16, pk);
-        exp2_pack_32(f2, cc2, mm, sa, sb, pk);
-        tmem_st_x16(s_col + 32, pk);
-        exp2_pack_32(f3, cc2, mm, sa, sb, pk);
-        tmem_st_x16(s_col + 48, pk);
-        l_run = l_run * alpha + ((sa.x + sa.y) + (sb.x + sb.y));
         if constexpr (kPaged) {
           // The context ends inside a page of this tile: its slots past the end may hold
           // anything, and a NaN there would survive p = 0. Both warpgroups clear their V rows
@@ -458,21 +601,23 @@ __global__ void __launch_bounds__(384, 1)
           const int left = k_end - k_org - j * BN;  // tokens of the context from the tile's first
           const int clear = imin(BN, (left + p.page_size - 1) & -p.page_size);
           if (left < clear) {
-            const int ev = e + 2 * (j - rng.lo) + 1;
+            const int ev = e + j - rng.lo;  // V came with the K that S was made of
             ok = __all_sync(kFull,
                             mbar_wait(&ctl->kv_full[ev % STAGES], (ev / STAGES) & 1, wc));
             if (!ok) break;
-            const uint32_t v0 = smem_u32(kv_s + (ev % STAGES) * C::kTileBytes);
+            const uint32_t v0 = smem_u32(kv_s + (ev % STAGES) * C::kStageBytes + C::kTileBytes);
             for (int i = left * 8 + r; i < clear * 8; i += 128)
 #pragma unroll
               for (int cp = 0; cp < C::kPanels; ++cp)
-                st_shared_v4(v0 + cp * C::kChunkBytes + i * 16, 0, 0, 0, 0);
+                st_shared_v4(v0 + cp * C::kPanelBytes + i * 16, 0, 0, 0, 0);
             fence_proxy_async_smem();
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&ctl->p_ready[m]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_ready[m][buf]);
+        ++sc;
         release_pending();
       }
       if (!ok) break;
@@ -485,8 +630,8 @@ __global__ void __launch_bounds__(384, 1)
             l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->both[quarter]);
-      ok = __all_sync(kFull, mbar_wait(&ctl->both[quarter], 0, wc) &&
-                                 mbar_wait(&ctl->o_done, un_done & 1, wc));
+      ok = wait_at(smem_u32(&ctl->both[quarter]), 0, wc) &&
+           wait_at(smem_u32(&ctl->o_done), un_done & 1, wc);
       if (!ok) break;
       tc_fence_after();
       const float f0 = ctl->coef[0][r], f1 = -ctl->coef[1][r];
@@ -514,7 +659,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       // The row's place in the staging area: this Q buffer, whose last MMA is done. Columns of
       // warpgroup m: rows of D bytes, 16-byte chunks swizzled as TMA expects them.
-      uint8_t* stage = q_s + (un_done % QB) * C::kTileBytes;
+      uint8_t* stage = q_s + (un_done % QB) * C::kQBytes;
       auto chunk_at = [&](int half, int ch) {
         const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
         return stage + half * (128 * D) + r * D + ((ch ^ sw) << 4);
@@ -525,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->both[quarter]);
-      ok = __all_sync(kFull, mbar_wait(&ctl->both[quarter], 1, wc));
+      ok = wait_at(smem_u32(&ctl->both[quarter]), 1, wc);
       if (!ok) break;
       // Two halves in a fixed order, so that both warps scale by the same number.
       const float mine = ss2.x + ss2.y, other = *reinterpret_cast<const float*>(chunk_at(m, 0));
@@ -563,7 +708,7 @@ __global__ void __launch_bounds__(384, 1)
       // key tile: it takes the Q of the unit after the next.
       pending_q = un_done % QB;
       ++un_done;
-      e += 2 * (rng.hi - rng.lo);
+      e += rng.hi - rng.lo;
     }
     release_pending();  // the last unit's store, before shared memory goes away
   }
