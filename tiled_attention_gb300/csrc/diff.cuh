@@ -482,13 +482,18 @@ __global__ void __launch_bounds__(384, 1)
       }
     };
     bool ok = true;
-    for (int k = 0; ok; ++k) {
+    auto next_unit = [&](int k) {
       const int u = unit_of(k);
-      if (u >= p.num_units) break;
-      const Unit un = diff_unit<PACK>(u, p, cur);  // warp-collective
-      if (!un.valid) break;
+      return u < p.num_units ? diff_unit<PACK>(u, p, cur) : Unit{0, 0, 0, 0, 0, 0, 0};
+    };
+    Unit ahead = next_unit(0);  // warp-collective
+    for (int k = 0; ok && ahead.valid; ++k) {
+      const Unit un = ahead;
       const KvRange rng = range_of(un);
-      if (rng.hi <= rng.lo) continue;
+      if (rng.hi <= rng.lo) {
+        ahead = next_unit(k + 1);
+        continue;
+      }
       const int k_org = un.k_org, k_end = un.k_end, bh = un.bh;
       const int row = un.q_row0 + r;
       // Keys that every row of the tile sees, and those that this row sees, from the range's first
@@ -502,97 +507,129 @@ __global__ void __launch_bounds__(384, 1)
       float l_run = 0.f;
       constexpr int kParts = BN / 32;
       const float2 cc2 = make_float2(c, c);
-      for (int j = rng.lo; j < rng.hi && ok; ++j) {
-        const int buf = sc & 1;
-        ok = wait_at(s_bar + 8 * buf, (sc >> 1) & 1, wc);
+      // Tiles [.., j_full) end before keys that some row of the tile does not see.
+      const int j_full = full_hi < 0 ? rng.lo : imin(rng.hi, rng.lo + full_hi / BN + 1);
+      int j = rng.lo;
+      // P of tile j is in TMEM: on to the next tile.
+      auto publish = [&]() {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_ready[m][sc & 1]);
+        ++sc;
+        ++j;
+        release_pending();
+      };
+      for (bool find = true; j < rng.hi; find = false) {
+        // Tiles that every row sees. Weights 2^(c s - m_run) against the reference max that the row
+        // has so far: weights are floating-point, so that a score far above it costs no accuracy,
+        // only range, and a sum above 2^64 tells of one. A row's first tile, such a one (S is still in
+        // TMEM) and boundary tiles take the longer way below. (One loop for both compiled to a
+        // slower one: causal 2 x 8192 1241 us, 1069 this way.)
+        if (!find && (j - rng.lo) * BN >= full_lo) {
+#pragma unroll 1
+          while (j < j_full) {
+            ok = wait_at(s_bar + 8 * (sc & 1), (sc >> 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t s_col = lane_base + (2 * m + (sc & 1)) * BN;
+            uint32_t s[kParts][32], pk[kParts][16];
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
+            float2 sa = make_float2(0.f, 0.f), sb = sa;
+            const float2 mm = make_float2(-m_run, -m_run);  // of a row yet without keys: +inf
+#pragma unroll
+            for (int y = 0; y < kParts; ++y)
+              exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, mm, sa, sb, pk[y]);
+            sa = __fadd2_rn(sa, sb);
+            const float sum = sa.x + sa.y;
+            find = __any_sync(kFull, !(sum <= kDiffRaise));
+            if (find) break;
+            l_run += sum;
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
+            publish();
+          }
+          if (!ok || j >= rng.hi) break;
+        }
+        ok = wait_at(s_bar + 8 * (sc & 1), (sc >> 1) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_col = lane_base + (2 * m + buf) * BN;
+        const uint32_t s_col = lane_base + (2 * m + (sc & 1)) * BN;
         const int at = (j - rng.lo) * BN;
-        // Weights 2^(c s - m_run) against the reference max that the row has so far: weights are
-        // floating-point, so that a score far above it costs no accuracy, only range, and a sum above
-        // 2^64 tells of one. A row's first tile, such a one and boundary tiles take the longer way
-        // below, which finds the max and hides what a row does not see; S is still in TMEM then.
-        bool slow = j == rng.lo || at < full_lo || at > full_hi;
-        if (!slow) {
+        const bool edge = at < full_lo || at > full_hi;
+        {
           uint32_t s[kParts][32], pk[kParts][16];
+          float2 sa, sb;
 #pragma unroll
           for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
 #pragma unroll
           for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
-          float2 sa = make_float2(0.f, 0.f), sb = sa;
-          const float2 mm = make_float2(-m_run, -m_run);  // of a row yet without keys: +inf
+          if (edge) {
 #pragma unroll
-          for (int y = 0; y < kParts; ++y)
-            exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, mm, sa, sb, pk[y]);
-          sa = __fadd2_rn(sa, sb);
-          const float sum = sa.x + sa.y;
-          slow = __any_sync(kFull, !(sum <= kDiffRaise));
-          if (!slow) {
-            l_run += sum;
-#pragma unroll
-            for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
-          }
-        }
-        if (slow) {
-          uint32_t f[32];
-          auto load = [&](int y) {
-            tmem_ld_x32(s_col + 32 * y, f);
-            tmem_wait_ld_x32(f);
-            if (at < full_lo || at > full_hi) {
+            for (int y = 0; y < kParts; ++y) {
               const uint32_t bits = vis_bits32(see_lo - at - 32 * y, see_hi - at - 32 * y);
 #pragma unroll
               for (int t = 0; t < 32; ++t)
-                if (!(bits & (1u << t))) f[t] = 0xff800000u;  // -inf
-            }
-          };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int y = 0; y < kParts; ++y) {
-            load(y);
-#pragma unroll
-            for (int t = 0; t < 32; t += 2)
-              mx = fmax3(mx, __uint_as_float(f[t]), __uint_as_float(f[t + 1]));
-          }
-          // Move the reference only when it grows by more than 8 (a factor of 256).
-          float alpha = 1.f;
-          if (mx * c > m_run + 8.f) {
-            alpha = fast_exp2(m_run - mx * c);  // 0 when m_run is -inf
-            m_run = mx * c;
-          }
-          l_run *= alpha;
-          if (j > rng.lo && __any_sync(kFull, alpha < 1.f)) {
-            // This tile's S was issued before the P V of the one before, which ends with its stage's
-            // release.
-            const int ep = e + j - 1 - rng.lo;
-            ok = wait_at(smem_u32(&ctl->kv_empty[ep % STAGES]), (ep / STAGES) & 1, wc);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t o_col = lane_base + C::kOCol + m * D;
-#pragma unroll 1
-            for (int cc = 0; cc < D; cc += 16) {
-              uint32_t ov[16];
-              tmem_ld_x16(o_col + cc, ov);
-              tmem_wait_ld_x16(ov);
-#pragma unroll
-              for (int t = 0; t < 16; ++t)
-                ov[t] = __float_as_uint(__uint_as_float(ov[t]) * alpha);
-              tmem_st_x16(o_col + cc, ov);
+                if (!(bits & (1u << t))) s[y][t] = 0xff800000u;  // -inf
             }
           }
-          const float msub = (m_run == -INFINITY) ? 0.f : m_run;
-          float2 sa = make_float2(0.f, 0.f), sb = sa;
-          // P of part y takes the place of columns whose S has been read.
 #pragma unroll 1
-          for (int y = 0; y < kParts; ++y) {
-            uint32_t pk[16];
-            load(y);
-            exp2_pack_32(reinterpret_cast<const float*>(f), cc2, make_float2(-msub, -msub), sa, sb,
-                         pk);
-            tmem_st_x16(s_col + 16 * y, pk);
+          for (;;) {
+            if (find) {
+              float mx[kParts];
+#pragma unroll
+              for (int y = 0; y < kParts; ++y) {
+                mx[y] = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 32; t += 2)
+                  mx[y] = fmax3(mx[y], __uint_as_float(s[y][t]), __uint_as_float(s[y][t + 1]));
+              }
+              const float top = fmax3(mx[0], mx[1], mx[kParts - 1]) * c;
+              // Move the reference only when it grows by more than 8 (a factor of 256).
+              float alpha = 1.f;
+              if (top > m_run + 8.f) {
+                alpha = fast_exp2(m_run - top);  // 0 when m_run is -inf
+                m_run = top;
+              }
+              l_run *= alpha;
+              if (j > rng.lo && __any_sync(kFull, alpha < 1.f)) {
+                // This tile's S was issued before the P V of the one before, which ends with its
+                // stage's release.
+                const int ep = e + j - 1 - rng.lo;
+                ok = wait_at(smem_u32(&ctl->kv_empty[ep % STAGES]), (ep / STAGES) & 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t o_col = lane_base + C::kOCol + m * D;
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 16) {
+                  uint32_t ov[16];
+                  tmem_ld_x16(o_col + cc, ov);
+                  tmem_wait_ld_x16(ov);
+#pragma unroll
+                  for (int t = 0; t < 16; ++t)
+                    ov[t] = __float_as_uint(__uint_as_float(ov[t]) * alpha);
+                  tmem_st_x16(o_col + cc, ov);
+                }
+              }
+            }
+            const float msub = find && m_run == -INFINITY ? 0.f : m_run;
+            sa = sb = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kParts; ++y)
+              exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, make_float2(-msub, -msub), sa,
+                           sb, pk[y]);
+            sa = __fadd2_rn(sa, sb);
+            if (find) break;
+            find = __any_sync(kFull, !(sa.x + sa.y <= kDiffRaise));
+            if (!find) break;
           }
-          sa = __fadd2_rn(sa, sb);
+          if (!ok) break;
           l_run += sa.x + sa.y;
+#pragma unroll
+          for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
         }
         if constexpr (kPaged) {
           // The context ends inside a page of this tile: its slots past the end may hold
@@ -613,12 +650,7 @@ __global__ void __launch_bounds__(384, 1)
             fence_proxy_async_smem();
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_ready[m][buf]);
-        ++sc;
-        release_pending();
+        publish();
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
@@ -630,33 +662,44 @@ __global__ void __launch_bounds__(384, 1)
             l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->both[quarter]);
+      ahead = next_unit(k + 1);  // while the last P V run
       ok = wait_at(smem_u32(&ctl->both[quarter]), 0, wc) &&
            wait_at(smem_u32(&ctl->o_done), un_done & 1, wc);
       if (!ok) break;
       tc_fence_after();
       const float f0 = ctl->coef[0][r], f1 = -ctl->coef[1][r];
-      float x[C::kHalf];
-      float2 ss2 = make_float2(0.f, 0.f);
+      constexpr int kX = C::kHalf / 32;
+      uint32_t xa[kX][32], xb[kX][32];
       const uint32_t o0 = lane_base + C::kOCol + m * C::kHalf;
 #pragma unroll
-      for (int cc = 0; cc < C::kHalf / 32; ++cc) {
-        uint32_t va[32], vb[32];
-        tmem_ld_x32(o0 + cc * 32, va);
-        tmem_ld_x32(o0 + D + cc * 32, vb);
-        tmem_wait_ld_x32(va);
-        tmem_wait_ld_x32(vb);
+      for (int y = 0; y < kX; ++y) {
+        tmem_ld_x32(o0 + y * 32, xa[y]);
+        tmem_ld_x32(o0 + D + y * 32, xb[y]);
+      }
+      float x[C::kHalf];
+      float2 ss2 = make_float2(0.f, 0.f), ss3 = ss2;
+#pragma unroll
+      for (int y = 0; y < kX; ++y) {
+        tmem_wait_ld_x32(xa[y]);
+        tmem_wait_ld_x32(xb[y]);
+      }
+#pragma unroll
+      for (int y = 0; y < kX; ++y)
 #pragma unroll
         for (int t = 0; t < 32; t += 2) {
-          const float2 y = __ffma2_rn(
-              make_float2(__uint_as_float(va[t]), __uint_as_float(va[t + 1])),
+          const float2 d2 = __ffma2_rn(
+              make_float2(__uint_as_float(xa[y][t]), __uint_as_float(xa[y][t + 1])),
               make_float2(f0, f0),
-              __fmul2_rn(make_float2(__uint_as_float(vb[t]), __uint_as_float(vb[t + 1])),
+              __fmul2_rn(make_float2(__uint_as_float(xb[y][t]), __uint_as_float(xb[y][t + 1])),
                          make_float2(f1, f1)));
-          x[cc * 32 + t] = y.x;
-          x[cc * 32 + t + 1] = y.y;
-          ss2 = __ffma2_rn(y, y, ss2);
+          x[y * 32 + t] = d2.x;
+          x[y * 32 + t + 1] = d2.y;
+          if (t & 2)
+            ss3 = __ffma2_rn(d2, d2, ss3);
+          else
+            ss2 = __ffma2_rn(d2, d2, ss2);
         }
-      }
+      ss2 = __fadd2_rn(ss2, ss3);
       // The row's place in the staging area: this Q buffer, whose last MMA is done. Columns of
       // warpgroup m: rows of D bytes, 16-byte chunks swizzled as TMA expects them.
       uint8_t* stage = q_s + (un_done % QB) * C::kQBytes;
