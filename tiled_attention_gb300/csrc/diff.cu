@@ -132,8 +132,7 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = mask_kind;
-  const int sms = sms_or_default();
-  const int grid = p.base.num_units < sms ? p.base.num_units : sms;
+  const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = d == 64 ? launch<64>(mask_kind, tq, tk, tv, to, p, grid, st)
                                 : launch<128>(mask_kind, tq, tk, tv, to, p, grid, st);
@@ -199,8 +198,7 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = kMaskPagedPrefill;
-  const int sms = sms_or_default();
-  const int grid = p.base.num_units < sms ? p.base.num_units : sms;
+  const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = d == 64 ? launch<64>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st)
                                 : launch<128>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st);

@@ -77,12 +77,21 @@ struct DiffCfg {
   static constexpr uint32_t kIdescO = idesc_bf16(BM, D, false, true);
 };
 
+// A work unit as the producer hands it to the other warps: what diff_unit found, and its key tiles.
+struct DiffTask {
+  Unit un;
+  KvRange rng;
+};
+
 struct DiffCtrl {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_ready[2][2], p_ready[2][2];  // of map m, buffer b
   uint64_t o_done, drain[2];
   uint64_t both[4];          // warps q of the two softmax warpgroups
+  uint64_t task_full[2], task_empty[2], asked[2];
+  alignas(16) uint4 answer[2];  // of the requests for another unit
+  DiffTask task[2];
   uint32_t tmem_base;
   int abort_flag;
   float coef[2][128];        // 1 / l of map 0's rows, lam / l of map 1's
@@ -190,6 +199,29 @@ __device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint64_t b,
         : "memory");
 }
 
+// Asks for the launch of a block that has not begun to be cancelled and handed to this CTA; the answer
+// (16 bytes) lands in `to` and on `bar`. One thread. Not to be asked again after a refusal.
+__device__ __forceinline__ void ask_unit(uint4* to, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_u32(to)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The cancelled block's index, -1 where none was left.
+__device__ __forceinline__ int unit_answer(const uint4* from) {
+  int x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y;\n ld.shared.b128 h, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}"
+      : "=r"(x)
+      : "r"(smem_u32(from))
+      : "memory");
+  return x;
+}
+
 // Work unit u in launch order: 128-row tiles from the last one down, then batch and head; packed
 // kinds take the two halves of prefill.cuh's 256-row units, the later (longer) one first. q_row0
 // may lie past the segment (an odd number of tiles): that unit has no key tiles.
@@ -256,6 +288,12 @@ __global__ void __launch_bounds__(384, 1)
       }
       mbar_init(&ctl->o_done, 2);
       for (int q = 0; q < 4; ++q) mbar_init(&ctl->both[q], 2);
+      const int readers = 10 + (kPaged && p.page_shift < 6 ? 1 : 0);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&ctl->task_full[s], 1);
+        mbar_init(&ctl->task_empty[s], readers);  // the issuers, softmax warps and V's producer
+        mbar_init(&ctl->asked[s], 1);
+      }
       fence_mbar_init();
       prefetch_tensormap(&tm_q);
       prefetch_tensormap(&tm_k);
@@ -276,29 +314,58 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
-  const int G = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
-  auto unit_of = [&](int k) { return k * G + ((k & 1) ? G - 1 - b : b); };
-  auto range_of = [&](const Unit& un) {
-    return kv_tile_range(mask, p.window, un.q_row0, BM, un.k_end, un.k_org, un.k_end, BN);
+  // Unit n of this CTA, from the producer; false at the end.
+  auto read_task = [&](int n, DiffTask& task) {
+    if (!wait_at(smem_u32(&ctl->task_full[n & 1]), (n >> 1) & 1, wc)) return false;
+    task = ctl->task[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->task_empty[n & 1]);
+    return task.un.valid != 0;
   };
-  UnitCursor cur{0, 0, 0, 0};  // this role's place in the packed unit list
 
   if (warp < 4) {
     regs_decrease<C::kRegsControl>();
     const bool split_v = kPaged && p.page_shift < 6;
     if (warp == 0 || (split_v && warp == 3)) {
       // -------------------------------------------------------------- TMA producer
+      // Warp 0 finds the CTA's units: the first by its block index, another by cancelling the launch of
+      // the next block that waits (the grid has a block a unit, longest units first), so that CTAs
+      // take units as they get done with theirs. It asks one unit ahead.
       int e = 0;   // K/V stages
       int qn = 0;  // Q loads issued
+      int asked = 0, answered = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int u = unit_of(k);
-        if (u >= p.num_units) break;
-        const Unit un = diff_unit<PACK>(u, p, cur);  // warp-collective
-        if (!un.valid) break;
-        const KvRange rng = range_of(un);
+      UnitCursor cur{0, 0, 0, 0};
+      int u = static_cast<int>(blockIdx.x);
+      DiffTask task;
+      for (int n = 0; ok;) {
+        if (warp == 0) {
+          if (lane == 0) ask_unit(&ctl->answer[asked & 1], &ctl->asked[asked & 1]);
+          ++asked;
+          task.un = diff_unit<PACK>(u, p, cur);  // warp-collective
+          task.rng = kv_tile_range(mask, p.window, task.un.q_row0, BM, task.un.k_end, task.un.k_org,
+                                   task.un.k_end, BN);
+          const bool work = task.un.valid && task.rng.hi > task.rng.lo;
+          if (work) {
+            ok = wait_at(smem_u32(&ctl->task_empty[n & 1]), ((n >> 1) & 1) ^ 1, wc);
+            if (!ok) break;
+            if (lane == 0) {
+              ctl->task[n & 1] = task;
+              mbar_arrive(&ctl->task_full[n & 1]);
+            }
+            __syncwarp();
+          } else {
+            task.rng.hi = task.rng.lo = 0;
+          }
+          if (work) ++n;
+        } else {
+          if (!read_task(n, task)) break;
+          ++n;
+        }
+        const Unit& un = task.un;
+        const KvRange rng = task.rng;
         const int npos = rng.hi - rng.lo;
-        if (npos <= 0) continue;
+        if (npos > 0) {
         if (lane == 0) {
           if (warp == 0) {
             const int qb = qn % QB;
@@ -370,9 +437,29 @@ __global__ void __launch_bounds__(384, 1)
             if (x + 1 < npos) pl_next = plane_of(rng.lo + x + 1);
           }
         }
+        }
+        if (warp == 0 && ok) {
+          ok = wait_at(smem_u32(&ctl->asked[answered & 1]), (answered >> 1) & 1, wc);
+          if (!ok) break;
+          const int before = u;
+          u = unit_answer(&ctl->answer[answered & 1]);
+          ++answered;
+          if (u < before) cur = UnitCursor{0, 0, 0, 0};  // the cursor only goes up
+          if (u < 0) {  // no unit left: tell the others
+            ok = wait_at(smem_u32(&ctl->task_empty[n & 1]), ((n >> 1) & 1) ^ 1, wc);
+            if (ok && lane == 0) {
+              ctl->task[n & 1].un.valid = 0;
+              mbar_arrive(&ctl->task_full[n & 1]);
+            }
+            break;
+          }
+        }
       }
       if (lane == 0) {
-        // Let copies still in flight land before the CTA can exit (no-op on the normal path).
+        // Let copies and answers still in flight land before the CTA can exit (no-op on the normal
+        // path).
+        for (; answered < asked; ++answered)
+          mbar_wait(&ctl->asked[answered & 1], (answered >> 1) & 1, wc_drain);
         for (int x = imax(0, e - STAGES); x < e; ++x)
           mbar_wait(&ctl->kv_full[x % STAGES], (x / STAGES) & 1, wc_drain);
         for (int x = imax(0, qn - QB); x < qn; ++x)
@@ -406,14 +493,9 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t ph_s = 0, ph_p = 0;
       uint32_t buf = 0;  // S buffer of the next P
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int u = unit_of(k);
-        if (u >= p.num_units) break;
-        const Unit un = diff_unit<PACK>(u, p, cur);  // warp-collective
-        if (!un.valid) break;
-        const KvRange rng = range_of(un);
-        const int npos = rng.hi - rng.lo;
-        if (npos <= 0) continue;
+      DiffTask task;
+      for (int n = 0; ok && read_task(n, task); ++n) {
+        const int npos = task.rng.hi - task.rng.lo;
         const uint64_t q_desc = q_desc0 + (qn % QB) * (C::kQBytes >> 4);
         auto issue_s = [&](uint32_t b) {
           mma_ss_steps<C::kSteps>(d_s + b * BN, q_desc, k_desc0 + st_s * (C::kStageBytes >> 4),
@@ -482,18 +564,10 @@ __global__ void __launch_bounds__(384, 1)
       }
     };
     bool ok = true;
-    auto next_unit = [&](int k) {
-      const int u = unit_of(k);
-      return u < p.num_units ? diff_unit<PACK>(u, p, cur) : Unit{0, 0, 0, 0, 0, 0, 0};
-    };
-    Unit ahead = next_unit(0);  // warp-collective
-    for (int k = 0; ok && ahead.valid; ++k) {
-      const Unit un = ahead;
-      const KvRange rng = range_of(un);
-      if (rng.hi <= rng.lo) {
-        ahead = next_unit(k + 1);
-        continue;
-      }
+    DiffTask task;
+    for (int n = 0; ok && read_task(n, task); ++n) {
+      const Unit un = task.un;
+      const KvRange rng = task.rng;
       const int k_org = un.k_org, k_end = un.k_end, bh = un.bh;
       const int row = un.q_row0 + r;
       // Keys that every row of the tile sees, and those that this row sees, from the range's first
@@ -662,7 +736,6 @@ __global__ void __launch_bounds__(384, 1)
             l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->both[quarter]);
-      ahead = next_unit(k + 1);  // while the last P V run
       ok = wait_at(smem_u32(&ctl->both[quarter]), 0, wc) &&
            wait_at(smem_u32(&ctl->o_done), un_done & 1, wc);
       if (!ok) break;
