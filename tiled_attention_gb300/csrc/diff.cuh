@@ -81,6 +81,9 @@ struct DiffCfg {
 struct DiffTask {
   Unit un;
   KvRange rng;
+  // Keys, counted from the first tile's, from which and up to which a tile begins if every row sees
+  // all of it; the tiles before j_full end before keys that some row does not see.
+  int full_lo, full_hi, j_full;
 };
 
 struct DiffCtrl {
@@ -95,7 +98,7 @@ struct DiffCtrl {
   uint32_t tmem_base;
   int abort_flag;
   float coef[2][128];        // 1 / l of map 0's rows, lam / l of map 1's
-  float weight[128];         // out_scale * w
+  alignas(16) float weight[128];  // out_scale * w
 };
 
 // Waits and commits by a barrier's shared-memory address. A wait looks at the clock every 64 polls
@@ -347,6 +350,13 @@ __global__ void __launch_bounds__(384, 1)
                                    task.un.k_end, BN);
           const bool work = task.un.valid && task.rng.hi > task.rng.lo;
           if (work) {
+            const int key0 = task.un.k_org + task.rng.lo * BN;
+            task.full_lo = vis_lo(mask, p.window, task.un.k_org,
+                                  imin(task.un.q_row0 + BM, task.un.k_end) - 1) - key0;
+            task.full_hi = vis_hi(mask, p.window, task.un.k_end, task.un.q_row0) - key0 - (BN - 1);
+            task.j_full = task.full_hi < 0
+                              ? task.rng.lo
+                              : imin(task.rng.hi, task.rng.lo + task.full_hi / BN + 1);
             ok = wait_at(smem_u32(&ctl->task_empty[n & 1]), ((n >> 1) & 1) ^ 1, wc);
             if (!ok) break;
             if (lane == 0) {
@@ -570,19 +580,15 @@ __global__ void __launch_bounds__(384, 1)
       const KvRange rng = task.rng;
       const int k_org = un.k_org, k_end = un.k_end, bh = un.bh;
       const int row = un.q_row0 + r;
-      // Keys that every row of the tile sees, and those that this row sees, from the range's first
-      // key on.
-      const int key0 = k_org + rng.lo * BN;
-      const int full_lo = vis_lo(mask, p.window, k_org, imin(un.q_row0 + BM, k_end) - 1) - key0;
-      const int full_hi = vis_hi(mask, p.window, k_end, un.q_row0) - key0 - (BN - 1);
+      const int full_lo = task.full_lo, full_hi = task.full_hi, j_full = task.j_full;
+      const int key0 = k_org + rng.lo * BN;  // keys that this row sees, counted from it
       const int see_lo = vis_lo(mask, p.window, k_org, row) - key0;
       const int see_hi = vis_hi(mask, p.window, k_end, row) - key0;
+      const float lam = m ? __ldg(dp.lam + bh % p.Hq) : 1.f;
       float m_run = -INFINITY;  // running max in log2 units (may trail the true max by < 8)
       float l_run = 0.f;
       constexpr int kParts = BN / 32;
       const float2 cc2 = make_float2(c, c);
-      // Tiles [.., j_full) end before keys that some row of the tile does not see.
-      const int j_full = full_hi < 0 ? rng.lo : imin(rng.hi, rng.lo + full_hi / BN + 1);
       int j = rng.lo;
       // P of tile j is in TMEM: on to the next tile.
       auto publish = [&]() {
@@ -729,13 +735,13 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
       // This row's factor of O_m, for both warps of the row.
-      ctl->coef[m][r] = l_run != 0.f ? (m ? __ldg(dp.lam + bh % p.Hq) : 1.f) / l_run : 0.f;
+      ctl->coef[m][r] = l_run != 0.f ? lam * __frcp_rn(l_run) : 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->both[quarter]);
       const bool live = row < k_end;
       if (live)
         p.lse[(static_cast<size_t>(bh) * 2 + m) * p.N + row] =
             l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->both[quarter]);
       ok = wait_at(smem_u32(&ctl->both[quarter]), 0, wc) &&
            wait_at(smem_u32(&ctl->o_done), un_done & 1, wc);
       if (!ok) break;
@@ -797,14 +803,18 @@ __global__ void __launch_bounds__(384, 1)
       const bool staged = PACK == kMaskNone || warp_row0 + 31 < k_end;
       uint8_t* orow = static_cast<uint8_t*>(p.o) +
                       (static_cast<size_t>(bh) * p.N + static_cast<size_t>(row)) * D * 2 + m * D;
+      const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
       for (int ch = 0; ch < C::kHalf / 8; ++ch) {
         uint32_t w[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 wt =
-              *reinterpret_cast<const float2*>(&ctl->weight[m * C::kHalf + ch * 8 + 2 * t]);
-          w[t] = pack_bf16x2(x[ch * 8 + 2 * t] * rs * wt.x, x[ch * 8 + 2 * t + 1] * rs * wt.y);
+        for (int t = 0; t < 2; ++t) {
+          const float4 wt = *reinterpret_cast<const float4*>(&ctl->weight[m * C::kHalf + ch * 8 + 4 * t]);
+          const float* xt = x + ch * 8 + 4 * t;
+          const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(xt[0], xt[1]), rs2), make_float2(wt.x, wt.y));
+          const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(xt[2], xt[3]), rs2), make_float2(wt.z, wt.w));
+          w[2 * t] = pack_bf16x2(y0.x, y0.y);
+          w[2 * t + 1] = pack_bf16x2(y1.x, y1.y);
         }
         if (staged)
           st_shared_v4(smem_u32(chunk_at(m, ch)), w[0], w[1], w[2], w[3]);
