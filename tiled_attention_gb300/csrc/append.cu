@@ -166,6 +166,7 @@ int axes_params(AxesRowParams* p, int maps, int axes, const uint8_t* pair_axis,
   p->axes = axes;
   p->map_shift = maps - 1;
   p->positions = positions;
+  p->resident = 2 * (kRowThreads / 32) * sms_or_default();
   p->quads = 1;
   for (int i = 0; axes > 1 && i < p->rot / 2; ++i) {
     if (pair_axis[i] >= axes)

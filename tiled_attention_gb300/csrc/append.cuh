@@ -58,6 +58,7 @@ struct RowParams {
 struct AxesRowParams : RowParams {  // positions: [axes, total]; heads and groups count rows
   int axes;                // 1 .. 4
   int map_shift;           // log2 of the rows of a head
+  int resident;            // warps that the GPU holds at once
   int quads;               // every four pairs 4 i .. 4 i + 3 go by one axis
   uint64_t axis_bits[2];   // axis of pair i: bits 2 (i % 32) of word i / 32
 };
@@ -141,6 +142,16 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.in[lane] +
                                                                    t * p.stride[lane]),
                  "r"(p.heads[lane] * 2 * D));
+
+  if constexpr (AXES) {
+    // Everything else of a token waits for its positions, and those of so many tokens on are read by
+    // the warps that come next: into L2 with them (2 x 8192 tokens of 32 + 8 heads 68 to 60 us, 16
+    // chunks appended 86 to 77).
+    const int a = static_cast<int>(threadIdx.x);
+    if (gridDim.y == 1 && p.rot && a < p.axes && p.total - t > p.resident)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          p.positions + static_cast<size_t>(a) * p.total + t + p.resident));
+  }
 
   int pos = 0, phys = -1;  // pos with AXES: the place in the context alone
   if constexpr (AXES && CACHE == kCacheNone) {
