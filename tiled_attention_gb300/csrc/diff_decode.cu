@@ -40,7 +40,7 @@ cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const DiffDec
   // The joining kernel may start before the decode kernel has ended (it waits for it).
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.Hq / p.join_heads, p.B);
-  cfg.blockDim = dim3(kDiffJoinThreads);
+  cfg.blockDim = dim3(kDiffJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

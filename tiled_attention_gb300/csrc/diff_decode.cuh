@@ -45,6 +45,7 @@ struct DiffDecodeParams {
 };
 
 constexpr int kDiffDecodeCtas = 2;  // per SM
+constexpr float kDiffDecodeRaise = 18446744073709551616.f;  // 2^64
 
 using DiffShare = Share<DiffDecodeParams, 64, 2, 32, 1>;
 
@@ -108,23 +109,21 @@ struct SegmentWalk {
   }
 };
 
-// Four columns of one head's row from both maps' sums: the difference, its norm over the `quads`
-// lanes that hold the row (a power of two, side by side), and the store.
+// Four columns of one head's row from both maps' sums: the difference, its norm over the D / 4
+// lanes that hold the row side by side, and the store.
 template <int D>
-__device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, int head, int quad,
-                                            float4 a0, float4 a1, float2 ml0, float2 ml1,
+__device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, float lam, float4 w,
+                                            int quad, float4 a0, float4 a1, float2 ml0, float2 ml1,
                                             unsigned lanes) {
   const bool some = ml0.y != 0.f;  // an empty context has its rows zero whatever eps is
-  const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? __ldg(p.lam + head) / ml1.y : 0.f;
-  float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
-                         a0.w * f0 - a1.w * f1);
+  const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? lam / ml1.y : 0.f;
+  const float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
+                               a0.w * f0 - a1.w * f1);
   float rs = p.out_scale;
-  float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
   if (p.weight) {
     float ss = (y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w);
 #pragma unroll
     for (int off = D / 8; off; off >>= 1) ss += __shfl_xor_sync(lanes, ss, off);
-    w = __ldg(reinterpret_cast<const float4*>(p.weight) + quad);
     if (some) rs *= rsqrtf(ss * (1.f / D) + p.eps);
   }
   *reinterpret_cast<uint2*>(p.o + row * D + 4 * quad) =
@@ -135,6 +134,11 @@ __device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t ro
         some ? make_float2((ml0.x + log2f(ml0.y)) * 0.69314718055994530942f,
                            (ml1.x + log2f(ml1.y)) * 0.69314718055994530942f)
              : make_float2(-INFINITY, -INFINITY);
+}
+// Four norm weights (ones without a norm).
+__device__ __forceinline__ float4 diff_weight(const DiffDecodeParams& p, int quad) {
+  return p.weight ? __ldg(reinterpret_cast<const float4*>(p.weight) + quad)
+                  : make_float4(1.f, 1.f, 1.f, 1.f);
 }
 
 // NT: tiles of eight query heads (1 or 2).
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
         qa[nt][kk][1] = here ? __ldg(from + 4) : 0u;
       }
     float o[NT][D / 8][4];
-    float mx[NT][2], l[NT][2];  // of rows r and r + 8; the max in log2 units, trailing by < 8
+    float mx[NT][2], l[NT][2];  // of rows r and r + 8: reference max in log2 units, sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[nt][0][x] = s[nt][1][x] = 0.f;
+          for (int x = 0; x < 8; ++x) s[nt][x >> 2][x & 3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < C::kSteps; ++kk) {
           uint32_t kb[4];
@@ -299,56 +303,66 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
           }
           __syncwarp();
         }
+        // Weights 2^(c s - mx) against the reference max of the row so far; one of a sum above 2^64 (a
+        // score far above it), and a row's first, has the max found. Element x of n-tile y: row
+        // r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the slice.
+        float w[NT][2][4], sum[NT][2], all = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (left < 16) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (8 * (x >> 2) + 2 * q + (x & 1) >= left) s[nt][x >> 2][x & 3] = -INFINITY;
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            w[nt][x >> 2][x & 3] = fast_exp2(fmaf(s[nt][x >> 2][x & 3], c, -mx[nt][(x & 3) >> 1]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sum[nt][h] = (w[nt][0][2 * h] + w[nt][0][2 * h + 1]) +
+                         (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
+            all += sum[nt][h];
+          }
+        }
+        if (__any_sync(0xffffffffu, !(all <= kDiffDecodeRaise))) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float top = fmaxf(fmaxf(s[nt][0][2 * h], s[nt][0][2 * h + 1]),
+                                fmaxf(s[nt][1][2 * h], s[nt][1][2 * h + 1])) * c;
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              // Move the reference only when it grows by more than 8 (a factor of 256).
+              if (top > mx[nt][h] + 8.f) {
+                const float al = fast_exp2(mx[nt][h] - top);  // 0 when the reference is -inf
+                mx[nt][h] = top;
+                l[nt][h] *= al;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) o[nt][i][2 * h] *= al, o[nt][i][2 * h + 1] *= al;
+              }
+              const float sub = mx[nt][h] == -INFINITY ? 0.f : mx[nt][h];
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 2 * h; x < 2 * h + 2; ++x)
+                  w[nt][y][x] = fast_exp2(fmaf(s[nt][y][x], c, -sub));
+              sum[nt][h] = (w[nt][0][2 * h] + w[nt][0][2 * h + 1]) +
+                           (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
+            }
+        }
+        // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P. (A second term
+        // with what this rounding leaves would take the weights' share of the error away, 1.9e-3 of
+        // |O| in 2-norm beside the output's 1.7e-3, for twice the products: 48 sequences of 16 heads a
+        // kv head 76 to 81 us, 32 of four 167.7 to 169.6.)
         uint32_t pa[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          // Element x of n-tile y: row r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the slice.
-          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              s[nt][y][x] = 8 * y + 2 * q + (x & 1) < left ? s[nt][y][x] * c : -INFINITY;
-              top[x >> 1] = fmaxf(top[x >> 1], s[nt][y][x]);
-            }
-          float al[2] = {1.f, 1.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-            // Move the reference max only when it grows by more than 8.
-            if (top[h] > mx[nt][h] + 8.f) {
-              al[h] = fast_exp2(mx[nt][h] - top[h]);
-              mx[nt][h] = top[h];
-            }
-          }
-          if (__any_sync(0xffffffffu, al[0] < 1.f || al[1] < 1.f)) {
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-              o[nt][t][0] *= al[0];
-              o[nt][t][1] *= al[0];
-              o[nt][t][2] *= al[1];
-              o[nt][t][3] *= al[1];
-            }
-            l[nt][0] *= al[0];
-            l[nt][1] *= al[1];
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float sub = mx[nt][h] == -INFINITY ? 0.f : mx[nt][h];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              s[nt][y][2 * h] = fast_exp2(s[nt][y][2 * h] - sub);
-              s[nt][y][2 * h + 1] = fast_exp2(s[nt][y][2 * h + 1] - sub);
-            }
-            l[nt][h] += (s[nt][0][2 * h] + s[nt][0][2 * h + 1]) +
-                        (s[nt][1][2 * h] + s[nt][1][2 * h + 1]);
-          }
-          // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P.
-          pa[nt][0] = pack_bf16x2(s[nt][0][0], s[nt][0][1]);
-          pa[nt][1] = pack_bf16x2(s[nt][0][2], s[nt][0][3]);
-          pa[nt][2] = pack_bf16x2(s[nt][1][0], s[nt][1][1]);
-          pa[nt][3] = pack_bf16x2(s[nt][1][2], s[nt][1][3]);
+          for (int f = 0; f < 4; ++f)
+            pa[nt][f] = pack_bf16x2(w[nt][f >> 1][2 * (f & 1)], w[nt][f >> 1][2 * (f & 1) + 1]);
+          l[nt][0] += sum[nt][0];
+          l[nt][1] += sum[nt][1];
         }
 #pragma unroll
         for (int pair = 0; pair < D / 16; ++pair) {
@@ -434,7 +448,8 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
         const int hg = 8 * nt + hh;
         if (whole) {
           const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
-          diff_finish<D>(p, head0 + hg, seg.g * G + hg, quad, a[0], a[1], ml[0], ml[1], lanes);
+          diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad, a[0],
+                         a[1], ml[0], ml[1], lanes);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -451,19 +466,23 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   }
 }
 
-// Joins the parts of contexts that several workers share, and writes the rows of empty ones. A CTA
-// takes join_heads heads of a (kv head, sequence); a thread four columns of both maps of one head,
-// and where that leaves threads over, set s of them takes the parts s, s + sets, ...; the sets' sums
-// are added in order.
-constexpr int kDiffJoinThreads = 256;
+// Joins the parts of contexts that several workers share, and writes the rows of empty ones:
+//   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  A = sum_c O_c 2^(m_c - M)  of each map.
+// A CTA takes join_heads heads of a (kv head, sequence). A warp takes one head, and set s of the
+// `sets` warps of a head the parts s, s + sets, ... (at D = 64 a half warp the even ones of those and
+// the other the odd); lanes hold the parts' m and l, of all parts in every warp, so that the sets'
+// sums of O are added as they are, in order. 32 parts at most (64 at D = 64) take one round trip to
+// L2. Eight parts a warp at once (64 a round) need 186 registers, with which a CTA does not fit beside
+// one that still decodes: one sequence of 16K tokens 19.7 us against 20.2, but 16 heads a kv head 81
+// against 76.6. 16 warps a CTA: 19.8 and 77.9.
+constexpr int kDiffJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kDiffJoinThreads) diff_join_kernel(const DiffDecodeParams p) {
-  constexpr int kQuads = D / 4, kBatch = 4;
-  __shared__ float2 sml[2][kDiffJoinThreads];
-  __shared__ float4 so[2][kDiffJoinThreads];
+__global__ void __launch_bounds__(kDiffJoinWarps * 32, 2) diff_join_kernel(const DiffDecodeParams p) {
+  constexpr int kQuads = D / 4, kHalves = 32 / kQuads, kBatch = 4;
+  __shared__ float4 so[2][kDiffJoinWarps][32];
   const int G = p.group, H = p.join_heads;
-  const int tid = static_cast<int>(threadIdx.x);
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
   const int g = h0 / G, hg = h0 % G;
   // Without keys this kernel runs alone, and reports what is wrong with the lengths.
@@ -473,9 +492,9 @@ __global__ void __launch_bounds__(kDiffJoinThreads) diff_join_kernel(const DiffD
   // Every CTA waits, those without work too: this kernel must not end before the first one.
   if (nb == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < H * kQuads; i += kDiffJoinThreads)
+    for (int i = tid; i < H * kQuads; i += kDiffJoinWarps * 32)
       reinterpret_cast<uint2*>(p.o + head0 * D)[i] = make_uint2(0, 0);
-    for (int i = tid; i < 2 * H; i += kDiffJoinThreads) p.lse[2 * head0 + i] = -INFINITY;
+    for (int i = tid; i < 2 * H; i += kDiffJoinWarps * 32) p.lse[2 * head0 + i] = -INFINITY;
     return;
   }
   // The context's first unit, and the workers of its first and last block; the first part is its
@@ -484,77 +503,95 @@ __global__ void __launch_bounds__(kDiffJoinThreads) diff_join_kernel(const DiffD
   const int c0 = share.worker_of(u0 + share.kStart);
   const int parts = share.worker_of(u0 + w - 1) - c0 + 1;
   const int slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
+  const int sets = imax(1, kDiffJoinWarps / H);
+  const int set = sets > 1 ? warp / H : 0;
+  const int quad = lane % kQuads, half = lane / kQuads;
+  const float4 weight = diff_weight(p, quad);
+  float lam = __ldg(p.lam + h0 + imin(sets > 1 ? warp % H : warp, H - 1));
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (parts == 1) return;  // one worker held the whole context
-  const int items = H * kQuads;
-  const int sets = imax(1, imin(kDiffJoinThreads / items, parts));
-  const int set = items < kDiffJoinThreads ? tid / items : 0;
-  for (int it0 = 0; it0 < items; it0 += kDiffJoinThreads) {
-    const int item = it0 + (items < kDiffJoinThreads ? tid % items : tid);
-    const bool here = item < items && set < sets;
-    const int hh = item / kQuads, quad = item % kQuads;
-    float2 ml[2];
-    float4 a[2];
+  const int take = sets * kHalves;                 // parts that are taken side by side
+  const int round = imin(kBatch * take, 64);       // parts of a round
+  for (int hh = sets > 1 ? warp % H : warp; hh < H || sets > 1; hh += kDiffJoinWarps) {
+    float4 a[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+    const bool here = set < sets;
+    for (int x0 = 0; here && x0 < parts; x0 += round) {
+      const int n = imin(round, parts - x0);
+      auto at = [&](int x, int m) {
+        return (static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * 2 + m) * G + hg + hh;
+      };
+      float2 ml[2][2];
+      float4 po[2][kBatch];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float M = -INFINITY, Ls = 0.f;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x0 = here ? set : parts; x0 < parts; x0 += sets * kBatch) {
-        float2 pm[kBatch];
-        float4 po[kBatch];
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ml[m][i] = lane + 32 * i < n
+                         ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(x0 + lane + 32 * i, m))
+                         : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int x = t * take + set * kHalves + half;
+          po[m][t] = x < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(x0 + x, m) * D) + quad)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float top = fmaxf(ml[m][0].x, ml[m][1].x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float Mn = fmaxf(M[m], top);
+        const float f = L[m] != 0.f ? exp2f(M[m] - Mn) : 0.f;
+        M[m] = Mn;
+        // A part whose sum is not 0 had scores; NaN among them alone leaves its max at -inf.
+        const float w0 = ml[m][0].y != 0.f ? exp2f(ml[m][0].x - Mn) : 0.f;
+        const float w1 = ml[m][1].y != 0.f ? exp2f(ml[m][1].x - Mn) : 0.f;
+        float sum = ml[m][0].y * w0 + ml[m][1].y * w1;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        L[m] = L[m] * f + sum;
+        a[m].x *= f, a[m].y *= f, a[m].z *= f, a[m].w *= f;
 #pragma unroll
         for (int t = 0; t < kBatch; ++t) {
-          const int x = imin(x0 + t * sets, parts - 1);
-          const size_t at =
-              (static_cast<size_t>(x ? 2 * (c0 + x) : slot0) * 2 + h) * G + hg + hh;
-          pm[t] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
-          po[t] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * quad));
+          const int x = t * take + set * kHalves + half;
+          const float v0 = __shfl_sync(0xffffffffu, w0, x & 31);
+          const float v1 = __shfl_sync(0xffffffffu, w1, x & 31);
+          const float wt = x < n ? (x < 32 ? v0 : v1) : 0.f;
+          a[m].x += po[m][t].x * wt, a[m].y += po[m][t].y * wt;
+          a[m].z += po[m][t].z * wt, a[m].w += po[m][t].w * wt;
         }
-        float Mn = M;
-#pragma unroll
-        for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, pm[t].x);
-        const float f = Ls != 0.f ? exp2f(M - Mn) : 0.f;
-        M = Mn;
-        Ls *= f;
-        s.x *= f, s.y *= f, s.z *= f, s.w *= f;
-#pragma unroll
-        for (int t = 0; t < kBatch; ++t)
-          if (x0 + t * sets < parts) {
-            const float wt = exp2f(pm[t].x - M);
-            Ls += pm[t].y * wt;
-            s.x += po[t].x * wt, s.y += po[t].y * wt, s.z += po[t].z * wt, s.w += po[t].w * wt;
-          }
       }
-      a[h] = s;
-      ml[h] = make_float2(M, Ls);
+    }
+    if (kHalves == 2) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        a[m].x += __shfl_xor_sync(0xffffffffu, a[m].x, 16);
+        a[m].y += __shfl_xor_sync(0xffffffffu, a[m].y, 16);
+        a[m].z += __shfl_xor_sync(0xffffffffu, a[m].z, 16);
+        a[m].w += __shfl_xor_sync(0xffffffffu, a[m].w, 16);
+      }
     }
     if (sets > 1) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) so[h][tid] = a[h], sml[h][tid] = ml[h];
+      so[0][warp][lane] = a[0], so[1][warp][lane] = a[1];
       __syncthreads();
-      if (set == 0) {
+      if (set == 0)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float M = ml[h].x, Ls = 0.f;
-          for (int i = 1; i < sets; ++i) M = fmaxf(M, sml[h][tid + i * items].x);
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i = 0; i < sets; ++i) {
-            const float2 z = sml[h][tid + i * items];
-            if (z.y == 0.f) continue;  // more sets than parts
-            const float f = exp2f(z.x - M);
-            const float4 x = so[h][tid + i * items];
-            Ls += z.y * f;
-            s.x += x.x * f, s.y += x.y * f, s.z += x.z * f, s.w += x.w * f;
+        for (int m = 0; m < 2; ++m)
+          for (int i = 1; i < sets; ++i) {
+            const float4 x = so[m][warp + i * H][lane];
+            a[m].x += x.x, a[m].y += x.y, a[m].z += x.z, a[m].w += x.w;
           }
-          a[h] = s;
-          ml[h] = make_float2(M, Ls);
-        }
-      }
     }
-    if (here && set == 0) {
-      const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (tid & 16);
-      diff_finish<D>(p, head0 + hh, h0 + hh, quad, a[0], a[1], ml[0], ml[1], lanes);
+    if (set == 0 && half == 0) {
+      const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu;
+      diff_finish<D>(p, head0 + hh, lam, weight, quad, a[0], a[1], make_float2(M[0], L[0]),
+                     make_float2(M[1], L[1]), lanes);
     }
+    if (sets > 1) break;
+    lam = __ldg(p.lam + h0 + imin(hh + kDiffJoinWarps, H - 1));
   }
 }
 
