@@ -918,6 +918,75 @@ def test_two_at_once_and_a_shared_workspace():
     a.check(), b.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_under_rising_scores(d):
+    """Values of 2^70 beside weights that grow by 2^57 along a row: products stay finite."""
+    rng = np.random.default_rng(25)
+    n = 700
+    w = Decode(rng, [n], 2, 1, d, 64, normed=False)
+    h = w.h
+    ramp = np.linspace(-20, 20, n)
+    kx = np.zeros((n, d))
+    kx[:, :d // 2], kx[:, d // 2:] = ramp[:, None] / (d // 2), -ramp[:, None] / (d // 2)
+    vx = rng.standard_normal((n, d)) * 2.0 ** 70
+    kb, vb = (I.f32_to_bf16_bits(x.astype(np.float32)) for x in (kx, vx))
+    kv, vv = (I.bf16_bits_to_f32(x).astype(np.float64)[None] for x in (kb, vb))
+    qb = I.f32_to_bf16_bits(np.full((1, 2, n, d), 1 / h.scale, np.float32))
+    qv = I.bf16_bits_to_f32(qb).astype(np.float64)
+    q, k, v = (bf16_tensor(x, "cuda") for x in (qb, kb[None, None], vb[None, None]))
+    o, lse = run_diff(h, q, k, v, attn.ATTN_MASK_NONE)
+    f, s = cache.slots(np.arange(n), w.table[0], 64)
+    f, s = dev(f, np.int64), dev(s, np.int64)
+    w.k[f, 0, s], w.v[f, 0, s] = k[0, 0], v[0, 0]
+    w.run(q=q[:, :, -1:].contiguous())
+    assert status() == 0
+    want = h.rows(qv[0], kv, vv, diff.visible("none", 0, n))
+    check(f64(o[0]), f64(lse[0]), want)
+    want = h.rows(qv[0][:, -1:], kv, vv, np.ones((1, n), bool))
+    check(f64(w.o[0]), f64(w.lse[0])[:, :, None], want)
+
+
+def test_shared_pages():
+    """Two sequences that hold the same pages of a common prefix."""
+    rng = np.random.default_rng(26)
+    c = Chunk(rng, [200, 300], [60, 90], 4, 2, 128, 32)
+    w = Decode(rng, [500, 129, 700], 8, 2, 64, 16)
+    for x, n in ((c, 192), (w, 128)):
+        x.table[1, :n // x.page] = x.table[0, :n // x.page]
+        x.d_table = dev(x.table)
+        x.ctx[1][:, :, :n] = x.ctx[0][:, :, :n]
+    o, lse = c.run()
+    w.run()
+    assert status() == 0
+    c.check(o, lse), w.check()
+
+
+def test_prefills_at_once():
+    """Dense, packed and chunk attention on three streams at once, each of more units than the GPU
+    holds, give the bits that they give alone."""
+    rng = np.random.default_rng(27)
+    h = Head(rng, 16, 128)
+    q, k, v = (draw(rng, 2, x, 1500, 128)[0] for x in (16, 4, 4))
+    h64 = Head(rng, 8, 64)
+    q64, k64, v64 = (draw(rng, 1, x, 5000, 64)[0] for x in (8, 4, 4))
+    cu = dev(np.array([0, 1300, 1300, 3100, 5000], np.int32))
+    lk = rng.integers(600, 900, 16)
+    c = Chunk(rng, lk, [300] * 16, 8, 2, 128, 32)
+
+    calls = [lambda: run_diff(h, q, k, v, attn.ATTN_MASK_CAUSAL),
+             lambda: run_diff(h64, q64, k64, v64, attn.ATTN_MASK_DOCUMENT, cu=cu, B=4), c.run]
+    alone = [call() for call in calls]
+    assert status() == 0
+    for _ in range(3):
+        got = []
+        for call in calls:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got.append(call())
+        assert status() == 0
+        for (o, lse), (po, pl) in zip(got, alone):
+            assert same_bits(o, po) and torch.equal(lse, pl)
+
+
 def test_far_pages():
     """Pools of more than 2^32 bytes: appended to, read by a chunk and by a decode at their end."""
     Hq, Hkv, d, page = 4, 2, 128, 64

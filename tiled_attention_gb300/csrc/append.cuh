@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                  "r"(p.heads[lane] * 2 * D));
 
   if constexpr (AXES) {
-    // Everything else of a token waits for its positions, and those of so many tokens on are read by
-    // the warps that come next: into L2 with them (2 x 8192 tokens of 32 + 8 heads 68 to 60 us, 16
-    // chunks appended 86 to 77).
+    // Everything else of a token waits for its positions, and those of so many tokens on are read
+    // by the warps that come next: into L2 with them (2 x 8192 tokens of 32 + 8 heads 68 to 60 us,
+    // 16 chunks appended 86 to 77).
     const int a = static_cast<int>(threadIdx.x);
     if (gridDim.y == 1 && p.rot && a < p.axes && p.total - t > p.resident)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(

@@ -7,26 +7,41 @@
 //
 // Both maps run over the same keys, so one pass over K and V serves them: a work unit is one
 // 128-row query tile of one (batch or segment, query head), and what the ordinary kernel's two
-// query tiles are there, the two maps are here. K_j and V_j are loaded once for both; the two
-// softmaxes alternate on the tensor core, S of one map under the other's exponentials; the
+// query tiles are there, the two maps are here. K_j and V_j are loaded once for both, and the
 // difference and the norm are taken in registers at the end, so that neither A_1 v nor A_2 v ever
 // leaves the SM. Each map keeps its own running max and sum (the sums differ, so the accumulators
 // cannot be joined before the end).
 //
-// Roles (384 threads), as in prefill.cuh:
-//   warp 0      TMA producer: the unit's Q tile, then K_j, V_j into a ring
-//   warp 1      MMA issuer: S_m = Q_m K_m^T (SS; map m is k-steps [m D/32, (m + 1) D/32) of the
-//               tile's swizzled rows) and O_m += P_m V_j (P from TMEM); owns TMEM
-//   warp 3      paged, pages under 64 tokens: the V entries
+// Roles (384 threads):
+//   warp 0      finds the CTA's units (below) and loads by TMA: the unit's Q tile, then K_j and V_j
+//               of a tile into one stage of a ring
+//   warps 1, 2  MMA issuers of map 0 and 1: S_m = Q_m K_m^T (SS; map m is k-steps [m D/32,
+//               (m + 1) D/32) of the tile's swizzled rows) and O_m += P_m V (P from TMEM); warp 1
+//               owns TMEM. One issuer for both maps kept the tensor core waiting (causal 2 x 8192
+//               1158 us against 1105).
+//   warp 3      paged, pages under 64 tokens: the V pages
 //   warps 4-7   softmax of map 0, warps 8-11 of map 1; a thread owns one query row. At the end
 //               warps q of both take columns [0, D/2) and [D/2, D) of both accumulators: x = O_0 /
 //               l_0 - lam O_1 / l_1, the row's sum of squares is exchanged through shared
 //               memory, and the scaled row goes out by TMA.
-// TMEM columns: S_0/P_0 [0, 128), S_1/P_1 [128, 256), O_0 and O_1 from 256 on, D each.
+// TMEM columns: S of map m, buffer b at (2 m + b) BN (P takes the place of its S), O_0 and O_1 from
+// 4 BN on, D each.
 //
-// Per key tile of 128 the tensor core needs 2 x (D/64) x 128 cycles for S and 2 x (D/128) x 512 for
-// P V at D = 128 (1536 in all), the exponentials 1024 (32 a cycle and SM), and shared memory moves
-// 192 KB (1536 cycles at 128 bytes).
+// Key tiles are of 64 keys with two S buffers a map (one tile of 128 and one buffer: causal 2 x
+// 8192 1253 us against 1105); 96 where d = 64 leaves the columns (window of 1000 161 us, 165 with
+// 64).
+//
+// Units: the grid has a block a unit, the longest first; a resident CTA takes over a block that has
+// not begun by cancelling its launch (cluster launch control), so that uneven units (chunks of many
+// lengths) spread as CTAs get done: 16 chunks 2926 to 2636 us against a fixed walk, five small ones
+// 78 to 57. Finding units costs warp 0 alone; the other warps read them from shared memory.
+//
+// What bounds it: a tile of 64 keys takes the tensor core 854 cycles for both maps at D = 128 (S
+// with N = 64 runs below the full rate; 768 would be the operations'), the exponentials 512 and the
+// loop 1068. P is rounded to bf16 (2^-8 of a weight at most), which is most of the output's error;
+// sums are those of the unrounded weights, in fp32. Measured (heads 32 over 8, D = 128): causal 2 x
+// 8192 1068 us = 1.54 PFLOP/s of the pairs under the mask; 16 chunks over 16K-token contexts 2.6
+// ms; D = 64, window of 1000 161 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -45,7 +60,9 @@ struct DiffParams {
   int mask;              // of the dense and document kinds
 };
 
-constexpr float kDiffRaise = 18446744073709551616.f;  // 2^64
+// A tile's sum of a row's weights above which its reference max is raised: 2^24, so that weights
+// times values stay finite for values up to 2^80.
+constexpr float kDiffRaise = 16777216.f;
 
 constexpr int imin_c(int a, int b) { return a < b ? a : b; }
 
@@ -113,8 +130,9 @@ __device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
-                                          int* status, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity,
+                                             unsigned long long timeout_ns, int* status, 
+                                             volatile int* abort_flag) {
   uint64_t t0 = 0;
   for (uint32_t polls = 0; polls < (1u << 20); ++polls) {
 #pragma unroll 1
@@ -137,13 +155,14 @@ __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const Wai
 __device__ __forceinline__ void commit_at(uint32_t bar, uint32_t lead) {
   asm volatile(
       "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          bar),
       "r"(lead)
       : "memory");
 }
 
-// N SS MMAs of one accumulator from the lane where `lead` is set: k-steps of 16 columns, 32 bytes apart in both
-// operands; the first overwrites D.
+// N SS MMAs of one accumulator from the lane where `lead` is set: k-steps of 16 columns, 32 bytes
+// apart in both operands; the first overwrites D.
 template <int N>
 __device__ __forceinline__ void mma_ss_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                              uint32_t lead) {
@@ -173,8 +192,8 @@ __device__ __forceinline__ void mma_ss_steps(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 
-// N TS MMAs of one accumulator from the lane where `lead` is set: A from TMEM, 8 columns a 16-key step, B an
-// MN-major operand whose steps are 2048 bytes apart; the first accumulates iff acc0.
+// N TS MMAs of one accumulator from the lane where `lead` is set: A from TMEM, 8 columns a 16-key
+// step, B an MN-major operand whose steps are 2048 bytes apart; the first accumulates iff acc0.
 template <int N>
 __device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                              uint32_t acc0, uint32_t lead) {
@@ -202,8 +221,8 @@ __device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint64_t b,
         : "memory");
 }
 
-// Asks for the launch of a block that has not begun to be cancelled and handed to this CTA; the answer
-// (16 bytes) lands in `to` and on `bar`. One thread. Not to be asked again after a refusal.
+// Asks for the launch of a block that has not begun to be cancelled and handed to this CTA; the
+// answer (16 bytes) lands in `to` and on `bar`. One thread. Not to be asked again after a refusal.
 __device__ __forceinline__ void ask_unit(uint4* to, uint64_t* bar) {
   mbar_arrive_expect_tx(bar, 16);
   asm volatile(
@@ -331,9 +350,9 @@ __global__ void __launch_bounds__(384, 1)
     const bool split_v = kPaged && p.page_shift < 6;
     if (warp == 0 || (split_v && warp == 3)) {
       // -------------------------------------------------------------- TMA producer
-      // Warp 0 finds the CTA's units: the first by its block index, another by cancelling the launch of
-      // the next block that waits (the grid has a block a unit, longest units first), so that CTAs
-      // take units as they get done with theirs. It asks one unit ahead.
+      // Warp 0 finds the CTA's units: the first by its block index, another by cancelling the
+      // launch of the next block that waits (the grid has a block a unit, longest units first), so
+      // that CTAs take units as they get done with theirs. It asks one unit ahead.
       int e = 0;   // K/V stages
       int qn = 0;  // Q loads issued
       int asked = 0, answered = 0;
@@ -376,77 +395,78 @@ __global__ void __launch_bounds__(384, 1)
         const KvRange rng = task.rng;
         const int npos = rng.hi - rng.lo;
         if (npos > 0) {
-        if (lane == 0) {
-          if (warp == 0) {
-            const int qb = qn % QB;
-            ok = mbar_wait(&ctl->q_empty[qb], ((qn / QB) & 1) ^ 1, wc);
-            if (ok) {
-              ++qn;
-              mbar_arrive_expect_tx(&ctl->q_full[qb], C::kQBytes);
-              for (int c = 0; c < C::kPanels; ++c)
-                tma_load_3d(q_s + qb * C::kQBytes + c * C::kQPanelBytes, &tm_q,
-                            &ctl->q_full[qb], c * 64, un.q_row0, un.bh);
-            }
-          }
-          for (int x = 0; !kPaged && x < npos && ok; ++x, ++e) {
-            const int st = e % STAGES;
-            ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&ctl->kv_full[st], C::kStageBytes);
-            uint8_t* dst = kv_s + st * C::kStageBytes;
-            const int key = un.k_org + (rng.lo + x) * BN;
-            for (int c = 0; c < C::kPanels; ++c)
-              tma_load_3d(dst + c * C::kPanelBytes, &tm_k, &ctl->kv_full[st], c * 64, key, un.kvh);
-            for (int c = 0; c < C::kPanels; ++c)
-              tma_load_3d(dst + C::kTileBytes + c * C::kPanelBytes, &tm_v, &ctl->kv_full[st], c * 64,
-                          key, un.kvh);
-          }
-        }
-        ok = __shfl_sync(kFull, ok, 0);
-        if constexpr (kPaged) {
-          // Lane sb owns page sb of every key tile (one half of a page of 128), as in prefill.cuh: it
-          // reads the page's entry a tile ahead and issues its boxes; pages past the context or
-          // outside the pool come from the zero-filled plane past it.
-          const int lp = p.page_shift;
-          const int run = imin(BN, 1 << lp), nb = BN / run;
-          const int lk = un.k_end - un.k_org;
-          const int* trow = p.table + static_cast<size_t>(un.seq) * p.max_pages;
-          auto plane_of = [&](int j) {
-            const int tok = j * BN + lane * run;
-            int pl = p.num_pages * p.Hkv;
-            if (lane < nb && tok < lk) {
-              const int raw = __ldg(trow + (tok >> lp));
-              if (raw < 0 || raw >= p.num_pages)
-                report_status(p.status, -5);
-              else
-                pl = raw * p.Hkv + un.kvh;
-            }
-            return pl;
-          };
-          // With pages under 64 tokens warp 0 brings K and warp 3 V, else warp 0 both.
-          const int first = warp == 3 ? 1 : 0, last = split_v && warp == 0 ? 0 : 1;
-          int pl_next = plane_of(rng.lo);
-          for (int x = 0; x < npos && ok; ++x, ++e) {
-            const int st = e % STAGES;
-            if (lane == 0) ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
-            ok = __shfl_sync(kFull, ok, 0);
-            if (!ok) break;
-            if (lane == 0)
-              for (int y = first; y <= last; ++y)
-                mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
-            __syncwarp();
-            const int pl = pl_next;
-            if (lane < nb) {
-              const int row0 = nb > 1 ? 0 : ((rng.lo + x) * BN) & ((1 << lp) - 1);
-              uint8_t* dst = kv_s + st * C::kStageBytes + lane * run * 128;
-              for (int y = first; y <= last; ++y)
+          if (lane == 0) {
+            if (warp == 0) {
+              const int qb = qn % QB;
+              ok = mbar_wait(&ctl->q_empty[qb], ((qn / QB) & 1) ^ 1, wc);
+              if (ok) {
+                ++qn;
+                mbar_arrive_expect_tx(&ctl->q_full[qb], C::kQBytes);
                 for (int c = 0; c < C::kPanels; ++c)
-                  tma_load_3d(dst + y * C::kTileBytes + c * C::kPanelBytes, y ? &tm_v : &tm_k,
-                              &ctl->kv_full[st], c * 64, row0, pl);
+                  tma_load_3d(q_s + qb * C::kQBytes + c * C::kQPanelBytes, &tm_q,
+                              &ctl->q_full[qb], c * 64, un.q_row0, un.bh);
+              }
             }
-            if (x + 1 < npos) pl_next = plane_of(rng.lo + x + 1);
+            for (int x = 0; !kPaged && x < npos && ok; ++x, ++e) {
+              const int st = e % STAGES;
+              ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&ctl->kv_full[st], C::kStageBytes);
+              uint8_t* dst = kv_s + st * C::kStageBytes;
+              const int key = un.k_org + (rng.lo + x) * BN;
+              for (int c = 0; c < C::kPanels; ++c)
+                tma_load_3d(dst + c * C::kPanelBytes, &tm_k, &ctl->kv_full[st], c * 64, key,
+                            un.kvh);
+              for (int c = 0; c < C::kPanels; ++c)
+                tma_load_3d(dst + C::kTileBytes + c * C::kPanelBytes, &tm_v, &ctl->kv_full[st],
+                            c * 64, key, un.kvh);
+            }
           }
-        }
+          ok = __shfl_sync(kFull, ok, 0);
+          if constexpr (kPaged) {
+            // Lane sb owns page sb of every key tile (one half of a page of 128), as in
+            // prefill.cuh: it reads the page's entry a tile ahead and issues its boxes; pages past
+            // the context or outside the pool come from the zero-filled plane past it.
+            const int lp = p.page_shift;
+            const int run = imin(BN, 1 << lp), nb = BN / run;
+            const int lk = un.k_end - un.k_org;
+            const int* trow = p.table + static_cast<size_t>(un.seq) * p.max_pages;
+            auto plane_of = [&](int j) {
+              const int tok = j * BN + lane * run;
+              int pl = p.num_pages * p.Hkv;
+              if (lane < nb && tok < lk) {
+                const int raw = __ldg(trow + (tok >> lp));
+                if (raw < 0 || raw >= p.num_pages)
+                  report_status(p.status, -5);
+                else
+                  pl = raw * p.Hkv + un.kvh;
+              }
+              return pl;
+            };
+            // With pages under 64 tokens warp 0 brings K and warp 3 V, else warp 0 both.
+            const int first = warp == 3 ? 1 : 0, last = split_v && warp == 0 ? 0 : 1;
+            int pl_next = plane_of(rng.lo);
+            for (int x = 0; x < npos && ok; ++x, ++e) {
+              const int st = e % STAGES;
+              if (lane == 0) ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
+              ok = __shfl_sync(kFull, ok, 0);
+              if (!ok) break;
+              if (lane == 0)
+                for (int y = first; y <= last; ++y)
+                  mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
+              __syncwarp();
+              const int pl = pl_next;
+              if (lane < nb) {
+                const int row0 = nb > 1 ? 0 : ((rng.lo + x) * BN) & ((1 << lp) - 1);
+                uint8_t* dst = kv_s + st * C::kStageBytes + lane * run * 128;
+                for (int y = first; y <= last; ++y)
+                  for (int c = 0; c < C::kPanels; ++c)
+                    tma_load_3d(dst + y * C::kTileBytes + c * C::kPanelBytes, y ? &tm_v : &tm_k,
+                                &ctl->kv_full[st], c * 64, row0, pl);
+              }
+              if (x + 1 < npos) pl_next = plane_of(rng.lo + x + 1);
+            }
+          }
         }
         if (warp == 0 && ok) {
           ok = wait_at(smem_u32(&ctl->asked[answered & 1]), (answered >> 1) & 1, wc);
@@ -477,10 +497,10 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == 1 || warp == 2) {
       // -------------------------------------------------------------- MMA issuers
-      // Warp 1 issues map 0's MMAs, warp 2 map 1's. S of positions 0 and 1 go first; step x is P V of
-      // position x, then S of x + 2 into the buffer that P V has just read (MMAs of one thread run
-      // in order), so the map's next S is there when its softmax is done with this one. Every ring
-      // entry takes one release from each issuer.
+      // Warp 1 issues map 0's MMAs, warp 2 map 1's. S of positions 0 and 1 go first; step x is P V
+      // of position x, then S of x + 2 into the buffer that P V has just read (MMAs of one thread
+      // run in order), so the map's next S is there when its softmax is done with this one. Every
+      // ring entry takes one release from each issuer.
       const int m = warp - 1;
       uint32_t lead;
       asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}"
@@ -522,8 +542,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (!ok) break;
         for (int x = 0; x < npos; ++x) {
-          // P and the next K together: looking at a barrier takes 80 cycles, and the tensor core may
-          // run dry meanwhile.
+          // P and the next K together: looking at a barrier takes 80 cycles, and the tensor core
+          // may run dry meanwhile.
           const bool more = x + 2 < npos;
           const bool rp = try_wait_at(p_bar + 8 * buf, ph_p);
           const bool rk = !more || try_wait_at(full0 + 8 * st_s, ph_s);
@@ -533,8 +553,8 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
           }
           tc_fence_after();
-          // The unit's first P V overwrites O_m: both warps of every row published this P after they
-          // had read O of the unit before.
+          // The unit's first P V overwrites O_m: both warps of every row published this P after
+          // they had read O of the unit before.
           mma_ts_steps<BN / 16>(d_o, d_s + buf * BN, v_desc0 + st_v * (C::kStageBytes >> 4),
                                 C::kIdescO, x > 0, lead);
           if (more) issue_s(buf);
@@ -603,8 +623,8 @@ __global__ void __launch_bounds__(384, 1)
       for (bool find = true; j < rng.hi; find = false) {
         // Tiles that every row sees. Weights 2^(c s - m_run) against the reference max that the row
         // has so far: weights are floating-point, so that a score far above it costs no accuracy,
-        // only range, and a sum above 2^64 tells of one. A row's first tile, such a one (S is still in
-        // TMEM) and boundary tiles take the longer way below. (One loop for both compiled to a
+        // only range, and a sum above 2^24 tells of one. A row's first tile, such a one (S is still
+        // in TMEM) and boundary tiles take the longer way below. (One loop for both compiled to a
         // slower one: causal 2 x 8192 1241 us, 1069 this way.)
         if (!find && (j - rng.lo) * BN >= full_lo) {
 #pragma unroll 1
@@ -809,10 +829,12 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t w[4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float4 wt = *reinterpret_cast<const float4*>(&ctl->weight[m * C::kHalf + ch * 8 + 4 * t]);
-          const float* xt = x + ch * 8 + 4 * t;
-          const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(xt[0], xt[1]), rs2), make_float2(wt.x, wt.y));
-          const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(xt[2], xt[3]), rs2), make_float2(wt.z, wt.w));
+          const int at = ch * 8 + 4 * t;
+          const float4 wt = *reinterpret_cast<const float4*>(&ctl->weight[m * C::kHalf + at]);
+          const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(x[at], x[at + 1]), rs2),
+                                       make_float2(wt.x, wt.y));
+          const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(x[at + 2], x[at + 3]), rs2),
+                                       make_float2(wt.z, wt.w));
           w[2 * t] = pack_bf16x2(y0.x, y0.y);
           w[2 * t + 1] = pack_bf16x2(y1.x, y1.y);
         }

@@ -8,15 +8,21 @@
 // channels leaves S_1 and S_2 in the two halves of one accumulator, and P of both maps is one A
 // fragment for V. Decode reads 512 bytes a token and kv head at D = 128 and is bound by HBM.
 //
-// Work: contexts are cut into 64-token blocks and shared out evenly over two CTAs an SM (share.cuh),
-// each of which walks its range of (sequence, kv head, block), one or more segments of one
-// (sequence, kv head). A producer warp brings 64-token stages into a ring by TMA, page by page
+// Work: contexts are cut into 64-token blocks and shared out evenly over two CTAs an SM
+// (share.cuh), each of which walks its range of (sequence, kv head, block), one or more segments of
+// one (sequence, kv head). A producer warp brings 64-token stages into a ring by TMA, page by page
 // through the block table, and runs ahead over the segments' ends. Each of four consumer warps owns
 // a 16-token slice of every stage with its own running max, sum and O; at a segment's end the four
 // are merged in the slot of its last stage. A segment that is its whole context writes O and LSE
 // itself, normed; the others (a CTA's first and last at most) leave O, max and sum of both maps in
 // the workspace, two slots a CTA, and a second kernel, under programmatic dependent launch, joins
 // them in the workers' order: results do not depend on timing.
+//
+// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.98 of the measured
+// copy rate; one sequence of 16K 20.2 us, of which the bytes are 9.9 and the rest is the launch, the
+// ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) the four
+// consumer warps bound it, 76.6 us where the bytes take 56.4: two tiles of MMAs a stage, of which
+// S takes 295 cycles, the softmax 321 and P V 522.
 #pragma once
 
 #include "decode.cuh"
@@ -45,7 +51,7 @@ struct DiffDecodeParams {
 };
 
 constexpr int kDiffDecodeCtas = 2;  // per SM
-constexpr float kDiffDecodeRaise = 18446744073709551616.f;  // 2^64
+constexpr float kDiffDecodeRaise = 16777216.f;  // 2^24
 
 using DiffShare = Share<DiffDecodeParams, 64, 2, 32, 1>;
 
@@ -112,9 +118,9 @@ struct SegmentWalk {
 // Four columns of one head's row from both maps' sums: the difference, its norm over the D / 4
 // lanes that hold the row side by side, and the store.
 template <int D>
-__device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, float lam, float4 w,
-                                            int quad, float4 a0, float4 a1, float2 ml0, float2 ml1,
-                                            unsigned lanes) {
+__device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, float lam,
+                                            float4 w, int quad, float4 a0, float4 a1, float2 ml0,
+                                            float2 ml1, unsigned lanes) {
   const bool some = ml0.y != 0.f;  // an empty context has its rows zero whatever eps is
   const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? lam / ml1.y : 0.f;
   const float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
@@ -303,8 +309,8 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
           }
           __syncwarp();
         }
-        // Weights 2^(c s - mx) against the reference max of the row so far; one of a sum above 2^64 (a
-        // score far above it), and a row's first, has the max found. Element x of n-tile y: row
+        // Weights 2^(c s - mx) against the reference max of the row so far; one of a sum above 2^24
+        // (a score far above it), and a row's first, has the max found. Element x of n-tile y: row
         // r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the slice.
         float w[NT][2][4], sum[NT][2], all = 0.f;
 #pragma unroll
@@ -351,10 +357,10 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
                            (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
             }
         }
-        // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P. (A second term
-        // with what this rounding leaves would take the weights' share of the error away, 1.9e-3 of
-        // |O| in 2-norm beside the output's 1.7e-3, for twice the products: 48 sequences of 16 heads a
-        // kv head 76 to 81 us, 32 of four 167.7 to 169.6.)
+        // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P. (A second
+        // term with what this rounding leaves would take the weights' share of the error away,
+        // 1.9e-3 of |O| in 2-norm beside the output's 1.7e-3, for twice the products: 48 sequences
+        // of 16 heads a kv head 76 to 81 us, 32 of four 167.7 to 169.6.)
         uint32_t pa[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -448,8 +454,8 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
         const int hg = 8 * nt + hh;
         if (whole) {
           const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
-          diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad, a[0],
-                         a[1], ml[0], ml[1], lanes);
+          diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad,
+                         a[0], a[1], ml[0], ml[1], lanes);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -469,16 +475,17 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
 // Joins the parts of contexts that several workers share, and writes the rows of empty ones:
 //   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  A = sum_c O_c 2^(m_c - M)  of each map.
 // A CTA takes join_heads heads of a (kv head, sequence). A warp takes one head, and set s of the
-// `sets` warps of a head the parts s, s + sets, ... (at D = 64 a half warp the even ones of those and
-// the other the odd); lanes hold the parts' m and l, of all parts in every warp, so that the sets'
-// sums of O are added as they are, in order. 32 parts at most (64 at D = 64) take one round trip to
-// L2. Eight parts a warp at once (64 a round) need 186 registers, with which a CTA does not fit beside
-// one that still decodes: one sequence of 16K tokens 19.7 us against 20.2, but 16 heads a kv head 81
-// against 76.6. 16 warps a CTA: 19.8 and 77.9.
+// `sets` warps of a head the parts s, s + sets, ... (at D = 64 a half warp the even ones of those
+// and the other the odd); lanes hold the parts' m and l, of all parts in every warp, so that the
+// sets' sums of O are added as they are, in order. 32 parts at most (64 at D = 64) take one round
+// trip to L2. Eight parts a warp at once (64 a round) need 186 registers, with which a CTA does not
+// fit beside one that still decodes: one sequence of 16K tokens 19.7 us against 20.2, but 16 heads
+// a kv head 81 against 76.6. 16 warps a CTA: 19.8 and 77.9.
 constexpr int kDiffJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kDiffJoinWarps * 32, 2) diff_join_kernel(const DiffDecodeParams p) {
+__global__ void __launch_bounds__(kDiffJoinWarps * 32, 2)
+    diff_join_kernel(const DiffDecodeParams p) {
   constexpr int kQuads = D / 4, kHalves = 32 / kQuads, kBatch = 4;
   __shared__ float4 so[2][kDiffJoinWarps][32];
   const int G = p.group, H = p.join_heads;
@@ -527,16 +534,17 @@ __global__ void __launch_bounds__(kDiffJoinWarps * 32, 2) diff_join_kernel(const
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          ml[m][i] = lane + 32 * i < n
-                         ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(x0 + lane + 32 * i, m))
-                         : make_float2(-INFINITY, 0.f);
+          ml[m][i] = lane + 32 * i < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) +
+                                                at(x0 + lane + 32 * i, m))
+                                       : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int t = 0; t < kBatch; ++t)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int x = t * take + set * kHalves + half;
-          po[m][t] = x < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(x0 + x, m) * D) + quad)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+          po[m][t] =
+              x < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(x0 + x, m) * D) + quad)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {

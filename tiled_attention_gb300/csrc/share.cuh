@@ -22,8 +22,8 @@ __device__ __forceinline__ int context_length(const P& p, int b, bool report) {
 // warp of a decode kernel and of the kernel that joins its parts works the shares out by itself,
 // from cu_seqlens alone: a context counts its blocks and START units before them for what beginning
 // it costs, and worker i of n takes an even share of the units, the first r workers q + 1, the
-// others q. A share that ends among a context's START units holds none of it. PER_SLOT: workers of a
-// CTA. PARTS: parts of a context that join well.
+// others q. A share that ends among a context's START units holds none of it. PER_SLOT: workers of
+// a CTA. PARTS: parts of a context that join well.
 template <class P, int TOK, int START, int PARTS, int PER_SLOT>
 struct Share {
   static constexpr int kTok = TOK;      // tokens of a block
