@@ -292,8 +292,9 @@ int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int t
  * axes      1 to 4.
  * pair_axis HOST array of rot_dim / 2 bytes, each below axes (else ATTN_ERR_INVALID), read during
  *           the call; may be NULL where axes is 1 or there is no rotation.
- * positions int32 device array [axes, total], required with a rotation. A token with a position
- *           outside [0, max_pos) on any axis sets ATTN_ERR_BOUNDS and its rows are not written.
+ * positions int32 device array [axes, total], required with a rotation, which no output may overlap
+ *           (ATTN_ERR_INVALID). A token with a position outside [0, max_pos) on any axis sets
+ *           ATTN_ERR_BOUNDS and its rows are not written.
  * Everything else as for attn_norm_rope: with axes = 1, maps = 1 and the same positions, the same
  * bits.
  */
@@ -454,7 +455,7 @@ size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d);
  *           finite (1 - lambda_init, usually).
  * d         64 or 128: maps of 32 or 64 channels.
  * scale     > 0, usually 1/sqrt(d/2).
- * o and lse must not overlap one another, q, k or v (ATTN_ERR_INVALID). Tensors are 16-byte aligned
+ * o and lse must not overlap one another or an input (ATTN_ERR_INVALID). Tensors are 16-byte aligned
  * (lam 4). No workspace; asynchronous on `stream`.
  */
 int attn_fwd_diff(const void *q, const void *k, const void *v, void *o, float *lse,

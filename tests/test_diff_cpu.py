@@ -107,6 +107,8 @@ ROW_REFUSALS = [
     (dict(k_out=_Ptr((1 << 20) + 4096)), INVALID),  # inside q
     (dict(q_out=_Ptr((1 << 20) - 16)), INVALID),
     (dict(q=None, k=None), INVALID),
+    (dict(positions=_Ptr((1 << 24) + 4)), INVALID),  # inside q_out
+    (dict(positions=_Ptr((1 << 25) - 4)), INVALID),  # k_out
 ])
 def test_norm_rope_axes_refusals(kw, code):
     assert _norm_rope(**kw) == code
@@ -130,6 +132,9 @@ def test_norm_rope_axes_refusals(kw, code):
     (dict(v_stride=248), INVALID),
     (dict(v_pool=_Ptr((1 << 28) + 8 * 2 * 64 * 256 - 16)), INVALID),  # the end of k_pool
     (dict(k_pool=_Ptr((1 << 20) + 256)), INVALID),
+    (dict(positions=_Ptr((1 << 24) + 4)), INVALID),  # inside q_out
+    (dict(positions=_Ptr((1 << 28) + 4)), INVALID),  # k_pool
+    (dict(positions=_Ptr((1 << 29) - 4)), INVALID),  # v_pool
 ])
 def test_append_axes_refusals(kw, code):
     assert _append(**kw) == code
@@ -201,6 +206,9 @@ DIFF_REFUSALS = [
     (dict(o=_Ptr((2 << 32) + 16)), INVALID),
     (dict(lse=_Ptr(3 << 32)), INVALID),
     (dict(lse=_Ptr((4 << 32) + 16)), INVALID),
+    (dict(o=_Ptr((6 << 32) - 2032)), INVALID),  # lam
+    (dict(lse=_Ptr(6 << 32)), INVALID),
+    (dict(o=_Ptr((1 << 20) + 128)), INVALID),  # norm_weight
 ]
 
 
@@ -212,6 +220,8 @@ DIFF_REFUSALS = [
     (dict(mask_kind=attn.ATTN_MASK_SLIDING, window=0), INVALID),
     (dict(mask_kind=attn.ATTN_MASK_PREFIX_LM, window=-1), INVALID),
     (dict(mask_kind=attn.ATTN_MASK_DOCUMENT), INVALID),  # no cu_seqlens
+    (dict(mask_kind=attn.ATTN_MASK_DOCUMENT, cu_seqlens=_Ptr((4 << 32) + 64)), INVALID),  # inside o
+    (dict(mask_kind=attn.ATTN_MASK_DOCUMENT, cu_seqlens=_Ptr(5 << 32)), INVALID),  # lse
     (dict(B=2 ** 30, N=2 ** 20), UNSUPPORTED),
 ])
 def test_diff_refusals(kw, code):
@@ -229,6 +239,9 @@ def test_diff_refusals(kw, code):
     (dict(block_table=None), INVALID),
     (dict(seqlens_k=None), INVALID),
     (dict(cu_seqlens_q=None), INVALID),
+    (dict(cu_seqlens_q=_Ptr(4 << 32)), INVALID),  # o
+    (dict(seqlens_k=_Ptr(5 << 32)), INVALID),  # lse
+    (dict(block_table=_Ptr((5 << 32) + 64)), INVALID),
 ])
 def test_diff_paged_prefill_refusals(kw, code):
     assert _chunk(**kw) == code

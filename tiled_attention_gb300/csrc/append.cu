@@ -177,6 +177,13 @@ int axes_params(AxesRowParams* p, int maps, int axes, const uint8_t* pair_axis,
   return ATTN_OK;
 }
 
+// Positions that other warps may still read must not lie in an output.
+int positions_apart(const AxesRowParams& p, const void* out, size_t n) {
+  if (p.rot && overlap(out, n, p.positions, sizeof(int32_t) * p.axes * static_cast<size_t>(p.total)))
+    return fail(ATTN_ERR_INVALID, "an output overlaps positions");
+  return ATTN_OK;
+}
+
 // Checks of norm and rotation that go by q, k and their outputs. Returns 1 if all is well and
 // there is work.
 int norm_rope_outputs(const RowParams& p, const void* q, const void* k, const void* q_out,
@@ -241,6 +248,9 @@ int attn_norm_rope_axes(const void* q, const void* k, void* q_out, void* k_out, 
   if ((rc = axes_params(&p, maps, axes, pair_axis, positions))) return rc;
   rc = norm_rope_outputs(p, q, k, q_out, k_out, total, Hq, Hkv, d, q_stride, k_stride);
   if (rc != 1) return rc;
+  if ((rc = positions_apart(p, q ? q_out : nullptr, static_cast<size_t>(total) * Hq * d * 2)) ||
+      (rc = positions_apart(p, k ? k_out : nullptr, static_cast<size_t>(total) * Hkv * d * 2)))
+    return rc;
   p.out[1] = static_cast<uint8_t*>(k_out);
   return launch_rows<kCacheNone>(p, d / maps, stream);
 }
@@ -288,6 +298,10 @@ int attn_append_paged_axes(const void* q, const void* k, const void* v, void* q_
                     page_size, num_pages, d / maps, 2 * (d / maps));
   if (rc) return rc;
   if (B == 0 || total_q == 0) return ATTN_OK;  // no new tokens
+  const size_t pool = static_cast<size_t>(num_pages) * Hkv * page_size * d * 2;
+  if ((rc = positions_apart(p, q ? q_out : nullptr, static_cast<size_t>(total_q) * Hq * d * 2)) ||
+      (rc = positions_apart(p, k_pool, pool)) || (rc = positions_apart(p, v_pool, pool)))
+    return rc;
   return launch_rows<kCacheBf16>(p, d / maps, stream);
 }
 

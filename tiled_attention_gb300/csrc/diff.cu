@@ -34,15 +34,15 @@ cudaError_t launch(int mask, const CUtensorMap& q, const CUtensorMap& k, const C
   return launch_one<D, kMaskNone>(q, k, v, o, p, grid, stream);
 }
 
-// Fields and checks the two prefill entry points share; o and lse are written while other CTAs
-// still read the inputs.
-int diff_outputs(const void* q, size_t q_bytes, const void* k, const void* v, size_t kv_bytes,
-                 const void* o, const float* lse, size_t lse_bytes) {
-  const struct { const void* x; size_t n; } out[2] = {{o, q_bytes}, {lse, lse_bytes}};
-  bool shared = overlap(o, q_bytes, lse, lse_bytes);
-  for (const auto& t : out)
-    shared |= overlap(t.x, t.n, q, q_bytes) || overlap(t.x, t.n, k, kv_bytes) ||
-              overlap(t.x, t.n, v, kv_bytes);
+// o and lse are written while other CTAs still read the inputs.
+struct Span {
+  const void* x;
+  size_t n;
+};
+template <int N>
+int diff_outputs(const Span (&in)[N], const Span& o, const Span& lse) {
+  bool shared = overlap(o.x, o.n, lse.x, lse.n);
+  for (const Span& t : in) shared |= overlap(o.x, o.n, t.x, t.n) || overlap(lse.x, lse.n, t.x, t.n);
   if (shared) return fail(ATTN_ERR_INVALID, "o or lse overlaps another tensor");
   return ATTN_OK;
 }
@@ -103,9 +103,12 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
       doc ? 2ll * Hq * (N / kUnitRows + static_cast<long long>(B)) : planes * tiles_for_rows(N);
   if (planes >= (1ll << 31) || units >= (1ll << 31) - 1 || N > INT32_MAX - 512)
     return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
-  rc = diff_outputs(q, static_cast<size_t>(planes) * N * d * 2, k, v,
-                    static_cast<size_t>(planes_kv) * N * d * 2, o, lse,
-                    static_cast<size_t>(planes) * N * 2 * sizeof(float));
+  const size_t q_bytes = static_cast<size_t>(planes) * N * d * 2;
+  const size_t kv_bytes = static_cast<size_t>(planes_kv) * N * d * 2;
+  const Span in[] = {{q, q_bytes}, {k, kv_bytes}, {v, kv_bytes}, {lam, sizeof(float) * Hq},
+                     {norm_weight, norm_weight ? sizeof(float) * d : 0},
+                     {cu_seqlens, doc ? sizeof(int32_t) * (B + size_t(1)) : 0}};
+  rc = diff_outputs(in, {o, q_bytes}, {lse, static_cast<size_t>(planes) * N * 2 * sizeof(float)});
   if (rc) return rc;
   DiffParams p{};
   if ((rc = status_ptr(&p.base.status))) return rc;
@@ -164,8 +167,14 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   if (units >= (1ll << 31) - 1 || total_q >= (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
   const size_t q_bytes = static_cast<size_t>(Hq) * total_q * d * 2;
-  rc = diff_outputs(q, q_bytes, k, v, static_cast<size_t>(num_pages) * Hkv * page_size * d * 2, o,
-                    lse, static_cast<size_t>(Hq) * total_q * 2 * sizeof(float));
+  const size_t pool = static_cast<size_t>(num_pages) * Hkv * page_size * d * 2;
+  const Span in[] = {{q, q_bytes}, {k, pool}, {v, pool}, {lam, sizeof(float) * Hq},
+                     {norm_weight, norm_weight ? sizeof(float) * d : 0},
+                     {cu_seqlens_q, sizeof(int32_t) * (B + size_t(1))},
+                     {seqlens_k, sizeof(int32_t) * B},
+                     {block_table, sizeof(int32_t) * B * static_cast<size_t>(max_pages)}};
+  rc = diff_outputs(in, {o, q_bytes},
+                    {lse, static_cast<size_t>(Hq) * total_q * 2 * sizeof(float)});
   if (rc) return rc;
   DiffParams p{};
   if ((rc = status_ptr(&p.base.status))) return rc;
