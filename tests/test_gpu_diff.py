@@ -961,6 +961,41 @@ def test_shared_pages():
     c.check(o, lse), w.check()
 
 
+@pytest.mark.parametrize("mask,window", [("none", 0), ("causal", 0), ("sliding", 200),
+                                         ("sliding_bidir", 130), ("prefix", 300), ("document", 0),
+                                         ("document_bidir", 0)])
+def test_more_units_than_three_an_sm(mask, window):
+    """d = 64: more than three 128-row units an SM go two CTAs an SM. A few planes of each."""
+    rng = np.random.default_rng(28)
+    doc = mask.startswith("document")
+    B, Hq, Hkv, n, cuts = (1, 48, 12, 1900, [0, 1, 130, 130, 1299, 1900]) if doc else (
+        3, 16, 4, 1399, [0, 1399])
+    h = Head(rng, Hq, 64)
+    (q, qv), (k, kv), (v, vv) = (draw(rng, B, x, n, 64) for x in (Hq, Hkv, Hkv))
+    o, lse = run_diff(h, q, k, v, KINDS[mask], window, dev(np.array(cuts, np.int32)) if doc else None,
+                      len(cuts) - 1 if doc else None)
+    assert status() == 0
+    lam = h.lam
+    for b, hq in ((0, 0), (B - 1, Hq - 1), (B // 2, Hq // 2 + 1)):
+        h.lam = lam[hq:hq + 1]
+        g = hq // (Hq // Hkv)
+        for lo, hi in zip(cuts, cuts[1:]):
+            if lo == hi:
+                continue
+            want = h.rows(qv[b, hq:hq + 1, lo:hi], kv[b, g:g + 1, lo:hi], vv[b, g:g + 1, lo:hi],
+                          diff.visible(mask, window, hi - lo))
+            check(f64(o[b, hq:hq + 1, lo:hi]), f64(lse[b, hq:hq + 1, :, lo:hi]), want)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_more_chunk_units_than_three_an_sm(page):
+    rng = np.random.default_rng(29 + page)
+    c = Chunk(rng, [900, 33, 777, 640, 128], [400, 33, 129, 1, 128], 48, 3, 64, page)
+    o, lse = c.run()
+    assert status() == 0
+    c.check(o, lse)
+
+
 def test_prefills_at_once():
     """Dense, packed and chunk attention on three streams at once, each of more units than the GPU
     holds, give the bits that they give alone."""

@@ -13,25 +13,41 @@
 namespace ta {
 namespace {
 
-template <int D, int PACK>
+template <int D, int PACK, int CTAS>
 cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
   static unsigned long long done = 0;
-  auto kern = diff_prefill_kernel<D, PACK>;
-  using C = DiffCfg<D, PACK>;
+  auto kern = diff_prefill_kernel<D, PACK, CTAS>;
+  using C = DiffCfg<D, PACK, CTAS>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(q, k, v, o, p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int CTAS>
 cudaError_t launch(int mask, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
   if (mask == kMaskPagedPrefill)
-    return launch_one<D, kMaskPagedPrefill>(q, k, v, o, p, grid, stream);
-  if (is_packed(mask)) return launch_one<D, kMaskDocument>(q, k, v, o, p, grid, stream);
-  return launch_one<D, kMaskNone>(q, k, v, o, p, grid, stream);
+    return launch_one<D, kMaskPagedPrefill, CTAS>(q, k, v, o, p, grid, stream);
+  if (is_packed(mask)) return launch_one<D, kMaskDocument, CTAS>(q, k, v, o, p, grid, stream);
+  return launch_one<D, kMaskNone, CTAS>(q, k, v, o, p, grid, stream);
+}
+
+// At d = 64 two CTAs fit an SM, each with one S buffer a map: four softmax warps a scheduler hide one
+// another's waits. With at most three units an SM one CTA with two buffers and longer key tiles
+// ends a unit sooner. One CTA and two: 16 heads, one causal row of 1024 13.9 and 17.5 us (0.8 units an
+// SM), two of 1500 30.8 and 31.6 (2.5), three of 5003 in a window of 1000 149 and 142 (12.6), two of
+// 8192 462 and 435; 8 chunks of up to 1024 tokens over 16K, 64 heads over 4, 1127 and 957.
+int ctas_of(int d, long long units) { return d == 64 && units > 3ll * sms_or_default() ? 2 : 1; }
+
+cudaError_t launch(int d, int ctas, int mask, const CUtensorMap& q, const CUtensorMap& k,
+                   const CUtensorMap& v, const CUtensorMap& o, const DiffParams& p,
+                   cudaStream_t stream) {
+  const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
+  if (d == 128) return launch<128, 1>(mask, q, k, v, o, p, grid, stream);
+  return ctas == 2 ? launch<64, 2>(mask, q, k, v, o, p, grid, stream)
+                   : launch<64, 1>(mask, q, k, v, o, p, grid, stream);
 }
 
 // o and lse are written while other CTAs still read the inputs.
@@ -115,7 +131,8 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   CUtensorMap tq, tk, tv, to;
   if ((rc = encode_3d(&tq, q, d, N, planes, 128))) return rc;
   if ((rc = encode_3d(&to, o, d, N, planes, 32, d / 2))) return rc;
-  const uint32_t tile = d == 64 ? DiffCfg<64, kMaskNone>::BN : DiffCfg<128, kMaskNone>::BN;
+  const int ctas = ctas_of(d, units);
+  const uint32_t tile = d == 64 && ctas == 1 ? DiffCfg<64, kMaskNone, 1>::BN : 64;
   if ((rc = encode_3d(&tk, k, d, N, planes_kv, tile))) return rc;
   if ((rc = encode_3d(&tv, v, d, N, planes_kv, tile))) return rc;
   p.base.o = o;
@@ -135,10 +152,8 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = mask_kind;
-  const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 64 ? launch<64>(mask_kind, tq, tk, tv, to, p, grid, st)
-                                : launch<128>(mask_kind, tq, tk, tv, to, p, grid, st);
+  const cudaError_t e =
+      launch(d, ctas, mask_kind, tq, tk, tv, to, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
   return ATTN_OK;
 }
@@ -207,10 +222,8 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = kMaskPagedPrefill;
-  const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 64 ? launch<64>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st)
-                                : launch<128>(kMaskPagedPrefill, tq, tk, tv, to, p, grid, st);
+  const cudaError_t e = launch(d, ctas_of(d, units), kMaskPagedPrefill, tq, tk, tv, to, p,
+                               static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "differential paged prefill launch");
   return ATTN_OK;
 }

@@ -24,12 +24,18 @@
 //               warps q of both take columns [0, D/2) and [D/2, D) of both accumulators: x = O_0 /
 //               l_0 - lam O_1 / l_1, the row's sum of squares is exchanged through shared
 //               memory, and the scaled row goes out by TMA.
-// TMEM columns: S of map m, buffer b at (2 m + b) BN (P takes the place of its S), O_0 and O_1 from
-// 4 BN on, D each.
+// TMEM columns: S of map m, buffer b of kSBufs at (kSBufs m + b) BN (P takes the place of its S),
+// then O_0 and O_1, D each.
 //
-// Key tiles are of 64 keys with two S buffers a map (one tile of 128 and one buffer: causal 2 x
-// 8192 1253 us against 1105); 96 where d = 64 leaves the columns (window of 1000 161 us, 165 with
-// 64).
+// Key tiles are of 64 keys with two S buffers a map (one tile of 128 and one buffer: causal 2 x 8192
+// 1253 us against 1105); 96 where d = 64 leaves the columns. At d = 64 and with many units two CTAs
+// share an SM, with one S buffer a map each: the softmax is what bounds it there, and four warps a
+// scheduler hide one another's waits (a window of 1000 over 3 x 5003 149 to 142 us, chunks of 64
+// heads over 16K contexts 1127 to 957). Their rows' scores are then held 32 columns at a time: all
+// 64 at once spilled (183 us).
+//
+// A warp goes by its own 32 rows: a tile that all of them see all of takes the short loop, one that
+// none sees gets P = 0 (by the unit's 128 rows: window 146 us against 142).
 //
 // Units: the grid has a block a unit, the longest first; a resident CTA takes over a block that has
 // not begun by cancelling its launch (cluster launch control), so that uneven units (chunks of many
@@ -41,7 +47,7 @@
 // loop 1068. P is rounded to bf16 (2^-8 of a weight at most), which is most of the output's error;
 // sums are those of the unrounded weights, in fp32. Measured (heads 32 over 8, D = 128): causal 2 x
 // 8192 1068 us = 1.54 PFLOP/s of the pairs under the mask; 16 chunks over 16K-token contexts 2.6
-// ms; D = 64, window of 1000 161 us.
+// ms; D = 64, 3 x 5003, window of 1000 141 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,10 +72,14 @@ constexpr float kDiffRaise = 16777216.f;
 
 constexpr int imin_c(int a, int b) { return a < b ? a : b; }
 
-template <int D, int PACK>
+// CTAS: of an SM.
+template <int D, int PACK, int CTAS>
 struct DiffCfg {
+  static_assert(CTAS == 1 || D == 64, "TMEM holds two CTAs' accumulators of 64 columns");
   static constexpr int BM = 128;
-  static constexpr int BN = D == 64 && PACK != kMaskPagedPrefill ? 96 : 64;
+  static constexpr int BN = D == 64 && PACK != kMaskPagedPrefill && CTAS == 1 ? 96 : 64;
+  static constexpr int kCtas = CTAS;
+  static constexpr int kSBufs = 3 - kCtas;           // S buffers a map
   static constexpr int kThreads = 384;
   static constexpr int kPanels = D / 64;
   static constexpr int kQPanelBytes = BM * 128;      // 64 columns of a Q tile
@@ -80,27 +90,26 @@ struct DiffCfg {
   static constexpr int kQBufs = 2;                   // this unit's and the next one's
   static constexpr int kCtrlBytes = 2048;
   static constexpr int kStages =
-      imin_c((232448 - 1024 - kCtrlBytes - kQBufs * kQBytes) / kStageBytes, 8);
+      imin_c((233472 / kCtas - 2048 - kCtrlBytes - kQBufs * kQBytes) / kStageBytes, 8);
   static constexpr int kSmemBytes = 1024 + kQBufs * kQBytes + kStages * kStageBytes + kCtrlBytes;
-  static constexpr int kTmemCols = 512;
-  static constexpr int kOCol = 4 * BN;
+  static constexpr int kTmemCols = 512 / kCtas;
+  static constexpr int kOCol = 2 * kSBufs * BN;
   static constexpr int kSteps = D / 32;              // 16-channel k-steps of one map
   static constexpr int kHalf = D / 2;                // columns of O a softmax warp writes
-  static constexpr uint32_t kRegsControl = 88, kRegsSoftmax = 208;
-  static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= 384 * 168, "register split");
-  static_assert(kSmemBytes <= 232448, "shared memory");
+  static constexpr int kRegsLaunch = 65536 / kCtas / kThreads / 8 * 8;
+  static constexpr uint32_t kRegsControl = CTAS == 1 ? 88 : 48;
+  static constexpr uint32_t kRegsSoftmax = CTAS == 1 ? 208 : 96;
+  static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= 384 * kRegsLaunch, "register split");
+  static_assert((kSmemBytes + 1024) * kCtas <= 233472, "shared memory");
   static_assert(kOCol + 2 * D <= kTmemCols, "TMEM columns");
   static constexpr uint32_t kIdescS = idesc_bf16(BM, BN, false, false);
   static constexpr uint32_t kIdescO = idesc_bf16(BM, D, false, true);
 };
 
-// A work unit as the producer hands it to the other warps: what diff_unit found, and its key tiles.
+// A work unit as the producer hands it to the other warps, with its key tiles.
 struct DiffTask {
   Unit un;
   KvRange rng;
-  // Keys, counted from the first tile's, from which and up to which a tile begins if every row sees
-  // all of it; the tiles before j_full end before keys that some row does not see.
-  int full_lo, full_hi, j_full;
 };
 
 struct DiffCtrl {
@@ -131,7 +140,7 @@ __device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity,
-                                             unsigned long long timeout_ns, int* status, 
+                                             unsigned long long timeout_ns, int* status,
                                              volatile int* abort_flag) {
   uint64_t t0 = 0;
   for (uint32_t polls = 0; polls < (1u << 20); ++polls) {
@@ -268,14 +277,15 @@ __device__ __forceinline__ Unit diff_unit(int u, const PrefillParams& p, UnitCur
   }
 }
 
-template <int D, int PACK>
-__global__ void __launch_bounds__(384, 1)
+template <int D, int PACK, int CTAS>
+__global__ void __launch_bounds__(384, CTAS)
     diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_o, const DiffParams dp) {
-  using C = DiffCfg<D, PACK>;
+  using C = DiffCfg<D, PACK, CTAS>;
   constexpr int BM = C::BM, BN = C::BN, STAGES = C::kStages, QB = C::kQBufs;
+  constexpr int SB = C::kSBufs;
   constexpr bool kPaged = PACK == kMaskPagedPrefill;
   constexpr unsigned kFull = 0xffffffffu;
   const PrefillParams& p = dp.base;
@@ -369,13 +379,6 @@ __global__ void __launch_bounds__(384, 1)
                                    task.un.k_end, BN);
           const bool work = task.un.valid && task.rng.hi > task.rng.lo;
           if (work) {
-            const int key0 = task.un.k_org + task.rng.lo * BN;
-            task.full_lo = vis_lo(mask, p.window, task.un.k_org,
-                                  imin(task.un.q_row0 + BM, task.un.k_end) - 1) - key0;
-            task.full_hi = vis_hi(mask, p.window, task.un.k_end, task.un.q_row0) - key0 - (BN - 1);
-            task.j_full = task.full_hi < 0
-                              ? task.rng.lo
-                              : imin(task.rng.hi, task.rng.lo + task.full_hi / BN + 1);
             ok = wait_at(smem_u32(&ctl->task_empty[n & 1]), ((n >> 1) & 1) ^ 1, wc);
             if (!ok) break;
             if (lane == 0) {
@@ -497,10 +500,10 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == 1 || warp == 2) {
       // -------------------------------------------------------------- MMA issuers
-      // Warp 1 issues map 0's MMAs, warp 2 map 1's. S of positions 0 and 1 go first; step x is P V
-      // of position x, then S of x + 2 into the buffer that P V has just read (MMAs of one thread
-      // run in order), so the map's next S is there when its softmax is done with this one. Every
-      // ring entry takes one release from each issuer.
+      // Warp 1 issues map 0's MMAs, warp 2 map 1's. S of the first SB positions go first; step x is
+      // P V of position x, then S of x + SB into the buffer that P V has just read (MMAs of one
+      // thread run in order). With two buffers the map's next S is there when its softmax is done
+      // with this one. Every ring entry takes one release from each issuer.
       const int m = warp - 1;
       uint32_t lead;
       asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}"
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t q_desc0 =
           sw128_desc(smem_u32(q_s), 16, 1024) +
           ((m / kPer * C::kQPanelBytes + m % kPer * C::kSteps * 32) >> 4);
-      const uint32_t d_s = tmem + 2 * m * BN, d_o = tmem + C::kOCol + m * D;
+      const uint32_t d_s = tmem + C::kSBufs * m * BN, d_o = tmem + C::kOCol + m * D;
       // Stage of the next S and of the next P V, the parity of the former's, and of Q's and P's.
       int st_s = 0, st_v = 0, qn = 0;
       uint32_t ph_s = 0, ph_p = 0;
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(384, 1)
           if (++st_s == STAGES) st_s = 0, ph_s ^= 1;
         };
         ok = wait_at(smem_u32(&ctl->q_full[qn % QB]), (qn / QB) & 1, wc);
-        for (int x = 0; x < 2 && x < npos && ok; ++x) {
+        for (int x = 0; x < SB && x < npos && ok; ++x) {
           ok = wait_at(full0 + 8 * st_s, ph_s, wc);
           if (!ok) break;
           tc_fence_after();
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int x = 0; x < npos; ++x) {
           // P and the next K together: looking at a barrier takes 80 cycles, and the tensor core
           // may run dry meanwhile.
-          const bool more = x + 2 < npos;
+          const bool more = x + SB < npos;
           const bool rp = try_wait_at(p_bar + 8 * buf, ph_p);
           const bool rk = !more || try_wait_at(full0 + 8 * st_s, ph_s);
           if (!__all_sync(kFull, rp && rk)) {
@@ -560,8 +563,8 @@ __global__ void __launch_bounds__(384, 1)
           if (more) issue_s(buf);
           commit_at(empty0 + 8 * st_v, lead);  // K and V of the stage are done with
           if (++st_v == STAGES) st_v = 0;
-          ph_p ^= buf;
-          buf ^= 1;
+          ph_p ^= buf | (SB == 1);
+          buf ^= SB - 1;
         }
         commit_at(smem_u32(&ctl->o_done), lead);
         ++qn;
@@ -600,14 +603,22 @@ __global__ void __launch_bounds__(384, 1)
       const KvRange rng = task.rng;
       const int k_org = un.k_org, k_end = un.k_end, bh = un.bh;
       const int row = un.q_row0 + r;
-      const int full_lo = task.full_lo, full_hi = task.full_hi, j_full = task.j_full;
-      const int key0 = k_org + rng.lo * BN;  // keys that this row sees, counted from it
-      const int see_lo = vis_lo(mask, p.window, k_org, row) - key0;
-      const int see_hi = vis_hi(mask, p.window, k_end, row) - key0;
+      const int key0 = k_org + rng.lo * BN;  // keys below are counted from it
+      // A row past the segment goes as the last one.
+      const int see_lo = vis_lo(mask, p.window, k_org, imin(row, k_end - 1)) - key0;
+      const int see_hi = vis_hi(mask, p.window, k_end, imin(row, k_end - 1)) - key0;
+      // This warp's rows: all of them see all of a tile that begins in [full_lo, full_hi], and the
+      // tiles before j_full begin by full_hi; none sees any of one outside [some_lo, some_hi].
+      const int full_lo = __shfl_sync(kFull, see_lo, 31);
+      const int full_hi = __shfl_sync(kFull, see_hi, 0) - (BN - 1);
+      const int some_lo = __shfl_sync(kFull, see_lo, 0) - (BN - 1);
+      const int some_hi = __shfl_sync(kFull, see_hi, 31);
+      const int j_full = full_hi < 0 ? rng.lo : imin(rng.hi, rng.lo + full_hi / BN + 1);
       const float lam = m ? __ldg(dp.lam + bh % p.Hq) : 1.f;
       float m_run = -INFINITY;  // running max in log2 units (may trail the true max by < 8)
       float l_run = 0.f;
       constexpr int kParts = BN / 32;
+      constexpr int kHeld = SB == 1 ? 1 : kParts;  // parts of a row's scores held in registers
       const float2 cc2 = make_float2(c, c);
       int j = rng.lo;
       // P of tile j is in TMEM: on to the next tile.
@@ -615,12 +626,13 @@ __global__ void __launch_bounds__(384, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_ready[m][sc & 1]);
+        if (lane == 0) mbar_arrive(&ctl->p_ready[m][sc % SB]);
         ++sc;
         ++j;
         release_pending();
       };
-      for (bool find = true; j < rng.hi; find = false) {
+      bool fresh = true;  // some row has no key yet
+      for (bool find = true; j < rng.hi; find = fresh) {
         // Tiles that every row sees. Weights 2^(c s - m_run) against the reference max that the row
         // has so far: weights are floating-point, so that a score far above it costs no accuracy,
         // only range, and a sum above 2^24 tells of one. A row's first tile, such a one (S is still
@@ -629,20 +641,27 @@ __global__ void __launch_bounds__(384, 1)
         if (!find && (j - rng.lo) * BN >= full_lo) {
 #pragma unroll 1
           while (j < j_full) {
-            ok = wait_at(s_bar + 8 * (sc & 1), (sc >> 1) & 1, wc);
+            ok = wait_at(s_bar + 8 * (sc % SB), (sc / SB) & 1, wc);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t s_col = lane_base + (2 * m + (sc & 1)) * BN;
-            uint32_t s[kParts][32], pk[kParts][16];
+            const uint32_t s_col = lane_base + (SB * m + sc % SB) * BN;
+            uint32_t s[kHeld][32], pk[kParts][16];
+            if constexpr (kHeld > 1) {
 #pragma unroll
-            for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
+              for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
 #pragma unroll
-            for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
+              for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
+            }
             float2 sa = make_float2(0.f, 0.f), sb = sa;
             const float2 mm = make_float2(-m_run, -m_run);  // of a row yet without keys: +inf
 #pragma unroll
-            for (int y = 0; y < kParts; ++y)
-              exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, mm, sa, sb, pk[y]);
+            for (int y = 0; y < kParts; ++y) {
+              if constexpr (kHeld == 1) {
+                tmem_ld_x32(s_col + 32 * y, s[0]);
+                tmem_wait_ld_x32(s[0]);
+              }
+              exp2_pack_32(reinterpret_cast<const float*>(s[y % kHeld]), cc2, mm, sa, sb, pk[y]);
+            }
             sa = __fadd2_rn(sa, sb);
             const float sum = sa.x + sa.y;
             find = __any_sync(kFull, !(sum <= kDiffRaise));
@@ -654,27 +673,37 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (!ok || j >= rng.hi) break;
         }
-        ok = wait_at(s_bar + 8 * (sc & 1), (sc >> 1) & 1, wc);
+        ok = wait_at(s_bar + 8 * (sc % SB), (sc / SB) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_col = lane_base + (2 * m + (sc & 1)) * BN;
+        const uint32_t s_col = lane_base + (SB * m + sc % SB) * BN;
         const int at = (j - rng.lo) * BN;
         const bool edge = at < full_lo || at > full_hi;
-        {
-          uint32_t s[kParts][32], pk[kParts][16];
+        if (at < some_lo || at > some_hi) {
+          const uint32_t none[16] = {};
+#pragma unroll
+          for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, none);
+        } else {
+          uint32_t s[kHeld][32], pk[kParts][16];
           float2 sa, sb;
-#pragma unroll
-          for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
-#pragma unroll
-          for (int y = 0; y < kParts; ++y) tmem_wait_ld_x32(s[y]);
-          if (edge) {
-#pragma unroll
-            for (int y = 0; y < kParts; ++y) {
+          auto masked = [&](int y) {
+            tmem_wait_ld_x32(s[y % kHeld]);
+            if (edge) {
               const uint32_t bits = vis_bits32(see_lo - at - 32 * y, see_hi - at - 32 * y);
 #pragma unroll
               for (int t = 0; t < 32; ++t)
-                if (!(bits & (1u << t))) s[y][t] = 0xff800000u;  // -inf
+                if (!(bits & (1u << t))) s[y % kHeld][t] = 0xff800000u;  // -inf
             }
+          };
+          auto load = [&](int y) {
+            tmem_ld_x32(s_col + 32 * y, s[0]);
+            masked(y);
+          };
+          if constexpr (kHeld > 1) {
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) tmem_ld_x32(s_col + 32 * y, s[y]);
+#pragma unroll
+            for (int y = 0; y < kParts; ++y) masked(y);
           }
 #pragma unroll 1
           for (;;) {
@@ -682,16 +711,19 @@ __global__ void __launch_bounds__(384, 1)
               float mx[kParts];
 #pragma unroll
               for (int y = 0; y < kParts; ++y) {
+                if constexpr (kHeld == 1) load(y);
                 mx[y] = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < 32; t += 2)
-                  mx[y] = fmax3(mx[y], __uint_as_float(s[y][t]), __uint_as_float(s[y][t + 1]));
+                  mx[y] = fmax3(mx[y], __uint_as_float(s[y % kHeld][t]),
+                                __uint_as_float(s[y % kHeld][t + 1]));
               }
               const float top = fmax3(mx[0], mx[1], mx[kParts - 1]) * c;
               // Move the reference only when it grows by more than 8 (a factor of 256).
               float alpha = 1.f;
               if (top > m_run + 8.f) {
-                alpha = fast_exp2(m_run - top);  // 0 when m_run is -inf
+                // (A row without keys so far has O = 0.)
+                alpha = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);
                 m_run = top;
               }
               l_run *= alpha;
@@ -718,15 +750,18 @@ __global__ void __launch_bounds__(384, 1)
             const float msub = find && m_run == -INFINITY ? 0.f : m_run;
             sa = sb = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int y = 0; y < kParts; ++y)
-              exp2_pack_32(reinterpret_cast<const float*>(s[y]), cc2, make_float2(-msub, -msub), sa,
-                           sb, pk[y]);
+            for (int y = 0; y < kParts; ++y) {
+              if constexpr (kHeld == 1) load(y);
+              exp2_pack_32(reinterpret_cast<const float*>(s[y % kHeld]), cc2,
+                           make_float2(-msub, -msub), sa, sb, pk[y]);
+            }
             sa = __fadd2_rn(sa, sb);
             if (find) break;
             find = __any_sync(kFull, !(sa.x + sa.y <= kDiffRaise));
             if (!find) break;
           }
           if (!ok) break;
+          fresh = fresh && __any_sync(kFull, m_run == -INFINITY);
           l_run += sa.x + sa.y;
 #pragma unroll
           for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
