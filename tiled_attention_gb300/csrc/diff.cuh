@@ -55,6 +55,7 @@
 #include "prefill.cuh"
 #include "ptx.cuh"
 #include "sched.h"
+#include "share.cuh"
 
 namespace ta {
 
@@ -127,40 +128,8 @@ struct DiffCtrl {
   alignas(16) float weight[128];  // out_scale * w
 };
 
-// Waits and commits by a barrier's shared-memory address. A wait looks at the clock every 64 polls
-// only.
-__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity,
-                                             unsigned long long timeout_ns, int* status,
-                                             volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t polls = 0; polls < (1u << 20); ++polls) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (try_wait_at(bar, parity)) return true;
-    if (*abort_flag) return false;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > timeout_ns) break;
-  }
-  *abort_flag = 1;
-  report_status(status, -4);
-  return false;
-}
-__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  return __all_sync(0xffffffffu, try_wait_at(bar, parity)) ||
-         __all_sync(0xffffffffu, wait_at_slow(bar, parity, w.timeout_ns, w.status, w.abort_flag));
-}
-// One lane's commit: `lead` is set in the lane that issues the MMAs.
+// One lane's commit to a barrier by its shared-memory address: `lead` is set in the lane that
+// issues the MMAs.
 __device__ __forceinline__ void commit_at(uint32_t bar, uint32_t lead) {
   asm volatile(
       "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
@@ -427,28 +396,15 @@ __global__ void __launch_bounds__(384, CTAS)
           }
           ok = __shfl_sync(kFull, ok, 0);
           if constexpr (kPaged) {
-            // Lane sb owns page sb of every key tile (one half of a page of 128), as in
-            // prefill.cuh: it reads the page's entry a tile ahead and issues its boxes; pages past
-            // the context or outside the pool come from the zero-filled plane past it.
+            // Lane sb issues the boxes of page sb of every key tile (one half of a page of 128);
+            // pages past the context or outside the pool come from the zero-filled plane past it.
             const int lp = p.page_shift;
             const int run = imin(BN, 1 << lp), nb = BN / run;
             const int lk = un.k_end - un.k_org;
             const int* trow = p.table + static_cast<size_t>(un.seq) * p.max_pages;
-            auto plane_of = [&](int j) {
-              const int tok = j * BN + lane * run;
-              int pl = p.num_pages * p.Hkv;
-              if (lane < nb && tok < lk) {
-                const int raw = __ldg(trow + (tok >> lp));
-                if (raw < 0 || raw >= p.num_pages)
-                  report_status(p.status, -5);
-                else
-                  pl = raw * p.Hkv + un.kvh;
-              }
-              return pl;
-            };
+            PageEntries pages(trow, rng.lo * BN, run, lp, lk);
             // With pages under 64 tokens warp 0 brings K and warp 3 V, else warp 0 both.
             const int first = warp == 3 ? 1 : 0, last = split_v && warp == 0 ? 0 : 1;
-            int pl_next = plane_of(rng.lo);
             for (int x = 0; x < npos && ok; ++x, ++e) {
               const int st = e % STAGES;
               if (lane == 0) ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
@@ -458,7 +414,12 @@ __global__ void __launch_bounds__(384, CTAS)
                 for (int y = first; y <= last; ++y)
                   mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
               __syncwarp();
-              const int pl = pl_next;
+              const int raw = pages.at(x * nb);
+              int pl = p.num_pages * p.Hkv;
+              if (raw >= 0 && raw < p.num_pages)
+                pl = raw * p.Hkv + un.kvh;
+              else if (lane < nb && (rng.lo + x) * BN + lane * run < lk)
+                report_status(p.status, -5);
               if (lane < nb) {
                 const int row0 = nb > 1 ? 0 : ((rng.lo + x) * BN) & ((1 << lp) - 1);
                 uint8_t* dst = kv_s + st * C::kStageBytes + lane * run * 128;
@@ -467,7 +428,6 @@ __global__ void __launch_bounds__(384, CTAS)
                     tma_load_3d(dst + y * C::kTileBytes + c * C::kPanelBytes, y ? &tm_v : &tm_k,
                                 &ctl->kv_full[st], c * 64, row0, pl);
               }
-              if (x + 1 < npos) pl_next = plane_of(rng.lo + x + 1);
             }
           }
         }

@@ -91,7 +91,7 @@ int attn_fwd_diff_paged_decode(const void* q, const void* k, const void* v, void
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || Hkv > 65535 || N > (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or context too large");
   const long long units =
-      (static_cast<long long>(N) + DiffShare::kTok - 1) / DiffShare::kTok + DiffShare::kStart;
+      (N + DiffShare<64>::kTok - 1ll) / DiffShare<64>::kTok + DiffShare<64>::kStart;
   if (B > 65535 || static_cast<long long>(B) * Hkv >= (1ll << 31) / units)
     return fail(ATTN_ERR_UNSUPPORTED, "decode batch too large");
   if (!keys && no_device()) return ATTN_OK;  // nor are there device rows to fill

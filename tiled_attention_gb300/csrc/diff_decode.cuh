@@ -18,11 +18,14 @@
 // the workspace, two slots a CTA, and a second kernel, under programmatic dependent launch, joins
 // them in the workers' order: results do not depend on timing.
 //
-// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.98 of the measured
-// copy rate; one sequence of 16K 20.2 us, of which the bytes are 9.9 and the rest is the launch, the
-// ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) the four
-// consumer warps bound it, 76.6 us where the bytes take 56.4: two tiles of MMAs a stage, of which
-// S takes 295 cycles, the softmax 321 and P V 522.
+// Up to 8 heads a kv head; with 9 to 16 there is a tile a map instead, whose rows are the heads.
+//
+// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.99 of the measured
+// copy rate; one sequence of 16K 20.1 us, of which the bytes are 9.9 and the rest is the launch, the
+// ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) 70.4 us,
+// where the bytes take 56.4. A copy that only streams takes 161 and 71 us (the latter with less even
+// shares): what is left is that some SMs get their bytes later than others, 135 to 160 us in the
+// batch.
 #pragma once
 
 #include "decode.cuh"
@@ -53,7 +56,12 @@ struct DiffDecodeParams {
 constexpr int kDiffDecodeCtas = 2;  // per SM
 constexpr float kDiffDecodeRaise = 16777216.f;  // 2^24
 
-using DiffShare = Share<DiffDecodeParams, 64, 2, 32, 1>;
+// Beginning a context costs a CTA's pipeline about as much at both head dims, and a block of d = 64
+// half the bytes. 48 sequences of up to 16K tokens, 16 heads a kv head, d = 64: 76.0 us with 2, 72.6
+// with 4, 70.4 with 8, 71.6 with 16; at d = 128 one sequence of 16K 20.1 with 2, 20.4 with 3 to 6,
+// batches within 1 %.
+template <int D>
+using DiffShare = Share<DiffDecodeParams, 64, D == 64 ? 8 : 2, 32, 1>;
 
 template <int D>
 struct DiffDecodeCfg {
@@ -178,17 +186,17 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     prefetch_tensormap(&tm_v);
   }
   const int worker = static_cast<int>(blockIdx.x);
-  const DiffShare share(p, 0, worker == 0 && warp == 0);
+  const DiffShare<D> share(p, 0, worker == 0 && warp == 0);
   __syncthreads();
   if (worker >= share.n) return;
-  SegmentWalk<DiffShare, DiffDecodeParams> seg(share, p, worker);
+  SegmentWalk<DiffShare<D>, DiffDecodeParams> seg(share, p, worker);
   const WaitCtl wc{p.timeout_ns, p.status, &ctl->abort_flag};
   const WaitCtl wc_drain{p.timeout_ns, p.status, nullptr};
 
   if (warp == C::kWarps) {
     // ---------------------------------------------------------------- TMA producer
     // A stage is one box a panel of a page of 64 tokens or of half a page of 128, or whole pages of
-    // 16 or 32, lane sb issuing page sb's boxes. Its table entry is read a stage ahead. A page past
+    // 16 or 32, lane sb issuing page sb's boxes. A page past
     // the context, or whose entry lies outside the pool (never addressed; the status word
     // reports it), comes from the plane past the pool, which TMA fills with zeros.
     const int lp = p.page_shift;
@@ -197,26 +205,18 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     bool ok = true;
     while (ok && seg.next(p)) {
       const int* row = p.table + static_cast<size_t>(seg.b) * p.max_pages;
-      auto plane_of = [&](int i) {
-        const int tok = (seg.blk0 + i) * C::kTok + lane * run;
-        int pl = p.num_pages * p.Hkv;
-        if (lane < nbox && tok < seg.L) {
-          const int raw = __ldg(row + (tok >> lp));
-          if (raw < 0 || raw >= p.num_pages)
-            report_status(p.status, -5);
-          else
-            pl = raw * p.Hkv + seg.g;
-        }
-        return pl;
-      };
-      int pl_next = plane_of(0);
+      PageEntries pages(row, seg.blk0 * C::kTok, run, lp, seg.L);
       for (int i = 0; i < seg.nblk; ++i, ++e) {
         const int st = e % S;
-        if (lane == 0) ok = mbar_wait(&ctl->empty[st], ((e / S) & 1) ^ 1, wc);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = wait_at(smem_u32(&ctl->empty[st]), ((e / S) & 1) ^ 1, wc);
         if (!ok) break;
         uint8_t* dst = ring + st * C::kStageBytes + lane * run * 128;
-        const int pl = pl_next;
+        const int raw = pages.at(i * nbox);
+        int pl = p.num_pages * p.Hkv;
+        if (raw >= 0 && raw < p.num_pages)
+          pl = raw * p.Hkv + seg.g;
+        else if (lane < nbox && (seg.blk0 + i) * C::kTok + lane * run < seg.L)
+          report_status(p.status, -5);
         const int row0 = ((seg.blk0 + i) * C::kTok) & ((1 << lp) - 1);  // 64: the page's second half
         if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], C::kStageBytes);
         __syncwarp();
@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
                         row0, pl);
           }
         }
-        if (i + 1 < seg.nblk) pl_next = plane_of(i + 1);
       }
     }
     if (lane == 0)
@@ -238,7 +237,11 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   }
 
   // ------------------------------------------------------------------ consumers
-  const int r = lane >> 2;  // tile rows r (map 0) and r + 8 (map 1) of head r of a tile
+  // A lane holds rows r and r + 8 of the tiles. One tile: head r's maps 0 and 1. Two: heads r and
+  // r + 8, tile m their map m, which no row shares with the other map, so that S_m takes the k-steps
+  // of its own channels alone (100 sequences of up to 8K, 12 heads a kv head, d = 128: 100 to 77 us,
+  // table entries included).
+  const int r = lane >> 2;
   const int q = lane & 3;
   const float c = p.scale_log2;
   const int tok_w = warp * 16;
@@ -252,16 +255,18 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   bool ok = true;
   for (bool first = true; seg.next(p); first = false) {
     const size_t head0 = (static_cast<size_t>(seg.b) * p.Hkv + seg.g) * G;
-    // Q as the A operand: k-step kk lies in map 2 kk / kSteps, whose rows alone are not zero.
+    // Q as the A operand. One tile: k-step kk lies in map 2 kk / kSteps, whose rows alone are not
+    // zero. Two: k-step kk of map m has rows r and r + 8 in qa[m][2 kk] and qa[m][2 kk + 1].
     uint32_t qa[NT][C::kSteps][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int kk = 0; kk < C::kSteps; ++kk) {
-        const bool here = 8 * nt + r < G;
-        const uint32_t* from = p.q + (head0 + 8 * nt + r) * (D / 2) + kk * 8 + q;
-        qa[nt][kk][0] = here ? __ldg(from) : 0u;
-        qa[nt][kk][1] = here ? __ldg(from + 4) : 0u;
+      for (int x = 0; x < C::kSteps; ++x) {
+        const int head = NT == 1 ? r : 8 * (x & 1) + r;
+        const int kk = NT == 1 ? x : nt * (C::kSteps / 2) + x / 2;
+        const uint32_t* from = p.q + (head0 + head) * (D / 2) + kk * 8 + q;
+        qa[nt][x][0] = head < G ? __ldg(from) : 0u;
+        qa[nt][x][1] = head < G ? __ldg(from + 4) : 0u;
       }
     float o[NT][D / 8][4];
     float mx[NT][2], l[NT][2];  // of rows r and r + 8: reference max in log2 units, sum
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     for (int i = 0; i < seg.nblk; ++i, ++e) {
       const int st = e % S;
       last_st = st;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (e / S) & 1, wc));
+      ok = wait_at(smem_u32(&ctl->full[st]), (e / S) & 1, wc);
       if (ok) {
         const uint32_t kp = smem_u32(ring + st * C::kStageBytes);
         const uint32_t vp = kp + C::kHalfBytes;
@@ -289,16 +294,18 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
         for (int kk = 0; kk < C::kSteps; ++kk) {
           uint32_t kb[4];
           ldmatrix_x4(kb, kp + page_chunk(k_token, kk * 16 + k_half));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const bool lo = kk < C::kSteps / 2;
-            const uint32_t a[4] = {lo ? qa[nt][kk][0] : 0u, lo ? 0u : qa[nt][kk][0],
-                                   lo ? qa[nt][kk][1] : 0u, lo ? 0u : qa[nt][kk][1]};
-            mma_bf16_16816(s[nt][0], a, kb[0], kb[1]);
-            mma_bf16_16816(s[nt][1], a, kb[2], kb[3]);
-          }
+          const int m = 2 * kk / C::kSteps;
+          const uint32_t(&x)[C::kSteps][2] = qa[NT == 1 ? 0 : m];
+          float(&sm)[2][4] = s[NT == 1 ? 0 : m];
+          const int at = NT == 1 ? kk : 2 * (kk - m * (C::kSteps / 2));
+          const uint32_t a[4] = {NT == 2 || m == 0 ? x[at][0] : 0u,
+                                 NT == 2 ? x[at + 1][0] : m == 1 ? x[at][0] : 0u,
+                                 NT == 2 || m == 0 ? x[at][1] : 0u,
+                                 NT == 2 ? x[at + 1][1] : m == 1 ? x[at][1] : 0u};
+          mma_bf16_16816(sm[0], a, kb[0], kb[1]);
+          mma_bf16_16816(sm[1], a, kb[2], kb[3]);
         }
-        const int left = seg.L - (seg.blk0 + i) * C::kTok - tok_w;  // of the context, from this slice
+        const int left = seg.L - (seg.blk0 + i) * C::kTok - tok_w;  // tokens from this slice on
         if (left < 16) {
           // Slots past the context may hold anything: their scores are dropped below, and their
           // values cleared, since a NaN would survive a weight of zero.
@@ -386,15 +393,17 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
       if (lane == 0 && i + 1 < seg.nblk) mbar_arrive(&ctl->empty[st]);
     }
     // ---------------------------------------------------------------- the segment's rows
+    // Heads 8 g .. 8 g + 7 at a time; map m of head 8 g + r is half h of tile nt's rows.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int g = 0; g < NT; ++g)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int m = 0; m < 2; ++m) {
+        const int nt = NT == 1 ? 0 : m, h = NT == 1 ? m : g;
         l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 1);
         l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 2);
         if (q == 0) {
-          red_m[(warp * NT + nt) * 16 + 8 * h + r] = mx[nt][h];
-          red_l[(warp * NT + nt) * 16 + 8 * h + r] = l[nt][h];
+          red_m[(warp * NT + g) * 16 + 8 * m + r] = mx[nt][h];
+          red_l[(warp * NT + g) * 16 + 8 * m + r] = l[nt][h];
         }
       }
     named_barrier_sync(1, C::kConsumers);  // and every consumer is past its last read of the slot
@@ -404,17 +413,18 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     const bool whole = seg.nblk == seg.nb;
     const size_t slot = 2 * static_cast<size_t>(worker) + (first ? 0 : 1);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt) named_barrier_sync(1, C::kConsumers);  // the tile before has been read
+    for (int g = 0; g < NT; ++g) {
+      if (g) named_barrier_sync(1, C::kConsumers);  // the heads before have been read
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = nt * 16 + 8 * h + r;
+      for (int m = 0; m < 2; ++m) {
+        const int nt = NT == 1 ? 0 : m, h = NT == 1 ? m : g;
+        const int at = g * 16 + 8 * m + r;
         float M = red_m[at];
 #pragma unroll
         for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * NT * 16 + at]);
         const float f = l[nt][h] != 0.f ? fast_exp2(mx[nt][h] - M) : 0.f;
-        if (8 * nt + r < G) {
-          float* to = buf + (warp * 16 + 8 * h + r) * D;
+        if (8 * g + r < G) {
+          float* to = buf + (warp * 16 + 8 * m + r) * D;
 #pragma unroll
           for (int t = 0; t < D / 8; ++t)
             *reinterpret_cast<float2*>(to + ((8 * t + 2 * q + 8 * r) & (D - 1))) =
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
       }
       named_barrier_sync(1, C::kConsumers);
       constexpr int kQuads = D / 4;
-      const int heads = imin(8, G - 8 * nt);
+      const int heads = imin(8, G - 8 * g);
       for (int idx = tid; idx < heads * kQuads; idx += C::kConsumers) {
         const int hh = idx / kQuads, quad = idx % kQuads;
         const int col = (4 * quad + 8 * hh) & (D - 1);
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
                              (w[0].y + w[2].y) + (w[1].y + w[3].y),
                              (w[0].z + w[2].z) + (w[1].z + w[3].z),
                              (w[0].w + w[2].w) + (w[1].w + w[3].w));
-          const int at = nt * 16 + 8 * h + hh;
+          const int at = g * 16 + 8 * h + hh;
           float M = red_m[at], Ls = 0.f;
 #pragma unroll
           for (int x = 1; x < C::kWarps; ++x) M = fmaxf(M, red_m[x * NT * 16 + at]);
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
           }
           ml[h] = make_float2(M, Ls);
         }
-        const int hg = 8 * nt + hh;
+        const int hg = 8 * g + hh;
         if (whole) {
           const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
           diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad,
@@ -493,7 +503,7 @@ __global__ void __launch_bounds__(kDiffJoinWarps * 32, 2)
   const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
   const int g = h0 / G, hg = h0 % G;
   // Without keys this kernel runs alone, and reports what is wrong with the lengths.
-  const DiffShare share(p, b, p.max_len == 0 && blockIdx.x == 0 && b == 0 && tid < 32);
+  const DiffShare<D> share(p, b, p.max_len == 0 && blockIdx.x == 0 && b == 0 && tid < 32);
   const int nb = share.blocks(context_length(p, b, false));
   const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
   // Every CTA waits, those without work too: this kernel must not end before the first one.

@@ -81,6 +81,39 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   return false;
 }
 
+// A warp's waits by a barrier's shared-memory address, which look at the clock every 64 polls only.
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_at_slow(uint32_t bar, uint32_t parity,
+                                             unsigned long long timeout_ns, int* status,
+                                             volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t polls = 0; polls < (1u << 20); ++polls) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_at(bar, parity)) return true;
+    if (*abort_flag) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > timeout_ns) break;
+  }
+  *abort_flag = 1;
+  report_status(status, -4);
+  return false;
+}
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  return __all_sync(0xffffffffu, try_wait_at(bar, parity)) ||
+         __all_sync(0xffffffffu, wait_at_slow(bar, parity, w.timeout_ns, w.status, w.abort_flag));
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2) {
