@@ -39,7 +39,7 @@ cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const DiffDec
   }
   // The joining kernel may start before the decode kernel has ended (it waits for it).
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.Hq / p.join_heads, p.B);
+  cfg.gridDim = dim3(p.join_workers ? p.slots : p.B * p.Hkv, p.group / p.join_heads);
   cfg.blockDim = dim3(kDiffJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute early{};
@@ -142,6 +142,7 @@ int attn_fwd_diff_paged_decode(const void* q, const void* k, const void* v, void
   p.slots = L.slots;
   // The joining kernel: a CTA a group once the groups fill the GPU, else a CTA a head.
   p.join_heads = static_cast<long long>(B) * Hkv >= sms_or_default() ? group : 1;
+  p.join_workers = static_cast<long long>(B) * Hkv > L.slots;
   p.scale_log2 = scale * kLog2e;
   p.eps = eps;
   p.out_scale = out_scale;

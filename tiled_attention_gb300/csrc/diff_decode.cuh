@@ -20,8 +20,8 @@
 //
 // Up to 8 heads a kv head; with 9 to 16 there is a tile a map instead, whose rows are the heads.
 //
-// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.99 of the measured
-// copy rate; one sequence of 16K 20.1 us, of which the bytes are 9.9 and the rest is the launch, the
+// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 165 us, 0.99 of the copy
+// rate; one sequence of 16K 19.8 us, of which the bytes are 9.9 and the rest is the launch, the
 // ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) 70.4 us,
 // where the bytes take 56.4. A copy that only streams takes 161 and 71 us (the latter with less even
 // shares): what is left is that some SMs get their bytes later than others, 135 to 160 us in the
@@ -48,6 +48,7 @@ struct DiffDecodeParams {
   int B, Hq, Hkv, max_pages, num_pages, group, page_shift, max_len;
   int slots;             // CTAs of the decode kernel
   int join_heads;        // query heads a CTA of the joining kernel takes
+  int join_workers;      // it goes by workers, not by contexts
   float scale_log2, eps, out_scale;
   int* status;
   unsigned long long timeout_ns;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
           pl = raw * p.Hkv + seg.g;
         else if (lane < nbox && (seg.blk0 + i) * C::kTok + lane * run < seg.L)
           report_status(p.status, -5);
-        const int row0 = ((seg.blk0 + i) * C::kTok) & ((1 << lp) - 1);  // 64: the page's second half
+        const int row0 = ((seg.blk0 + i) * C::kTok) & ((1 << lp) - 1);  // second half of a page
         if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], C::kStageBytes);
         __syncwarp();
         if (lane < nbox) {
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   for (bool first = true; seg.next(p); first = false) {
     const size_t head0 = (static_cast<size_t>(seg.b) * p.Hkv + seg.g) * G;
     // Q as the A operand. One tile: k-step kk lies in map 2 kk / kSteps, whose rows alone are not
-    // zero. Two: k-step kk of map m has rows r and r + 8 in qa[m][2 kk] and qa[m][2 kk + 1].
+    // zero. Two: k-step kk of map m has rows r and r + 8 in qa[m][2 kk] and qa[m][2 kk + 1]. (Asking
+    // for the next segment's before this one's rows are joined gained nothing.)
     uint32_t qa[NT][C::kSteps][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -484,7 +486,10 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
 
 // Joins the parts of contexts that several workers share, and writes the rows of empty ones:
 //   M = max_c m_c,  L = sum_c l_c 2^(m_c - M),  A = sum_c O_c 2^(m_c - M)  of each map.
-// A CTA takes join_heads heads of a (kv head, sequence). A warp takes one head, and set s of the
+// A CTA takes join_heads heads of a (kv head, sequence); where there are more of those than workers
+// it goes by a worker instead, and joins the context that this worker's share is the first to cut
+// (512 sequences of 20 to 400 tokens, 8 kv heads: 130 us in all by contexts, whose 4096 CTAs mostly
+// find a whole one, and 101; 256 of 1K 189 and 179). A warp takes one head, and set s of the
 // `sets` warps of a head the parts s, s + sets, ... (at D = 64 a half warp the even ones of those
 // and the other the odd); lanes hold the parts' m and l, of all parts in every warp, so that the
 // sets' sums of O are added as they are, in order. 32 parts at most (64 at D = 64) take one round
@@ -500,23 +505,48 @@ __global__ void __launch_bounds__(kDiffJoinWarps * 32, 2)
   __shared__ float4 so[2][kDiffJoinWarps][32];
   const int G = p.group, H = p.join_heads;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int h0 = static_cast<int>(blockIdx.x) * H, b = static_cast<int>(blockIdx.y);
-  const int g = h0 / G, hg = h0 % G;
+  const int idx = static_cast<int>(blockIdx.x);  // the (sequence, kv head), or the worker
+  const bool workers = p.join_workers != 0;
   // Without keys this kernel runs alone, and reports what is wrong with the lengths.
-  const DiffShare<D> share(p, b, p.max_len == 0 && blockIdx.x == 0 && b == 0 && tid < 32);
-  const int nb = share.blocks(context_length(p, b, false));
+  const bool report = p.max_len == 0 && idx == 0 && blockIdx.y == 0 && tid < 32;
+  int b = workers ? 0 : idx / p.Hkv, g = idx % p.Hkv;
+  const DiffShare<D> share(p, b, report);
+  // The context's first unit, its blocks and units.
+  int u0 = 0, nb = 0, w = 0;
+  const bool cut = !workers || (idx > 0 && idx < share.n);
+  if (workers && cut) {
+    int ahead;
+    share.find(p, share.start(idx), b, ahead);
+    nb = share.blocks(context_length(p, b, false));
+    w = share.units(nb);
+    g = (share.start(idx) - ahead * p.Hkv) / w;
+    u0 = ahead * p.Hkv + g * w;
+  } else if (cut) {
+    nb = share.blocks(context_length(p, b, false));
+    w = share.units(nb);
+    u0 = share.before * p.Hkv + g * w;
+  }
+  const int h0 = g * G + static_cast<int>(blockIdx.y) * H, hg = static_cast<int>(blockIdx.y) * H;
   const size_t head0 = static_cast<size_t>(b) * p.Hq + h0;
-  // Every CTA waits, those without work too: this kernel must not end before the first one.
+  // Rows of empty contexts. (Every CTA waits, those without work too: this kernel must not end
+  // before the first one.)
+  auto clear = [&](size_t row, int rows) {
+    for (int i = tid; i < rows * kQuads; i += kDiffJoinWarps * 32)
+      reinterpret_cast<uint2*>(p.o + row * D)[i] = make_uint2(0, 0);
+    for (int i = tid; i < 2 * rows; i += kDiffJoinWarps * 32) p.lse[2 * row + i] = -INFINITY;
+  };
+  if (workers && blockIdx.y == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int s = idx; s < p.B; s += static_cast<int>(gridDim.x))
+      if (context_length(p, s, false) == 0) clear(static_cast<size_t>(s) * p.Hq, p.Hq);
+  }
   if (nb == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < H * kQuads; i += kDiffJoinWarps * 32)
-      reinterpret_cast<uint2*>(p.o + head0 * D)[i] = make_uint2(0, 0);
-    for (int i = tid; i < 2 * H; i += kDiffJoinWarps * 32) p.lse[2 * head0 + i] = -INFINITY;
+    if (!workers) clear(head0, H);
     return;
   }
-  // The context's first unit, and the workers of its first and last block; the first part is its
-  // worker's first segment only if that has no block of a context before.
-  const int w = share.units(nb), u0 = share.before * p.Hkv + g * w;
+  // The workers of the context's first and last block; the first part is its worker's first segment
+  // only if that has no block of a context before.
   const int c0 = share.worker_of(u0 + share.kStart);
   const int parts = share.worker_of(u0 + w - 1) - c0 + 1;
   const int slot0 = 2 * c0 + (share.start(c0) >= u0 ? 0 : 1);
@@ -526,7 +556,8 @@ __global__ void __launch_bounds__(kDiffJoinWarps * 32, 2)
   const float4 weight = diff_weight(p, quad);
   float lam = __ldg(p.lam + h0 + imin(sets > 1 ? warp % H : warp, H - 1));
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (parts == 1) return;  // one worker held the whole context
+  // One worker held the whole context, or another CTA joins it.
+  if (parts == 1 || (workers && c0 + 1 != idx)) return;
   const int take = sets * kHalves;                 // parts that are taken side by side
   const int round = imin(kBatch * take, 64);       // parts of a round
   for (int hh = sets > 1 ? warp % H : warp; hh < H || sets > 1; hh += kDiffJoinWarps) {
