@@ -367,7 +367,8 @@ class Decode(Pages):
             if b in skip:
                 continue
             k, v = self.ctx[b]
-            want = self.h.rows(self.qv[b], k, v, np.ones((1, n), bool))
+            # Weights as two bf16 terms, each half a step of what it rounds: 2^-8 of 2^-8.
+            want = self.h.rows(self.qv[b], k, v, np.ones((1, n), bool), 2.0 ** -16)
             check(o[b], lse[b][:, :, None], want)
 
 

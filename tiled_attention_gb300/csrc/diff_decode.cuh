@@ -20,9 +20,9 @@
 //
 // Up to 8 heads a kv head; with 9 to 16 there is a tile a map instead, whose rows are the heads.
 //
-// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 165 us, 0.99 of the copy
-// rate; one sequence of 16K 19.8 us, of which the bytes are 9.9 and the rest is the launch, the
-// ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) 70.4 us,
+// Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.98 of the copy
+// rate; one sequence of 16K 20.0 us, of which the bytes are 9.9 and the rest is the launch, the
+// ring's fill and the join. With 16 heads a kv head (D = 64, pages of 16, 48 sequences) 69.8 us,
 // where the bytes take 56.4. A copy that only streams takes 161 and 71 us (the latter with less even
 // shares): what is left is that some SMs get their bytes later than others, 135 to 160 us in the
 // batch.
@@ -366,16 +366,21 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
                            (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
             }
         }
-        // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P. (A second
-        // term with what this rounding leaves would take the weights' share of the error away,
-        // 1.9e-3 of |O| in 2-norm beside the output's 1.7e-3, for twice the products: 48 sequences
-        // of 16 heads a kv head 76 to 81 us, 32 of four 167.7 to 169.6.)
-        uint32_t pa[NT][4];
+        // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P; what their
+        // rounding leaves goes in as a second term, so that weights are good to 2^-16. One term
+        // would leave 1.9e-3 of |O| (2-norm) beside the output's own 1.7e-3, and the products have
+        // time while the bytes come: 32 sequences 166.2 us against 163.8 with one term, 48 of 16
+        // heads a kv head 69.8 against 70.8, 512 short ones 101.8 against 100.2.
+        uint32_t pa[NT][4], pb[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            pa[nt][f] = pack_bf16x2(w[nt][f >> 1][2 * (f & 1)], w[nt][f >> 1][2 * (f & 1) + 1]);
+          for (int f = 0; f < 4; ++f) {
+            const float w0 = w[nt][f >> 1][2 * (f & 1)], w1 = w[nt][f >> 1][2 * (f & 1) + 1];
+            pa[nt][f] = pack_bf16x2(w0, w1);
+            pb[nt][f] = pack_bf16x2(w0 - __uint_as_float(pa[nt][f] << 16),
+                                    w1 - __uint_as_float(pa[nt][f] & 0xffff0000u));
+          }
           l[nt][0] += sum[nt][0];
           l[nt][1] += sum[nt][1];
         }
@@ -387,6 +392,8 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
           for (int nt = 0; nt < NT; ++nt) {
             mma_bf16_16816(o[nt][2 * pair], pa[nt], vb[0], vb[1]);
             mma_bf16_16816(o[nt][2 * pair + 1], pa[nt], vb[2], vb[3]);
+            mma_bf16_16816(o[nt][2 * pair], pb[nt], vb[0], vb[1]);
+            mma_bf16_16816(o[nt][2 * pair + 1], pb[nt], vb[2], vb[3]);
           }
         }
       }
