@@ -37,7 +37,8 @@ cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const DiffDec
     kern<<<p.slots, C::kThreads, C::kSmemBytes, stream>>>(k, v, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  // The joining kernel may start before the decode kernel has ended (it waits for it).
+  // The joining kernel may start before the decode kernel has ended (it waits for it); alone, it
+  // starts after all that is on the stream, since it reads the lengths before it waits.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.join_workers ? p.slots : p.B * p.Hkv, p.group / p.join_heads);
   cfg.blockDim = dim3(kDiffJoinWarps * 32);
@@ -46,7 +47,7 @@ cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const DiffDec
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.max_len > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, diff_join_kernel<D>, p);
 }
 
