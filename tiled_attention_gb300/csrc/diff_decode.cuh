@@ -18,7 +18,8 @@
 // the workspace, two slots a CTA, and a second kernel, under programmatic dependent launch, joins
 // them in the workers' order: results do not depend on timing.
 //
-// Up to 8 heads a kv head; with 9 to 16 there is a tile a map instead, whose rows are the heads.
+// So with up to 8 heads a kv head; with 9 to 16 a warp takes one map, whose tile has a row a head,
+// over twice the tokens.
 //
 // Measured (32 heads over 8, D = 128): 32 sequences of 1K to 16K tokens 166 us, 0.98 of the copy
 // rate; one sequence of 16K 20.0 us, of which the bytes are 9.9 and the rest is the launch, the
@@ -77,7 +78,7 @@ struct DiffDecodeCfg {
   static constexpr int kStages = (96 * 1024) / kStageBytes;  // 3 (D = 128), 6 (D = 64)
   static constexpr int kSteps = D / 16;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kMiscBytes = 1280;
+  static constexpr int kMiscBytes = 768;
   static constexpr int kSmemBytes = 1024 + kRingBytes + kMiscBytes;
   static_assert(kWarps * 16 * D * 4 <= kStageBytes, "a tile's rows are merged in one slot");
   static_assert(kDiffDecodeCtas * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -156,7 +157,7 @@ __device__ __forceinline__ float4 diff_weight(const DiffDecodeParams& p, int qua
                   : make_float4(1.f, 1.f, 1.f, 1.f);
 }
 
-// NT: tiles of eight query heads (1 or 2).
+// NT: 1 for up to 8 heads a kv head, 2 for up to 16.
 template <int D, int NT>
 __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     diff_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -171,9 +172,9 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   DiffDecodeCtrl* ctl = reinterpret_cast<DiffDecodeCtrl*>(ring + C::kRingBytes);
-  float* red_m = reinterpret_cast<float*>(ring + C::kRingBytes + 256);  // [warps][NT][16]
-  float* red_l = red_m + C::kWarps * 32;
-  static_assert(256 + 2 * C::kWarps * 32 * 4 <= C::kMiscBytes, "misc area");
+  float* red_m = reinterpret_cast<float*>(ring + C::kRingBytes + 256);  // [warps][16]
+  float* red_l = red_m + C::kWarps * 16;
+  static_assert(256 + 2 * C::kWarps * 16 * 4 <= C::kMiscBytes, "misc area");
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == C::kConsumers) {
@@ -238,47 +239,47 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   }
 
   // ------------------------------------------------------------------ consumers
-  // A lane holds rows r and r + 8 of the tiles. One tile: head r's maps 0 and 1. Two: heads r and
-  // r + 8, tile m their map m, which no row shares with the other map, so that S_m takes the k-steps
-  // of its own channels alone (100 sequences of up to 8K, 12 heads a kv head, d = 128: 100 to 77 us,
-  // table entries included).
+  // A lane holds rows r and r + 8 of its warp's tile. NT = 1: head r's maps 0 and 1, over a slice of
+  // 16 tokens of every stage. NT = 2: heads r and r + 8 of map warp & 1, over 32 tokens. (With both
+  // maps' tiles in every warp D = 128 needs more registers than two CTAs leave: 100 sequences of up
+  // to 8K, 12 heads on one kv head 81 us against 51; with both maps in one tile, as for NT = 1, 100.)
+  constexpr int kTiles = NT;                         // 16-token tiles of a slice
+  constexpr int kQSteps = C::kSteps / NT;            // k-steps of a warp's S
+  constexpr int kMerge = C::kWarps / NT;             // warps that hold the same rows
   const int r = lane >> 2;
   const int q = lane & 3;
   const float c = p.scale_log2;
-  const int tok_w = warp * 16;
+  const int map = NT == 2 ? warp & 1 : 0;
+  const int tok_w = (NT == 2 ? warp >> 1 : warp) * 16 * kTiles;
   // ldmatrix row addresses: lane -> (matrix, row).
   const int mrow = lane & 7, msel = lane >> 3;
   const int k_token = tok_w + 8 * (msel >> 1) + mrow;  // K: matrices (n-tile, k half)
-  const int k_half = (msel & 1) * 8;
+  const int k_half = (msel & 1) * 8 + map * (D / 2);
   const int v_token = tok_w + 8 * (msel & 1) + mrow;   // V: matrices (n-tile, token half)
   const int v_sub = (msel >> 1) * 8;
   int e = 0;
   bool ok = true;
   for (bool first = true; seg.next(p); first = false) {
     const size_t head0 = (static_cast<size_t>(seg.b) * p.Hkv + seg.g) * G;
-    // Q as the A operand. One tile: k-step kk lies in map 2 kk / kSteps, whose rows alone are not
-    // zero. Two: k-step kk of map m has rows r and r + 8 in qa[m][2 kk] and qa[m][2 kk + 1]. (Asking
-    // for the next segment's before this one's rows are joined gained nothing.)
-    uint32_t qa[NT][C::kSteps][2];
+    // Q as the A operand, rows r and r + 8 and both halves of a k-step. NT = 1: k-step kk lies in
+    // map 2 kk / kSteps, whose rows alone are not zero. (Asking for the next segment's before this
+    // one's rows are joined gained nothing.)
+    uint32_t qa[kQSteps][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int kk = 0; kk < kQSteps; ++kk)
 #pragma unroll
-      for (int x = 0; x < C::kSteps; ++x) {
-        const int head = NT == 1 ? r : 8 * (x & 1) + r;
-        const int kk = NT == 1 ? x : nt * (C::kSteps / 2) + x / 2;
-        const uint32_t* from = p.q + (head0 + head) * (D / 2) + kk * 8 + q;
-        qa[nt][x][0] = head < G ? __ldg(from) : 0u;
-        qa[nt][x][1] = head < G ? __ldg(from + 4) : 0u;
+      for (int h = 0; h < NT; ++h) {
+        const int head = 8 * h + r;
+        const uint32_t* from = p.q + (head0 + head) * (D / 2) + map * (D / 4) + kk * 8 + q;
+        qa[kk][h][0] = head < G ? __ldg(from) : 0u;
+        qa[kk][h][1] = head < G ? __ldg(from + 4) : 0u;
       }
-    float o[NT][D / 8][4];
-    float mx[NT][2], l[NT][2];  // of rows r and r + 8: reference max in log2 units, sum
+    float o[D / 8][4];
+    float mx[2], l[2];  // of rows r and r + 8: reference max in log2 units, sum
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      mx[nt][0] = mx[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-    }
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    mx[0] = mx[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
     int last_st = 0;
     for (int i = 0; i < seg.nblk; ++i, ++e) {
       const int st = e % S;
@@ -287,113 +288,114 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
       if (ok) {
         const uint32_t kp = smem_u32(ring + st * C::kStageBytes);
         const uint32_t vp = kp + C::kHalfBytes;
-        float s[NT][2][4];
+        float s[kTiles][2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int tt = 0; tt < kTiles; ++tt)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) s[nt][x >> 2][x & 3] = 0.f;
+          for (int x = 0; x < 8; ++x) s[tt][x >> 2][x & 3] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < C::kSteps; ++kk) {
-          uint32_t kb[4];
-          ldmatrix_x4(kb, kp + page_chunk(k_token, kk * 16 + k_half));
-          const int m = 2 * kk / C::kSteps;
-          const uint32_t(&x)[C::kSteps][2] = qa[NT == 1 ? 0 : m];
-          float(&sm)[2][4] = s[NT == 1 ? 0 : m];
-          const int at = NT == 1 ? kk : 2 * (kk - m * (C::kSteps / 2));
-          const uint32_t a[4] = {NT == 2 || m == 0 ? x[at][0] : 0u,
-                                 NT == 2 ? x[at + 1][0] : m == 1 ? x[at][0] : 0u,
-                                 NT == 2 || m == 0 ? x[at][1] : 0u,
-                                 NT == 2 ? x[at + 1][1] : m == 1 ? x[at][1] : 0u};
-          mma_bf16_16816(sm[0], a, kb[0], kb[1]);
-          mma_bf16_16816(sm[1], a, kb[2], kb[3]);
+        for (int kk = 0; kk < kQSteps; ++kk) {
+          const bool lo = kk < kQSteps / 2;  // NT = 1: map 0's
+          const uint32_t a[4] = {NT == 2 || lo ? qa[kk][0][0] : 0u,
+                                 NT == 2 ? qa[kk][NT - 1][0] : lo ? 0u : qa[kk][0][0],
+                                 NT == 2 || lo ? qa[kk][0][1] : 0u,
+                                 NT == 2 ? qa[kk][NT - 1][1] : lo ? 0u : qa[kk][0][1]};
+#pragma unroll
+          for (int tt = 0; tt < kTiles; ++tt) {
+            uint32_t kb[4];
+            ldmatrix_x4(kb, kp + page_chunk(k_token + 16 * tt, kk * 16 + k_half));
+            mma_bf16_16816(s[tt][0], a, kb[0], kb[1]);
+            mma_bf16_16816(s[tt][1], a, kb[2], kb[3]);
+          }
         }
         const int left = seg.L - (seg.blk0 + i) * C::kTok - tok_w;  // tokens from this slice on
-        if (left < 16) {
+        if (left < 16 * kTiles) {
           // Slots past the context may hold anything: their scores are dropped below, and their
           // values cleared, since a NaN would survive a weight of zero.
-          for (int x = lane; x < 16 * (D / 8); x += 32) {
+          for (int x = lane; x < 16 * kTiles * (D / 8); x += 32) {
             const int tok = x / (D / 8);
             if (tok >= left)
               st_shared_v4(vp + page_chunk(tok_w + tok, (x % (D / 8)) * 8), 0, 0, 0, 0);
           }
           __syncwarp();
+#pragma unroll
+          for (int tt = 0; tt < kTiles; ++tt)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (16 * tt + 8 * (x >> 2) + 2 * q + (x & 1) >= left)
+                s[tt][x >> 2][x & 3] = -INFINITY;
         }
         // Weights 2^(c s - mx) against the reference max of the row so far; one of a sum above 2^24
         // (a score far above it), and a row's first, has the max found. Element x of n-tile y: row
-        // r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the slice.
-        float w[NT][2][4], sum[NT][2], all = 0.f;
+        // r + 8 (x >> 1), token 8 y + 2 q + (x & 1) of the tile.
+        float w[kTiles][2][4], sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (left < 16) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (8 * (x >> 2) + 2 * q + (x & 1) >= left) s[nt][x >> 2][x & 3] = -INFINITY;
-          }
+        for (int tt = 0; tt < kTiles; ++tt) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            w[nt][x >> 2][x & 3] = fast_exp2(fmaf(s[nt][x >> 2][x & 3], c, -mx[nt][(x & 3) >> 1]));
+            w[tt][x >> 2][x & 3] = fast_exp2(fmaf(s[tt][x >> 2][x & 3], c, -mx[(x & 3) >> 1]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            sum[h] += (w[tt][0][2 * h] + w[tt][0][2 * h + 1]) +
+                      (w[tt][1][2 * h] + w[tt][1][2 * h + 1]);
+        }
+        if (__any_sync(0xffffffffu, !(sum[0] + sum[1] <= kDiffDecodeRaise))) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            sum[nt][h] = (w[nt][0][2 * h] + w[nt][0][2 * h + 1]) +
-                         (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
-            all += sum[nt][h];
-          }
-        }
-        if (__any_sync(0xffffffffu, !(all <= kDiffDecodeRaise))) {
+            float top = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int tt = 0; tt < kTiles; ++tt)
+              top = fmaxf(top, fmaxf(fmaxf(s[tt][0][2 * h], s[tt][0][2 * h + 1]),
+                                     fmaxf(s[tt][1][2 * h], s[tt][1][2 * h + 1])) * c);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // Move the reference only when it grows by more than 8 (a factor of 256).
+            if (top > mx[h] + 8.f) {
+              const float al = fast_exp2(mx[h] - top);  // 0 when the reference is -inf
+              mx[h] = top;
+              l[h] *= al;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float top = fmaxf(fmaxf(s[nt][0][2 * h], s[nt][0][2 * h + 1]),
-                                fmaxf(s[nt][1][2 * h], s[nt][1][2 * h + 1])) * c;
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-              // Move the reference only when it grows by more than 8 (a factor of 256).
-              if (top > mx[nt][h] + 8.f) {
-                const float al = fast_exp2(mx[nt][h] - top);  // 0 when the reference is -inf
-                mx[nt][h] = top;
-                l[nt][h] *= al;
+              for (int i = 0; i < D / 8; ++i) o[i][2 * h] *= al, o[i][2 * h + 1] *= al;
+            }
+            const float sub = mx[h] == -INFINITY ? 0.f : mx[h];
+            sum[h] = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[nt][i][2 * h] *= al, o[nt][i][2 * h + 1] *= al;
-              }
-              const float sub = mx[nt][h] == -INFINITY ? 0.f : mx[nt][h];
+            for (int tt = 0; tt < kTiles; ++tt) {
 #pragma unroll
               for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int x = 2 * h; x < 2 * h + 2; ++x)
-                  w[nt][y][x] = fast_exp2(fmaf(s[nt][y][x], c, -sub));
-              sum[nt][h] = (w[nt][0][2 * h] + w[nt][0][2 * h + 1]) +
-                           (w[nt][1][2 * h] + w[nt][1][2 * h + 1]);
+                  w[tt][y][x] = fast_exp2(fmaf(s[tt][y][x], c, -sub));
+              sum[h] += (w[tt][0][2 * h] + w[tt][0][2 * h + 1]) +
+                        (w[tt][1][2 * h] + w[tt][1][2 * h + 1]);
             }
+          }
         }
+        l[0] += sum[0];
+        l[1] += sum[1];
         // The accumulators of the two n-tiles are, as bf16 pairs, the A fragment of P; what their
         // rounding leaves goes in as a second term, so that weights are good to 2^-16. One term
         // would leave 1.9e-3 of |O| (2-norm) beside the output's own 1.7e-3, and the products have
         // time while the bytes come: 32 sequences 166.2 us against 163.8 with one term, 48 of 16
         // heads a kv head 69.8 against 70.8, 512 short ones 101.8 against 100.2.
-        uint32_t pa[NT][4], pb[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int tt = 0; tt < kTiles; ++tt) {
+          uint32_t pa[4], pb[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const float w0 = w[nt][f >> 1][2 * (f & 1)], w1 = w[nt][f >> 1][2 * (f & 1) + 1];
-            pa[nt][f] = pack_bf16x2(w0, w1);
-            pb[nt][f] = pack_bf16x2(w0 - __uint_as_float(pa[nt][f] << 16),
-                                    w1 - __uint_as_float(pa[nt][f] & 0xffff0000u));
+            const float w0 = w[tt][f >> 1][2 * (f & 1)], w1 = w[tt][f >> 1][2 * (f & 1) + 1];
+            pa[f] = pack_bf16x2(w0, w1);
+            pb[f] = pack_bf16x2(w0 - __uint_as_float(pa[f] << 16),
+                                w1 - __uint_as_float(pa[f] & 0xffff0000u));
           }
-          l[nt][0] += sum[nt][0];
-          l[nt][1] += sum[nt][1];
-        }
 #pragma unroll
-        for (int pair = 0; pair < D / 16; ++pair) {
-          uint32_t vb[4];
-          ldmatrix_x4_trans(vb, vp + page_chunk(v_token, pair * 16 + v_sub));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_16816(o[nt][2 * pair], pa[nt], vb[0], vb[1]);
-            mma_bf16_16816(o[nt][2 * pair + 1], pa[nt], vb[2], vb[3]);
-            mma_bf16_16816(o[nt][2 * pair], pb[nt], vb[0], vb[1]);
-            mma_bf16_16816(o[nt][2 * pair + 1], pb[nt], vb[2], vb[3]);
+          for (int pair = 0; pair < D / 16; ++pair) {
+            uint32_t vb[4];
+            ldmatrix_x4_trans(vb, vp + page_chunk(v_token + 16 * tt, pair * 16 + v_sub));
+            mma_bf16_16816(o[2 * pair], pa, vb[0], vb[1]);
+            mma_bf16_16816(o[2 * pair + 1], pa, vb[2], vb[3]);
+            mma_bf16_16816(o[2 * pair], pb, vb[0], vb[1]);
+            mma_bf16_16816(o[2 * pair + 1], pb, vb[2], vb[3]);
           }
         }
       }
@@ -402,19 +404,17 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
       if (lane == 0 && i + 1 < seg.nblk) mbar_arrive(&ctl->empty[st]);
     }
     // ---------------------------------------------------------------- the segment's rows
-    // Heads 8 g .. 8 g + 7 at a time; map m of head 8 g + r is half h of tile nt's rows.
+    // Row 8 h + r of a warp's tile is map h of head r (NT = 1) or the warp's map of head 8 h + r;
+    // warps w, w + NT, ... hold the same rows.
 #pragma unroll
-    for (int g = 0; g < NT; ++g)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int nt = NT == 1 ? 0 : m, h = NT == 1 ? m : g;
-        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 1);
-        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 2);
-        if (q == 0) {
-          red_m[(warp * NT + g) * 16 + 8 * m + r] = mx[nt][h];
-          red_l[(warp * NT + g) * 16 + 8 * m + r] = l[nt][h];
-        }
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (q == 0) {
+        red_m[warp * 16 + 8 * h + r] = mx[h];
+        red_l[warp * 16 + 8 * h + r] = l[h];
       }
+    }
     named_barrier_sync(1, C::kConsumers);  // and every consumer is past its last read of the slot
     // Each warp's rows, rescaled to the common max: [warp][16][D] fp32, columns rotated by eight a
     // row against bank conflicts.
@@ -422,66 +422,59 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
     const bool whole = seg.nblk == seg.nb;
     const size_t slot = 2 * static_cast<size_t>(worker) + (first ? 0 : 1);
 #pragma unroll
-    for (int g = 0; g < NT; ++g) {
-      if (g) named_barrier_sync(1, C::kConsumers);  // the heads before have been read
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * h + r;
+      float M = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kMerge; ++x) M = fmaxf(M, red_m[((warp & (NT - 1)) + x * NT) * 16 + row]);
+      const float f = l[h] != 0.f ? fast_exp2(mx[h] - M) : 0.f;
+      if ((NT == 2 ? row : r) < G) {
+        float* to = buf + (warp * 16 + row) * D;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t)
+          *reinterpret_cast<float2*>(to + ((8 * t + 2 * q + 8 * r) & (D - 1))) =
+              make_float2(o[t][2 * h] * f, o[t][2 * h + 1] * f);
+      }
+    }
+    named_barrier_sync(1, C::kConsumers);
+    constexpr int kQuads = D / 4;
+    for (int idx = tid; idx < G * kQuads; idx += C::kConsumers) {
+      const int hg = idx / kQuads, quad = idx % kQuads;
+      const int col = (4 * quad + 8 * (hg & 7)) & (D - 1);
+      float4 a[2];
+      float2 ml[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int nt = NT == 1 ? 0 : m, h = NT == 1 ? m : g;
-        const int at = g * 16 + 8 * m + r;
-        float M = red_m[at];
+        const int w0 = NT == 2 ? m : 0, row = NT == 2 ? hg : 8 * m + hg;
+        const float* from = buf + (w0 * 16 + row) * D + col;
+        float4 w[kMerge];
 #pragma unroll
-        for (int w = 1; w < C::kWarps; ++w) M = fmaxf(M, red_m[w * NT * 16 + at]);
-        const float f = l[nt][h] != 0.f ? fast_exp2(mx[nt][h] - M) : 0.f;
-        if (8 * g + r < G) {
-          float* to = buf + (warp * 16 + 8 * m + r) * D;
+        for (int x = 0; x < kMerge; ++x)
+          w[x] = *reinterpret_cast<const float4*>(from + x * NT * 16 * D);
+        a[m] = make_float4(w[0].x + w[1].x, w[0].y + w[1].y, w[0].z + w[1].z, w[0].w + w[1].w);
+        if constexpr (kMerge == 4)
+          a[m] = make_float4(a[m].x + (w[2].x + w[3].x), a[m].y + (w[2].y + w[3].y),
+                             a[m].z + (w[2].z + w[3].z), a[m].w + (w[2].w + w[3].w));
+        float M = -INFINITY, Ls = 0.f;
 #pragma unroll
-          for (int t = 0; t < D / 8; ++t)
-            *reinterpret_cast<float2*>(to + ((8 * t + 2 * q + 8 * r) & (D - 1))) =
-                make_float2(o[nt][t][2 * h] * f, o[nt][t][2 * h + 1] * f);
+        for (int x = 0; x < kMerge; ++x) M = fmaxf(M, red_m[(w0 + x * NT) * 16 + row]);
+#pragma unroll
+        for (int x = 0; x < kMerge; ++x) {
+          const float lw = red_l[(w0 + x * NT) * 16 + row];
+          if (lw != 0.f) Ls += lw * fast_exp2(red_m[(w0 + x * NT) * 16 + row] - M);
         }
+        ml[m] = make_float2(M, Ls);
       }
-      named_barrier_sync(1, C::kConsumers);
-      constexpr int kQuads = D / 4;
-      const int heads = imin(8, G - 8 * g);
-      for (int idx = tid; idx < heads * kQuads; idx += C::kConsumers) {
-        const int hh = idx / kQuads, quad = idx % kQuads;
-        const int col = (4 * quad + 8 * hh) & (D - 1);
-        float4 a[2];
-        float2 ml[2];
+      if (whole) {
+        const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+        diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad,
+                       a[0], a[1], ml[0], ml[1], lanes);
+      } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float* from = buf + (8 * h + hh) * D + col;
-          float4 w[C::kWarps];
-#pragma unroll
-          for (int x = 0; x < C::kWarps; ++x)
-            w[x] = *reinterpret_cast<const float4*>(from + x * 16 * D);
-          a[h] = make_float4((w[0].x + w[2].x) + (w[1].x + w[3].x),
-                             (w[0].y + w[2].y) + (w[1].y + w[3].y),
-                             (w[0].z + w[2].z) + (w[1].z + w[3].z),
-                             (w[0].w + w[2].w) + (w[1].w + w[3].w));
-          const int at = g * 16 + 8 * h + hh;
-          float M = red_m[at], Ls = 0.f;
-#pragma unroll
-          for (int x = 1; x < C::kWarps; ++x) M = fmaxf(M, red_m[x * NT * 16 + at]);
-#pragma unroll
-          for (int x = 0; x < C::kWarps; ++x) {
-            const float lw = red_l[x * NT * 16 + at];
-            if (lw != 0.f) Ls += lw * fast_exp2(red_m[x * NT * 16 + at] - M);
-          }
-          ml[h] = make_float2(M, Ls);
-        }
-        const int hg = 8 * g + hh;
-        if (whole) {
-          const unsigned lanes = kQuads == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
-          diff_finish<D>(p, head0 + hg, __ldg(p.lam + seg.g * G + hg), diff_weight(p, quad), quad,
-                         a[0], a[1], ml[0], ml[1], lanes);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const size_t at = (slot * 2 + h) * G + hg;
-            *reinterpret_cast<float4*>(p.part_o + at * D + 4 * quad) = a[h];
-            if (quad == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = ml[h];
-          }
+        for (int m = 0; m < 2; ++m) {
+          const size_t at = (slot * 2 + m) * G + hg;
+          *reinterpret_cast<float4*>(p.part_o + at * D + 4 * quad) = a[m];
+          if (quad == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = ml[m];
         }
       }
     }
