@@ -997,6 +997,43 @@ def test_more_chunk_units_than_three_an_sm(page):
     c.check(o, lse)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (12, 1), (6, 2), (32, 2), (16, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_share_a_tile(Hq, Hkv, d):
+    """Chunks and document segments whose last 128-row tile has few rows, of heads that share a kv
+    head: powers of two that divide the group go into one tile."""
+    rng = np.random.default_rng(30 + Hq + d)
+    lq = [1, 8, 9, 16, 17, 32, 33, 64, 65, 0, 130, 192, 193, 257, 5]
+    c = Chunk(rng, [n + int(x) for n, x in zip(lq, rng.integers(0, 300, len(lq)))], lq, Hq, Hkv, d, 16)
+    o, lse = c.run()
+    assert status() == 0
+    c.check(o, lse)
+    n, h = sum(lq), c.h
+    cu = np.concatenate([[0], np.cumsum(lq)]).astype(np.int32)
+    (k, kv), (v, vv) = (draw(rng, 1, Hkv, n, d) for _ in range(2))
+    for mask in ("document", "document_bidir"):
+        o, lse = run_diff(h, c.q, k, v, KINDS[mask], 0, dev(cu), len(lq))
+        assert status() == 0
+        o, lse = f64(o[0]), f64(lse[0])
+        for a, b in zip(cu[:-1], cu[1:]):
+            if a < b:
+                check(o[:, a:b], lse[:, :, a:b], h.rows(c.qv[0][:, a:b], kv[0][:, a:b],
+                                                        vv[0][:, a:b], diff.visible(mask, 0, b - a)))
+
+
+@pytest.mark.parametrize("n", [1, 7, 8, 17, 40, 64, 65, 150, 192, 200])
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_dense_rows_share_a_tile(n, d):
+    rng = np.random.default_rng(31 + n + d)
+    h = Head(rng, 24, d)
+    for mask, window in (("none", 0), ("causal", 0), ("sliding", 9), ("prefix", 5)):
+        (q, qv), (k, kv), (v, vv) = (draw(rng, 9, x, n, d) for x in (24, 3, 3))
+        o, lse = run_diff(h, q, k, v, KINDS[mask], window)
+        assert status() == 0
+        for b in range(0, 9, 4):
+            check(f64(o[b]), f64(lse[b]), h.rows(qv[b], kv[b], vv[b], diff.visible(mask, window, n)))
+
+
 def test_prefills_at_once():
     """Dense, packed and chunk attention on three streams at once, each of more units than the GPU
     holds, give the bits that they give alone."""

@@ -13,25 +13,29 @@
 namespace ta {
 namespace {
 
+// Q by tiles of 128 rows and by boxes of 8, K and V, and O by boxes of 32 rows of half a head.
+struct DiffMaps {
+  CUtensorMap q, q8, k, v, o;
+};
+
 template <int D, int PACK, int CTAS>
-cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                       const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_one(const DiffMaps& t, const DiffParams& p, int grid, cudaStream_t stream) {
   static unsigned long long done = 0;
   auto kern = diff_prefill_kernel<D, PACK, CTAS>;
   using C = DiffCfg<D, PACK, CTAS>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(q, k, v, o, p);
+  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(t.q, t.q8, t.k, t.v, t.o, p);
   return cudaGetLastError();
 }
 
 template <int D, int CTAS>
-cudaError_t launch(int mask, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const CUtensorMap& o, const DiffParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch(int mask, const DiffMaps& t, const DiffParams& p, int grid,
+                   cudaStream_t stream) {
   if (mask == kMaskPagedPrefill)
-    return launch_one<D, kMaskPagedPrefill, CTAS>(q, k, v, o, p, grid, stream);
-  if (is_packed(mask)) return launch_one<D, kMaskDocument, CTAS>(q, k, v, o, p, grid, stream);
-  return launch_one<D, kMaskNone, CTAS>(q, k, v, o, p, grid, stream);
+    return launch_one<D, kMaskPagedPrefill, CTAS>(t, p, grid, stream);
+  if (is_packed(mask)) return launch_one<D, kMaskDocument, CTAS>(t, p, grid, stream);
+  return launch_one<D, kMaskNone, CTAS>(t, p, grid, stream);
 }
 
 // At d = 64 two CTAs fit an SM, each with one S buffer a map: four softmax warps a scheduler hide
@@ -41,13 +45,21 @@ cudaError_t launch(int mask, const CUtensorMap& q, const CUtensorMap& k, const C
 // of 8192 462 and 435; 8 chunks of up to 1024 tokens over 16K, 64 heads over 4, 1127 and 957.
 int ctas_of(int d, long long units) { return d == 64 && units > 3ll * sms_or_default() ? 2 : 1; }
 
-cudaError_t launch(int d, int ctas, int mask, const CUtensorMap& q, const CUtensorMap& k,
-                   const CUtensorMap& v, const CUtensorMap& o, const DiffParams& p,
+cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParams& p,
                    cudaStream_t stream) {
   const int grid = p.base.num_units;  // a block a unit: resident ones take over those that wait
-  if (d == 128) return launch<128, 1>(mask, q, k, v, o, p, grid, stream);
-  return ctas == 2 ? launch<64, 2>(mask, q, k, v, o, p, grid, stream)
-                   : launch<64, 1>(mask, q, k, v, o, p, grid, stream);
+  if (d == 128) return launch<128, 1>(mask, t, p, grid, stream);
+  return ctas == 2 ? launch<64, 2>(mask, t, p, grid, stream)
+                   : launch<64, 1>(mask, t, p, grid, stream);
+}
+
+// Query heads of one kv head that may share a tile, as a power of two. Units that the GPU holds at
+// once go apart (one prompt of 64 tokens, 32 heads: 6.3 us, two heads a tile 8.4).
+int head_shift(int group, long long units) {
+  int s = 0;
+  if (units <= sms_or_default()) return 0;
+  while (s < 4 && group % (2 << s) == 0) ++s;
+  return s;
 }
 
 // o and lse are written while other CTAs still read the inputs.
@@ -128,13 +140,14 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   if (rc) return rc;
   DiffParams p{};
   if ((rc = status_ptr(&p.base.status))) return rc;
-  CUtensorMap tq, tk, tv, to;
-  if ((rc = encode_3d(&tq, q, d, N, planes, 128))) return rc;
-  if ((rc = encode_3d(&to, o, d, N, planes, 32, d / 2))) return rc;
+  DiffMaps t;
+  if ((rc = encode_3d(&t.q, q, d, N, planes, 128))) return rc;
+  if ((rc = encode_3d(&t.q8, q, d, N, planes, 8))) return rc;
+  if ((rc = encode_3d(&t.o, o, d, N, planes, 32, d / 2))) return rc;
   const int ctas = ctas_of(d, units);
   const uint32_t tile = d == 64 && ctas == 1 ? DiffCfg<64, kMaskNone, 1>::BN : 64;
-  if ((rc = encode_3d(&tk, k, d, N, planes_kv, tile))) return rc;
-  if ((rc = encode_3d(&tv, v, d, N, planes_kv, tile))) return rc;
+  if ((rc = encode_3d(&t.k, k, d, N, planes_kv, tile))) return rc;
+  if ((rc = encode_3d(&t.v, v, d, N, planes_kv, tile))) return rc;
   p.base.o = o;
   p.base.lse = lse;
   p.base.cu_seqlens = cu_seqlens;
@@ -143,6 +156,7 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   p.base.Hkv = Hkv;
   p.base.N = N;
   p.base.group = Hq / Hkv;
+  p.head_shift = head_shift(Hq / Hkv, units);
   p.base.num_units = static_cast<int>(units);
   p.base.window = window;
   p.base.scale_log2 = scale * kLog2e;
@@ -153,7 +167,7 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   p.out_scale = out_scale;
   p.mask = mask_kind;
   const cudaError_t e =
-      launch(d, ctas, mask_kind, tq, tk, tv, to, p, static_cast<cudaStream_t>(stream));
+      launch(d, ctas, mask_kind, t, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
   return ATTN_OK;
 }
@@ -193,13 +207,14 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   if (rc) return rc;
   DiffParams p{};
   if ((rc = status_ptr(&p.base.status))) return rc;
-  CUtensorMap tq, tk, tv, to;
-  if ((rc = encode_3d(&tq, q, d, total_q, Hq, 128))) return rc;
-  if ((rc = encode_3d(&to, o, d, total_q, Hq, 32, d / 2))) return rc;
+  DiffMaps t;
+  if ((rc = encode_3d(&t.q, q, d, total_q, Hq, 128))) return rc;
+  if ((rc = encode_3d(&t.q8, q, d, total_q, Hq, 8))) return rc;
+  if ((rc = encode_3d(&t.o, o, d, total_q, Hq, 32, d / 2))) return rc;
   const uint64_t planes = static_cast<uint64_t>(num_pages) * Hkv;
   const uint32_t box = page_size < 64 ? page_size : 64;  // rows of a page in one 64-key tile
-  if ((rc = encode_3d(&tk, k, d, page_size, planes, box))) return rc;
-  if ((rc = encode_3d(&tv, v, d, page_size, planes, box))) return rc;
+  if ((rc = encode_3d(&t.k, k, d, page_size, planes, box))) return rc;
+  if ((rc = encode_3d(&t.v, v, d, page_size, planes, box))) return rc;
   p.base.o = o;
   p.base.lse = lse;
   p.base.cu_seqlens = cu_seqlens_q;
@@ -214,6 +229,7 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.base.Hkv = Hkv;
   p.base.N = total_q;
   p.base.group = Hq / Hkv;
+  p.head_shift = head_shift(Hq / Hkv, units);
   p.base.num_units = static_cast<int>(units);
   p.base.scale_log2 = scale * kLog2e;
   p.base.timeout_ns = kTimeoutNs;
@@ -222,7 +238,7 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = kMaskPagedPrefill;
-  const cudaError_t e = launch(d, ctas_of(d, units), kMaskPagedPrefill, tq, tk, tv, to, p,
+  const cudaError_t e = launch(d, ctas_of(d, units), kMaskPagedPrefill, t, p,
                                static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "differential paged prefill launch");
   return ATTN_OK;
