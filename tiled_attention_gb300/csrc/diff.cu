@@ -127,8 +127,8 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   if ((rc = diff_checks(q, k, v, o, lse, lam, norm_weight, eps, out_scale))) return rc;
   const long long planes = doc ? Hq : static_cast<long long>(B) * Hq;
   const long long planes_kv = doc ? Hkv : static_cast<long long>(B) * Hkv;
-  const long long units =
-      doc ? 2ll * Hq * (N / kUnitRows + static_cast<long long>(B)) : planes * tiles_for_rows(N);
+  const int tiles = tiles_for_rows(N);
+  long long units = doc ? 2ll * Hq * (N / kUnitRows + static_cast<long long>(B)) : planes * tiles;
   if (planes >= (1ll << 31) || units >= (1ll << 31) - 1 || N > INT32_MAX - 512)
     return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
   const size_t q_bytes = static_cast<size_t>(planes) * N * d * 2;
@@ -144,6 +144,9 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   if ((rc = encode_3d(&t.q, q, d, N, planes, 128))) return rc;
   if ((rc = encode_3d(&t.q8, q, d, N, planes, 8))) return rc;
   if ((rc = encode_3d(&t.o, o, d, N, planes, 32, d / 2))) return rc;
+  p.head_shift = head_shift(Hq / Hkv, units);
+  if (!doc)  // units of several heads' last rows
+    units -= planes - (planes >> (7 - tile_rows_log2(N - 128 * (tiles - 1), p.head_shift)));
   const int ctas = ctas_of(d, units);
   const uint32_t tile = d == 64 && ctas == 1 ? DiffCfg<64, kMaskNone, 1>::BN : 64;
   if ((rc = encode_3d(&t.k, k, d, N, planes_kv, tile))) return rc;
@@ -156,7 +159,6 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   p.base.Hkv = Hkv;
   p.base.N = N;
   p.base.group = Hq / Hkv;
-  p.head_shift = head_shift(Hq / Hkv, units);
   p.base.num_units = static_cast<int>(units);
   p.base.window = window;
   p.base.scale_log2 = scale * kLog2e;

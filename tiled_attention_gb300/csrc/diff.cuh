@@ -110,9 +110,9 @@ struct DiffCfg {
 
 // A work unit as the producer hands it to the other warps, with its key tiles. Where at most 64 rows
 // of a segment are left, the tile takes those of several heads of one kv head, a power of two (at
-// least 8) of rows each, and the units of all but the first of them have no work (32 chunks of up to
-// 16 tokens over 500-4000, 64 heads over 4, d = 64: 278 to 97 us; 32 over 8, d = 128: 192 to 101;
-// 64 dense prompts of 40 tokens 43 to 34).
+// least 8) of rows each; the other heads' units are not there (dense masks) or have no work (32 chunks
+// of up to 16 tokens over 500-4000, 64 heads over 4, d = 64: 278 to 97 us; 32 over 8, d = 128: 192 to
+// 101; 64 dense prompts of 40 tokens 43 to 30).
 struct DiffTask {
   Unit un;
   KvRange rng;
@@ -228,11 +228,20 @@ __device__ __forceinline__ int unit_answer(const uint4* from) {
   return x;
 }
 
+// log2 of one head's rows in a tile that begins with `left` rows of a segment left.
+TA_HD int tile_rows_log2(int left, int head_shift) {
+  int log2 = 7 - head_shift;
+  if (log2 < 3) log2 = 3;
+  while (log2 < 7 && (1 << log2) < left) ++log2;
+  return log2;
+}
+
 // Work unit u in launch order: 128-row tiles from the last one down, then batch and head; packed
 // kinds take the two halves of prefill.cuh's 256-row units, the later (longer) one first. q_row0
 // may lie past the segment (an odd number of tiles): that unit has no key tiles.
 template <int PACK>
-__device__ __forceinline__ Unit diff_unit(int u, const PrefillParams& p, UnitCursor& cur) {
+__device__ __forceinline__ Unit diff_unit(int u, const DiffParams& dp, UnitCursor& cur) {
+  const PrefillParams& p = dp.base;
   if constexpr (PACK != kMaskNone) {
     Unit r = decode_unit<PACK>(u >> 1, p, cur);
     if (r.valid && !(u & 1)) r.q_row0 += 128;
@@ -240,9 +249,13 @@ __device__ __forceinline__ Unit diff_unit(int u, const PrefillParams& p, UnitCur
   } else {
     Unit r{0, 0, 0, 0, 0, 0, 0};
     const int per_level = p.B * p.Hq;
-    const int level = tiles_for_rows(p.N) - 1 - u / per_level;
+    // The last tiles, several heads of which may be one unit.
+    const int top = tiles_for_rows(p.N) - 1;
+    const int s = 7 - tile_rows_log2(p.N - 128 * top, dp.head_shift);
+    const int over = u - (per_level >> s);
+    const int level = over < 0 ? top : top - 1 - over / per_level;
     if (level < 0) return r;
-    const int bh = u % per_level;
+    const int bh = over < 0 ? u << s : over % per_level;
     r.valid = 1;
     r.bh = bh;
     r.kvh = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / p.group;
@@ -350,13 +363,9 @@ __global__ void __launch_bounds__(384, CTAS)
         if (warp == 0) {
           if (lane == 0) ask_unit(&ctl->answer[asked & 1], &ctl->asked[asked & 1]);
           ++asked;
-          task.un = diff_unit<PACK>(u, p, cur);  // warp-collective
-          task.rows_log2 = 7;
-          const int left = task.un.k_end - task.un.q_row0;
-          if (task.un.valid && left > 0 && left <= 64) {
-            task.rows_log2 = imax(imax(3, 32 - __clz(left - 1)), 7 - dp.head_shift);
-            task.un.valid = (task.un.bh & ((128 >> task.rows_log2) - 1)) == 0;
-          }
+          task.un = diff_unit<PACK>(u, dp, cur);  // warp-collective
+          task.rows_log2 = tile_rows_log2(task.un.k_end - task.un.q_row0, dp.head_shift);
+          if (task.un.bh & ((128 >> task.rows_log2) - 1)) task.un.valid = 0;
           task.rng = kv_tile_range(mask, p.window, task.un.q_row0, BM, task.un.k_end, task.un.k_org,
                                    task.un.k_end, BN);
           const bool work = task.un.valid && task.rng.hi > task.rng.lo;
