@@ -438,8 +438,7 @@ __global__ void __launch_bounds__(384, CTAS)
             const int first = warp == 3 ? 1 : 0, last = split_v && warp == 0 ? 0 : 1;
             for (int x = 0; x < npos && ok; ++x, ++e) {
               const int st = e % STAGES;
-              if (lane == 0) ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
-              ok = __shfl_sync(kFull, ok, 0);
+              ok = wait_at(smem_u32(&ctl->kv_empty[st]), ((e / STAGES) & 1) ^ 1, wc);
               if (!ok) break;
               if (lane == 0)
                 for (int y = first; y <= last; ++y)
