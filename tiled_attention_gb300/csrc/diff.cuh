@@ -409,28 +409,22 @@ __global__ void __launch_bounds__(384, CTAS)
                             un.bh + (at >> task.rows_log2));
             }
           }
-          if (lane == 0) {
-            for (int x = 0; !kPaged && x < npos && ok; ++x, ++e) {
-              const int st = e % STAGES;
-              ok = mbar_wait(&ctl->kv_empty[st], ((e / STAGES) & 1) ^ 1, wc);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&ctl->kv_full[st], C::kStageBytes);
-              uint8_t* dst = kv_s + st * C::kStageBytes;
-              const int key = un.k_org + (rng.lo + x) * BN;
-              for (int c = 0; c < C::kPanels; ++c)
-                tma_load_3d(dst + c * C::kPanelBytes, &tm_k, &ctl->kv_full[st], c * 64, key,
-                            un.kvh);
-              for (int c = 0; c < C::kPanels; ++c)
-                tma_load_3d(dst + C::kTileBytes + c * C::kPanelBytes, &tm_v, &ctl->kv_full[st],
-                            c * 64, key, un.kvh);
-            }
+          for (int x = 0; !kPaged && x < npos; ++x, ++e) {
+            const int st = e % STAGES;
+            ok = wait_at(smem_u32(&ctl->kv_empty[st]), ((e / STAGES) & 1) ^ 1, wc);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[st], C::kStageBytes);
+            __syncwarp();
+            if (lane < 2 * C::kPanels)  // panels of K, then of V
+              tma_load_3d(kv_s + st * C::kStageBytes + lane * C::kPanelBytes,
+                          lane < C::kPanels ? &tm_k : &tm_v, &ctl->kv_full[st],
+                          lane % C::kPanels * 64, un.k_org + (rng.lo + x) * BN, un.kvh);
           }
-          ok = __shfl_sync(kFull, ok, 0);
           if constexpr (kPaged) {
-            // Lane sb issues the boxes of page sb of every key tile (one half of a page of 128);
+            // A lane issues a box of a page of the key tile (one half of a page of 128);
             // pages past the context or outside the pool come from the zero-filled plane past it.
             const int lp = p.page_shift;
-            const int run = imin(BN, 1 << lp), nb = BN / run;
+            const int run = imin(BN, 1 << lp), nb = BN / run, sb = lane & (nb - 1);
             const int lk = un.k_end - un.k_org;
             const int* trow = p.table + static_cast<size_t>(un.seq) * p.max_pages;
             PageEntries pages(trow, rng.lo * BN, run, lp, lk);
@@ -444,19 +438,18 @@ __global__ void __launch_bounds__(384, CTAS)
                 for (int y = first; y <= last; ++y)
                   mbar_arrive_expect_tx(&ctl->kv_full[st], C::kTileBytes);
               __syncwarp();
-              const int raw = pages.at(x * nb);
+              const int raw = pages.at(x * nb, sb);
               int pl = p.num_pages * p.Hkv;
               if (raw >= 0 && raw < p.num_pages)
                 pl = raw * p.Hkv + un.kvh;
-              else if (lane < nb && (rng.lo + x) * BN + lane * run < lk)
+              else if (lane < nb && (rng.lo + x) * BN + sb * run < lk)
                 report_status(p.status, -5);
-              if (lane < nb) {
+              const int kind = first * C::kPanels + lane / nb;  // panels of K, then of V
+              if (kind < (last + 1) * C::kPanels) {
                 const int row0 = nb > 1 ? 0 : ((rng.lo + x) * BN) & ((1 << lp) - 1);
-                uint8_t* dst = kv_s + st * C::kStageBytes + lane * run * 128;
-                for (int y = first; y <= last; ++y)
-                  for (int c = 0; c < C::kPanels; ++c)
-                    tma_load_3d(dst + y * C::kTileBytes + c * C::kPanelBytes, y ? &tm_v : &tm_k,
-                                &ctl->kv_full[st], c * 64, row0, pl);
+                tma_load_3d(kv_s + st * C::kStageBytes + kind * C::kPanelBytes + sb * run * 128,
+                            kind < C::kPanels ? &tm_k : &tm_v, &ctl->kv_full[st],
+                            kind % C::kPanels * 64, row0, pl);
               }
             }
           }

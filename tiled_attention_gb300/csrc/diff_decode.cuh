@@ -198,11 +198,11 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
   if (warp == C::kWarps) {
     // ---------------------------------------------------------------- TMA producer
     // A stage is one box a panel of a page of 64 tokens or of half a page of 128, or whole pages of
-    // 16 or 32, lane sb issuing page sb's boxes. A page past
+    // 16 or 32, a lane a box. A page past
     // the context, or whose entry lies outside the pool (never addressed; the status word
     // reports it), comes from the plane past the pool, which TMA fills with zeros.
     const int lp = p.page_shift;
-    const int run = imin(C::kTok, 1 << lp), nbox = C::kTok / run;
+    const int run = imin(C::kTok, 1 << lp), nbox = C::kTok / run, sb = lane & (nbox - 1);
     int e = 0;  // stages issued
     bool ok = true;
     while (ok && seg.next(p)) {
@@ -212,24 +212,20 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
         const int st = e % S;
         ok = wait_at(smem_u32(&ctl->empty[st]), ((e / S) & 1) ^ 1, wc);
         if (!ok) break;
-        uint8_t* dst = ring + st * C::kStageBytes + lane * run * 128;
-        const int raw = pages.at(i * nbox);
+        const int raw = pages.at(i * nbox, sb);
         int pl = p.num_pages * p.Hkv;
         if (raw >= 0 && raw < p.num_pages)
           pl = raw * p.Hkv + seg.g;
-        else if (lane < nbox && (seg.blk0 + i) * C::kTok + lane * run < seg.L)
+        else if (lane < nbox && (seg.blk0 + i) * C::kTok + sb * run < seg.L)
           report_status(p.status, -5);
         const int row0 = ((seg.blk0 + i) * C::kTok) & ((1 << lp) - 1);  // second half of a page
         if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], C::kStageBytes);
         __syncwarp();
-        if (lane < nbox) {
-#pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn) {
-            tma_load_3d(dst + pn * C::kPanelBytes, &tm_k, &ctl->full[st], pn * 64, row0, pl);
-            tma_load_3d(dst + C::kHalfBytes + pn * C::kPanelBytes, &tm_v, &ctl->full[st], pn * 64,
-                        row0, pl);
-          }
-        }
+        const int kind = lane / nbox;  // panels of K, then of V
+        if (kind < 2 * C::kPanels)
+          tma_load_3d(ring + st * C::kStageBytes + kind * C::kPanelBytes + sb * run * 128,
+                      kind < C::kPanels ? &tm_k : &tm_v, &ctl->full[st], kind % C::kPanels * 64, row0,
+                      pl);
       }
     }
     if (lane == 0)

@@ -37,14 +37,14 @@ struct PageEntries {
     const int tok = first + (box + static_cast<int>(lane_id())) * run;
     return tok < length ? __ldg(row + (tok >> page_shift)) : -1;
   }
-  // Entry of box `box` + lane (-1 past the context), for lanes below the boxes a tile has, a power
-  // of two. Warp-collective, for multiples of those in order from 0 on.
-  __device__ __forceinline__ int at(int box) {
+  // Entry of box `box` + i (-1 past the context), i below the boxes a tile has, a power of two.
+  // Warp-collective, for multiples of those in order from 0 on.
+  __device__ __forceinline__ int at(int box, int i) {
     if ((box & 31) == 0) {
       now = next;
       next = load(box + 32);
     }
-    return __shfl_sync(0xffffffffu, now, (box + static_cast<int>(lane_id())) & 31);
+    return __shfl_sync(0xffffffffu, now, (box + i) & 31);
   }
 };
 
