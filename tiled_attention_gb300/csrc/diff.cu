@@ -38,11 +38,11 @@ cudaError_t launch(int mask, const DiffMaps& t, const DiffParams& p, int grid,
   return launch_one<D, kMaskNone, CTAS>(t, p, grid, stream);
 }
 
-// At d = 64 two CTAs fit an SM, each with one S buffer a map: four softmax warps a scheduler hide
-// one another's waits. With at most three units an SM one CTA with two buffers and longer key tiles
-// ends a unit sooner. One CTA and two: 16 heads, one causal row of 1024 13.9 and 17.5 us (0.8 units
-// an SM), two of 1500 30.8 and 31.6 (2.5), three of 5003 in a window of 1000 149 and 142 (12.6), two
-// of 8192 462 and 435; 8 chunks of up to 1024 tokens over 16K, 64 heads over 4, 1127 and 957.
+// At d = 64 two CTAs fit an SM, each with one S buffer a map. With at most three units an SM one CTA
+// with two buffers and longer key tiles ends a unit sooner. One CTA and two: 16 heads, one causal row
+// of 1024 13.9 and 17.5 us (0.8 units an SM), two of 1500 30.8 and 29.2 (2.5), three of 5003 in a
+// window of 1000 149 and 131 (12.6), two of 8192 462 and 429; 8 chunks of up to 1024 tokens over 16K,
+// 64 heads over 4, 1127 and 862.
 int ctas_of(int d, long long units) { return d == 64 && units > 3ll * sms_or_default() ? 2 : 1; }
 
 cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParams& p,

@@ -12,7 +12,7 @@
 // leaves the SM. Each map keeps its own running max and sum (the sums differ, so the accumulators
 // cannot be joined before the end).
 //
-// Roles (384 threads):
+// Roles (384 threads, or 256):
 //   warp 0      finds the CTA's units (below) and loads by TMA: the unit's Q tile, then K_j and V_j
 //               of a tile into one stage of a ring
 //   warps 1, 2  MMA issuers of map 0 and 1: S_m = Q_m K_m^T (SS; map m is k-steps [m D/32,
@@ -23,16 +23,18 @@
 //   warps 4-7   softmax of map 0, warps 8-11 of map 1; a thread owns one query row. At the end
 //               warps q of both take columns [0, D/2) and [D/2, D) of both accumulators: x = O_0 /
 //               l_0 - lam O_1 / l_1, the row's sum of squares is exchanged through shared
-//               memory, and the scaled row goes out by TMA.
+//               memory, and the scaled row goes out by TMA. (Or four warps take both maps in turn,
+//               and a thread has all of its row.)
 // TMEM columns: S of map m, buffer b of kSBufs at (kSBufs m + b) BN (P takes the place of its S),
 // then O_0 and O_1, D each.
 //
 // Key tiles are of 64 keys with two S buffers a map (one tile of 128 and one buffer: causal 2 x 8192
 // 1253 us against 1105); 96 where d = 64 leaves the columns. At d = 64 and with many units two CTAs
-// share an SM, with one S buffer a map each: the softmax is what bounds it there, and four warps a
-// scheduler hide one another's waits (a window of 1000 over 3 x 5003 149 to 142 us, chunks of 64
-// heads over 16K contexts 1127 to 957). Their rows' scores are then held 32 columns at a time: all
-// 64 at once spilled (183 us).
+// share an SM, with one S buffer a map each: the softmax is what bounds it there, and more of it is
+// in flight (a window of 1000 over 3 x 5003 149 to 130 us, chunks of 64 heads over 16K contexts 1127
+// to 862). Over pages eight softmax warps a CTA hide one another's waits, with 32 columns of scores
+// in registers at a time (all 64 spilled: 183 us of the window). Else four warps, which take both
+// maps in turn (window 141 to 130, 200 prompts of 17 tokens 55 to 48; over pages 862 to 897).
 //
 // A warp goes by its own 32 rows: a tile that all of them see all of takes the short loop, one that
 // none sees gets P = 0 (by the unit's 128 rows: window 146 us against 142).
@@ -48,7 +50,7 @@
 // sums are those of the unrounded weights, in fp32.
 //
 // Measured (heads 32 over 8, D = 128): causal 2 x 8192 1060 us = 1.55 PFLOP/s of the pairs under the
-// mask; 16 chunks of up to 2048 tokens over up to 16K 2.28 ms; D = 64, 3 x 5003, window of 1000 141
+// mask; 16 chunks of up to 2048 tokens over up to 16K 2.28 ms; D = 64, 3 x 5003, window of 1000 131
 // us.
 #pragma once
 
@@ -84,7 +86,9 @@ struct DiffCfg {
   static constexpr int BN = D == 64 && PACK != kMaskPagedPrefill && CTAS == 1 ? 96 : 64;
   static constexpr int kCtas = CTAS;
   static constexpr int kSBufs = 3 - kCtas;           // S buffers a map
-  static constexpr int kThreads = 384;
+  static constexpr int kMapsPerWarp = CTAS == 2 && PACK != kMaskPagedPrefill ? 2 : 1;
+  static constexpr int kSoftmaxWarps = 8 / kMapsPerWarp;
+  static constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
   static constexpr int kPanels = D / 64;
   static constexpr int kQPanelBytes = BM * 128;      // 64 columns of a Q tile
   static constexpr int kQBytes = BM * D * 2;
@@ -102,8 +106,9 @@ struct DiffCfg {
   static constexpr int kHalf = D / 2;                // columns of O a softmax warp writes
   static constexpr int kRegsLaunch = 65536 / kCtas / kThreads / 8 * 8;
   static constexpr uint32_t kRegsControl = CTAS == 1 ? 88 : 48;
-  static constexpr uint32_t kRegsSoftmax = CTAS == 1 ? 208 : 96;
-  static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= 384 * kRegsLaunch, "register split");
+  static constexpr uint32_t kRegsSoftmax = CTAS == 2 && kMapsPerWarp == 1 ? 96 : 208;
+  static_assert(128 * kRegsControl + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * kRegsLaunch,
+                "register split");
   static_assert((kSmemBytes + 1024) * kCtas <= 233472, "shared memory");
   static_assert(kOCol + 2 * D <= kTmemCols, "TMEM columns");
   static constexpr uint32_t kIdescS = idesc_bf16(BM, BN, false, false);
@@ -268,7 +273,7 @@ __device__ __forceinline__ Unit diff_unit(int u, const DiffParams& dp, UnitCurso
 }
 
 template <int D, int PACK, int CTAS>
-__global__ void __launch_bounds__(384, CTAS)
+__global__ void __launch_bounds__((DiffCfg<D, PACK, CTAS>::kThreads), CTAS)
     diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_q8,
                         const __grid_constant__ CUtensorMap tm_k,
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(384, CTAS)
                         const __grid_constant__ CUtensorMap tm_o, const DiffParams dp) {
   using C = DiffCfg<D, PACK, CTAS>;
   constexpr int BM = C::BM, BN = C::BN, STAGES = C::kStages, QB = C::kQBufs;
-  constexpr int SB = C::kSBufs;
+  constexpr int SB = C::kSBufs, MW = C::kMapsPerWarp;
   constexpr bool kPaged = PACK == kMaskPagedPrefill;
   constexpr unsigned kFull = 0xffffffffu;
   const PrefillParams& p = dp.base;
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(384, CTAS)
       ctl->abort_flag = 0;
       for (int q = 0; q < QB; ++q) {
         mbar_init(&ctl->q_full[q], 1);
-        mbar_init(&ctl->q_empty[q], 8);  // one arrival per softmax warp
+        mbar_init(&ctl->q_empty[q], C::kSoftmaxWarps);  // one arrival per softmax warp
       }
       for (int s = 0; s < STAGES; ++s) {
         mbar_init(&ctl->kv_full[s], kPaged ? 2 : 1);  // an arrival for K, one for V
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(384, CTAS)
       }
       mbar_init(&ctl->o_done, 2);
       for (int q = 0; q < 4; ++q) mbar_init(&ctl->both[q], 2);
-      const int readers = 10 + (kPaged && p.page_shift < 6 ? 1 : 0);
+      const int readers = 2 + C::kSoftmaxWarps + (kPaged && p.page_shift < 6 ? 1 : 0);
       for (int s = 0; s < 2; ++s) {
         mbar_init(&ctl->task_full[s], 1);
         mbar_init(&ctl->task_empty[s], readers);  // the issuers, softmax warps and V's producer
@@ -561,13 +566,15 @@ __global__ void __launch_bounds__(384, CTAS)
   } else {
     regs_increase<C::kRegsSoftmax>();
     // ---------------------------------------------------------------- softmax warpgroups
-    const int m = (warp - 4) >> 2;          // map
+    // A warp takes one map, or both in turn, so that one map's products run under the other's
+    // exponentials.
+    int m = MW == 2 ? 0 : (warp - 4) >> 2;  // map
     const int quarter = warp & 3;           // TMEM lanes [32*quarter, 32*quarter + 32)
     const int r = quarter * 32 + lane;      // row inside the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_bar = smem_u32(ctl->s_ready[m]);
+    const uint32_t s_bar0 = smem_u32(ctl->s_ready);
     const float c = p.scale_log2;
-    int sc = 0;          // S tiles consumed
+    int sc = 0;          // S tiles of a map consumed
     int un_done = 0;     // units with work finished
     int e = 0;           // stage of the unit's first key tile
     int pending_q = -1;  // Q buffer whose O store may still be reading it
@@ -602,11 +609,13 @@ __global__ void __launch_bounds__(384, CTAS)
       const int some_lo = __shfl_sync(kFull, see_lo, 0) - (BN - 1);
       const int some_hi = __shfl_sync(kFull, see_hi, last);
       const int j_full = full_hi < 0 ? rng.lo : imin(rng.hi, rng.lo + full_hi / BN + 1);
-      const float lam = m ? __ldg(dp.lam + bh % p.Hq) : 1.f;
-      float m_run = -INFINITY;  // running max in log2 units (may trail the true max by < 8)
-      float l_run = 0.f;
+      const float lam = MW == 2 || m ? __ldg(dp.lam + bh % p.Hq) : 1.f;
+      // Reference max in log2 units and sum of the map in hand, and of the other one.
+      float m_run = -INFINITY, m_other = -INFINITY;
+      float l_run = 0.f, l_other = 0.f;
       constexpr int kParts = BN / 32;
-      constexpr int kHeld = SB == 1 ? 1 : kParts;  // parts of a row's scores held in registers
+      // Parts of a row's scores held in registers: all, but one where those are few.
+      constexpr int kHeld = C::kRegsSoftmax < 128 ? 1 : kParts;
       const float2 cc2 = make_float2(c, c);
       int j = rng.lo;
       // P of tile j is in TMEM: on to the next tile.
@@ -615,11 +624,18 @@ __global__ void __launch_bounds__(384, CTAS)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_ready[m][sc % SB]);
-        ++sc;
-        ++j;
-        release_pending();
+        if (MW == 1 || m == 1) {
+          ++sc;
+          ++j;
+          release_pending();
+        }
+        if constexpr (MW == 2) {
+          const float mo = m_other, lo = l_other;
+          m_other = m_run, l_other = l_run, m_run = mo, l_run = lo;
+          m ^= 1;
+        }
       };
-      bool fresh = true;  // some row has no key yet
+      bool fresh = true;  // some row has no key yet (of either map)
       for (bool find = true; j < rng.hi; find = fresh) {
         // Tiles that every row sees. Weights 2^(c s - m_run) against the reference max that the row
         // has so far: weights are floating-point, so that a score far above it costs no accuracy,
@@ -629,7 +645,7 @@ __global__ void __launch_bounds__(384, CTAS)
         if (!find && (j - rng.lo) * BN >= full_lo) {
 #pragma unroll 1
           while (j < j_full) {
-            ok = wait_at(s_bar + 8 * (sc % SB), (sc / SB) & 1, wc);
+            ok = wait_at(s_bar0 + 16 * m + 8 * (sc % SB), (sc / SB) & 1, wc);
             if (!ok) break;
             tc_fence_after();
             const uint32_t s_col = lane_base + (SB * m + sc % SB) * BN;
@@ -661,7 +677,7 @@ __global__ void __launch_bounds__(384, CTAS)
           }
           if (!ok || j >= rng.hi) break;
         }
-        ok = wait_at(s_bar + 8 * (sc % SB), (sc / SB) & 1, wc);
+        ok = wait_at(s_bar0 + 16 * m + 8 * (sc % SB), (sc / SB) & 1, wc);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_col = lane_base + (SB * m + sc % SB) * BN;
@@ -679,8 +695,8 @@ __global__ void __launch_bounds__(384, CTAS)
             if (edge) {
               const uint32_t bits = vis_bits32(see_lo - at - 32 * y, see_hi - at - 32 * y);
 #pragma unroll
-              for (int t = 0; t < 32; ++t)
-                if (!(bits & (1u << t))) s[y % kHeld][t] = 0xff800000u;  // -inf
+              for (int x = 0; x < 32; ++x)
+                if (!(bits & (1u << x))) s[y % kHeld][x] = 0xff800000u;  // -inf
             }
           };
           auto load = [&](int y) {
@@ -700,11 +716,11 @@ __global__ void __launch_bounds__(384, CTAS)
 #pragma unroll
               for (int y = 0; y < kParts; ++y) {
                 if constexpr (kHeld == 1) load(y);
+                const uint32_t(&sy)[32] = s[y % kHeld];
                 mx[y] = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < 32; t += 2)
-                  mx[y] = fmax3(mx[y], __uint_as_float(s[y % kHeld][t]),
-                                __uint_as_float(s[y % kHeld][t + 1]));
+                  mx[y] = fmax3(mx[y], __uint_as_float(sy[t]), __uint_as_float(sy[t + 1]));
               }
               const float top = fmax3(mx[0], mx[1], mx[kParts - 1]) * c;
               // Move the reference only when it grows by more than 8 (a factor of 256).
@@ -749,7 +765,7 @@ __global__ void __launch_bounds__(384, CTAS)
             if (!find) break;
           }
           if (!ok) break;
-          fresh = fresh && __any_sync(kFull, m_run == -INFINITY);
+          fresh = fresh && __any_sync(kFull, m_run == -INFINITY || (MW == 2 && m_other == -INFINITY));
           l_run += sa.x + sa.y;
 #pragma unroll
           for (int y = 0; y < kParts; ++y) tmem_st_x16(s_col + 16 * y, pk[y]);
@@ -760,7 +776,7 @@ __global__ void __launch_bounds__(384, CTAS)
           // (the first P V may be either's).
           const int left = k_end - k_org - j * BN;  // tokens of the context from the tile's first
           const int clear = imin(BN, (left + p.page_size - 1) & -p.page_size);
-          if (left < clear) {
+          if (left < clear && (MW == 1 || m == 0)) {
             const int ev = e + j - rng.lo;  // V came with the K that S was made of
             ok = __all_sync(kFull,
                             mbar_wait(&ctl->kv_full[ev % STAGES], (ev / STAGES) & 1, wc));
@@ -777,29 +793,40 @@ __global__ void __launch_bounds__(384, CTAS)
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      // This row's factor of O_m, for both warps of the row.
-      ctl->coef[m][r] = l_run != 0.f ? lam * __frcp_rn(l_run) : 0.f;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->both[quarter]);
       const bool live = row < k_end;
-      if (live)
-        p.lse[(static_cast<size_t>(bh) * 2 + m) * p.N + row] =
-            l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
-      ok = wait_at(smem_u32(&ctl->both[quarter]), 0, wc) &&
+      float f0, f1;  // of O_0 and O_1
+      if constexpr (MW == 2) {
+        f0 = l_run != 0.f ? __frcp_rn(l_run) : 0.f;
+        f1 = l_other != 0.f ? -lam * __frcp_rn(l_other) : 0.f;
+      } else {
+        ctl->coef[m][r] = l_run != 0.f ? lam * __frcp_rn(l_run) : 0.f;  // for both warps of the row
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->both[quarter]);
+      }
+      if (live) {
+        float* to = p.lse + (static_cast<size_t>(bh) * 2 + m) * p.N + row;
+        *to = l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+        if (MW == 2)
+          to[p.N] =
+              l_other != 0.f ? (m_other + log2f(l_other)) * 0.69314718055994530942f : -INFINITY;
+      }
+      ok = (MW == 2 || wait_at(smem_u32(&ctl->both[quarter]), 0, wc)) &&
            wait_at(smem_u32(&ctl->o_done), un_done & 1, wc);
       if (!ok) break;
       tc_fence_after();
-      const float f0 = ctl->coef[0][r], f1 = -ctl->coef[1][r];
-      constexpr int kX = C::kHalf / 32;
+      if constexpr (MW == 1) f0 = ctl->coef[0][r], f1 = -ctl->coef[1][r];
+      // This warp's columns of the row: one half of the head's or both.
+      constexpr int kCols = C::kHalf * MW, kX = kCols / 32;
+      const int half0 = MW == 2 ? 0 : m;
+      const uint32_t o0 = lane_base + C::kOCol + half0 * C::kHalf;
+      float x[kCols];
+      float2 ss2 = make_float2(0.f, 0.f), ss3 = ss2;
       uint32_t xa[kX][32], xb[kX][32];
-      const uint32_t o0 = lane_base + C::kOCol + m * C::kHalf;
 #pragma unroll
       for (int y = 0; y < kX; ++y) {
         tmem_ld_x32(o0 + y * 32, xa[y]);
         tmem_ld_x32(o0 + D + y * 32, xb[y]);
       }
-      float x[C::kHalf];
-      float2 ss2 = make_float2(0.f, 0.f), ss3 = ss2;
 #pragma unroll
       for (int y = 0; y < kX; ++y) {
         tmem_wait_ld_x32(xa[y]);
@@ -822,56 +849,67 @@ __global__ void __launch_bounds__(384, CTAS)
             ss2 = __ffma2_rn(d2, d2, ss2);
         }
       ss2 = __fadd2_rn(ss2, ss3);
-      // The row's place in the staging area: this Q buffer, whose last MMA is done. Columns of
-      // warpgroup m: rows of D bytes, 16-byte chunks swizzled as TMA expects them.
+      // The row's place in the staging area: this Q buffer, whose last MMA is done. Columns of half
+      // a head: rows of D bytes, 16-byte chunks swizzled as TMA expects them.
       uint8_t* stage = q_s + (un_done % QB) * C::kQBytes;
       auto chunk_at = [&](int half, int ch) {
         const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
         return stage + half * (128 * D) + r * D + ((ch ^ sw) << 4);
       };
-      // Half a row's squares, put where the partner's first chunk will be, which it writes only
-      // after it has read them.
-      *reinterpret_cast<float*>(chunk_at(1 - m, 0)) = ss2.x + ss2.y;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->both[quarter]);
-      ok = wait_at(smem_u32(&ctl->both[quarter]), 1, wc);
-      if (!ok) break;
-      // Two halves in a fixed order, so that both warps scale by the same number.
-      const float mine = ss2.x + ss2.y, other = *reinterpret_cast<const float*>(chunk_at(m, 0));
-      const float ss = m ? other + mine : mine + other;
+      float ss = ss2.x + ss2.y;
+      if constexpr (MW == 1) {
+        // Half a row's squares, put where the partner's first chunk will be, which it writes only
+        // after it has read them.
+        *reinterpret_cast<float*>(chunk_at(1 - m, 0)) = ss;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->both[quarter]);
+        ok = wait_at(smem_u32(&ctl->both[quarter]), 1, wc);
+        if (!ok) break;
+        // Two halves in a fixed order, so that both warps scale by the same number.
+        const float other = *reinterpret_cast<const float*>(chunk_at(m, 0));
+        ss = m ? other + ss : ss + other;
+      } else {
+        tc_fence_before();
+        __syncwarp();
+      }
       // A row without keys stays zero whatever eps is.
       const float rs = dp.weight && l_run != 0.f ? rsqrtf(ss * (1.f / D) + dp.eps) : 1.f;
       const int warp_row0 = un.q_row0 + quarter * 32;
       const bool staged = rl == 7 && (PACK == kMaskNone || warp_row0 + 31 < k_end);
       uint8_t* orow = static_cast<uint8_t*>(p.o) +
-                      (static_cast<size_t>(bh) * p.N + static_cast<size_t>(row)) * D * 2 + m * D;
+                      (static_cast<size_t>(bh) * p.N + static_cast<size_t>(row)) * D * 2;
       const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-      for (int ch = 0; ch < C::kHalf / 8; ++ch) {
-        uint32_t w[4];
+      for (int hh = 0; hh < MW; ++hh)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int at = ch * 8 + 4 * t;
-          const float4 wt = *reinterpret_cast<const float4*>(&ctl->weight[m * C::kHalf + at]);
-          const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(x[at], x[at + 1]), rs2),
-                                       make_float2(wt.x, wt.y));
-          const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(x[at + 2], x[at + 3]), rs2),
-                                       make_float2(wt.z, wt.w));
-          w[2 * t] = pack_bf16x2(y0.x, y0.y);
-          w[2 * t + 1] = pack_bf16x2(y1.x, y1.y);
+        for (int ch = 0; ch < C::kHalf / 8; ++ch) {
+          uint32_t w[4];
+          const int half = half0 + hh;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int at = ch * 8 + 4 * t;
+            const float* xt = x + hh * C::kHalf + at;
+            const float4 wt = *reinterpret_cast<const float4*>(&ctl->weight[half * C::kHalf + at]);
+            const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(xt[0], xt[1]), rs2),
+                                         make_float2(wt.x, wt.y));
+            const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(xt[2], xt[3]), rs2),
+                                         make_float2(wt.z, wt.w));
+            w[2 * t] = pack_bf16x2(y0.x, y0.y);
+            w[2 * t + 1] = pack_bf16x2(y1.x, y1.y);
+          }
+          if (staged)
+            st_shared_v4(smem_u32(chunk_at(half, ch)), w[0], w[1], w[2], w[3]);
+          else if (live)
+            st_global_v4(orow + half * D + ch * 16, w[0], w[1], w[2], w[3]);
         }
-        if (staged)
-          st_shared_v4(smem_u32(chunk_at(m, ch)), w[0], w[1], w[2], w[3]);
-        else if (live)
-          st_global_v4(orow + ch * 16, w[0], w[1], w[2], w[3]);
-      }
       if (staged && warp_row0 < k_end) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&tm_o, stage + m * (128 * D) + quarter * 32 * D, m * C::kHalf, warp_row0,
-                       un.bh);
+          for (int half = half0; half < half0 + MW; ++half)
+            tma_store_3d(&tm_o, stage + half * (128 * D) + quarter * 32 * D, half * C::kHalf,
+                         warp_row0, un.bh);
           bulk_commit_group();
         }
       }
