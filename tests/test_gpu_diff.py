@@ -965,12 +965,12 @@ def test_shared_pages():
 @pytest.mark.parametrize("mask,window", [("none", 0), ("causal", 0), ("sliding", 200),
                                          ("sliding_bidir", 130), ("prefix", 300), ("document", 0),
                                          ("document_bidir", 0)])
-def test_more_units_than_three_an_sm(mask, window):
-    """d = 64: more than three 128-row units an SM go two CTAs an SM. A few planes of each."""
+def test_more_units_than_four_an_sm(mask, window):
+    """d = 64: more than four 128-row units an SM go two CTAs an SM. A few planes of each."""
     rng = np.random.default_rng(28)
     doc = mask.startswith("document")
     B, Hq, Hkv, n, cuts = (1, 48, 12, 1900, [0, 1, 130, 130, 1299, 1900]) if doc else (
-        3, 16, 4, 1399, [0, 1399])
+        4, 16, 4, 1399, [0, 1399])
     h = Head(rng, Hq, 64)
     (q, qv), (k, kv), (v, vv) = (draw(rng, B, x, n, 64) for x in (Hq, Hkv, Hkv))
     o, lse = run_diff(h, q, k, v, KINDS[mask], window, dev(np.array(cuts, np.int32)) if doc else None,
@@ -989,7 +989,7 @@ def test_more_units_than_three_an_sm(mask, window):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
-def test_more_chunk_units_than_three_an_sm(page):
+def test_more_chunk_units_than_four_an_sm(page):
     rng = np.random.default_rng(29 + page)
     c = Chunk(rng, [900, 33, 777, 640, 128], [400, 33, 129, 1, 128], 48, 3, 64, page)
     o, lse = c.run()

@@ -38,12 +38,13 @@ cudaError_t launch(int mask, const DiffMaps& t, const DiffParams& p, int grid,
   return launch_one<D, kMaskNone, CTAS>(t, p, grid, stream);
 }
 
-// At d = 64 two CTAs fit an SM, each with one S buffer a map. With at most three units an SM one CTA
-// with two buffers and longer key tiles ends a unit sooner. One CTA and two: 16 heads, one causal row
-// of 1024 13.9 and 17.5 us (0.8 units an SM), two of 1500 30.8 and 29.2 (2.5), three of 5003 in a
-// window of 1000 149 and 131 (12.6), two of 8192 462 and 429; 8 chunks of up to 1024 tokens over 16K,
-// 64 heads over 4, 1127 and 862.
-int ctas_of(int d, long long units) { return d == 64 && units > 3ll * sms_or_default() ? 2 : 1; }
+// At d = 64 two CTAs fit an SM, each with one S buffer a map. With at most four units an SM one CTA
+// with two buffers and longer key tiles ends a unit sooner. One CTA and two, 16 heads: one causal row
+// of 1024 14.0 and 18.3 us (0.8 units an SM), two of 1500 29.8 and 34.1 (2.5), two of 2000 44.6 and
+// 48.0 (3.4; without a mask 75.6 and 72.4), two of 3000 81.2 and 80.4 (5.1), three of 5003 in a
+// window of 1000 148 and 131 (12.6), two of 8192 469 and 429; 8 chunks of up to 1024 tokens over 16K,
+// 64 heads over 4, 1022 and 863.
+int ctas_of(int d, long long units) { return d == 64 && units > 4ll * sms_or_default() ? 2 : 1; }
 
 cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParams& p,
                    cudaStream_t stream) {
