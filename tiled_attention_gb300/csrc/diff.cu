@@ -13,7 +13,8 @@
 namespace ta {
 namespace {
 
-// Q by tiles of 128 rows and by boxes of 8, K and V, and O by boxes of 32 rows of half a head.
+// Q by tiles of 128 rows and by boxes of 8 (where heads may share a tile), K and V, and O by boxes of
+// 32 rows of half a head.
 struct DiffMaps {
   CUtensorMap q, q8, k, v, o;
 };
@@ -143,9 +144,10 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   if ((rc = status_ptr(&p.base.status))) return rc;
   DiffMaps t;
   if ((rc = encode_3d(&t.q, q, d, N, planes, 128))) return rc;
-  if ((rc = encode_3d(&t.q8, q, d, N, planes, 8))) return rc;
   if ((rc = encode_3d(&t.o, o, d, N, planes, 32, d / 2))) return rc;
   p.head_shift = head_shift(Hq / Hkv, units);
+  t.q8 = t.q;
+  if (p.head_shift && (rc = encode_3d(&t.q8, q, d, N, planes, 8))) return rc;
   if (!doc)  // units of several heads' last rows
     units -= planes - (planes >> (7 - tile_rows_log2(N - 128 * (tiles - 1), p.head_shift)));
   const int ctas = ctas_of(d, units);
@@ -212,7 +214,9 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   if ((rc = status_ptr(&p.base.status))) return rc;
   DiffMaps t;
   if ((rc = encode_3d(&t.q, q, d, total_q, Hq, 128))) return rc;
-  if ((rc = encode_3d(&t.q8, q, d, total_q, Hq, 8))) return rc;
+  p.head_shift = head_shift(Hq / Hkv, units);
+  t.q8 = t.q;
+  if (p.head_shift && (rc = encode_3d(&t.q8, q, d, total_q, Hq, 8))) return rc;
   if ((rc = encode_3d(&t.o, o, d, total_q, Hq, 32, d / 2))) return rc;
   const uint64_t planes = static_cast<uint64_t>(num_pages) * Hkv;
   const uint32_t box = page_size < 64 ? page_size : 64;  // rows of a page in one 64-key tile
@@ -232,7 +236,6 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.base.Hkv = Hkv;
   p.base.N = total_q;
   p.base.group = Hq / Hkv;
-  p.head_shift = head_shift(Hq / Hkv, units);
   p.base.num_units = static_cast<int>(units);
   p.base.scale_log2 = scale * kLog2e;
   p.base.timeout_ns = kTimeoutNs;
