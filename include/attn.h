@@ -444,6 +444,8 @@ size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d);
  *                                                                   o = out_scale * y)
  * in fp32 from the accumulators on, rounded to bf16 once; the softmax weights enter the product
  * with v in bf16 (decode: as two bf16 terms), their sums stay fp32. A row that sees no key gets o = 0.
+ * So does one whose y is all zeros, whatever eps. The norm takes y of any size (rows whose squares leave
+ * fp32 are scaled by a power of two first); values up to 2^80 keep y finite under any scores.
  * q, o      bf16 [B,Hq,N,d] (document kinds [1,Hq,N,d]); k, v bf16 [B,Hkv,N,d]; layouts, masks,
  *           window, cu_seqlens, B, Hq, Hkv and N as for attn_fwd's prefill kinds (NONE, CAUSAL,
  *           SLIDING, SLIDING_BIDIR, DOCUMENT, DOCUMENT_BIDIR, PREFIX_LM; others: ATTN_ERR_INVALID).

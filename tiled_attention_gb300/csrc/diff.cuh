@@ -56,6 +56,7 @@
 
 #include <cuda_bf16.h>
 
+#include "diff_norm.cuh"
 #include "prefill.cuh"
 #include "ptx.cuh"
 #include "sched.h"
@@ -857,24 +858,47 @@ __global__ void __launch_bounds__((DiffCfg<D, PACK, CTAS>::kThreads), CTAS)
         return stage + half * (128 * D) + r * D + ((ch ^ sw) << 4);
       };
       float ss = ss2.x + ss2.y;
-      if constexpr (MW == 1) {
-        // Half a row's squares, put where the partner's first chunk will be, which it writes only
-        // after it has read them.
-        *reinterpret_cast<float*>(chunk_at(1 - m, 0)) = ss;
+      // Half a row's squares go to the warp with the other half where its chunk `ch` will be, which it
+      // writes only after it has read them. Two halves in a fixed order, so that both warps scale by
+      // the same number.
+      auto whole_row = [&](int ch, uint32_t phase) {
+        *reinterpret_cast<float*>(chunk_at(1 - m, ch)) = ss;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->both[quarter]);
-        ok = wait_at(smem_u32(&ctl->both[quarter]), 1, wc);
-        if (!ok) break;
-        // Two halves in a fixed order, so that both warps scale by the same number.
-        const float other = *reinterpret_cast<const float*>(chunk_at(m, 0));
+        if (!wait_at(smem_u32(&ctl->both[quarter]), phase, wc)) return false;
+        const float other = *reinterpret_cast<const float*>(chunk_at(m, ch));
         ss = m ? other + ss : ss + other;
+        return true;
+      };
+      if constexpr (MW == 1) {
+        ok = whole_row(0, 1);
+        if (!ok) break;
       } else {
         tc_fence_before();
         __syncwarp();
       }
+      const float by = dp.weight ? norm_scale(ss, dp.eps) : 1.f;
+      if (__any_sync(kFull, by != 1.f)) {  // in both warps of these rows
+        const float as_it_is = ss;
+        ss = 0.f;
+#pragma unroll
+        for (int t = 0; t < kCols; ++t) {
+          x[t] *= by;
+          ss = fmaf(x[t], x[t], ss);
+        }
+        if constexpr (MW == 1) {
+          ok = whole_row(1, 0);
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->both[quarter]);  // the next unit begins at phase 0
+          ok = wait_at(smem_u32(&ctl->both[quarter]), 1, wc);
+          if (!ok) break;
+        }
+        if (by == 1.f) ss = as_it_is;
+      }
       // A row without keys stays zero whatever eps is.
-      const float rs = dp.weight && l_run != 0.f ? rsqrtf(ss * (1.f / D) + dp.eps) : 1.f;
+      const float rs = dp.weight && l_run != 0.f ? norm_factor<D>(ss, by, dp.eps) : 1.f;
       const int warp_row0 = un.q_row0 + quarter * 32;
       const bool staged = rl == 7 && (PACK == kMaskNone || warp_row0 + 31 < k_end);
       uint8_t* orow = static_cast<uint8_t*>(p.o) +

@@ -30,6 +30,7 @@
 #pragma once
 
 #include "decode.cuh"
+#include "diff_norm.cuh"
 #include "ptx.cuh"
 #include "sched.h"
 #include "share.cuh"
@@ -133,14 +134,23 @@ __device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t ro
                                             float2 ml1, unsigned lanes) {
   const bool some = ml0.y != 0.f;  // an empty context has its rows zero whatever eps is
   const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? lam / ml1.y : 0.f;
-  const float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
-                               a0.w * f0 - a1.w * f1);
+  float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
+                         a0.w * f0 - a1.w * f1);
   float rs = p.out_scale;
   if (p.weight) {
-    float ss = (y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w);
+    auto squares = [&] {  // the same bits in all of the row's lanes
+      float ss = (y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w);
 #pragma unroll
-    for (int off = D / 8; off; off >>= 1) ss += __shfl_xor_sync(lanes, ss, off);
-    if (some) rs *= rsqrtf(ss * (1.f / D) + p.eps);
+      for (int off = D / 8; off; off >>= 1) ss += __shfl_xor_sync(lanes, ss, off);
+      return ss;
+    };
+    float ss = squares();
+    const float by = norm_scale(ss, p.eps);
+    if (by != 1.f) {
+      y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+      ss = squares();
+    }
+    if (some) rs *= norm_factor<D>(ss, by, p.eps);
   }
   *reinterpret_cast<uint2*>(p.o + row * D + 4 * quad) =
       make_uint2(pack_bf16x2(y.x * rs * w.x, y.y * rs * w.y),
