@@ -1,5 +1,5 @@
-"""Differential attention at the edges of its numbers: rows whose squares leave fp32. Against plain
-64-bit numpy, through the C ABI."""
+"""Differential attention at the edges of its numbers: rows whose squares leave fp32, scores of -inf.
+Against plain 64-bit numpy, through the C ABI."""
 import numpy as np
 import pytest
 import torch
@@ -89,3 +89,91 @@ def test_rows_of_zero_are_zero(d):
     assert (c.run()[0] == 0).all()
     w.run()
     assert status() == 0 and (w.o == 0).all()
+
+
+# ------------------------------------------------------------------ scores of -inf
+OUT = [(1, 4)]  # keys (first, every) out of a map's sight
+
+
+def maps_apart(h, q, k, v, here, step):
+    """(o, its bound, LSE [Hq, 2, n], its bound) where map m sees the keys here[m] [n, m] alone: y from
+    oracle.diff.Rows of each map by itself, the norm and its bound as there."""
+    half = q.shape[-1] // 2
+    one = []
+    for m in (0, 1):
+        both = [np.concatenate([x[..., m * half:(m + 1) * half]] * 2, -1) for x in (q, k)]
+        one.append(diff.Rows(*both, v, here[m], np.zeros_like(h.lam), h.scale, None, 0, 1.0, step))
+    lam = h.lam.astype(np.float64)[:, None, None]
+    y, err = one[0].o - lam * one[1].o, one[0].o_tol + np.abs(lam) * one[1].o_tol
+    if h.weight is not None:
+        rms, off = (np.sqrt((x * x).mean(-1, keepdims=True) + e) for x, e in ((y, h.eps), (err, 0.0)))
+        low = np.where(rms > off, rms - off, 0.0)
+        w = h.weight.astype(np.float64)
+        with np.errstate(divide="ignore"):
+            err = (err + np.abs(y) * off / rms) / low * np.abs(w)
+        y = y / rms * w
+    o = h.out_scale * y
+    return (o, abs(h.out_scale) * err + 2.0 ** -8 * np.abs(o) + 1e-37,
+            np.stack([x.lse[:, 0] for x in one], 1), np.stack([x.lse_tol[:, 0] for x in one], 1))
+
+
+def check_apart(h, o, lse, q, k, v, here, step=2.0 ** -8):
+    want, tol, want_lse, lse_tol = maps_apart(h, q, k, v, here, step)
+    assert np.all(np.abs(o - want) <= tol), float(np.max(np.abs(o - want) - tol))
+    dead = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(lse), dead)
+    assert np.all(np.abs(np.where(dead, 0, lse) - np.where(dead, 0, want_lse)) <= lse_tol)
+
+
+def drown(q, qv, k, m, keys):
+    """Scores of map m with `keys` (an index of k's rows) are -inf: a key channel of -inf against a
+    query channel above zero."""
+    at = m * q.shape[-1] // 2
+    q[..., at], qv[..., at] = 1.0, 1.0
+    k[keys + (at,)] = float("-inf")
+
+
+def seen(here, m, first, every):
+    """What each map sees where keys first, first + every, ... are out of map m's sight."""
+    left = here & (np.arange(here.shape[1]) % every != first)
+    return (left, here) if m == 0 else (here, left)
+
+
+@pytest.mark.parametrize("m", [0, 1])
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,n,d", FORMS)
+@pytest.mark.parametrize("first,every", OUT)
+def test_scores_of_minus_infinity(B, Hq, Hkv, n, d, normed, m, first, every):
+    rng = np.random.default_rng(n + d + m)
+    h = Head(rng, Hq, d, normed)
+    (q, qv), (k, kv), (v, vv) = (draw(rng, B, x, n, d) for x in (Hq, Hkv, Hkv))
+    drown(q, qv, k, m, (slice(None), slice(None), slice(first, None, every)))
+    o, lse = run_diff(h, q, k, v, attn.ATTN_MASK_CAUSAL)
+    assert status() == 0
+    here = seen(diff.visible("causal", 0, n), m, first, every)
+    for b in (0, B - 1):
+        check_apart(h, f64(o[b]), f64(lse[b]), qv[b], kv[b], vv[b], here)
+
+
+@pytest.mark.parametrize("m", [0, 1])
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("d,Hq", [(64, 6), (128, 6), (64, 24), (128, 24)])
+@pytest.mark.parametrize("first,every", OUT)
+def test_scores_of_minus_infinity_over_pages(d, Hq, normed, m, first, every):
+    rng = np.random.default_rng(d + Hq + m)
+    c = Chunk(rng, [300, 40], [150, 1], Hq, 2, d, 16, normed)
+    w = Decode(rng, [1, 70, 5000], Hq, 2, d, 64, normed)
+    for x in (c, w):  # (pages hold multiples of `every` slots)
+        drown(x.q, x.qv, x.k, m, (slice(None), slice(None), slice(first, None, every)))
+    o, lse = c.run()
+    w.run()
+    assert status() == 0
+    o, lse, at = f64(o[0]), f64(lse[0]), 0
+    for b, (L, n) in enumerate(zip(c.lk, c.lq)):
+        here = np.arange(L)[None] <= np.arange(L - n, L)[:, None]
+        cut = slice(at, at + n)
+        at += n
+        check_apart(c.h, o[:, cut], lse[:, :, cut], c.qv[0][:, cut], *c.ctx[b], seen(here, m, first, every))
+    for b, L in enumerate(w.lk):
+        check_apart(w.h, f64(w.o[b]), f64(w.lse[b])[:, :, None], w.qv[b], *w.ctx[b],
+                    seen(np.ones((1, L), bool), m, first, every), 2.0 ** -16)

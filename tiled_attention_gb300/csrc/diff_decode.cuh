@@ -4,8 +4,8 @@
 // K and V are read once for both maps, and both maps' products cost as many MMAs as one map of
 // ordinary attention with up to 16 heads a kv head: rows r < 8 of an m16n8k16 tile are head r's
 // first map, rows r + 8 its second. K holds the maps' channels side by side, so the queries enter
-// block-diagonally, (q_1, 0) in rows r and (0, q_2) in rows r + 8: one chain of k-steps over all D
-// channels leaves S_1 and S_2 in the two halves of one accumulator, and P of both maps is one A
+// block-diagonally, (q_1, 0) in rows r and (0, q_2) in rows r + 8: the k-steps over the first D / 2
+// channels leave S_1 in rows r, those over the others S_2 in rows r + 8, and P of both maps is one A
 // fragment for V. Decode reads 512 bytes a token and kv head at D = 128 and is bound by HBM.
 //
 // Work: contexts are cut into 64-token blocks and shared out evenly over two CTAs an SM
@@ -28,6 +28,8 @@
 // shares): what is left is that some SMs get their bytes later than others, 135 to 160 us in the
 // batch.
 #pragma once
+
+#include <type_traits>
 
 #include "decode.cuh"
 #include "diff_norm.cuh"
@@ -294,42 +296,58 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
       if (ok) {
         const uint32_t kp = smem_u32(ring + st * C::kStageBytes);
         const uint32_t vp = kp + C::kHalfBytes;
-        float s[kTiles][2][4];
-#pragma unroll
-        for (int tt = 0; tt < kTiles; ++tt)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) s[tt][x >> 2][x & 3] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < kQSteps; ++kk) {
-          const bool lo = kk < kQSteps / 2;  // NT = 1: map 0's
-          const uint32_t a[4] = {NT == 2 || lo ? qa[kk][0][0] : 0u,
-                                 NT == 2 ? qa[kk][NT - 1][0] : lo ? 0u : qa[kk][0][0],
-                                 NT == 2 || lo ? qa[kk][0][1] : 0u,
-                                 NT == 2 ? qa[kk][NT - 1][1] : lo ? 0u : qa[kk][0][1]};
-#pragma unroll
-          for (int tt = 0; tt < kTiles; ++tt) {
-            uint32_t kb[4];
-            ldmatrix_x4(kb, kp + page_chunk(k_token + 16 * tt, kk * 16 + k_half));
-            mma_bf16_16816(s[tt][0], a, kb[0], kb[1]);
-            mma_bf16_16816(s[tt][1], a, kb[2], kb[3]);
-          }
-        }
         const int left = seg.L - (seg.blk0 + i) * C::kTok - tok_w;  // tokens from this slice on
+        float s[kTiles][2][4];
+        // Scores; apart (NT = 1): each map's rows from its own k-steps alone.
+        auto scores = [&](auto apart) {
+          constexpr bool kApart = decltype(apart)::value;
+          float rows[2][2];
+#pragma unroll
+          for (int tt = 0; tt < kTiles; ++tt)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) s[tt][x >> 2][x & 3] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < kQSteps; ++kk) {
+            const bool lo = kk < kQSteps / 2;  // NT = 1: map 0's
+            const uint32_t a[4] = {NT == 2 || lo ? qa[kk][0][0] : 0u,
+                                   NT == 2 ? qa[kk][NT - 1][0] : lo ? 0u : qa[kk][0][0],
+                                   NT == 2 || lo ? qa[kk][0][1] : 0u,
+                                   NT == 2 ? qa[kk][NT - 1][1] : lo ? 0u : qa[kk][0][1]};
+            if (kApart && kk == kQSteps / 2)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                rows[y][0] = s[0][y][0], rows[y][1] = s[0][y][1];
+                s[0][y][2] = s[0][y][3] = 0.f;
+              }
+#pragma unroll
+            for (int tt = 0; tt < kTiles; ++tt) {
+              uint32_t kb[4];
+              ldmatrix_x4(kb, kp + page_chunk(k_token + 16 * tt, kk * 16 + k_half));
+              mma_bf16_16816(s[tt][0], a, kb[0], kb[1]);
+              mma_bf16_16816(s[tt][1], a, kb[2], kb[3]);
+            }
+          }
+          if constexpr (kApart)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s[0][y][0] = rows[y][0], s[0][y][1] = rows[y][1];
+          // Slots past the context may hold anything.
+          if (left < 16 * kTiles)
+#pragma unroll
+            for (int tt = 0; tt < kTiles; ++tt)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (16 * tt + 8 * (x >> 2) + 2 * q + (x & 1) >= left)
+                  s[tt][x >> 2][x & 3] = -INFINITY;
+        };
+        scores(std::false_type{});
         if (left < 16 * kTiles) {
-          // Slots past the context may hold anything: their scores are dropped below, and their
-          // values cleared, since a NaN would survive a weight of zero.
+          // Values past the context are cleared: a NaN would survive a weight of zero.
           for (int x = lane; x < 16 * kTiles * (D / 8); x += 32) {
             const int tok = x / (D / 8);
             if (tok >= left)
               st_shared_v4(vp + page_chunk(tok_w + tok, (x % (D / 8)) * 8), 0, 0, 0, 0);
           }
           __syncwarp();
-#pragma unroll
-          for (int tt = 0; tt < kTiles; ++tt)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (16 * tt + 8 * (x >> 2) + 2 * q + (x & 1) >= left)
-                s[tt][x >> 2][x & 3] = -INFINITY;
         }
         // Weights 2^(c s - mx) against the reference max of the row so far; one of a sum above 2^24
         // (a score far above it), and a row's first, has the max found. Element x of n-tile y: row
@@ -346,6 +364,14 @@ __global__ void __launch_bounds__(160, kDiffDecodeCtas)
                       (w[tt][1][2 * h] + w[tt][1][2 * h + 1]);
         }
         if (__any_sync(0xffffffffu, !(sum[0] + sum[1] <= kDiffDecodeRaise))) {
+          if constexpr (NT == 1) {
+            // An infinite key channel of one map is NaN times the other one's zeros. (Both maps apart
+            // from the start spill at D = 128: 512 short contexts 102.5 to 107 us.)
+            bool nan = false;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) nan |= isnan(s[0][x >> 2][x & 3]);
+            if (__any_sync(0xffffffffu, nan)) scores(std::true_type{});
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float top = -INFINITY;
