@@ -92,7 +92,7 @@ def test_rows_of_zero_are_zero(d):
 
 
 # ------------------------------------------------------------------ scores of -inf
-OUT = [(1, 4)]  # keys (first, every) out of a map's sight
+OUT = [(1, 4), (0, 1)]  # keys (first, every) out of a map's sight: some, all
 
 
 def maps_apart(h, q, k, v, here, step):

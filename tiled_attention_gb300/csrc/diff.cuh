@@ -897,8 +897,7 @@ __global__ void __launch_bounds__((DiffCfg<D, PACK, CTAS>::kThreads), CTAS)
         }
         if (by == 1.f) ss = as_it_is;
       }
-      // A row without keys stays zero whatever eps is.
-      const float rs = dp.weight && l_run != 0.f ? norm_factor<D>(ss, by, dp.eps) : 1.f;
+      const float rs = dp.weight ? norm_factor<D>(ss, by, dp.eps) : 1.f;
       const int warp_row0 = un.q_row0 + quarter * 32;
       const bool staged = rl == 7 && (PACK == kMaskNone || warp_row0 + 31 < k_end);
       uint8_t* orow = static_cast<uint8_t*>(p.o) +

@@ -134,8 +134,8 @@ template <int D>
 __device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t row, float lam,
                                             float4 w, int quad, float4 a0, float4 a1, float2 ml0,
                                             float2 ml1, unsigned lanes) {
-  const bool some = ml0.y != 0.f;  // an empty context has its rows zero whatever eps is
-  const float f0 = some ? 1.f / ml0.y : 0.f, f1 = some ? lam / ml1.y : 0.f;
+  // A map without a score above -inf (an empty context has none in either) adds nothing.
+  const float f0 = ml0.y != 0.f ? 1.f / ml0.y : 0.f, f1 = ml1.y != 0.f ? lam / ml1.y : 0.f;
   float4 y = make_float4(a0.x * f0 - a1.x * f1, a0.y * f0 - a1.y * f1, a0.z * f0 - a1.z * f1,
                          a0.w * f0 - a1.w * f1);
   float rs = p.out_scale;
@@ -152,16 +152,15 @@ __device__ __forceinline__ void diff_finish(const DiffDecodeParams& p, size_t ro
       y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
       ss = squares();
     }
-    if (some) rs *= norm_factor<D>(ss, by, p.eps);
+    rs *= norm_factor<D>(ss, by, p.eps);
   }
   *reinterpret_cast<uint2*>(p.o + row * D + 4 * quad) =
       make_uint2(pack_bf16x2(y.x * rs * w.x, y.y * rs * w.y),
                  pack_bf16x2(y.z * rs * w.z, y.w * rs * w.w));
-  if (quad == 0)
-    *reinterpret_cast<float2*>(p.lse + 2 * row) =
-        some ? make_float2((ml0.x + log2f(ml0.y)) * 0.69314718055994530942f,
-                           (ml1.x + log2f(ml1.y)) * 0.69314718055994530942f)
-             : make_float2(-INFINITY, -INFINITY);
+  auto lse = [](float2 ml) {
+    return ml.y != 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994530942f : -INFINITY;
+  };
+  if (quad == 0) *reinterpret_cast<float2*>(p.lse + 2 * row) = make_float2(lse(ml0), lse(ml1));
 }
 // Four norm weights (ones without a norm).
 __device__ __forceinline__ float4 diff_weight(const DiffDecodeParams& p, int quad) {
