@@ -155,6 +155,12 @@ def test_pair_axis_has_an_axis_for_every_pair():
             assert e.value.code == INVALID and "pair_axis" in str(e.value)
 
 
+@pytest.mark.parametrize("pairs", [[0] * 31 + [1], bytes([3] * 32), [0, 1, 2, 0] * 8])
+def test_pair_axis_is_looked_at_with_one_axis_too(pairs):
+    for call in (_norm_rope, _append):
+        assert call(axes=1, pair_axis=pairs) == INVALID and "axis" in attn.last_error()
+
+
 def _apart(names):
     return {n: _Ptr(i << 32) for i, n in enumerate(names, 1)}
 

@@ -168,7 +168,7 @@ int axes_params(AxesRowParams* p, int maps, int axes, const uint8_t* pair_axis,
   p->positions = positions;
   p->resident = 2 * (kRowThreads / 32) * sms_or_default();
   p->quads = 1;
-  for (int i = 0; axes > 1 && i < p->rot / 2; ++i) {
+  for (int i = 0; pair_axis && i < p->rot / 2; ++i) {
     if (pair_axis[i] >= axes)
       return fail(ATTN_ERR_INVALID, "pair %d goes by axis %d of %d", i, pair_axis[i], axes);
     p->axis_bits[i / 32] |= static_cast<uint64_t>(pair_axis[i]) << (2 * (i % 32));
