@@ -926,15 +926,15 @@ __global__ void __launch_bounds__((DiffCfg<D, PACK, CTAS>::kThreads), CTAS)
           else if (live)
             st_global_v4(orow + half * D + ch * 16, w[0], w[1], w[2], w[3]);
         }
-      if (staged && warp_row0 < k_end) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          for (int half = half0; half < half0 + MW; ++half)
-            tma_store_3d(&tm_o, stage + half * (128 * D) + quarter * 32 * D, half * C::kHalf,
-                         warp_row0, un.bh);
-          bulk_commit_group();
-        }
+      // What every lane read and wrote of the buffer comes before TMA's reads of it here and before its
+      // next Q there, whether this warp's rows go out by TMA or not.
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (staged && warp_row0 < k_end && lane == 0) {
+        for (int half = half0; half < half0 + MW; ++half)
+          tma_store_3d(&tm_o, stage + half * (128 * D) + quarter * 32 * D, half * C::kHalf, warp_row0,
+                       un.bh);
+        bulk_commit_group();
       }
       // The buffer goes back to the producer once the store has read it, after this warp's next
       // key tile: it takes the Q of the unit after the next.
