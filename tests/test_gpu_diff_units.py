@@ -69,3 +69,27 @@ def test_segment_rows_of_many_units(d, Hq, Hkv, mask):
                                                    diff.visible(mask, 0, b - a)))
     repeat(call, o, lse)
     assert status() == 0
+
+
+def test_units_taken_over():
+    """Thousands of units of uneven length, most of them taken over from blocks that have not begun
+    (an answer and a request a unit and CTA), those without work among them: each row is written, and
+    the same each time."""
+    rng = np.random.default_rng(5)
+    for d, Hq, Hkv in ((64, 64, 4), (128, 32, 8)):
+        lens = [int(x) for x in rng.integers(0, 90, 60)] + [700, 0, 1300]
+        n, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        h = Head(rng, Hq, d)
+        (q, qv), (k, kv), (v, vv) = (draw(rng, 1, x, n, d) for x in (Hq, Hkv, Hkv))
+        call = lambda: run_diff(h, q, k, v, attn.ATTN_MASK_DOCUMENT, 0, dev(cu),  # noqa: E731
+                                len(lens))
+        o, lse = call()
+        assert status() == 0 and not torch.isnan(o).any() and not torch.isnan(lse).any()
+        got, sums = f64(o[0]), f64(lse[0])
+        for a, b in list(zip(cu[:-1], cu[1:]))[::7]:
+            if a < b:
+                check(got[:, a:b], sums[:, :, a:b], h.rows(qv[0][:, a:b], kv[0][:, a:b],
+                                                           vv[0][:, a:b],
+                                                           diff.visible("document", 0, b - a)))
+        repeat(call, o, lse, 20)
+        assert status() == 0

@@ -467,6 +467,9 @@ __global__ void __launch_bounds__((DiffCfg<D, PACK, CTAS>::kThreads), CTAS)
           if (!ok) break;
           const int before = u;
           u = unit_answer(&ctl->answer[answered & 1]);
+          // Every lane's read of the answer comes before the request that has its place next.
+          fence_proxy_async_smem();
+          __syncwarp();
           ++answered;
           if (u < before) cur = UnitCursor{0, 0, 0, 0};  // the cursor only goes up
           if (u < 0) {  // no unit left: tell the others
