@@ -1119,11 +1119,11 @@ __global__ void __launch_bounds__(384, 1)
       // The warp's 32 rows go out through shared memory and one TMA store per 64-column
       // panel, staged in this tile's Q buffer (its last S MMA completed before o_done) in the
       // 128-byte-swizzled layout the store expects; the buffer goes back to the producer once
-      // the stores have read it. Rows past the tensor's extent are clipped by the store; a
-      // DOCUMENT warp whose rows run past its segment writes them one thread per row instead,
-      // so the next segment's rows stay untouched.
+      // the stores have read it. Rows past the tensor's extent are clipped by the store, and a warp
+      // wholly past it leaves the buffer alone; a DOCUMENT warp whose rows run past its segment
+      // writes them one thread per row instead, so the next segment's rows stay untouched.
       const int warp_row0 = q_row0 + i * BM + quarter * 32;
-      const bool staged = !is_packed(MASK) || warp_row0 + 31 < row_end;
+      const bool staged = (is_packed(MASK) ? warp_row0 + 31 : warp_row0) < row_end;
       uint8_t* stage = q_s + (qn % QB) * C::kQBytes;
       uint8_t* orow = static_cast<uint8_t*>(p.o) +
                       (static_cast<size_t>(bh) * p.N + static_cast<size_t>(row)) * D * 2;
@@ -1144,14 +1144,14 @@ __global__ void __launch_bounds__(384, 1)
           for (int v4 = 0; v4 < 4; ++v4)
             st_shared_v4(rbase + ((((cc & 1) * 4 + v4) ^ (r & 7)) << 4), w[4 * v4],
                          w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
-        } else if (live) {
+        } else if (is_packed(MASK) && live) {
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4)
             st_global_v4(orow + cc * 64 + v4 * 16, w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2],
                          w[4 * v4 + 3]);
         }
       }
-      if (staged && warp_row0 < row_end) {
+      if (staged) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
