@@ -102,3 +102,37 @@ class Rows:
                 y = np.where(some[:, None], y / rms * np.asarray(weight, np.float64), 0.0)
         self.o = out_scale * y
         self.o_tol = abs(out_scale) * err + 2.0 ** -8 * np.abs(self.o) + 1e-37
+
+
+def two_norm(q, k, v, here, lam, scale, weight, eps, out_scale, weight_step=2.0 ** -8):
+    """(o, bound [Hq, n]): Rows' o, and for every row a bound on the square of a kernel's error in
+    2-norm, to be summed over many rows of a head.
+
+    Roundings of different weights and outputs are independent of one another, so their squares add
+    where Rows adds their sizes: with r = weight_step + 2 e_m + 2^-17 (Rows' relative error of one
+    weight)
+        E |dy_c|^2 <= r^2 sum_j (w_1j^2 + lam^2 w_2j^2) v_jc^2,
+    the norm takes dy to at most |out_scale w_c dy_c| / rms (it drops the part along y), and the
+    output's rounding adds (2^-8 o_c)^2. The bound takes each rounding at its largest; a rounding to
+    bf16 is 0.43 of that in root mean square (uniform over a step, of mantissas from 1 to 2), so that
+    the sum over a block of rows is about a fifth of the bound's."""
+    rows = Rows(q, k, v, here, lam, scale, weight, eps, out_scale, weight_step)
+    hq, n, d = q.shape
+    g, half = hq // k.shape[0], d // 2
+    bound = np.zeros((hq, n))
+    some = here.any(1)
+    for h in range(hq):
+        kk, vv = k[h // g], v[h // g]
+        y, var = np.zeros((n, d)), np.zeros((n, d))
+        for m, f in ((0, 1.0), (1, -float(lam[h]))):
+            cut = slice(m * half, (m + 1) * half)
+            s = np.where(here, q[h][:, cut] @ kk[:, cut].T * scale, -np.inf)
+            big = np.where(here, np.abs(q[h][:, cut]) @ np.abs(kk[:, cut]).T * scale, 0).max(1)
+            w = np.exp(s - np.where(some, rows.lse[h, m], 0.0)[:, None])
+            r = weight_step + 2.0 ** -17 * big + 2.0 ** -17
+            y += f * (w @ vv)
+            var += (f * r[:, None]) ** 2 * ((w * w) @ (vv * vv))
+        if weight is not None:
+            var *= (np.asarray(weight, np.float64)) ** 2 / ((y * y).mean(-1, keepdims=True) + eps)
+        bound[h] = (out_scale * out_scale * var + (2.0 ** -8 * rows.o[h]) ** 2).sum(1)
+    return rows.o, bound

@@ -372,6 +372,42 @@ def test_diff_rows_pins():
     assert (none.o == 0).all() and (none.lse == -np.inf).all() and (none.o_tol < 1e-30).all()
 
 
+@pytest.mark.parametrize("n", [145, 641, 1900])
+@pytest.mark.parametrize("normed", [False, True])
+def test_two_norm_bounds_catch_small_mistakes(n, normed):
+    """Blocks of 64 rows with lam, the norm's eps or weights rounded wrong are outside the bound; the
+    same rows with P and the output rounded to bf16 inside."""
+    rng = np.random.default_rng(n)
+    d, rows = 64, 64
+    q, k, v = rng.standard_normal((1, rows, d)), rng.standard_normal((1, n, d)), rng.standard_normal(
+        (1, n, d))
+    here, lam, scale = np.ones((rows, n), bool), np.array([0.6]), 32 ** -0.5
+    w = 1 + 0.3 * rng.standard_normal(d) if normed else None
+    want, bound = diff.two_norm(q, k, v, here, lam, scale, w, 1e-5, 0.8)
+    assert bound.sum() <= 2.0 ** -14 * (want ** 2).sum()
+
+    def bf16(x):
+        return torch.from_numpy(np.ascontiguousarray(x)).to(torch.bfloat16).double().numpy()
+
+    def run(lam=0.6, drop=0, cut=lambda x: x):
+        y = 0
+        for m, f in ((0, 1.0), (1, -lam)):
+            s = q[0][:, 32 * m:32 * m + 32] @ k[0][:, 32 * m:32 * m + 32].T * scale
+            p = np.exp(s - s.max(1, keepdims=True))
+            y = y + f * ((cut(p)[:, drop:] @ v[0][drop:]) / p.sum(1, keepdims=True))
+        if normed:
+            y = y / np.sqrt((y * y).mean(1, keepdims=True) + 1e-5) * w
+        return 0.8 * y
+
+    def inside(o):
+        return ((o - want[0]) ** 2).sum() <= bound.sum()
+
+    assert inside(bf16(run(cut=bf16)))
+    for o in (run(lam=0.62), run(drop=1), run(cut=lambda x: bf16(x) * 1.02) if not normed else
+              run(lam=0.58), run(cut=lambda x: np.floor(x * 32) / 32)):
+        assert not inside(bf16(o))
+
+
 def _cases():
     path = os.path.join(ROOT, "perf", "more_operators.py")
     spec = importlib.util.spec_from_file_location("more_operators_under_test", path)
