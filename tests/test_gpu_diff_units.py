@@ -93,3 +93,37 @@ def test_units_taken_over():
                                                            diff.visible("document", 0, b - a)))
         repeat(call, o, lse, 20)
         assert status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(96, 6), (64, 4), (24, 24)])
+def test_chunks_of_one_and_two_ctas_an_sm(page, Hq, Hkv):
+    """d = 64, on both sides of four tiles an SM (960, 640 and 240), tiles shared and not; a norm whose
+    squares leave fp32 in some heads' values too."""
+    rng = np.random.default_rng(page + Hq)
+    for amp in (1.0, 2.0 ** 80):
+        c = Chunk(rng, [900, 33, 777, 640, 128], [400, 33, 129, 1, 128], Hq, Hkv, 64, page)
+        c.v[:, 0] *= amp
+        for x in c.ctx:
+            x[1, 0] *= amp
+        o, lse = c.run()
+        assert status() == 0
+        c.check(o, lse)
+        repeat(c.run, o, lse, 2)
+
+
+@pytest.mark.parametrize("lens", [[64] * 3, [32] * 4, [64] * 5, [128, 30, 1], [17] * 30])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_documents(lens, d):
+    """Documents whose tiles the GPU holds at once, and a few more."""
+    rng = np.random.default_rng(len(lens) + d)
+    n, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    h = Head(rng, 32, d)
+    (q, qv), (k, kv), (v, vv) = (draw(rng, 1, x, n, d) for x in (32, 8, 8))
+    for mask in ("document", "document_bidir"):
+        o, lse = run_diff(h, q, k, v, KINDS[mask], 0, dev(cu), len(lens))
+        assert status() == 0
+        o, lse = f64(o[0]), f64(lse[0])
+        for a, b in zip(cu[:-1], cu[1:]):
+            check(o[:, a:b], lse[:, :, a:b], h.rows(qv[0][:, a:b], kv[0][:, a:b], vv[0][:, a:b],
+                                                    diff.visible(mask, 0, b - a)))

@@ -43,8 +43,13 @@ cudaError_t launch(int mask, const DiffMaps& t, const DiffParams& p, int grid,
 // with two buffers and longer key tiles ends a unit sooner. One CTA and two, 16 heads: one causal row
 // of 1024 14.0 and 18.3 us (0.8 units an SM), two of 1500 29.8 and 34.1 (2.5), two of 2000 44.6 and
 // 48.0 (3.4; without a mask 75.6 and 72.4), two of 3000 81.2 and 80.4 (5.1), three of 5003 in a
-// window of 1000 148 and 131 (12.6), two of 8192 469 and 429; 8 chunks of up to 1024 tokens over 16K,
-// 64 heads over 4, 1022 and 863.
+// window of 1000 148 and 131 (12.6), two of 8192 469 and 429. Packed segments count the blocks that
+// are launched, those without work too (packed_blocks), chunks the tiles that may have rows
+// (packed_tiles). 16 heads, documents: 16 of 100 18.0 and 15.8 us (704 blocks, at most 448 tiles), 8 of
+// 300 21.9 and 21.0 (544, 416), 4 of 700 24.5 and 25.2 (448, 400). Chunks: 20 of 100 tokens over 2000
+// 70.6 and 78.9 (864, 560), 10 of 16 with 32 heads over 8 48.9 and 62.3 (640, 352), 5 of 40 over 3000
+// with 64 heads over 4 67 and 100 (640, 384), 12 of 100 with 32 heads 84.7 and 78.7 (1024, 672), 32 of
+// 16 with 64 heads 90 and 84 (4352, 2304), 8 of up to 1024 over 16K with 64 heads 1022 and 863.
 int ctas_of(int d, long long units) { return d == 64 && units > 4ll * sms_or_default() ? 2 : 1; }
 
 cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParams& p,
@@ -56,12 +61,24 @@ cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParam
 }
 
 // Query heads of one kv head that may share a tile, as a power of two. Units that the GPU holds at
-// once go apart (one prompt of 64 tokens, 32 heads: 6.3 us, two heads a tile 8.4).
+// once go apart (one prompt of 64 tokens, 32 heads: 6.3 us, two heads a tile 8.4). Documents count the
+// tiles that may have rows (three of 64, 32 heads over 8, d = 128: 192 blocks, at most 128 tiles, 11.0
+// us and 13.5 shared; 40 of 64, 16 over 4, d = 64: 25.1 and 22.5), chunks the blocks, since heads that
+// share a tile read a context once (three of 16 tokens over 2000, 32 over 8: 192 blocks, 46 and 32 us).
 int head_shift(int group, long long units) {
   int s = 0;
   if (units <= sms_or_default()) return 0;
   while (s < 4 && group % (2 << s) == 0) ++s;
   return s;
+}
+
+// Blocks of a packed launch, both halves of every 256-row unit that the segments may have, and the
+// 128-row tiles that may have rows, by the numbers that the host has.
+long long packed_blocks(int heads, int tokens, int segments) {
+  return 2ll * heads * (tokens / kUnitRows + static_cast<long long>(segments));
+}
+long long packed_tiles(int heads, int tokens, int segments) {
+  return static_cast<long long>(heads) * (tokens / 128 + static_cast<long long>(segments));
 }
 
 // o and lse are written while other CTAs still read the inputs.
@@ -130,7 +147,7 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   const long long planes = doc ? Hq : static_cast<long long>(B) * Hq;
   const long long planes_kv = doc ? Hkv : static_cast<long long>(B) * Hkv;
   const int tiles = tiles_for_rows(N);
-  long long units = doc ? 2ll * Hq * (N / kUnitRows + static_cast<long long>(B)) : planes * tiles;
+  long long units = doc ? packed_blocks(Hq, N, B) : planes * tiles;
   if (planes >= (1ll << 31) || units >= (1ll << 31) - 1 || N > INT32_MAX - 512)
     return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
   const size_t q_bytes = static_cast<size_t>(planes) * N * d * 2;
@@ -145,7 +162,7 @@ int attn_fwd_diff(const void* q, const void* k, const void* v, void* o, float* l
   DiffMaps t;
   if ((rc = encode_3d(&t.q, q, d, N, planes, 128))) return rc;
   if ((rc = encode_3d(&t.o, o, d, N, planes, 32, d / 2))) return rc;
-  p.head_shift = head_shift(Hq / Hkv, units);
+  p.head_shift = head_shift(Hq / Hkv, doc ? packed_tiles(Hq, N, B) : units);
   t.q8 = t.q;
   if (p.head_shift && (rc = encode_3d(&t.q8, q, d, N, planes, 8))) return rc;
   if (!doc)  // units of several heads' last rows
@@ -197,7 +214,7 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   const long long keys = static_cast<long long>(max_pages) * page_size;
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || keys >= (1ll << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "page pool or block table too large");
-  const long long units = 2ll * Hq * (total_q / kUnitRows + static_cast<long long>(B));
+  const long long units = packed_blocks(Hq, total_q, B);
   if (units >= (1ll << 31) - 1 || total_q >= (1 << 30))
     return fail(ATTN_ERR_UNSUPPORTED, "too many work units");
   const size_t q_bytes = static_cast<size_t>(Hq) * total_q * d * 2;
@@ -244,7 +261,7 @@ int attn_fwd_diff_paged_prefill(const void* q, const void* k, const void* v, voi
   p.eps = eps;
   p.out_scale = out_scale;
   p.mask = kMaskPagedPrefill;
-  const cudaError_t e = launch(d, ctas_of(d, units), kMaskPagedPrefill, t, p,
+  const cudaError_t e = launch(d, ctas_of(d, packed_tiles(Hq, total_q, B)), kMaskPagedPrefill, t, p,
                                static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "differential paged prefill launch");
   return ATTN_OK;
