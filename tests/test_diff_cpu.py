@@ -161,6 +161,22 @@ def test_pair_axis_is_looked_at_with_one_axis_too(pairs):
         assert call(axes=1, pair_axis=pairs) == INVALID and "axis" in attn.last_error()
 
 
+@pytest.mark.parametrize("pairs", [np.array([0, 1, 2, 0] * 8, np.int32), np.array([0, 1, 2, 0] * 8),
+                                   torch.tensor([0, 1, 2, 0] * 8), (0, 1, 2, 0) * 8,
+                                   bytearray([0, 1, 2, 0] * 8)])
+def test_pair_axis_of_any_whole_numbers(pairs):
+    for call in (_norm_rope, _append):
+        assert call(pair_axis=pairs, axes=2) == INVALID and "pair 2 goes by axis 2" in attn.last_error()
+
+
+@pytest.mark.parametrize("pairs", [32, [0] * 31 + [-1], [0] * 31 + [256], [0.0] * 32, "0" * 32])
+def test_pair_axis_of_anything_else_is_refused(pairs):
+    for call in (_norm_rope, _append):
+        with pytest.raises(attn.AttnError) as e:
+            call(pair_axis=pairs)
+        assert e.value.code == INVALID and "pair_axis" in str(e.value)
+
+
 def _apart(names):
     return {n: _Ptr(i << 32) for i, n in enumerate(names, 1)}
 

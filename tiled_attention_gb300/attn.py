@@ -301,7 +301,11 @@ def _pair_bytes(pair_axis, rot_dim):
     """Axis of every rotated pair as host bytes: bytes, or whole numbers below 256."""
     if pair_axis is None:
         return None
-    pair_axis = bytes(pair_axis)
+    if not isinstance(pair_axis, bytes):
+        try:
+            pair_axis = bytes(list(pair_axis))
+        except (TypeError, ValueError) as e:
+            raise AttnError(ATTN_ERR_INVALID, f"pair_axis: {e}") from None
     if len(pair_axis) != rot_dim // 2:
         raise AttnError(ATTN_ERR_INVALID,
                         f"pair_axis of {len(pair_axis)} pairs, rot_dim {rot_dim}")
