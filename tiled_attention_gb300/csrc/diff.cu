@@ -41,15 +41,17 @@ cudaError_t launch(int mask, const DiffMaps& t, const DiffParams& p, int grid,
 
 // At d = 64 two CTAs fit an SM, each with one S buffer a map. With at most four units an SM one CTA
 // with two buffers and longer key tiles ends a unit sooner. One CTA and two, 16 heads: one causal row
-// of 1024 14.0 and 18.3 us (0.8 units an SM), two of 1500 29.8 and 34.1 (2.5), two of 2000 44.6 and
-// 48.0 (3.4; without a mask 75.6 and 72.4), two of 3000 81.2 and 80.4 (5.1), three of 5003 in a
-// window of 1000 148 and 131 (12.6), two of 8192 469 and 429. Packed segments count the blocks that
-// are launched, those without work too (packed_blocks), chunks the tiles that may have rows
+// of 1024 14.1 and 18.4 us (0.8 units an SM), two of 1500 29.7 and 34.5 (2.5), two of 2000 43.5 and
+// 49.4 (3.4; without a mask 75.3 and 71.6), two of 3000 81.5 and 77.5 (5.1), three of 5003 in a
+// window of 1000 150 and 131 (12.6), two of 8192 468 and 428. Documents count the blocks that are
+// launched, those without work too (packed_blocks), chunks the tiles that may have rows
 // (packed_tiles). 16 heads, documents: 16 of 100 18.0 and 15.8 us (704 blocks, at most 448 tiles), 8 of
 // 300 21.9 and 21.0 (544, 416), 4 of 700 24.5 and 25.2 (448, 400). Chunks: 20 of 100 tokens over 2000
 // 70.6 and 78.9 (864, 560), 10 of 16 with 32 heads over 8 48.9 and 62.3 (640, 352), 5 of 40 over 3000
-// with 64 heads over 4 67 and 100 (640, 384), 12 of 100 with 32 heads 84.7 and 78.7 (1024, 672), 32 of
-// 16 with 64 heads 90 and 84 (4352, 2304), 8 of up to 1024 over 16K with 64 heads 1022 and 863.
+// with 64 heads over 4 67 and 100 (640, 384), 12 of 100 with 32 heads 84.7 and 78.7 (1024, 672), 8 of up
+// to 1024 over 16K with 64 heads 1030 and 863. Tiles are counted before heads share them: of 32 chunks
+// of up to 16 over 500-4000 with 64 heads that is 2176, where about 200 have rows and take 80 and 96,
+// but 128 of up to 4 over 100-2000 take 167 and 109 for their 16384 blocks.
 int ctas_of(int d, long long units) { return d == 64 && units > 4ll * sms_or_default() ? 2 : 1; }
 
 cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParams& p,
@@ -61,10 +63,11 @@ cudaError_t launch(int d, int ctas, int mask, const DiffMaps& t, const DiffParam
 }
 
 // Query heads of one kv head that may share a tile, as a power of two. Units that the GPU holds at
-// once go apart (one prompt of 64 tokens, 32 heads: 6.3 us, two heads a tile 8.4). Documents count the
-// tiles that may have rows (three of 64, 32 heads over 8, d = 128: 192 blocks, at most 128 tiles, 11.0
-// us and 13.5 shared; 40 of 64, 16 over 4, d = 64: 25.1 and 22.5), chunks the blocks, since heads that
-// share a tile read a context once (three of 16 tokens over 2000, 32 over 8: 192 blocks, 46 and 32 us).
+// once go apart (one prompt of 64 tokens, 32 heads over 8, d = 128: 6.7 us, shared 8.8). Documents
+// count the tiles that may have rows (three of 64, 32 heads over 8, d = 128: 192 blocks, at most 128
+// tiles, 11.0 us and 13.5 shared; 40 of 64, 16 over 4, d = 64: 25.1 and 22.5), chunks the blocks, since
+// heads that share a tile read a context once (three of 16 tokens over 2000, 32 over 8: 192 blocks, 46
+// and 32 us).
 int head_shift(int group, long long units) {
   int s = 0;
   if (units <= sms_or_default()) return 0;

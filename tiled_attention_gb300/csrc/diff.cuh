@@ -31,27 +31,34 @@
 // Key tiles are of 64 keys with two S buffers a map (one tile of 128 and one buffer: causal 2 x 8192
 // 1253 us against 1105); 96 where d = 64 leaves the columns. At d = 64 and with many units two CTAs
 // share an SM, with one S buffer a map each: the softmax is what bounds it there, and more of it is
-// in flight (a window of 1000 over 3 x 5003 149 to 130 us, chunks of 64 heads over 16K contexts 1127
-// to 862). Over pages eight softmax warps a CTA hide one another's waits, with 32 columns of scores
-// in registers at a time (all 64 spilled: 183 us of the window). Else four warps, which take both
-// maps in turn (window 141 to 130, 200 prompts of 17 tokens 55 to 48; over pages 862 to 897).
+// in flight (a window of 1000 over 3 x 5003 150 us with one CTA and 131 with two, chunks of 64 heads
+// over 16K contexts 1030 and 863). Over pages eight softmax warps a CTA hide one another's waits, with
+// 32 columns of scores in registers at a time (all 64 spilled: the window 183 us with eight warps,
+// which take 141 without spills). Else four warps, which take both maps in turn (window 131, 200
+// prompts of 17 tokens 48 against 55; over pages they take 897 against 862).
 //
 // A warp goes by its own 32 rows: a tile that all of them see all of takes the short loop, one that
 // none sees gets P = 0 (by the unit's 128 rows: window 146 us against 142).
 //
-// Units: the grid has a block a unit, the longest first; a resident CTA takes over a block that has
-// not begun by cancelling its launch (cluster launch control), so that uneven units (chunks of many
-// lengths) spread as CTAs get done: 16 chunks 2926 to 2636 us against a fixed walk, five small ones
-// 78 to 57. Finding units costs warp 0 alone; the other warps read them from shared memory.
+// Units: the grid has a block a unit, the longest first (two-sided documents go in the order of causal
+// ones: the first units of a long one, as long as its last, begin at the end); a resident CTA takes
+// over a block that has not begun by cancelling its launch (cluster launch control), so that uneven
+// units (chunks of many lengths) spread as CTAs get done: 16 chunks 2926 to 2636 us against a fixed
+// walk, five small ones 78 to 57. Finding units costs warp 0 alone; the other warps read them from
+// shared memory.
 //
 // What bounds it: a tile of 64 keys takes the tensor core 854 cycles for both maps at D = 128 (S
 // with N = 64 runs below the full rate; 768 would be the operations'), the exponentials 512 and the
-// loop 1068. P is rounded to bf16 (2^-8 of a weight at most), which is most of the output's error;
-// sums are those of the unrounded weights, in fp32.
+// loop 1068. P is rounded to bf16 (2^-8 of a weight at most), which is most of the output's error:
+// 2.6e-3 of |O| in 2-norm, where the output's own rounding is 1.7e-3. The rounding's rest as a second
+// bf16 term in the other half of S's columns leaves 1.7e-3 and costs a quarter to a third: causal 2 x
+// 8192 1080 to 1387 us, 16 chunks 2356 to 3035, window of 1000 131 to 165, chunks of 64 heads over 16K
+// 864 to 1175. So one term; sums are those of the unrounded weights, in fp32.
 //
-// Measured (heads 32 over 8, D = 128): causal 2 x 8192 1060 us = 1.55 PFLOP/s of the pairs under the
-// mask; 16 chunks of up to 2048 tokens over up to 16K 2.28 ms; D = 64, 3 x 5003, window of 1000 131
-// us.
+// Measured (heads 32 over 8, D = 128): causal 2 x 8192 1077 us in bursts of three at 2.07 GHz = 1.53
+// PFLOP/s of the pairs under the mask, and 1171 on end, where the power limit holds the clock at 1.90
+// GHz; 16 chunks of up to 2048 tokens over up to 16K 2.33 ms, and 2.56 at 1.83 GHz. D = 64, 3 x 5003,
+// window of 1000 131 to 134 us at 2.07 GHz either way.
 #pragma once
 
 #include <cuda_bf16.h>
