@@ -122,6 +122,8 @@ enum attn_status {
  *           is 0). Its contents need not be initialised; concurrent calls need separate ones.
  * stream    cudaStream_t to launch on.
  * A sequence with L_b = 0 gets O = 0 and LSE = -inf.
+ * Values at masked places (later keys, other documents) have to be finite: their probabilities are
+ * exactly zero, and zero times a non-finite value is not zero.
  */
 int attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
              int Hkv, int N, int d, float scale, int mask_kind, int window,
@@ -444,13 +446,15 @@ size_t attn_workspace_bytes_fp4(int B, int Hq, int Hkv, int N, int d);
  *                                                                   o = out_scale * y)
  * in fp32 from the accumulators on, rounded to bf16 once; the softmax weights enter the product
  * with v in bf16 (decode: as two bf16 terms), their sums stay fp32. A row that sees no key gets o = 0.
- * So does one whose y is all zeros, whatever eps; a map whose scores are all -inf adds nothing to y, and
- * its LSE is -inf. The norm takes y of any size (rows whose squares leave fp32 are scaled by a power of
- * two first); values up to 2^80 keep y finite under any scores.
+ * So does one whose y is all zeros, whatever eps; a map whose scores are all -inf adds nothing to y,
+ * and its LSE is -inf. The norm takes y of any size (rows whose squares leave fp32 are scaled by a
+ * power of two first); values up to 2^80 keep y finite under any scores.
  * q, o      bf16 [B,Hq,N,d] (document kinds [1,Hq,N,d]); k, v bf16 [B,Hkv,N,d]; layouts, masks,
  *           window, cu_seqlens, B, Hq, Hkv and N as for attn_fwd's prefill kinds (NONE, CAUSAL,
  *           SLIDING, SLIDING_BIDIR, DOCUMENT, DOCUMENT_BIDIR, PREFIX_LM; others: ATTN_ERR_INVALID).
- *           Values at masked places have to be finite, as for attn_fwd.
+ *           Values at masked places have to be finite, as for attn_fwd (a weight of zero times NaN
+ *           is NaN): those of later keys under a causal mask, and those of the next document, which
+ *           may lie in the same tile of keys. Keys there may hold anything.
  * lse       fp32 [B,Hq,2,N] (document kinds [1,Hq,2,N]): each map's natural log-sum-exp; -inf where
  *           a row sees no key, or none with a score above -inf.
  * lam       fp32 [Hq]: the second map's factor, of either sign.
