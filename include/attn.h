@@ -257,6 +257,7 @@ size_t attn_noalloc_scratch_bytes(void);
  *
  * A row x of d channels, in fp32, rounded to bf16 once at the end:
  *   norm      y_c = x_c * weight_c / sqrt(mean_c x_c^2 + eps)        (weight NULL: y = x)
+ *             for rows of any size; a row of zeros stays zero, with eps = 0 too
  *   rotation  for i < rot_dim / 2 the pair (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved,
  *             turns by the angle of position pos:  a' = a cos - b sin,  b' = b cos + a sin;
  *             channels >= rot_dim pass              (rot_dim 0: no rotation)

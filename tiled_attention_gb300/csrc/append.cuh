@@ -4,6 +4,7 @@
 //
 // Mathematics of one row x of D channels, all in fp32:
 //   norm      y_c = x_c * rsqrt(mean_c x_c^2 + eps) * w_c                   (optional)
+//             rows whose squares leave fp32 are taken times a power of two first (norm.cuh)
 //   rotation  pairs (i, i + R/2), or (2i, 2i + 1), i < R/2, by the position's angle i:
 //             a' = a cos - b sin,  b' = b cos + a sin                       (optional)
 //             for keys that go to 4 bits each product and sum is rounded on its own (no FMA):
@@ -27,6 +28,7 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "norm.cuh"
 #include "ptx.cuh"
 #include "sched.h"
 
@@ -294,154 +296,183 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       dst = p.pool[kind - 1] + static_cast<size_t>(phys) * (heads >> ms) * dst_step;
       if (CACHE == kCacheBf16) dst += static_cast<size_t>(slot) * (2 * D) << ms;
     }
-    for (int gb = g0; gb < g1; gb += kBatch) {
-      uint4 va[kBatch], vb[kBatch];
+    // All of the groups. any_size: each row taken times its power of two for the norm (norm.cuh);
+    // else whether a row's squares left fp32 is returned.
+    auto pass = [&](auto any_size) {
+      constexpr bool kAnySize = decltype(any_size)::value;
+      bool left = false;
+      for (int gb = g0; gb < g1; gb += kBatch) {
+        uint4 va[kBatch], vb[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int head = (gb + i) * kRows + rr;
-        va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-        if (gb + i < g1 && head < heads) {
-          const uint4* from =
-              reinterpret_cast<const uint4*>(src + static_cast<size_t>(head) * (2 * D));
-          va[i] = __ldg(from + ca);
-          vb[i] = __ldg(from + cb);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (gb + i >= g1) break;  // the same for the whole warp
-        const int head = (gb + i) * kRows + rr;
-        const bool live = head < heads && dst != nullptr;
-        uint8_t* to = dst + static_cast<size_t>(head >> ms) * dst_step;
-        if constexpr (AXES) to += (head & ((1 << ms) - 1)) * (2 * D);
-        if constexpr (kind == 2 && CACHE == kCacheBf16) {
-          if (live) {
-            reinterpret_cast<uint4*>(to)[ca] = va[i];
-            reinterpret_cast<uint4*>(to)[cb] = vb[i];
-          }
-          continue;
-        }
-        float2 a[4], b[4];
-        {
-          const uint32_t xa[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
-          const uint32_t xb[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = make_float2(__uint_as_float(xa[e] << 16), __uint_as_float(xa[e] & 0xFFFF0000u));
-            b[e] = make_float2(__uint_as_float(xb[e] << 16), __uint_as_float(xb[e] & 0xFFFF0000u));
+        for (int i = 0; i < kBatch; ++i) {
+          const int head = (gb + i) * kRows + rr;
+          va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+          if (gb + i < g1 && head < heads) {
+            const uint4* from =
+                reinterpret_cast<const uint4*>(src + static_cast<size_t>(head) * (2 * D));
+            va[i] = __ldg(from + ca);
+            vb[i] = __ldg(from + cb);
           }
         }
-        if (kind < 2 && w) {
-          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s2 = __ffma2_rn(a[e], a[e], s2);
-            s2 = __ffma2_rn(b[e], b[e], s2);
-          }
-          float ss = s2.x + s2.y;
-#pragma unroll
-          for (int off = R / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-          const float2 rs2 = make_float2(rs, rs);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = __fmul2_rn(__fmul2_rn(a[e], rs2), wa[e]);
-            b[e] = __fmul2_rn(__fmul2_rn(b[e], rs2), wb[e]);
-          }
-        }
-        if (kind < 2 && p.rot) {
-          if (split) {
-            if (paired) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 x = a[e], y = b[e];
-                if constexpr (CACHE == kCacheFp4 && kind == 1) {
-                  // Scalar: packed products and sums get contracted, whatever their rounding.
-                  a[e] = make_float2(__fsub_rn(__fmul_rn(x.x, cs[e].x), __fmul_rn(y.x, sn[e].x)),
-                                     __fsub_rn(__fmul_rn(x.y, cs[e].y), __fmul_rn(y.y, sn[e].y)));
-                  b[e] = make_float2(__fadd_rn(__fmul_rn(y.x, cs[e].x), __fmul_rn(x.x, sn[e].x)),
-                                     __fadd_rn(__fmul_rn(y.y, cs[e].y), __fmul_rn(x.y, sn[e].y)));
-                } else {
-                  a[e] = __ffma2_rn(x, cs[e], __fmul2_rn(y, ns[e]));
-                  b[e] = __ffma2_rn(y, cs[e], __fmul2_rn(x, sn[e]));
-                }
-              }
+        for (int i = 0; i < kBatch; ++i) {
+          if (gb + i >= g1) break;  // the same for the whole warp
+          const int head = (gb + i) * kRows + rr;
+          const bool live = head < heads && dst != nullptr;
+          uint8_t* to = dst + static_cast<size_t>(head >> ms) * dst_step;
+          if constexpr (AXES) to += (head & ((1 << ms) - 1)) * (2 * D);
+          if constexpr (kind == 2 && CACHE == kCacheBf16) {
+            if (live) {
+              reinterpret_cast<uint4*>(to)[ca] = va[i];
+              reinterpret_cast<uint4*>(to)[cb] = vb[i];
             }
-          } else {
+            continue;
+          }
+          float2 a[4], b[4];
+          {
+            const uint32_t xa[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
+            const uint32_t xb[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              auto turn = [](float2& v, float c, float s) {
-                v = make_float2(__fsub_rn(__fmul_rn(v.x, c), __fmul_rn(v.y, s)),
-                                __fadd_rn(__fmul_rn(v.y, c), __fmul_rn(v.x, s)));
-              };
-              const int h = e >> 1;
-              if (turn_a) turn(a[e], e & 1 ? cs[h].y : cs[h].x, e & 1 ? sn[h].y : sn[h].x);
-              if (turn_b)
-                turn(b[e], e & 1 ? cs[2 + h].y : cs[2 + h].x, e & 1 ? sn[2 + h].y : sn[2 + h].x);
+              a[e] = make_float2(__uint_as_float(xa[e] << 16),
+                                 __uint_as_float(xa[e] & 0xFFFF0000u));
+              b[e] = make_float2(__uint_as_float(xb[e] << 16),
+                                 __uint_as_float(xb[e] & 0xFFFF0000u));
             }
           }
-        }
-        if constexpr (CACHE == kCacheFp4 && kind >= 1) {
-          // 16-channel blocks: this lane's chunk a with the partner lane's (chunk a ^ 1), and
-          // b with its; past the rotated channels of a half-split, a with b.
-          const float2 inv = make_float2(p.inv_scale[kind - 1], p.inv_scale[kind - 1]);
-          float ma = 0.f, mb = 0.f;
+          if (kind < 2 && w) {
+            auto squares = [&] {
+              float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = __fmul2_rn(a[e], inv);
-            b[e] = __fmul2_rn(b[e], inv);
-            ma = fmax_nan(ma, fmax_nan(fabsf(a[e].x), fabsf(a[e].y)));
-            mb = fmax_nan(mb, fmax_nan(fabsf(b[e].x), fabsf(b[e].y)));
-          }
-          const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
-          const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
-          if (paired) {
-            ma = fmax_nan(ma, oa), mb = fmax_nan(mb, ob);
-          } else {
-            ma = mb = fmax_nan(ma, mb);
-          }
-          // From kFp4Large on scale and codes saturate (448 * 6 < kFp4Large); infinities would
-          // not go through the divisions below. A NaN stays, gives its block the scale NaN and,
-          // as that is not > 0, zero codes.
-          if (ma >= kFp4Large) {
-            ma = kFp4Large;
+              for (int e = 0; e < 4; ++e) {
+                s2 = __ffma2_rn(a[e], a[e], s2);
+                s2 = __ffma2_rn(b[e], b[e], s2);
+              }
+              float ss = s2.x + s2.y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = clamp2(a[e], kFp4Large);
-          }
-          if (mb >= kFp4Large) {
-            mb = kFp4Large;
+              for (int off = R / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+              return ss;
+            };
+            float ss = squares(), rs;
+            const float by = norm_scale(ss, p.eps);
+            if constexpr (kAnySize) {
+              const float2 by2 = make_float2(by, by);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[e] = clamp2(b[e], kFp4Large);
+              for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(a[e], by2), b[e] = __fmul2_rn(b[e], by2);
+              rs = norm_factor<D>(squares(), by, p.eps);  // (times 1: the same squares again)
+            } else {
+              left |= by != 1.f;
+              rs = rsqrtf(ss * (1.f / D) + p.eps);
+            }
+            const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = __fmul2_rn(__fmul2_rn(a[e], rs2), wa[e]);
+              b[e] = __fmul2_rn(__fmul2_rn(b[e], rs2), wb[e]);
+            }
           }
-          // max / 6, correctly rounded as in divide8, then to E4M3.
-          constexpr float kSixth = 1.f / 6.f;
-          const float qa = ma * kSixth, qm = mb * kSixth;
-          const float da = fmaf(fmaf(qa, -6.f, ma), kSixth, qa);
-          const float db = fmaf(fmaf(qm, -6.f, mb), kSixth, qm);
-          const uint32_t sf = f32x2_to_e4m3(da, db);
-          const uint32_t sh = e4m3x2_to_f16(sf);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sh));
-          // A zero scale: zeros, not quotients.
-          divide8(a, f.x, f.x > 0.f ? __frcp_rn(f.x) : 0.f);
-          divide8(b, f.y, f.y > 0.f ? __frcp_rn(f.y) : 0.f);
-          if (live) {
-            uint32_t* codes = reinterpret_cast<uint32_t*>(to + slot * fp4_code_bytes(D));
-            uint8_t* scales = to + (fp4_code_bytes(D) << p.page_shift) + slot * fp4_scale_bytes(D);
-            codes[ca] = f.x > 0.f ? f32x8_to_e2m1(a) : 0u;
-            codes[cb] = f.y > 0.f ? f32x8_to_e2m1(b) : 0u;
-            if (!(ca & 1)) scales[ca >> 1] = static_cast<uint8_t>(sf);
-            if (!(cb & 1)) scales[cb >> 1] = static_cast<uint8_t>(sf >> 8);
+          if (kind < 2 && p.rot) {
+            if (split) {
+              if (paired) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 x = a[e], y = b[e];
+                  if constexpr (CACHE == kCacheFp4 && kind == 1) {
+                    // Scalar: packed products and sums get contracted, whatever their rounding.
+                    a[e] = make_float2(__fsub_rn(__fmul_rn(x.x, cs[e].x), __fmul_rn(y.x, sn[e].x)),
+                                       __fsub_rn(__fmul_rn(x.y, cs[e].y), __fmul_rn(y.y, sn[e].y)));
+                    b[e] = make_float2(__fadd_rn(__fmul_rn(y.x, cs[e].x), __fmul_rn(x.x, sn[e].x)),
+                                       __fadd_rn(__fmul_rn(y.y, cs[e].y), __fmul_rn(x.y, sn[e].y)));
+                  } else {
+                    a[e] = __ffma2_rn(x, cs[e], __fmul2_rn(y, ns[e]));
+                    b[e] = __ffma2_rn(y, cs[e], __fmul2_rn(x, sn[e]));
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                auto turn = [](float2& v, float c, float s) {
+                  v = make_float2(__fsub_rn(__fmul_rn(v.x, c), __fmul_rn(v.y, s)),
+                                  __fadd_rn(__fmul_rn(v.y, c), __fmul_rn(v.x, s)));
+                };
+                const int h = e >> 1;
+                if (turn_a) turn(a[e], e & 1 ? cs[h].y : cs[h].x, e & 1 ? sn[h].y : sn[h].x);
+                if (turn_b)
+                  turn(b[e], e & 1 ? cs[2 + h].y : cs[2 + h].x, e & 1 ? sn[2 + h].y : sn[2 + h].x);
+              }
+            }
           }
-        } else if (live) {
-          reinterpret_cast<uint4*>(to)[ca] =
-              make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y),
-                         pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[3].x, a[3].y));
-          reinterpret_cast<uint4*>(to)[cb] =
-              make_uint4(pack_bf16x2(b[0].x, b[0].y), pack_bf16x2(b[1].x, b[1].y),
-                         pack_bf16x2(b[2].x, b[2].y), pack_bf16x2(b[3].x, b[3].y));
+          if constexpr (CACHE == kCacheFp4 && kind >= 1) {
+            // 16-channel blocks: this lane's chunk a with the partner lane's (chunk a ^ 1), and
+            // b with its; past the rotated channels of a half-split, a with b.
+            const float2 inv = make_float2(p.inv_scale[kind - 1], p.inv_scale[kind - 1]);
+            float ma = 0.f, mb = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = __fmul2_rn(a[e], inv);
+              b[e] = __fmul2_rn(b[e], inv);
+              ma = fmax_nan(ma, fmax_nan(fabsf(a[e].x), fabsf(a[e].y)));
+              mb = fmax_nan(mb, fmax_nan(fabsf(b[e].x), fabsf(b[e].y)));
+            }
+            const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
+            const float ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+            if (paired) {
+              ma = fmax_nan(ma, oa), mb = fmax_nan(mb, ob);
+            } else {
+              ma = mb = fmax_nan(ma, mb);
+            }
+            // From kFp4Large on scale and codes saturate (448 * 6 < kFp4Large); infinities would
+            // not go through the divisions below. A NaN stays, gives its block the scale NaN and,
+            // as that is not > 0, zero codes.
+            if (ma >= kFp4Large) {
+              ma = kFp4Large;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[e] = clamp2(a[e], kFp4Large);
+            }
+            if (mb >= kFp4Large) {
+              mb = kFp4Large;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = clamp2(b[e], kFp4Large);
+            }
+            // max / 6, correctly rounded as in divide8, then to E4M3.
+            constexpr float kSixth = 1.f / 6.f;
+            const float qa = ma * kSixth, qm = mb * kSixth;
+            const float da = fmaf(fmaf(qa, -6.f, ma), kSixth, qa);
+            const float db = fmaf(fmaf(qm, -6.f, mb), kSixth, qm);
+            const uint32_t sf = f32x2_to_e4m3(da, db);
+            const uint32_t sh = e4m3x2_to_f16(sf);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sh));
+            // A zero scale: zeros, not quotients.
+            divide8(a, f.x, f.x > 0.f ? __frcp_rn(f.x) : 0.f);
+            divide8(b, f.y, f.y > 0.f ? __frcp_rn(f.y) : 0.f);
+            if (live) {
+              uint32_t* codes = reinterpret_cast<uint32_t*>(to + slot * fp4_code_bytes(D));
+              uint8_t* scales =
+                  to + (fp4_code_bytes(D) << p.page_shift) + slot * fp4_scale_bytes(D);
+              codes[ca] = f.x > 0.f ? f32x8_to_e2m1(a) : 0u;
+              codes[cb] = f.y > 0.f ? f32x8_to_e2m1(b) : 0u;
+              if (!(ca & 1)) scales[ca >> 1] = static_cast<uint8_t>(sf);
+              if (!(cb & 1)) scales[cb >> 1] = static_cast<uint8_t>(sf >> 8);
+            }
+          } else if (live) {
+            reinterpret_cast<uint4*>(to)[ca] =
+                make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y),
+                           pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[3].x, a[3].y));
+            reinterpret_cast<uint4*>(to)[cb] =
+                make_uint4(pack_bf16x2(b[0].x, b[0].y), pack_bf16x2(b[1].x, b[1].y),
+                           pack_bf16x2(b[2].x, b[2].y), pack_bf16x2(b[3].x, b[3].y));
+          }
         }
       }
-    }
+      return left;
+    };
+    // Such rows are rare, and all of the warp's are then taken again. (A check and a branch a group
+    // keep the groups' sums from running side by side: 2 x 8192 tokens 56 to 59 us, 16 chunks of 1024
+    // appended in 4 bits 71 to 77; this way 56 and 72.)
+    const bool left = pass(std::false_type{});
+    if constexpr (kind < 2)
+      if (__any_sync(0xffffffffu, left)) pass(std::true_type{});
   };
   // This warp's share of the token's row groups: [g0, g1) of q's, then k's, then v's.
   const int g0 = static_cast<int>(blockIdx.y) * p.groups_per_task;

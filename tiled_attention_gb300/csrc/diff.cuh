@@ -63,7 +63,7 @@
 
 #include <cuda_bf16.h>
 
-#include "diff_norm.cuh"
+#include "norm.cuh"
 #include "prefill.cuh"
 #include "ptx.cuh"
 #include "sched.h"

@@ -32,7 +32,7 @@
 #include <type_traits>
 
 #include "decode.cuh"
-#include "diff_norm.cuh"
+#include "norm.cuh"
 #include "ptx.cuh"
 #include "sched.h"
 #include "share.cuh"

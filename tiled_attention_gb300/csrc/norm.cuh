@@ -1,5 +1,5 @@
-// diff_norm.cuh — the norm of differential attention's rows, y / sqrt(mean y^2 + eps), for rows of any
-// size that fp32 holds.
+// norm.cuh — the norm y / sqrt(mean y^2 + eps) of the token rows and of differential attention's rows,
+// for rows of any size that fp32 holds.
 //
 // Squares in fp32 overflow from |y| = 2^64 on and vanish below 2^-75. A row whose squares would is
 // taken times a power of two first, and eps times its square, which leaves the quotient as it is. Other
